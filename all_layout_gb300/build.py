@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libxs.so")
-SOURCES = ("attn.cu", "scatter.cu", "api.cu", "noalloc.cu", "probe.cu")
+SOURCES = ("attn.cu", "scatter.cu", "api.cu", "noalloc.cu", "probe.cu", "rope.cu")
 HEADERS = (os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "attn_wide.cuh"),
            os.path.join(ROOT, "include", "xs.h"))

@@ -14,7 +14,28 @@
 
 #define XS_API extern "C" __attribute__((visibility("default")))
 
+namespace xs {
+
+int sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  static std::mutex mu;
+  static int cached[64] = {0};
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 0 || dev >= 64) return -1;
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+}  // namespace xs
+
 namespace {
+
+using xs::sm_count;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -36,21 +57,6 @@ EncodeTiledFn encode_fn() {
       fn = reinterpret_cast<EncodeTiledFn>(ptr);
   });
   return fn;
-}
-
-int sm_count() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  static std::mutex mu;
-  static int cached[64] = {0};
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev < 0 || dev >= 64) return -1;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -158,9 +164,9 @@ xs_status validate(const void *const *ptrs, int nptrs, void *const *shards, int 
 struct MapKey {
   const void *base;
   int rank;
-  cuuint64_t dims[3];
-  cuuint64_t strides[2];
-  cuuint32_t box[3];
+  cuuint64_t dims[4];
+  cuuint64_t strides[3];
+  cuuint32_t box[4];
 };
 struct MapEntry {
   MapKey key;
@@ -194,7 +200,7 @@ bool encode(CUtensorMap *m, void *base, int rank, const cuuint64_t *dims,
   }
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
   if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), base, dims,
          strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -350,6 +356,24 @@ bool empty(int B, int N, int H) { return B == 0 || N == 0 || H == 0; }
 
 }  // namespace
 
+namespace xs {
+
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+bool encode_map(CUtensorMap *m, const void *base, int rank, const unsigned long long *dims,
+                const unsigned long long *strides_bytes, const unsigned *box) {
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i + 1 < rank) st[i] = strides_bytes[i];
+  }
+  return encode(m, const_cast<void *>(base), rank, d, st, bx);
+}
+
+}  // namespace xs
+
 XS_API xs_status xs_attn_fused(const void *q, const void *k, const void *v,
                                void *const *out_shards, int B, int N, int H, int d, int P,
                                int store_tile, void *stream) {
@@ -457,8 +481,8 @@ XS_API const char *xs_status_string(xs_status s) {
     case XS_OK: return "ok";
     case XS_ERR_INVALID: return "invalid argument";
     case XS_ERR_UNSUPPORTED:
-      return "unsupported shape (d must be 64, 128 or 256, N a multiple of 128; d = 256 needs "
-             "store_tile 8)";
+      return "unsupported shape or type (attention: d must be 64, 128 or 256, N a multiple of 128, "
+             "d = 256 needs store_tile 8; other calls: see their comments in xs.h)";
     case XS_ERR_ALIGN: return "pointer not 16-byte aligned";
     case XS_ERR_CUDA: return "CUDA error";
     case XS_ERR_TIMEOUT: return "on-chip wait timed out";

@@ -1284,6 +1284,10 @@ cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+cudaError_t device_status_word(int **out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_status);
+}
+
 cudaError_t read_and_clear_status(cudaStream_t s, int *out) {
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return e;

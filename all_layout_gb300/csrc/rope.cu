@@ -1,0 +1,358 @@
+// Rotary positions with several axes, with the per-head RMS norm of q and k, from
+// the token-major output of the QKV projection [B][N][heads][d] to the head-major
+// tensors [B][heads][N][d] that attention reads (any strides on both sides; in
+// place when a tensor's two sides are the same).
+//
+// Per row x (one token, one head) of a tensor with a weight w:
+//     x <- x / sqrt(mean(x^2) + eps) * w,
+// and of a rotated tensor, for every pair (a, b) of its first `rot` columns, with
+// the pair's axis and frequency f: angle = pos[axis] * f,
+//     (a, b) <- (a cos - b sin, b cos + a sin).
+//
+// Angles. A frequency is held as a 64-bit fixed-point fraction of a turn, so
+// pos * f modulo one turn is one wrapping integer product: exact for every 32-bit
+// position, negative ones included, with no range reduction. Its top 32 bits, as a
+// signed fraction of a half turn, go to sincospif in fp32 (error below 2^-24 of a
+// turn plus sincospif's own).
+//
+// Bound: HBM. Every value is read once and written once. A thread keeps one token and eight
+// columns and walks the heads, so the four (adjacent pairs) or eight (half pairs)
+// sines and cosines of its columns are computed once and stay in registers for all
+// heads of q and k; the norm's sum runs over the lanes of the row by shuffles, and
+// the partner columns of half pairs come from their lane by shuffles. There is no
+// shared memory and no barrier. UNROLL rows are loaded before the first is used.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/xs.h"
+#include "internal.h"
+
+namespace xs {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxPairs = 128;
+
+struct RopeTensor {
+  const void *x;
+  void *y;
+  const float *w;                 // [d] or null
+  long long x_b, x_n, x_h;        // strides in elements: batch, token, head
+  long long y_b, y_n, y_h;
+  int heads, rotate;
+};
+
+struct RopeParams {
+  RopeTensor t[3];
+  int n_tensors, items;           // items: heads of all tensors
+  const int *pos;                 // [B or 1][N][n_axes]
+  long long pos_b;                // elements between batch entries (0: shared)
+  int n_axes, adjacent;
+  int B, N, d, rot;
+  int lanes;                      // lanes per row, the power of two >= d / 8
+  int items_per_block;            // of the heads of all tensors, per blockIdx.y
+  float eps;
+  unsigned long long freq[kRopeMaxPairs];   // turns per position step, 64-bit fraction
+  unsigned char axis[kRopeMaxPairs];
+};
+
+__device__ __forceinline__ uint4 ld16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Eight values of a type as they lie in memory, and as fp32.
+template <class T>
+struct Eight {
+  uint4 v[sizeof(T) * 8 / 16];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = ld16(p + i * (16 / sizeof(T)));
+  }
+};
+__device__ __forceinline__ void widen(const Eight<__nv_bfloat16> &e, float (&f)[8]) {
+  const uint32_t u[4] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(const Eight<__half> &e, float (&f)[8]) {
+  const uint32_t u[4] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2 h;
+    memcpy(&h, &u[i], 4);
+    const float2 g = __half22float2(h);
+    f[2 * i] = g.x;
+    f[2 * i + 1] = g.y;
+  }
+}
+__device__ __forceinline__ void widen(const Eight<float> &e, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = __uint_as_float(e.v[i].x);
+    f[4 * i + 1] = __uint_as_float(e.v[i].y);
+    f[4 * i + 2] = __uint_as_float(e.v[i].z);
+    f[4 * i + 3] = __uint_as_float(e.v[i].w);
+  }
+}
+// The one rounding of an output value, to nearest even.
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    memcpy(&u[i], &h, 4);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    memcpy(&u[i], &h, 4);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// cos and sin of a pair at position `pos`.
+__device__ __forceinline__ void pair_angle(const RopeParams &p, const int *pos, int pair, float &c,
+                                           float &s) {
+  const long long at = pos[p.axis[pair]];
+  const unsigned long long turn = static_cast<unsigned long long>(at) * p.freq[pair];
+  const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
+  sincospif(half_turns, &s, &c);
+}
+
+template <class TI, class TO, bool ADJ>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int UNROLL = sizeof(TI) == 2 ? 4 : 2;
+  constexpr int NP = ADJ ? 4 : 8;   // pairs that touch this thread's columns
+  const int lanes = p.lanes;
+  const int c = threadIdx.x & (lanes - 1);            // eight columns from 8 * c
+  const long long token = static_cast<long long>(blockIdx.x) * (kRopeThreads / lanes) +
+                          threadIdx.x / lanes;
+  const long long tokens = static_cast<long long>(p.B) * p.N;
+  // Idle lanes (past the row, past the last token) load nothing and store nothing but take part in the shuffles.
+  const bool live = token < tokens && c * 8 < p.d;
+  const int b = live ? static_cast<int>(token / p.N) : 0;
+  const int n = live ? static_cast<int>(token - static_cast<long long>(b) * p.N) : 0;
+
+  const int half = p.rot / 2;
+  // Half pairs: columns [0, half) pair with [half, rot); both are whole eights.
+  const bool low = c * 8 < half;
+  const bool turned = c * 8 < p.rot;
+  const int partner = (threadIdx.x & 31) + (!turned ? 0 : low ? half / 8 : -(half / 8));
+  float cs[NP], sn[NP];
+  {
+    const int *pos = p.pos + b * p.pos_b + static_cast<long long>(n) * p.n_axes;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int pair = ADJ ? 4 * c + i : (low ? 8 * c + i : 8 * c + i - half);
+      cs[i] = 1.f;
+      sn[i] = 0.f;
+      if (live && (ADJ ? pair < half : turned)) {
+        pair_angle(p, pos, pair, cs[i], sn[i]);
+        if (!ADJ && low) sn[i] = -sn[i];   // own * cos + partner * sn, for either side
+      }
+    }
+  }
+
+  const int item0 = blockIdx.y * p.items_per_block;
+  const int item1 = min(item0 + p.items_per_block, p.items);
+  int first = 0;   // item of the tensor's head 0
+#pragma unroll 1
+  for (int ti = 0; ti < p.n_tensors; ++ti) {
+    const RopeTensor &t = p.t[ti];
+    const int h0 = max(item0 - first, 0), h1 = min(item1 - first, t.heads);
+    first += t.heads;
+    if (h0 >= h1) continue;
+    const TI *x = static_cast<const TI *>(t.x) + b * t.x_b + n * t.x_n + c * 8;
+    TO *y = static_cast<TO *>(t.y) + b * t.y_b + n * t.y_n + c * 8;
+    const bool norm = t.w != nullptr;
+    float w[8];
+    if (norm && live) {
+      const float4 w0 = __ldg(reinterpret_cast<const float4 *>(t.w) + 2 * c);
+      const float4 w1 = __ldg(reinterpret_cast<const float4 *>(t.w) + 2 * c + 1);
+      w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
+      w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    }
+#pragma unroll 1
+    for (int h = h0; h < h1; h += UNROLL) {
+      Eight<TI> raw[UNROLL];
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k) {
+        memset(&raw[k], 0, sizeof(raw[k]));
+        if (live && h + k < h1) raw[k].load(x + (h + k) * t.x_h);
+      }
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k) {
+        if (h + k >= h1) break;
+        float f[8];
+        widen(raw[k], f);
+        if (norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+          for (int o = lanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float r = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= r * w[i];
+        }
+        if (t.rotate) {
+          if constexpr (ADJ) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = f[2 * i], e = f[2 * i + 1];
+              if (4 * c + i < half) {   // the columns past rot stay, infinities among them
+                f[2 * i] = a * cs[i] - e * sn[i];
+                f[2 * i + 1] = e * cs[i] + a * sn[i];
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float e = __shfl_sync(0xffffffffu, f[i], partner);
+              if (turned) f[i] = f[i] * cs[i] + e * sn[i];
+            }
+          }
+        }
+        if (live) store8(y + (h + k) * t.y_h, f);
+      }
+    }
+  }
+}
+
+template <class TI, class TO>
+cudaError_t launch_typed(const RopeParams &p, dim3 grid, cudaStream_t s) {
+  if (p.adjacent)
+    rope_kernel<TI, TO, true><<<grid, kRopeThreads, 0, s>>>(p);
+  else
+    rope_kernel<TI, TO, false><<<grid, kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope(const RopeParams &p, int in, int out, dim3 grid, cudaStream_t s) {
+  if (in == XS_BF16 && out == XS_BF16) return launch_typed<__nv_bfloat16, __nv_bfloat16>(p, grid, s);
+  if (in == XS_FP16 && out == XS_FP16) return launch_typed<__half, __half>(p, grid, s);
+  if (in == XS_FP16) return launch_typed<__half, __nv_bfloat16>(p, grid, s);
+  if (out == XS_FP32) return launch_typed<float, float>(p, grid, s);
+  return launch_typed<float, __nv_bfloat16>(p, grid, s);
+}
+
+bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+}  // namespace
+}  // namespace xs
+
+extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
+    const xs_rope_tensor *tensors, int n_tensors, const int *pos, long long pos_batch_stride,
+    const int *axis_dims, int n_axes, const double *freqs, int B, int N, int d, float eps,
+    int flags, int in_type, int out_type, void *stream) {
+  using namespace xs;
+  if (!tensors || !pos || !axis_dims || !freqs || n_tensors < 1 || n_tensors > 3 || B < 0 ||
+      N < 0 || d < 0 || n_axes < 1 || n_axes > 4 || (flags & ~XS_ROPE_ADJACENT) != 0 ||
+      !(eps >= 0.f) || std::isinf(eps) || pos_batch_stride < 0)
+    return XS_ERR_INVALID;
+  for (int t : {in_type, out_type})
+    if (t != XS_BF16 && t != XS_FP16 && t != XS_FP32) return XS_ERR_INVALID;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int a = 0; a < n_axes; ++a) {
+    if (axis_dims[a] < 2 || axis_dims[a] % 2 != 0 || axis_dims[a] > d - p.rot) return XS_ERR_INVALID;
+    p.rot += axis_dims[a];
+  }
+  const bool adjacent = (flags & XS_ROPE_ADJACENT) != 0;
+  long long items = 0;
+  // The strides of a tensor without rows say nothing.
+  auto has_rows = [&](const xs_rope_tensor &t) { return B > 0 && N > 0 && t.heads > 0; };
+  for (int i = 0; i < n_tensors; ++i) {
+    const xs_rope_tensor &t = tensors[i];
+    if (!t.x || !t.y || t.heads < 0) return XS_ERR_INVALID;
+    if (!has_rows(t)) {
+      items += t.heads;
+      continue;
+    }
+    const long long extent[3] = {B, N, t.heads};
+    bool same = true;
+    for (int k = 0; k < 3; ++k) {
+      if (t.x_stride[k] < 0 || t.y_stride[k] < 0) return XS_ERR_INVALID;
+      if (extent[k] > 1 && t.y_stride[k] < d) return XS_ERR_INVALID;   // rows of y would overlap
+      if (extent[k] > 1 && t.x_stride[k] != t.y_stride[k]) same = false;
+    }
+    // In place only where every row is written to where it was read.
+    if (t.x == t.y && (!same || in_type != out_type)) return XS_ERR_INVALID;
+    items += t.heads;
+  }
+  if (d < 8 || d > 256 || d % 8 != 0 || (!adjacent && p.rot % 16 != 0)) return XS_ERR_UNSUPPORTED;
+  if (!(in_type == out_type || (in_type != XS_BF16 && out_type == XS_BF16))) return XS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * N > 0x7fffffffLL || items > 65535) return XS_ERR_UNSUPPORTED;
+  const int in_vec = in_type == XS_FP32 ? 4 : 8, out_vec = out_type == XS_FP32 ? 4 : 8;
+  for (int i = 0; i < n_tensors; ++i) {
+    const xs_rope_tensor &t = tensors[i];
+    if (!aligned(t.x, 16) || !aligned(t.y, 16) || !aligned(t.weight, 16)) return XS_ERR_ALIGN;
+    const long long extent[3] = {B, N, t.heads};
+    for (int k = 0; k < 3; ++k)
+      if (extent[k] > 1 && (t.x_stride[k] % in_vec != 0 || t.y_stride[k] % out_vec != 0))
+        return XS_ERR_ALIGN;
+  }
+  if (!aligned(pos, 4)) return XS_ERR_ALIGN;
+  for (int a = 0, pair = 0; a < n_axes; ++a)
+    for (int i = 0; i < axis_dims[a] / 2; ++i, ++pair) {
+      if (!std::isfinite(freqs[pair])) return XS_ERR_INVALID;
+      double turns = freqs[pair] / 6.283185307179586476925;
+      turns -= std::floor(turns);   // whole turns per step do not show at integer positions
+      p.freq[pair] = turns < 1.0 ? static_cast<unsigned long long>(turns * 0x1p64) : 0ull;
+      p.axis[pair] = static_cast<unsigned char>(a);
+    }
+  if (B == 0 || N == 0 || items == 0) return XS_OK;
+  for (int i = 0; i < n_tensors; ++i) {
+    const xs_rope_tensor &t = tensors[i];
+    p.t[i] = RopeTensor{t.x, t.y, t.weight, t.x_stride[0], t.x_stride[1], t.x_stride[2],
+                        t.y_stride[0], t.y_stride[1], t.y_stride[2], t.heads, t.rotate};
+  }
+  p.n_tensors = n_tensors;
+  p.items = static_cast<int>(items);
+  p.pos = pos;
+  p.pos_b = pos_batch_stride;
+  p.n_axes = n_axes;
+  p.adjacent = adjacent;
+  p.B = B;
+  p.N = N;
+  p.d = d;
+  p.eps = eps;
+  p.lanes = 1;
+  while (p.lanes * 8 < d) p.lanes *= 2;
+  const int sms = sm_count();
+  if (sms <= 0) return XS_ERR_CUDA;
+  const long long rows = kRopeThreads / p.lanes;   // tokens of a block
+  const long long gx = (static_cast<long long>(B) * N + rows - 1) / rows;
+  // Few tokens: the heads are spread over blocks too, down to four per block, until there are
+  // enough blocks for every SM; each repeats its tokens' sines and cosines.
+  long long gy = (2LL * sms + gx - 1) / gx;
+  if (gy > (items + 3) / 4) gy = (items + 3) / 4;
+  p.items_per_block = static_cast<int>((items + gy - 1) / gy);
+  gy = (items + p.items_per_block - 1) / p.items_per_block;
+  return launch_rope(p, in_type, out_type, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)),
+                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? XS_OK
+             : XS_ERR_CUDA;
+}

@@ -8,6 +8,7 @@ loudly if the library has not been built; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -20,6 +21,10 @@ _HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__)
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_ALIGN, ERR_CUDA, ERR_TIMEOUT = range(6)
 FLAG_COMPLETION_COUPLED = 1
 MAX_SHARDS = 8
+
+
+ROPE_ADJACENT = 1
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class XsError(RuntimeError):
@@ -61,6 +66,17 @@ _lib.xs_set_workspace.restype = _i
 _lib.xs_workspace_bytes.argtypes = [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_ulonglong),
                                     ctypes.POINTER(ctypes.c_int)]
 _lib.xs_workspace_bytes.restype = _i
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", _vp), ("y", _vp), ("weight", _vp), ("x_stride", ctypes.c_longlong * 3),
+                ("y_stride", ctypes.c_longlong * 3), ("heads", _i), ("rotate", _i)]
+
+
+_lib.xs_rope.argtypes = [ctypes.POINTER(_RopeTensor), _i, _vp, ctypes.c_longlong,
+                         ctypes.POINTER(_i), _i, ctypes.POINTER(ctypes.c_double), _i, _i, _i,
+                         ctypes.c_float, _i, _i, _i, _vp]
+_lib.xs_rope.restype = _i
 
 
 def library():
@@ -179,6 +195,93 @@ def attn_serial_noalloc(q, k, v, shards, stream=None):
     pp, keep = _shard_array(shards)
     _check(_lib.xs_attn_serial_noalloc(_ptr(q), _ptr(k), _ptr(v), pp, B, N, H, d, len(shards),
                                        _stream(stream)), "xs_attn_serial_noalloc")
+
+
+def _require(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(device, call, stream, *args):
+    """call(*args, stream) with `device` current; the default stream is that device's current one."""
+    if torch.cuda.current_device() == device.index:
+        return call(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return call(*args, _stream(stream))
+
+
+def _cuda_operand(name, t, dtype, shape, device):
+    _require(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
+    _require(t.device == device, f"{name} is on {t.device}, not on {device}")
+    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _require(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_axes(axis_dims, theta, freqs):
+    """Host arrays (axis_dims, radians per position step of every pair) for the C call."""
+    if freqs is None:
+        freqs = [float(theta) ** (-2.0 * i / a) for a in axis_dims for i in range(a // 2)]
+    dims = (_i * max(1, len(axis_dims)))(*axis_dims)
+    return dims, (ctypes.c_double * max(1, len(freqs)))(*freqs)
+
+
+def qkv_rope(q_in, k_in, v_in, q, k, v, pos, axis_dims, *, theta: float = 10000.0, freqs=None,
+             q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = True,
+             stream=None):
+    """Rotary positions with several axes, with the RMS norm of q and k (see xs_rope in xs.h).
+
+    q_in, k_in, v_in: [B, N, heads, d] views of the projection's output (any strides, d
+    contiguous; bf16, fp16 or fp32); q, k, v: the outputs [B, heads, N, d], views of any strides
+    too (an input's own .transpose(1, 2) updates it in place), of the same type or bf16. k and v
+    may be None, in pairs with their inputs; v is moved without a rotation. pos: int32 [N, axes]
+    or [B, N, axes]. axis_dims: columns of each axis (their sum is rotated); pair i of an axis
+    of a columns turns by theta**(-2i/a) radians a step, or by freqs, one value a pair.
+    interleaved: columns (2i, 2i + 1) are a pair; otherwise (i, i + rotated/2).
+    q_weight, k_weight: fp32 [d], or None for no norm."""
+    _require(isinstance(q_in, torch.Tensor) and q_in.is_cuda and q_in.dim() == 4,
+             "q_in must be a CUDA tensor [B, N, heads, d]")
+    B, N, _, d = q_in.shape
+    dev, src = q_in.device, q_in.dtype
+    _require(src in _TYPES, f"q_in must be bf16, fp16 or fp32, not {src}")
+    dst = q.dtype if isinstance(q, torch.Tensor) else None
+    _require(dst in _TYPES, "q must be a bf16, fp16 or fp32 tensor")
+    axis_dims = tuple(int(a) for a in axis_dims)
+    n_axes, rot = len(axis_dims), sum(axis_dims)
+    _require(1 <= n_axes <= 4, "axis_dims must name 1 to 4 axes")
+    _require(isinstance(pos, torch.Tensor) and pos.dim() in (2, 3), "pos must be [N, axes] or [B, N, axes]")
+    _cuda_operand("pos", pos, torch.int32, ((B, N, n_axes) if pos.dim() == 3 else (N, n_axes)), dev)
+    _require(pos.is_contiguous(), "pos must be contiguous")
+    if freqs is not None:
+        freqs = tuple(float(f) for f in freqs)
+        _require(len(freqs) == rot // 2, f"freqs must have {rot // 2} entries")
+    arr, n = (_RopeTensor * 3)(), 0
+    for name, x, y, weight, rotate in (("q", q_in, q, q_weight, 1), ("k", k_in, k, k_weight, 1),
+                                       ("v", v_in, v, None, 0)):
+        _require((x is None) == (y is None), f"{name}_in and {name} must both be given, or neither")
+        if x is None:
+            continue
+        _require(isinstance(x, torch.Tensor) and x.dim() == 4, f"{name}_in must be [B, N, heads, d]")
+        h = x.shape[2]
+        _cuda_operand(name + "_in", x, src, (B, N, h, d), dev)
+        _cuda_operand(name, y, dst, (B, h, N, d), dev)
+        xs, ys = x.stride(), y.stride()
+        _require(d == 1 or (xs[3] == 1 and ys[3] == 1), f"the last dimension of {name}_in and {name} must be contiguous")
+        t = arr[n]
+        t.x, t.y, t.heads, t.rotate = x.data_ptr() or None, y.data_ptr() or None, h, rotate
+        t.x_stride[:] = xs[:3]
+        t.y_stride[:] = (ys[0], ys[2], ys[1])
+        if weight is not None:
+            _cuda_operand(name + "_weight", weight, torch.float32, (d,), dev)
+            _require(weight.is_contiguous(), f"{name}_weight must be contiguous")
+            t.weight = weight.data_ptr()
+        n += 1
+    if q_in.numel() == 0 and (k_in is None or k_in.numel() == 0) and (v_in is None or v_in.numel() == 0):
+        return
+    dims, table = _rope_axes(axis_dims, float(theta), freqs)
+    _check(_on(dev, _lib.xs_rope, stream, arr, n, pos.data_ptr(),
+               pos.stride(0) if pos.dim() == 3 and B > 1 else 0, dims, n_axes, table, B, N, d,
+               float(eps), ROPE_ADJACENT if interleaved else 0, _TYPES[src], _TYPES[dst]), "xs_rope")
 
 
 def store_burst_probe(dst, K, burst_bytes, n_bursts, gap_ns, mode, times, stream=None):

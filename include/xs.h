@@ -248,6 +248,61 @@ xs_status xs_set_workspace(void *ws, unsigned long long bytes, void *stream);
  * the device cannot be queried. */
 xs_status xs_workspace_bytes(int B, int N, int H, int d, unsigned long long *bytes, int *cut);
 
+/* Element types of the calls that take more than bf16. */
+#define XS_BF16 0
+#define XS_FP16 1
+#define XS_FP32 2
+
+/* One tensor of an xs_rope call: `heads` heads of rows of d contiguous values on
+ * both sides, strides in elements (batch, token, head). */
+typedef struct {
+  const void *x;           /* input, device */
+  void *y;                 /* output, device; x itself for an update in place */
+  const float *weight;     /* [d] fp32 (device): RMS-norm the row first; NULL: no norm */
+  long long x_stride[3];   /* batch, token, head; 0 repeats one row */
+  long long y_stride[3];
+  int heads;
+  int rotate;              /* 0: the row keeps its position (v, or text tokens) */
+} xs_rope_tensor;
+
+/* Flag of xs_rope: column 2i pairs with 2i + 1; without it column i of the
+ * rotated part pairs with i + rot/2. */
+#define XS_ROPE_ADJACENT 1
+
+/* Rotary positions with several axes (time, height, width of an image or video
+ * token), with the per-head RMS norm of q and k that goes before them: the step
+ * between the QKV projection and attention (Figure 5 (a)-(c): sequence-partitioned
+ * tokens become head partitions; the figure does not show positions, this call is
+ * this library's). Up to three tensors (q, k, v) in one launch, typically from the
+ * projection's token-major [B][N][heads][d] to the head-major [B][heads][N][d] of
+ * the attention calls, or in place in the sequence shards that xs_attn_ulysses
+ * reads. Per row, in fp32, rounded once at the end:
+ *     x <- x / sqrt(mean(x^2) + eps) * weight            where weight is given
+ *     (x_a, x_b) <- (x_a cos t - x_b sin t, x_b cos t + x_a sin t),  t = pos[axis] * f
+ * for every pair of the first rot = sum(axis_dims) columns of a rotated tensor; the
+ * other columns stay. Pair i (in the order of the axes) has frequency freqs[i] and
+ * belongs to the axis whose axis_dims[a]/2 pairs hold it. t is exact modulo a turn
+ * for every 32-bit position; negated positions undo a rotation.
+ *   pos               int32 (device), token n of batch entry b at
+ *                     pos + b*pos_batch_stride + n*n_axes; stride 0 shares one list
+ *   axis_dims, freqs  HOST arrays (n_axes entries; rot/2 radians per step), read
+ *                     during the call
+ *   in_type, out_type XS_BF16, XS_FP16 or XS_FP32; equal, or out_type XS_BF16
+ * Outputs must not overlap each other or another tensor's input.
+ * XS_ERR_INVALID for NULL pointers (weight aside), n_tensors not in [1, 3], negative
+ * sizes or strides, n_axes not in [1, 4], an axis width that is odd, below 2 or past
+ * d, eps negative or not finite, a frequency that is not finite, unknown flags or
+ * types, output rows that overlap (a stride below d over more than one row), or
+ * x == y with other strides or another type. XS_ERR_UNSUPPORTED for d not a multiple
+ * of 8 in [8, 256], pairs i, i + rot/2 with rot not a multiple of 16, other type
+ * pairs, B*N >= 2^31 or more than 65535 heads. XS_ERR_ALIGN unless x, y and weight are
+ * 16-byte aligned and every stride over more than one row is a multiple of 16 bytes.
+ * Empty problems return XS_OK. */
+xs_status xs_rope(const xs_rope_tensor *tensors, int n_tensors, const int *pos,
+                  long long pos_batch_stride, const int *axis_dims, int n_axes,
+                  const double *freqs, int B, int N, int d, float eps, int flags,
+                  int in_type, int out_type, void *stream);
+
 /* Static English text for a status code; never NULL. */
 const char *xs_status_string(xs_status s);
 
