@@ -15,12 +15,19 @@
 // signed fraction of a half turn, go to sincospif in fp32 (error below 2^-24 of a
 // turn plus sincospif's own).
 //
-// Bound: HBM. Every value is read once and written once. A thread keeps one token and eight
-// columns and walks the heads, so the four (adjacent pairs) or eight (half pairs)
-// sines and cosines of its columns are computed once and stay in registers for all
-// heads of q and k; the norm's sum runs over the lanes of the row by shuffles, and
-// the partner columns of half pairs come from their lane by shuffles. There is no
-// shared memory and no barrier. UNROLL rows are loaded before the first is used.
+// Bound: HBM. Every value is read once and written once. A thread keeps one token
+// and eight columns and walks the heads, so the sines and cosines of its four pairs
+// are computed once and stay in registers for all heads of q and k; the norm's sum
+// runs over the lanes of the row by shuffles. Half pairs: a thread takes four columns
+// and their four partners (two 8-byte accesses), which needs no exchange between
+// lanes. There is no shared memory and no barrier; UNROLL rows are loaded before the
+// first is used, and blocks of 128 threads at no more than 64 registers keep 32 warps
+// on an SM. Measured (GB300, device time): 65536 tokens x 72 heads x 128 with the norm
+// 378 us = 6.39 TB/s, 94% of the copy rate; 4096 tokens of the same 30.9 us (72%: one
+// wave, whose start and end show); 16384 tokens x 36 x 256 fp16 half pairs 105.9 us
+// (84%). Tried: blocks of 256 threads 381, 34.1 and 107.3 us; the weight and the
+// rotation as two factors per column (fewer operations, 72-90 registers) 402, 36 and
+// 174 us; the partner columns by shuffle 384, 32.6 and 119.7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,7 +41,7 @@
 namespace xs {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxPairs = 128;
 
 struct RopeTensor {
@@ -55,79 +62,93 @@ struct RopeParams {
   int B, N, d, rot;
   int lanes;                      // lanes per row, the power of two >= d / 8
   int items_per_block;            // of the heads of all tensors, per blockIdx.y
-  float eps;
+  float eps, inv_d;
   unsigned long long freq[kRopeMaxPairs];   // turns per position step, 64-bit fraction
   unsigned char axis[kRopeMaxPairs];
 };
 
-__device__ __forceinline__ uint4 ld16(const void *p) {
-  uint4 v;
+// Four values of a type: 8 bytes (bf16, fp16) or 16 (fp32), to and from fp32.
+template <class T>
+struct Quad {
+  uint32_t u[sizeof(T)];
+};
+__device__ __forceinline__ void ld(Quad<float> &q, const float *p) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "=r"(q.u[0]), "=r"(q.u[1]), "=r"(q.u[2]), "=r"(q.u[3])
                : "l"(p)
                : "memory");
-  return v;
 }
-
-// Eight values of a type as they lie in memory, and as fp32.
 template <class T>
-struct Eight {
-  uint4 v[sizeof(T) * 8 / 16];
-  __device__ __forceinline__ void load(const T *p) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = ld16(p + i * (16 / sizeof(T)));
-  }
-};
-__device__ __forceinline__ void widen(const Eight<__nv_bfloat16> &e, float (&f)[8]) {
-  const uint32_t u[4] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+__device__ __forceinline__ void ld(Quad<T> &q, const T *p) {
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(q.u[0]), "=r"(q.u[1])
+               : "l"(p)
+               : "memory");
+}
+// A thread's eight columns: two quads, next to each other (PAIRED: one 16-byte access for
+// 2-byte types) or half a rotation apart.
+template <bool PAIRED, class T>
+__device__ __forceinline__ void ld_row(Quad<T> (&q)[2], const T *a, const T *b) {
+  if constexpr (PAIRED && sizeof(T) == 2) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q[0].u[0]), "=r"(q[0].u[1]), "=r"(q[1].u[0]), "=r"(q[1].u[1])
+                 : "l"(a)
+                 : "memory");
+  } else {
+    ld(q[0], a);
+    ld(q[1], b);
   }
 }
-__device__ __forceinline__ void widen(const Eight<__half> &e, float (&f)[8]) {
-  const uint32_t u[4] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w};
+__device__ __forceinline__ void widen(const Quad<float> &q, float *f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(q.u[i]);
+}
+__device__ __forceinline__ void widen(const Quad<__nv_bfloat16> &q, float *f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[2 * i] = __uint_as_float(q.u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(q.u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(const Quad<__half> &q, float *f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
     __half2 h;
-    memcpy(&h, &u[i], 4);
+    memcpy(&h, &q.u[i], 4);
     const float2 g = __half22float2(h);
     f[2 * i] = g.x;
     f[2 * i + 1] = g.y;
   }
 }
-__device__ __forceinline__ void widen(const Eight<float> &e, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(e.v[i].x);
-    f[4 * i + 1] = __uint_as_float(e.v[i].y);
-    f[4 * i + 2] = __uint_as_float(e.v[i].z);
-    f[4 * i + 3] = __uint_as_float(e.v[i].w);
-  }
-}
 // The one rounding of an output value, to nearest even.
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    memcpy(&u[i], &h, 4);
-  }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+__device__ __forceinline__ uint2 narrow(const float *f, __nv_bfloat16) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  uint2 u;
+  memcpy(&u.x, &a, 4);
+  memcpy(&u.y, &b, 4);
+  return u;
 }
-__device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-    memcpy(&u[i], &h, 4);
-  }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+__device__ __forceinline__ uint2 narrow(const float *f, __half) {
+  const __half2 a = __floats2half2_rn(f[0], f[1]), b = __floats2half2_rn(f[2], f[3]);
+  uint2 u;
+  memcpy(&u.x, &a, 4);
+  memcpy(&u.y, &b, 4);
+  return u;
 }
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <bool PAIRED, class T>
+__device__ __forceinline__ void st_row(T *a, T *b, const float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4 *>(a) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4 *>(b) = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    const uint2 lo = narrow(f, T()), hi = narrow(f + 4, T());
+    if constexpr (PAIRED) {
+      *reinterpret_cast<uint4 *>(a) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+      *reinterpret_cast<uint2 *>(a) = lo;
+      *reinterpret_cast<uint2 *>(b) = hi;
+    }
+  }
 }
 
 // cos and sin of a pair at position `pos`.
@@ -140,36 +161,34 @@ __device__ __forceinline__ void pair_angle(const RopeParams &p, const int *pos, 
 }
 
 template <class TI, class TO, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 1024 / kRopeThreads)
+    rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int UNROLL = sizeof(TI) == 2 ? 4 : 2;
-  constexpr int NP = ADJ ? 4 : 8;   // pairs that touch this thread's columns
   const int lanes = p.lanes;
-  const int c = threadIdx.x & (lanes - 1);            // eight columns from 8 * c
+  const int c = threadIdx.x & (lanes - 1);
   const long long token = static_cast<long long>(blockIdx.x) * (kRopeThreads / lanes) +
                           threadIdx.x / lanes;
   const long long tokens = static_cast<long long>(p.B) * p.N;
-  // Idle lanes (past the row, past the last token) load nothing and store nothing but take part in the shuffles.
+  // Idle lanes (past the row, past the last token) load nothing and store nothing but take part
+  // in the shuffles.
   const bool live = token < tokens && c * 8 < p.d;
   const int b = live ? static_cast<int>(token / p.N) : 0;
   const int n = live ? static_cast<int>(token - static_cast<long long>(b) * p.N) : 0;
 
+  // The thread's columns: eight in a row, or (half pairs, rotated part) four and their partners.
   const int half = p.rot / 2;
-  // Half pairs: columns [0, half) pair with [half, rot); both are whole eights.
-  const bool low = c * 8 < half;
   const bool turned = c * 8 < p.rot;
-  const int partner = (threadIdx.x & 31) + (!turned ? 0 : low ? half / 8 : -(half / 8));
-  float cs[NP], sn[NP];
+  const int col_a = ADJ || !turned ? 8 * c : 4 * c;
+  const int col_b = ADJ || !turned ? 8 * c + 4 : half + 4 * c;
+  float cs[4], sn[4];
   {
     const int *pos = p.pos + b * p.pos_b + static_cast<long long>(n) * p.n_axes;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int pair = ADJ ? 4 * c + i : (low ? 8 * c + i : 8 * c + i - half);
+    for (int i = 0; i < 4; ++i) {
+      const int pair = 4 * c + i;
       cs[i] = 1.f;
       sn[i] = 0.f;
-      if (live && (ADJ ? pair < half : turned)) {
-        pair_angle(p, pos, pair, cs[i], sn[i]);
-        if (!ADJ && low) sn[i] = -sn[i];   // own * cos + partner * sn, for either side
-      }
+      if (live && pair < half) pair_angle(p, pos, pair, cs[i], sn[i]);
     }
   }
 
@@ -182,60 +201,56 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int h0 = max(item0 - first, 0), h1 = min(item1 - first, t.heads);
     first += t.heads;
     if (h0 >= h1) continue;
-    const TI *x = static_cast<const TI *>(t.x) + b * t.x_b + n * t.x_n + c * 8;
-    TO *y = static_cast<TO *>(t.y) + b * t.y_b + n * t.y_n + c * 8;
-    const bool norm = t.w != nullptr;
+    const TI *x = static_cast<const TI *>(t.x) + b * t.x_b + n * t.x_n + col_a;
+    TO *y = static_cast<TO *>(t.y) + b * t.y_b + n * t.y_n + col_a;
+    const int step = col_b - col_a;
+    const bool norm = t.w != nullptr, rotate = t.rotate != 0;
     float w[8];
-    if (norm && live) {
-      const float4 w0 = __ldg(reinterpret_cast<const float4 *>(t.w) + 2 * c);
-      const float4 w1 = __ldg(reinterpret_cast<const float4 *>(t.w) + 2 * c + 1);
-      w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
-      w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (norm && live) {
+      const float4 wa = __ldg(reinterpret_cast<const float4 *>(t.w + col_a));
+      const float4 wb = __ldg(reinterpret_cast<const float4 *>(t.w + col_b));
+      w[0] = wa.x, w[1] = wa.y, w[2] = wa.z, w[3] = wa.w;
+      w[4] = wb.x, w[5] = wb.y, w[6] = wb.z, w[7] = wb.w;
     }
 #pragma unroll 1
     for (int h = h0; h < h1; h += UNROLL) {
-      Eight<TI> raw[UNROLL];
+      Quad<TI> raw[UNROLL][2];
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k) {
         memset(&raw[k], 0, sizeof(raw[k]));
-        if (live && h + k < h1) raw[k].load(x + (h + k) * t.x_h);
+        const TI *row = x + (h + k) * t.x_h;
+        if (live && h + k < h1) ld_row<ADJ>(raw[k], row, row + step);
       }
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k) {
         if (h + k >= h1) break;
         float f[8];
-        widen(raw[k], f);
+        widen(raw[k][0], f);
+        widen(raw[k][1], f + 4);
         if (norm) {
           float ss = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-          for (int o = lanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+          for (int m = lanes / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+          const float r = rsqrtf(ss * p.inv_d + p.eps);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= r * w[i];
         }
-        if (t.rotate) {
-          if constexpr (ADJ) {
+        if (rotate) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = f[2 * i], e = f[2 * i + 1];
-              if (4 * c + i < half) {   // the columns past rot stay, infinities among them
-                f[2 * i] = a * cs[i] - e * sn[i];
-                f[2 * i + 1] = e * cs[i] + a * sn[i];
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float e = __shfl_sync(0xffffffffu, f[i], partner);
-              if (turned) f[i] = f[i] * cs[i] + e * sn[i];
+          for (int i = 0; i < 4; ++i) {
+            const int ia = ADJ ? 2 * i : i, ib = ADJ ? 2 * i + 1 : i + 4;
+            const float a = f[ia], e = f[ib];
+            if (4 * c + i < half) {   // the columns past rot stay, infinities among them
+              f[ia] = a * cs[i] - e * sn[i];
+              f[ib] = e * cs[i] + a * sn[i];
             }
           }
         }
-        if (live) store8(y + (h + k) * t.y_h, f);
+        TO *row = y + (h + k) * t.y_h;
+        if (live) st_row<ADJ>(row, row + step, f);
       }
     }
   }
@@ -302,7 +317,7 @@ extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
     if (t.x == t.y && (!same || in_type != out_type)) return XS_ERR_INVALID;
     items += t.heads;
   }
-  if (d < 8 || d > 256 || d % 8 != 0 || (!adjacent && p.rot % 16 != 0)) return XS_ERR_UNSUPPORTED;
+  if (d < 8 || d > 256 || d % 8 != 0 || (!adjacent && p.rot % 8 != 0)) return XS_ERR_UNSUPPORTED;
   if (!(in_type == out_type || (in_type != XS_BF16 && out_type == XS_BF16))) return XS_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * N > 0x7fffffffLL || items > 65535) return XS_ERR_UNSUPPORTED;
   const int in_vec = in_type == XS_FP32 ? 4 : 8, out_vec = out_type == XS_FP32 ? 4 : 8;
@@ -339,6 +354,7 @@ extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
   p.N = N;
   p.d = d;
   p.eps = eps;
+  p.inv_d = 1.f / static_cast<float>(d);
   p.lanes = 1;
   while (p.lanes * 8 < d) p.lanes *= 2;
   const int sms = sm_count();
@@ -346,8 +362,9 @@ extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
   const long long rows = kRopeThreads / p.lanes;   // tokens of a block
   const long long gx = (static_cast<long long>(B) * N + rows - 1) / rows;
   // Few tokens: the heads are spread over blocks too, down to four per block, until there are
-  // enough blocks for every SM; each repeats its tokens' sines and cosines.
-  long long gy = (2LL * sms + gx - 1) / gx;
+  // four blocks for every SM; each repeats its tokens' sines and cosines. (Measured at 4096
+  // tokens x 72 heads: 4 blocks 30.9 us, 8 32.9, 16 34.0.)
+  long long gy = (4LL * sms + gx - 1) / gx;
   if (gy > (items + 3) / 4) gy = (items + 3) / 4;
   p.items_per_block = static_cast<int>((items + gy - 1) / gy);
   gy = (items + p.items_per_block - 1) / p.items_per_block;

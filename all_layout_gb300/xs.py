@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import re
+import struct
 
 import torch
 
@@ -68,14 +69,10 @@ _lib.xs_workspace_bytes.argtypes = [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_ulon
 _lib.xs_workspace_bytes.restype = _i
 
 
-class _RopeTensor(ctypes.Structure):
-    _fields_ = [("x", _vp), ("y", _vp), ("weight", _vp), ("x_stride", ctypes.c_longlong * 3),
-                ("y_stride", ctypes.c_longlong * 3), ("heads", _i), ("rotate", _i)]
-
-
-_lib.xs_rope.argtypes = [ctypes.POINTER(_RopeTensor), _i, _vp, ctypes.c_longlong,
-                         ctypes.POINTER(_i), _i, ctypes.POINTER(ctypes.c_double), _i, _i, _i,
-                         ctypes.c_float, _i, _i, _i, _vp]
+# struct xs_rope_tensor: x, y, weight, x_stride[3], y_stride[3], heads, rotate.
+_ROPE_TENSOR = struct.Struct("@3P6q2i")
+_lib.xs_rope.argtypes = [_vp, _i, _vp, ctypes.c_longlong, _vp, _i, _vp, _i, _i, _i, ctypes.c_float,
+                         _i, _i, _i, _vp]
 _lib.xs_rope.restype = _i
 
 
@@ -202,28 +199,47 @@ def _require(ok, what):
         raise ValueError(what)
 
 
-def _on(device, call, stream, *args):
-    """call(*args, stream) with `device` current; the default stream is that device's current one."""
-    if torch.cuda.current_device() == device.index:
-        return call(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return call(*args, _stream(stream))
+def _on(index, stream, call, *args):
+    """call(*args, stream) with device `index` current; the default stream is its current one.
+    (The raw handle: building a Stream object takes longer than a small launch.)"""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _on(index, stream, call, *args)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    return call(*args, handle)
 
 
-def _cuda_operand(name, t, dtype, shape, device):
-    _require(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
-    _require(t.device == device, f"{name} is on {t.device}, not on {device}")
-    _require(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _require(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+def _operand(name, t, dtype, shape, index):
+    """Checks an operand's type, place and shape; its strides."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on cuda:{index}, not "
+                         f"{t.dtype} of shape {tuple(t.shape)} on {t.device}")
+    return t.stride()
+
+
+def _vector(name, t, dtype, size, index):
+    """Checks an optional vector operand; its address or 0."""
+    if t is None:
+        return 0
+    if _operand(name, t, dtype, (size,), index)[0] != 1 and size > 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 @functools.lru_cache(maxsize=64)
 def _rope_axes(axis_dims, theta, freqs):
-    """Host arrays (axis_dims, radians per position step of every pair) for the C call."""
+    """Host arrays of the C call (axis_dims; radians per position step of every pair) and the
+    number of axes."""
+    axis_dims = tuple(int(a) for a in axis_dims)
+    n_axes, rot = len(axis_dims), sum(axis_dims)
+    _require(1 <= n_axes <= 4 and all(a >= 2 and a % 2 == 0 for a in axis_dims),
+             "axis_dims must name 1 to 4 axes of an even number of columns each")
     if freqs is None:
         freqs = [float(theta) ** (-2.0 * i / a) for a in axis_dims for i in range(a // 2)]
-    dims = (_i * max(1, len(axis_dims)))(*axis_dims)
-    return dims, (ctypes.c_double * max(1, len(freqs)))(*freqs)
+    _require(len(freqs) == rot // 2, f"freqs must have {rot // 2} entries")
+    return (_i * n_axes)(*axis_dims), (ctypes.c_double * len(freqs))(*freqs), n_axes
 
 
 def qkv_rope(q_in, k_in, v_in, q, k, v, pos, axis_dims, *, theta: float = 10000.0, freqs=None,
@@ -242,46 +258,35 @@ def qkv_rope(q_in, k_in, v_in, q, k, v, pos, axis_dims, *, theta: float = 10000.
     _require(isinstance(q_in, torch.Tensor) and q_in.is_cuda and q_in.dim() == 4,
              "q_in must be a CUDA tensor [B, N, heads, d]")
     B, N, _, d = q_in.shape
-    dev, src = q_in.device, q_in.dtype
-    _require(src in _TYPES, f"q_in must be bf16, fp16 or fp32, not {src}")
+    dev, src = q_in.get_device(), q_in.dtype
     dst = q.dtype if isinstance(q, torch.Tensor) else None
-    _require(dst in _TYPES, "q must be a bf16, fp16 or fp32 tensor")
-    axis_dims = tuple(int(a) for a in axis_dims)
-    n_axes, rot = len(axis_dims), sum(axis_dims)
-    _require(1 <= n_axes <= 4, "axis_dims must name 1 to 4 axes")
-    _require(isinstance(pos, torch.Tensor) and pos.dim() in (2, 3), "pos must be [N, axes] or [B, N, axes]")
-    _cuda_operand("pos", pos, torch.int32, ((B, N, n_axes) if pos.dim() == 3 else (N, n_axes)), dev)
+    _require(src in _TYPES and dst in _TYPES, "q_in and q must be bf16, fp16 or fp32")
+    dims, table, n_axes = _rope_axes(tuple(axis_dims), theta, None if freqs is None else tuple(freqs))
+    _require(isinstance(pos, torch.Tensor), "pos must be [N, axes] or [B, N, axes]")
+    shared = pos.dim() == 2
+    ps = _operand("pos", pos, torch.int32, (N, n_axes) if shared else (B, N, n_axes), dev)
     _require(pos.is_contiguous(), "pos must be contiguous")
-    if freqs is not None:
-        freqs = tuple(float(f) for f in freqs)
-        _require(len(freqs) == rot // 2, f"freqs must have {rot // 2} entries")
-    arr, n = (_RopeTensor * 3)(), 0
+    packed, n, rows = b"", 0, 0
     for name, x, y, weight, rotate in (("q", q_in, q, q_weight, 1), ("k", k_in, k, k_weight, 1),
                                        ("v", v_in, v, None, 0)):
-        _require((x is None) == (y is None), f"{name}_in and {name} must both be given, or neither")
-        if x is None:
+        if x is None or y is None:
+            _require(x is y, f"{name}_in and {name} must both be given, or neither")
             continue
         _require(isinstance(x, torch.Tensor) and x.dim() == 4, f"{name}_in must be [B, N, heads, d]")
         h = x.shape[2]
-        _cuda_operand(name + "_in", x, src, (B, N, h, d), dev)
-        _cuda_operand(name, y, dst, (B, h, N, d), dev)
-        xs, ys = x.stride(), y.stride()
-        _require(d == 1 or (xs[3] == 1 and ys[3] == 1), f"the last dimension of {name}_in and {name} must be contiguous")
-        t = arr[n]
-        t.x, t.y, t.heads, t.rotate = x.data_ptr() or None, y.data_ptr() or None, h, rotate
-        t.x_stride[:] = xs[:3]
-        t.y_stride[:] = (ys[0], ys[2], ys[1])
-        if weight is not None:
-            _cuda_operand(name + "_weight", weight, torch.float32, (d,), dev)
-            _require(weight.is_contiguous(), f"{name}_weight must be contiguous")
-            t.weight = weight.data_ptr()
+        a = _operand(name + "_in", x, src, (B, N, h, d), dev)
+        b = _operand(name, y, dst, (B, h, N, d), dev)
+        if (a[3] != 1 or b[3] != 1) and d > 1:
+            raise ValueError(f"the last dimension of {name}_in and {name} must be contiguous")
+        packed += _ROPE_TENSOR.pack(x.data_ptr(), y.data_ptr(), _vector(name + "_weight", weight, torch.float32, d, dev),
+                                    a[0], a[1], a[2], b[0], b[2], b[1], h, rotate)
         n += 1
-    if q_in.numel() == 0 and (k_in is None or k_in.numel() == 0) and (v_in is None or v_in.numel() == 0):
+        rows += B * h * N
+    if rows == 0:
         return
-    dims, table = _rope_axes(axis_dims, float(theta), freqs)
-    _check(_on(dev, _lib.xs_rope, stream, arr, n, pos.data_ptr(),
-               pos.stride(0) if pos.dim() == 3 and B > 1 else 0, dims, n_axes, table, B, N, d,
-               float(eps), ROPE_ADJACENT if interleaved else 0, _TYPES[src], _TYPES[dst]), "xs_rope")
+    _check(_on(dev, stream, _lib.xs_rope, packed, n, pos.data_ptr(), 0 if shared or B == 1 else ps[0], dims,
+               n_axes, table, B, N, d, eps, ROPE_ADJACENT if interleaved else 0, _TYPES[src], _TYPES[dst]),
+           "xs_rope")
 
 
 def store_burst_probe(dst, K, burst_bytes, n_bursts, gap_ns, mode, times, stream=None):

@@ -294,7 +294,7 @@ typedef struct {
  * d, eps negative or not finite, a frequency that is not finite, unknown flags or
  * types, output rows that overlap (a stride below d over more than one row), or
  * x == y with other strides or another type. XS_ERR_UNSUPPORTED for d not a multiple
- * of 8 in [8, 256], pairs i, i + rot/2 with rot not a multiple of 16, other type
+ * of 8 in [8, 256], pairs i, i + rot/2 with rot not a multiple of 8, other type
  * pairs, B*N >= 2^31 or more than 65535 heads. XS_ERR_ALIGN unless x, y and weight are
  * 16-byte aligned and every stride over more than one row is a multiple of 16 bytes.
  * Empty problems return XS_OK. */

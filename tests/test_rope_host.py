@@ -20,11 +20,9 @@ def xs():
 
 def _call(xs, x=A, y=2 * A, w=None, xst=None, yst=None, heads=4, n=1, pos=A, pos_b=0, axes=(16, 24, 24),
           n_axes=None, freqs="default", B=2, N=8, d=64, eps=1e-6, flags=1, it=0, ot=0, tensors=True):
-    arr = (xs._RopeTensor * 3)()
-    for t in arr:
-        t.x, t.y, t.weight, t.heads, t.rotate = x, y, w, heads, 1
-        t.x_stride[:] = xst or (N * 4 * 64, 4 * 64, 64)
-        t.y_stride[:] = yst or (N * 4 * 64, 64, N * 64)
+    one = xs._ROPE_TENSOR.pack(x or 0, y or 0, w or 0, *(xst or (N * 4 * 64, 4 * 64, 64)),
+                               *(yst or (N * 4 * 64, 64, N * 64)), heads, 1)
+    arr = one * 3
     dims = (ctypes.c_int * max(1, len(axes)))(*axes)
     f = [0.5] * 128 if freqs == "default" else freqs
     table = None if f is None else (ctypes.c_double * len(f))(*f)
@@ -42,7 +40,7 @@ def _call(xs, x=A, y=2 * A, w=None, xst=None, yst=None, heads=4, n=1, pos=A, pos
     (dict(y=A), 1),                                                  # in place with other strides
     (dict(y=A, yst=(2048, 256, 64), it=1, ot=0), 1),                 # in place with another type
     (dict(d=60, axes=(16,)), 2), (dict(d=264, axes=(16,), yst=(8448, 264, 2112)), 2), (dict(d=4, axes=(2,)), 2),
-    (dict(flags=0, axes=(16, 24)), 2),                               # 40 columns in halves of 20
+    (dict(flags=0, axes=(16, 26)), 2),                               # 42 columns in halves of 21
     (dict(it=0, ot=1), 2), (dict(it=0, ot=2), 2), (dict(it=1, ot=2), 2),
     (dict(B=1 << 16, N=1 << 16), 2), (dict(heads=40000, n=3), 2),
     (dict(x=A + 8), 3), (dict(y=2 * A + 2), 3), (dict(w=A + 4), 3), (dict(pos=A + 2), 3),
@@ -67,8 +65,8 @@ def test_binding_refuses_before_the_library(xs):
 
 
 def test_default_frequencies(xs):
-    dims, table = xs._rope_axes((4, 6), 10000.0, None)
-    assert list(dims) == [4, 6]
+    dims, table, n_axes = xs._rope_axes((4, 6), 10000.0, None)
+    assert list(dims) == [4, 6] and n_axes == 2
     want = [1.0, 1e4 ** -0.5, 1.0, 1e4 ** (-1 / 3), 1e4 ** (-2 / 3)]
     assert list(table) == pytest.approx(want, rel=1e-15)
 
