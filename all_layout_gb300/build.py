@@ -17,9 +17,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libxs.so")
-SOURCES = ("attn.cu", "scatter.cu", "api.cu", "noalloc.cu", "probe.cu", "rope.cu")
+SOURCES = ("attn.cu", "scatter.cu", "api.cu", "noalloc.cu", "probe.cu", "rope.cu",
+           "attn_diff.cu", "diff_api.cu")
 HEADERS = (os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "internal.h"),
-           os.path.join(CSRC, "attn_wide.cuh"),
+           os.path.join(CSRC, "attn_wide.cuh"), os.path.join(CSRC, "diff.h"),
            os.path.join(ROOT, "include", "xs.h"))
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden"]

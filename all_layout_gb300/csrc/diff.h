@@ -1,0 +1,42 @@
+// Internal interface between the differential-attention entry points (diff_api.cu) and
+// their kernels (attn_diff.cu).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace xs {
+
+struct DiffParams {
+  // q [B][H][Nq][d], k and v [B][Hk][Nk][d], any strides: 4-D maps {d, rows, heads, batch},
+  // box {64, 128, 1, 1}, 128-byte swizzle.
+  CUtensorMap tm_q, tm_k, tm_v;
+  void *shards[kMaxShards];           // shard_mode 1: [B][Nq/P][H][d] each
+  void *o;                            // shard_mode 0: strides in elements
+  long long o_b, o_h, o_n;
+  const float *lambda;                // [H]
+  const float *weight;                // [d] or null: no norm
+  const int *kv_len;                  // [B] or null: Nk keys everywhere
+  int B, H, group, Nq, Nk;            // group: query heads per k/v head
+  int shard_mode, rows_per_shard;
+  int n_qtiles, v_parts;              // 128-row query tiles; halves of v's columns (2 at d = 256)
+  int units_b, n_units;               // units of a batch entry (H * n_qtiles * v_parts), of all
+  // Work list of a CTA (G = gridDim.x): units blockIdx.x + k*G, all of them (split = 0) or the
+  // first `waves` (split = 1); then the KV tiles of the remaining units, unit-major, in equal
+  // contiguous ranges.
+  int split, waves;
+  float scale_log2, eps, out_scale;
+  float *parts;                       // split: [G][2 slots] partial results
+  int *count;                         // split: pieces done of the unit that begins in CTA c's range
+  float *stage;                       // d = 256 with the norm: [B][H][Nq][256] fp32
+  int *status;
+  unsigned long long wait_limit_ns;
+};
+
+int diff_part_floats(int d);          // fp32 values of one piece's partial result
+cudaError_t launch_attn_diff(const DiffParams &p, int d, int grid, cudaStream_t s);
+cudaError_t launch_diff_zero(const DiffParams &p, int d, int grid, cudaStream_t s);   // no keys at all
+cudaError_t launch_diff_norm(const DiffParams &p, int grid, cudaStream_t s);
+
+}  // namespace xs

@@ -1,0 +1,212 @@
+// C-ABI entry points of differential attention (declared in include/xs.h): argument
+// validation, tensor maps, the schedule's plan and the launches. Host code only.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/xs.h"
+#include "diff.h"
+
+#define XS_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace xs;
+
+bool aligned(const void *p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+unsigned long long stage_bytes(int B, int H, int Nq, int d, bool norm) {
+  if (d != 256 || !norm) return 0;   // d <= 128: the norm is fused
+  const unsigned long long n = static_cast<unsigned long long>(B) * H * Nq * d * 4;
+  return (n + 255) / 256 * 256;
+}
+
+unsigned long long parts_bytes(int grid, int d) {
+  return static_cast<unsigned long long>(grid) * 2 * diff_part_floats(d) * 4;
+}
+
+// Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split
+// schedule. A cut unit costs about kMerge KV tiles more (its partial results are written and
+// merged), an item about kItem (its first loads and its epilogue).
+struct Plan {
+  int split, waves, grid;
+};
+constexpr long kItem = 2, kMerge = 3, kMinTiles = 4;
+
+Plan plan(long long units, int sms, int nk, bool ragged, int d, unsigned long long room) {
+  const int grid0 = units < sms ? static_cast<int>(units) : sms;
+  const Plan whole{0, 0, grid0};
+  if (nk < 2 || (units >= sms && units % sms == 0 && !ragged)) return whole;
+  const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
+  const long long T = (units - static_cast<long long>(waves) * sms) * nk;
+  long long per = (T + sms - 1) / sms;
+  int grid = sms;
+  if (waves == 0) {
+    if (per < kMinTiles) per = kMinTiles;
+    grid = static_cast<int>((T + per - 1) / per);
+  }
+  if (parts_bytes(grid, d) > room || grid > static_cast<int>(XS_WORKSPACE_HEADER_BYTES / sizeof(int)))
+    return whole;
+  const long long items = (per + nk - 1) / nk + 1;
+  const long long cost_split = waves * (nk + kItem) + per + items * kItem + 2 * kMerge;
+  const long long cost_whole = (units + grid0 - 1) / grid0 * (nk + kItem);
+  return cost_split < cost_whole || ragged ? Plan{1, waves, grid} : whole;
+}
+
+// One operand as a 4-D map {d, rows, heads, batch}; strides of single extents do not matter.
+bool encode_operand(CUtensorMap *m, const void *base, int B, int H, int N, int d,
+                    const long long *stride) {
+  const unsigned long long dims[4] = {static_cast<unsigned long long>(d), static_cast<unsigned long long>(N),
+                                      static_cast<unsigned long long>(H), static_cast<unsigned long long>(B)};
+  unsigned long long st[3] = {static_cast<unsigned long long>(stride[2]) * 2,
+                              static_cast<unsigned long long>(stride[1]) * 2,
+                              static_cast<unsigned long long>(stride[0]) * 2};
+  for (int i = 0; i < 3; ++i)
+    if (dims[i + 1] == 1) st[i] = static_cast<unsigned long long>(d) * 2;
+  const unsigned box[4] = {64, kTileRows, 1, 1};
+  return encode_map(m, base, 4, dims, st, box);
+}
+
+xs_status check_operand(const long long *stride, int B, int H, int N, int d) {
+  const long long extent[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1 && stride[i] < d) return XS_ERR_INVALID;
+  return XS_OK;
+}
+bool strides_aligned(const long long *stride, int B, int H, int N) {
+  const long long extent[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1 && (stride[i] % 8 != 0 || stride[i] >= (1LL << 38))) return false;
+  return true;
+}
+
+xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, void *const *shards,
+                    int P, void *ws, unsigned long long ws_bytes, void *stream) {
+  if (!a || !a->q || !a->lambda) return XS_ERR_INVALID;
+  const int B = a->B, H = a->H, Hk = a->H_kv, Nq = a->Nq, Nk = a->Nk, d = a->d;
+  if (B < 0 || H < 0 || Hk < 0 || Nq < 0 || Nk < 0) return XS_ERR_INVALID;
+  if (Nk > 0 && (!a->k || !a->v)) return XS_ERR_INVALID;
+  if (H > 0 && (Hk < 1 || H % Hk != 0)) return XS_ERR_INVALID;
+  if (!(a->scale > 0.f) || std::isinf(a->scale) || !(a->eps >= 0.f) || std::isinf(a->eps) ||
+      !std::isfinite(a->out_scale))
+    return XS_ERR_INVALID;
+  if (shards) {
+    if (P < 1 || P > kMaxShards || Nq % P != 0) return XS_ERR_INVALID;
+    for (int p = 0; p < P; ++p)
+      if (!shards[p]) return XS_ERR_INVALID;
+  } else if (!o || !o_stride) {
+    return XS_ERR_INVALID;
+  }
+  if (!ws && ws_bytes != 0) return XS_ERR_INVALID;
+  const bool empty = B == 0 || H == 0 || Nq == 0;
+  xs_status st = XS_OK;
+  if (!empty) {
+    st = check_operand(a->q_stride, B, H, Nq, d);
+    if (st == XS_OK && Nk > 0) st = check_operand(a->k_stride, B, Hk, Nk, d);
+    if (st == XS_OK && Nk > 0) st = check_operand(a->v_stride, B, Hk, Nk, d);
+    if (st == XS_OK && !shards) st = check_operand(o_stride, B, H, Nq, d);
+    if (st != XS_OK) return st;
+  }
+  if (d != 64 && d != 128 && d != 256) return XS_ERR_UNSUPPORTED;
+  const long long qtiles = (static_cast<long long>(Nq) + kTileRows - 1) / kTileRows;
+  const int v_parts = d == 256 ? 2 : 1;
+  if (static_cast<double>(B) * H * static_cast<double>(qtiles) * v_parts > 2147483647.0 ||
+      Nk > 0x7fffff00 || Nq > 0x7fffff00)
+    return XS_ERR_UNSUPPORTED;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(o, 16) ||
+      !aligned(a->norm_weight, 16) || !aligned(a->lambda, 4) || !aligned(a->kv_len, 4) ||
+      !aligned(ws, 256))
+    return XS_ERR_ALIGN;
+  if (shards)
+    for (int p = 0; p < P; ++p)
+      if (!aligned(shards[p], 16)) return XS_ERR_ALIGN;
+  if (empty) return XS_OK;
+  if (!strides_aligned(a->q_stride, B, H, Nq) ||
+      (Nk > 0 && (!strides_aligned(a->k_stride, B, Hk, Nk) || !strides_aligned(a->v_stride, B, Hk, Nk))) ||
+      (!shards && !strides_aligned(o_stride, B, H, Nq)))
+    return XS_ERR_ALIGN;
+  const bool norm = a->norm_weight != nullptr;
+  const unsigned long long stage = stage_bytes(B, H, Nq, d, norm);
+  if (stage > 0 && Nk > 0 && ws_bytes < XS_WORKSPACE_HEADER_BYTES + stage) return XS_ERR_INVALID;
+
+  DiffParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.B = B;
+  p.H = H;
+  p.group = H / Hk;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  if (shards) {
+    for (int i = 0; i < P; ++i) p.shards[i] = shards[i];
+    p.shard_mode = 1;
+    p.rows_per_shard = Nq / P;
+  } else {
+    p.o = o;
+    p.o_b = o_stride[0];
+    p.o_h = o_stride[1];
+    p.o_n = o_stride[2];
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return XS_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (Nk == 0) return launch_diff_zero(p, d, sms * 8, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
+  if (!encode_operand(&p.tm_q, a->q, B, H, Nq, d, a->q_stride) ||
+      !encode_operand(&p.tm_k, a->k, B, Hk, Nk, d, a->k_stride) ||
+      !encode_operand(&p.tm_v, a->v, B, Hk, Nk, d, a->v_stride))
+    return XS_ERR_CUDA;
+  p.lambda = a->lambda;
+  p.weight = a->norm_weight;
+  p.kv_len = a->kv_len;
+  p.n_qtiles = static_cast<int>(qtiles);
+  p.v_parts = v_parts;
+  p.units_b = H * p.n_qtiles * v_parts;
+  p.n_units = B * p.units_b;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
+  p.eps = a->eps;
+  p.out_scale = a->out_scale;
+  if (device_status_word(&p.status) != cudaSuccess) return XS_ERR_CUDA;
+  p.wait_limit_ns = wait_limit_ns();
+  // Workspace: counters | fp32 rows (d = 256 with the norm) | partial results.
+  unsigned long long room = 0;
+  if (ws && ws_bytes >= XS_WORKSPACE_HEADER_BYTES + stage) {
+    p.count = static_cast<int *>(ws);
+    p.stage = reinterpret_cast<float *>(static_cast<char *>(ws) + XS_WORKSPACE_HEADER_BYTES);
+    p.parts = p.stage + stage / 4;
+    room = ws_bytes - XS_WORKSPACE_HEADER_BYTES - stage;
+  }
+  const Plan pl = plan(p.n_units, sms, (Nk + kTileRows - 1) / kTileRows, a->kv_len != nullptr, d, room);
+  p.split = pl.split;
+  p.waves = pl.waves;
+  if (launch_attn_diff(p, d, pl.grid, s) != cudaSuccess) return XS_ERR_CUDA;
+  if (stage > 0 && launch_diff_norm(p, sms * 8, s) != cudaSuccess) return XS_ERR_CUDA;
+  return XS_OK;
+}
+
+}  // namespace
+
+XS_API xs_status xs_diff_attn(const xs_diff_args *args, void *o, const long long *o_stride, void *ws,
+                              unsigned long long ws_bytes, void *stream) {
+  return diff_call(args, o, o_stride, nullptr, 0, ws, ws_bytes, stream);
+}
+
+XS_API xs_status xs_diff_attn_fused(const xs_diff_args *args, void *const *out_shards, int P,
+                                    void *ws, unsigned long long ws_bytes, void *stream) {
+  if (!out_shards) return XS_ERR_INVALID;
+  return diff_call(args, nullptr, nullptr, out_shards, P, ws, ws_bytes, stream);
+}
+
+XS_API xs_status xs_diff_workspace_bytes(int B, int H, int Nq, int Nk, int d, int norm,
+                                         unsigned long long *bytes) {
+  if (!bytes || B < 0 || H < 0 || Nq < 0 || Nk < 0) return XS_ERR_INVALID;
+  if (d != 64 && d != 128 && d != 256) return XS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (B == 0 || H == 0 || Nq == 0 || Nk == 0) return XS_OK;
+  const int sms = sm_count();
+  if (sms <= 0) return XS_ERR_CUDA;
+  *bytes = XS_WORKSPACE_HEADER_BYTES + stage_bytes(B, H, Nq, d, norm != 0) + parts_bytes(sms, d);
+  return XS_OK;
+}

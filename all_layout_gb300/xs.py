@@ -75,6 +75,16 @@ _lib.xs_rope.argtypes = [_vp, _i, _vp, ctypes.c_longlong, _vp, _i, _vp, _i, _i, 
                          _i, _i, _i, _vp]
 _lib.xs_rope.restype = _i
 
+# struct xs_diff_args: q, k, v, their strides, lambda, norm_weight, kv_len, scale, eps, out_scale,
+# B, H, H_kv, Nq, Nk, d.
+_DIFF_ARGS = struct.Struct("@3P9q3P3f6i0q")
+_lib.xs_diff_attn.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_ulonglong, _vp]
+_lib.xs_diff_attn_fused.argtypes = [_vp, _vp, _i, _vp, ctypes.c_ulonglong, _vp]
+_lib.xs_diff_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_ulonglong)]
+for _f in ("xs_diff_attn", "xs_diff_attn_fused", "xs_diff_workspace_bytes"):
+    getattr(_lib, _f).restype = _i
+_STRIDES = struct.Struct("@3q")
+
 
 def library():
     """The loaded ctypes library (for direct C-ABI calls)."""
@@ -287,6 +297,80 @@ def qkv_rope(q_in, k_in, v_in, q, k, v, pos, axis_dims, *, theta: float = 10000.
     _check(_on(dev, stream, _lib.xs_rope, packed, n, pos.data_ptr(), 0 if shared or B == 1 else ps[0], dims,
                n_axes, table, B, N, d, eps, ROPE_ADJACENT if interleaved else 0, _TYPES[src], _TYPES[dst]),
            "xs_rope")
+
+
+def _diff_args(q, k, v, lam, kv_len, norm_weight, eps, out_scale, scale):
+    """(struct xs_diff_args, B, H, Nq, d, device index) of checked operands."""
+    _require(isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 4, "q must be a CUDA tensor [B, H, Nq, d]")
+    _require(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be a CUDA tensor [B, H_kv, Nk, d]")
+    B, H, Nq, d = q.shape
+    Hk, Nk = k.shape[1], k.shape[2]
+    dev, bf16 = q.get_device(), torch.bfloat16
+    qs = _operand("q", q, bf16, q.shape, dev)
+    ks = _operand("k", k, bf16, (B, Hk, Nk, d), dev)
+    vs = _operand("v", v, bf16, (B, Hk, Nk, d), dev)
+    if (qs[3] != 1 or ks[3] != 1 or vs[3] != 1) and d > 1:
+        raise ValueError("the last dimension of q, k and v must be contiguous")
+    packed = _DIFF_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs[:3], *ks[:3], *vs[:3],
+                             _vector("lam", lam, torch.float32, H, dev),
+                             _vector("norm_weight", norm_weight, torch.float32, d, dev),
+                             _vector("kv_len", kv_len, torch.int32, B, dev),
+                             (d / 2) ** -0.5 if scale is None else scale, eps, out_scale, B, H, Hk, Nq, Nk, d)
+    return packed, B, H, Nq, d, dev
+
+
+def _diff_workspace(ws, index):
+    if ws is None:
+        return 0, 0
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def diff_attn(q, k, v, o, lam, *, kv_len=None, norm_weight=None, eps: float = 1e-5,
+              out_scale: float = 1.0, scale=None, workspace=None, stream=None):
+    """Differential attention into o (see xs_diff_attn in xs.h). q: [B, H, Nq, d]; k, v:
+    [B, H_kv, Nk, d]; o: [B, H, Nq, d]; bf16 views of any strides, d contiguous. The first d/2
+    columns of q and k are the first map's. lam: fp32 [H]; norm_weight: fp32 [d] or None; kv_len:
+    int32 [B] (keys that count) or None; scale: of the scores, 1/sqrt(d/2) if None; workspace:
+    from alloc_diff_workspace, or None."""
+    packed, B, H, Nq, d, dev = _diff_args(q, k, v, lam, kv_len, norm_weight, eps, out_scale, scale)
+    os_ = _operand("o", o, torch.bfloat16, q.shape, dev)
+    if os_[3] != 1 and d > 1:
+        raise ValueError("the last dimension of o must be contiguous")
+    if o.numel() == 0:
+        return
+    ws, n = _diff_workspace(workspace, dev)
+    _check(_on(dev, stream, _lib.xs_diff_attn, packed, o.data_ptr(), _STRIDES.pack(*os_[:3]), ws, n), "xs_diff_attn")
+
+
+def diff_attn_fused(q, k, v, shards, lam, *, kv_len=None, norm_weight=None, eps: float = 1e-5,
+                    out_scale: float = 1.0, scale=None, workspace=None, stream=None):
+    """diff_attn with the fused shard layout: shards are P tensors [B, Nq/P, H, d] bf16
+    (alloc_shards), as in attn_fused."""
+    packed, B, H, Nq, d, dev = _diff_args(q, k, v, lam, kv_len, norm_weight, eps, out_scale, scale)
+    P = len(shards)
+    _require(1 <= P <= MAX_SHARDS and Nq % P == 0, f"1 to {MAX_SHARDS} shards that divide Nq = {Nq} are needed, not {P}")
+    pointers = []
+    for s in shards:
+        _operand("shards", s, torch.bfloat16, (B, Nq // P, H, d), dev)
+        _require(s.is_contiguous(), "shards must be contiguous")
+        pointers.append(s.data_ptr())
+    if q.numel() == 0:
+        return
+    ws, n = _diff_workspace(workspace, dev)
+    _check(_on(dev, stream, _lib.xs_diff_attn_fused, packed, (ctypes.c_void_p * P)(*pointers), P, ws, n),
+           "xs_diff_attn_fused")
+
+
+def alloc_diff_workspace(B: int, H: int, Nq: int, Nk: int, d: int, norm: bool = False, device="cuda"):
+    """A zeroed workspace (through torch) with which diff_attn and diff_attn_fused of this shape can
+    take every schedule; larger shapes' workspaces serve smaller ones."""
+    n = ctypes.c_ulonglong(0)
+    with torch.cuda.device(device):
+        _check(_lib.xs_diff_workspace_bytes(B, H, Nq, Nk, d, 1 if norm else 0, ctypes.byref(n)),
+               "xs_diff_workspace_bytes")
+        return torch.zeros(int(n.value), dtype=torch.uint8, device=device)
 
 
 def store_burst_probe(dst, K, burst_bytes, n_bursts, gap_ns, mode, times, stream=None):

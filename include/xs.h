@@ -303,6 +303,66 @@ xs_status xs_rope(const xs_rope_tensor *tensors, int n_tensors, const int *pos,
                   const double *freqs, int B, int N, int d, float eps, int flags,
                   int in_type, int out_type, void *stream);
 
+/* Operands of differential attention. q [B][H][Nq][d], k and v [B][H_kv][Nk][d] bf16
+ * (device), rows of d contiguous values, strides in elements (batch, head, row);
+ * head h reads k/v head h / (H / H_kv). */
+typedef struct {
+  const void *q, *k, *v;
+  long long q_stride[3], k_stride[3], v_stride[3];
+  const float *lambda;        /* [H] fp32 (device): the second map's weight, per head */
+  const float *norm_weight;   /* [d] fp32 (device), or NULL: no norm */
+  const int *kv_len;          /* [B] int32 (device), or NULL: Nk keys everywhere */
+  float scale;                /* of the scores; 1/sqrt(d/2) is the usual one */
+  float eps, out_scale;       /* of the norm; a factor on the result */
+  int B, H, H_kv, Nq, Nk, d;
+} xs_diff_args;
+
+/* Differential attention (this library's own addition beside xs_attn: same element
+ * type, head dimensions and output layouts). A head's d columns hold two maps,
+ * q = [q1 | q2] and k = [k1 | k2] of d/2 columns each, over one v of d columns:
+ *     x = (softmax(q1 k1^T * scale) - lambda[h] softmax(q2 k2^T * scale)) v
+ *     o = x / sqrt(mean(x^2) + eps) * norm_weight * out_scale
+ * (norm_weight NULL: o = x * out_scale), both softmaxes over the first kv_len[b] keys
+ * (taken into [0, Nk]; what lies behind them is not used, NaN and infinity included),
+ * non-causal. A batch entry without keys gives zeros. fp32 accumulation and statistics,
+ * softmax weights rounded to bf16 for the product with v, output rounded to bf16.
+ * lambda is taken as it is: a model computes it once from its learned vectors, for
+ * example exp(a1.b1) - exp(a2.b2) + lambda_init, with out_scale = 1 - lambda_init.
+ * Nq, Nk: any size, also 1 (one new token against a long sequence); not multiples of
+ * 128 either.
+ *   o, o_stride  [B][H][Nq][d] bf16 (device), strides in elements (batch, head, row)
+ *   out_shards   host array of P device pointers, shard p [B][Nq/P][H][d] bf16, as in
+ *                xs_attn_fused; the CTA that finishes a row stores it in its shard
+ *   ws           caller-owned device memory, 256-byte aligned, whose first
+ *                XS_WORKSPACE_HEADER_BYTES are zero before the first call (each call
+ *                leaves them zero), or NULL. With xs_diff_workspace_bytes of it a
+ *                launch may cut units into ranges of keys over all SMs (few queries,
+ *                a last wave that is not full, ragged lengths); with less it takes
+ *                whole units. d = 256 with a norm needs it, for fp32 rows. Calls that
+ *                share one workspace must not overlap on the GPU. After a timeout
+ *                (xs_last_device_status) zero the header again.
+ * Results are the same from launch to launch on one GPU model; they differ in fp32
+ * rounding between workspace and none.
+ * XS_ERR_INVALID for NULL args, q, lambda, output or (Nk > 0) k, v; negative sizes;
+ * H not a multiple of H_kv; scale not positive and finite, eps negative or not finite,
+ * out_scale not finite; P not in [1, 8], Nq % P != 0; a stride below d over more than
+ * one row (rows that overlap or repeat); ws NULL with ws_bytes > 0; too small a
+ * workspace at d = 256 with a norm. XS_ERR_UNSUPPORTED for d not in {64, 128, 256} or
+ * more than 2^31 - 1 tiles of 128 queries. XS_ERR_ALIGN for q, k, v, norm_weight or an
+ * output that is not 16-byte aligned, strides over more than one row that are not
+ * multiples of 8, or a ws that is not 256-byte aligned. Empty problems return XS_OK. */
+xs_status xs_diff_attn(const xs_diff_args *args, void *o, const long long *o_stride,
+                       void *ws, unsigned long long ws_bytes, void *stream);
+xs_status xs_diff_attn_fused(const xs_diff_args *args, void *const *out_shards, int P,
+                             void *ws, unsigned long long ws_bytes, void *stream);
+
+/* *bytes = the workspace with which a call of this shape on the current device (norm:
+ * 1 if it has a norm weight) can take every schedule. XS_ERR_INVALID for a NULL bytes
+ * or negative sizes, XS_ERR_UNSUPPORTED for d not in {64, 128, 256}, XS_ERR_CUDA if
+ * the device cannot be queried. */
+xs_status xs_diff_workspace_bytes(int B, int H, int Nq, int Nk, int d, int norm,
+                                  unsigned long long *bytes);
+
 /* Static English text for a status code; never NULL. */
 const char *xs_status_string(xs_status s);
 
