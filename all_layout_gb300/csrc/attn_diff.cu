@@ -52,8 +52,10 @@ namespace xs {
 namespace {
 
 constexpr int BM = kTileRows, BN = kTileRows;
-constexpr int kDiffThreads = 320;
-constexpr int kDiffMmaWarp = 8, kDiffLoadWarp = 9;
+constexpr int BC = 64;                              // keys of half a KV tile
+constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
+constexpr int kDiffThreads = kSoftThreads + 96;
+constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadWarp = kSoftWarps + 2;
 constexpr int kDiffHalf = BM * 128;                 // one 64-column half of a 128-row tile
 constexpr uint32_t kDiffSleepNs = 100000;
 constexpr float kDiffRescale = 8.0f;                // log2 units: rescale O only past a growth of 2^8
@@ -71,8 +73,8 @@ struct DCfg {
   static constexpr bool NORM = DQ == DV;            // the whole row is in one unit: the norm is fused
   static constexpr int OFF_RING = QB;
   static constexpr int OFF_BAR = OFF_RING + STAGES * SLOT;
-  static constexpr int OFF_EXCH = OFF_BAR + 1024;
-  static constexpr int SMEM = OFF_EXCH + (NORM ? 2 : 1) * 1024 + 1024;   // + slack to align the base
+  static constexpr int OFF_EXCH = OFF_BAR + 640;    // [512] words, twice where the norm is fused
+  static constexpr int SMEM = OFF_EXCH + (NORM ? 2 : 1) * 4 * kSoftThreads;
   static constexpr uint32_t COL_O = 256;
   static constexpr int PART = 2 * DV * 128 + 4 * 128;   // floats of one piece's partial result
   static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -159,16 +161,20 @@ struct DWalk {
 struct DBars {
   uint64_t q_full, q_empty;
   uint64_t kv_full[10], kv_empty[10];
-  uint64_t s_full[2], p_full[2];
-  uint64_t o_full, drain;
+  uint64_t e_full[2], e_free[2];   // [map]: the early half's scores written; read into registers
+  uint64_t l_full[2];              // the late half's scores written
+  uint64_t p_full[2][2];           // [map][half]: the weights written
+  uint64_t pv_done[2];             // the tile's products done
+  uint64_t o_full, drain[2];
   DPlan plan;
-  DWalk walk[8];      // the softmax warps' places in the work list and their items: kept here, as
-  DItem item[8];      // registers are short while a row of scores is held
+  DWalk walk;         // the softmax warps' place in the work list, their item and the one after it
+  DItem item[2];      // (written by one thread; here, as registers are short while scores are held)
+  int more[2];        // whether item[] holds one
   uint32_t tmem_base;
   int abort, last;
-  float red[8];
+  float red[kSoftWarps];
 };
-static_assert(sizeof(DBars) <= 1024, "barrier block too large");
+static_assert(sizeof(DBars) <= 640, "barrier block too large");
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
                                             int y, int z, int w) {
@@ -178,14 +184,36 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
-// Meeting of the eight softmax warps.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Meeting of all softmax warps.
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 9, %0;" ::"n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// The wait for tmem_ld16, naming its registers so that no use of them moves before it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 
 // Bounded wait on a barrier phase; false after a timeout here or elsewhere in the CTA.
 __device__ __noinline__ bool diff_wait_slow(uint32_t bar, uint32_t parity, DBars *bars, int *status,
                                             uint64_t limit) {
   volatile int *abort_flag = &bars->abort;
-  const bool sleepy = threadIdx.x / 32 != kDiffMmaWarp;   // the issuer polls
+  const int warp = threadIdx.x / 32;
+  const bool sleepy = warp != kScoreWarp && warp != kProductWarp;   // the issuers poll
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (sleepy ? mbar_try_wait_sleep(bar, parity, kDiffSleepNs) : mbar_try_wait(bar, parity))
@@ -204,6 +232,28 @@ __device__ __forceinline__ bool diff_wait(uint32_t bar, uint32_t parity, DBars *
                                           const DiffParams &p) {
   const bool ok = mbar_try_wait(bar, parity) ||
                   diff_wait_slow(bar, parity, bars, p.status, p.wait_limit_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+// The same with no call, for waits made while most registers are live.
+__device__ __forceinline__ bool diff_wait_inline(uint32_t bar, uint32_t parity, DBars *bars,
+                                                 const DiffParams &p) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    volatile int *abort_flag = &bars->abort;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      ok = mbar_try_wait_sleep(bar, parity, kDiffSleepNs);
+      if (ok) break;
+      if ((it & 15u) == 0) {
+        if (*abort_flag) break;
+        if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+          *abort_flag = 1;
+          atomicExch(p.status, kDevTimeout);
+          break;
+        }
+      }
+    }
+  }
   return __all_sync(0xffffffffu, ok);
 }
 // Tear-down: waits for this thread's own copies or MMAs in flight, whatever the abort flag and
@@ -314,11 +364,11 @@ __device__ void diff_loader(const DiffParams &p, uint8_t *smem, DBars *bars) {
   if (items > 0) diff_drain(q_full, (items - 1) & 1);
 }
 
-// ------------------------------------------------------------------ MMA issuer
-// S_t = Q_t K_t^T: DH columns from t * DH of the Q tile and of the K tile.
+// ------------------------------------------------------------------ MMA issuers
+// S = Q_t K_t^T for 64 keys: DH columns from t * DH of the Q tile and of the K tile.
 template <class C>
 __device__ __forceinline__ void diff_qk(uint32_t dcol, uint64_t qdesc, uint64_t kdesc, int t) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0);
+  constexpr uint32_t idesc = idesc_bf16_f32(128, BC, 0);
 #pragma unroll
   for (int kk = 0; kk < C::DH / 16; ++kk) {
     const int qc = t * C::DH + kk * 16;                            // column within the Q tile
@@ -333,52 +383,84 @@ __device__ __forceinline__ void diff_pv(uint32_t dcol, uint32_t pcol, uint64_t v
                                         uint32_t accumulate) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, C::DV, 1);
 #pragma unroll
-  for (int kk = 0; kk < BN / 16; ++kk)
+  for (int kk = 0; kk < BC / 16; ++kk)
     tc_mma_ts(dcol, pcol + kk * 8, vdesc + static_cast<uint64_t>((kk * 2048) >> 4), idesc,
               (kk > 0 || accumulate) ? 1u : 0u);
 }
-
+// The ring use of a step's K (map t) or V tile, its barriers and its place in a descriptor.
 template <class C>
-__device__ void diff_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
+struct DRing {
+  DBars *bars;
+  __device__ __forceinline__ uint32_t slot(uint32_t use) const { return use % C::STAGES; }
+  __device__ __forceinline__ bool full(uint32_t use, const DiffParams &p) const {
+    return diff_wait(smem_u32(&bars->kv_full[slot(use)]), (use / C::STAGES) & 1, bars, p);
+  }
+  __device__ __forceinline__ uint32_t empty(uint32_t use) const {
+    return smem_u32(&bars->kv_empty[slot(use)]);
+  }
+  __device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t use) const {
+    return desc + static_cast<uint64_t>(slot(use) * (C::SLOT >> 4));
+  }
+};
+constexpr uint64_t kChunkRows = (BC * 128) >> 4;   // descriptor step to a tile's second 64 keys
+
+// The score issuer. The first 64 keys of a tile (the early half) go out as soon as the softmax
+// holds those of the tile before in registers; the others (the late half), which share their
+// columns with P, once the products of the tile before have read it (pv_done: a wait, as the
+// order of two threads' tcgen05 operations, or of two shapes, is not given).
+template <class C>
+__device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_in, 0);
-  const int lane = threadIdx.x & 31;
-  uint32_t it = 0, items = 0;
-  uint32_t pc = 0;                                    // P phases, the same for both maps
-  const uint32_t q_full = smem_u32(&bars->q_full), q_empty = smem_u32(&bars->q_empty);
+  uint32_t use = 0, items = 0, step = 0;   // ring use of the tile's K, items, tiles
+  const DRing<C> ring{bars};
   const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
+  DWalk walk;
+  walk.start(p, bars->plan);
+  DItem item;
+  for (; walk.next(p, item); ++items) {
+    const int nk = item.kv1 - item.kv0;
+    if (!diff_wait(smem_u32(&bars->q_full), items & 1, bars, p)) goto drain;
+    for (int j = 0; j < nk; ++j, ++step, use += C::USES) {
+      for (int half = 0; half < 2; ++half)
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t ku = use + (C::KSL == 2 ? t : 0);
+          if (half == 0 && (C::KSL == 2 || t == 0) && !ring.full(ku, p)) goto drain;
+          const uint32_t ready = smem_u32(half == 0 ? &bars->e_free[t] : &bars->pv_done[t]);
+          if (step >= 1 && !diff_wait(ready, (step - 1) & 1, bars, p)) goto drain;
+          tc_fence_after();
+          if (elect_one()) {
+            diff_qk<C>(tmem + t * 128 + (half == 0 ? BC : 0), qdesc,
+                       ring.at(kdesc0, ku) + (half == 0 ? 0 : kChunkRows), t);
+            tc_commit(smem_u32(half == 0 ? &bars->e_full[t] : &bars->l_full[t]));
+            if (half == 1 && (C::KSL == 2 || t == 1)) tc_commit(ring.empty(ku));
+            if (half == 1 && j == nk - 1 && t == 1) tc_commit(smem_u32(&bars->q_empty));
+          }
+          __syncwarp();
+        }
+    }
+  }
+drain:
+  // All MMAs issued must finish before Tensor Memory is released.
+  if (elect_one()) tc_commit(smem_u32(&bars->drain[0]));
+  __syncwarp();
+  diff_drain(smem_u32(&bars->drain[0]), 0);
+}
+
+template <class C>
+__device__ void diff_product_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_in, 0);
+  const int lane = threadIdx.x & 31;
+  uint32_t use = C::KSL, items = 0, step = 0;   // ring use of the tile's V
+  const DRing<C> ring{bars};
   const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_RING), kDiffHalf, 1024);
-  auto slot_of = [&](uint32_t use) { return use % C::STAGES; };
-  auto full = [&](uint32_t use) {
-    return diff_wait(smem_u32(&bars->kv_full[slot_of(use)]), (use / C::STAGES) & 1, bars, p);
-  };
-  auto empty = [&](uint32_t use) { return smem_u32(&bars->kv_empty[slot_of(use)]); };
-  auto at = [&](uint64_t d, uint32_t use) {
-    return d + static_cast<uint64_t>(slot_of(use) * (C::SLOT >> 4));
-  };
-  // S_t of the step whose K uses start at `use`; its slots are released after their last reader.
-  auto issue_qk = [&](int t, uint32_t use, bool last) {
-    const uint32_t ku = use + (C::KSL == 2 ? t : 0);
-    if (C::KSL == 2 || t == 0) {
-      if (!full(ku)) return false;
-      tc_fence_after();
-    }
-    if (elect_one()) {
-      diff_qk<C>(tmem + t * 128, qdesc, at(kdesc0, ku), t);
-      tc_commit(smem_u32(&bars->s_full[t]));
-      if (C::KSL == 2 || t == 1) tc_commit(empty(ku));
-      if (last && t == 1) tc_commit(q_empty);
-    }
-    __syncwarp();
-    return true;
-  };
   // A key past the batch entry's length has weight 0, but what lies in its row of V may not
   // be a number: the rows behind the last key are cleared before the products read them.
   // (Rows past Nk were filled with zeros by the load.)
-  auto clear_tail = [&](uint32_t use, int keys, int j) {
+  auto clear_tail = [&](int keys, int j) {
     const int valid = keys - j * BN;
     if (valid >= BN || keys >= p.Nk) return;
-    uint8_t *tile = smem + C::OFF_RING + slot_of(use) * C::SLOT;
+    uint8_t *tile = smem + C::OFF_RING + ring.slot(use) * C::SLOT;
     for (int hf = 0; hf < C::DV / 64; ++hf)
       for (int o = valid * 128 + lane * 16; o < kDiffHalf; o += 512)
         *reinterpret_cast<uint4 *>(tile + hf * kDiffHalf + o) = make_uint4(0, 0, 0, 0);
@@ -390,34 +472,32 @@ __device__ void diff_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uin
   DItem item;
   for (; walk.next(p, item); ++items) {
     const int nk = item.kv1 - item.kv0;
-    if (!diff_wait(q_full, items & 1, bars, p)) goto drain;
-    for (int t = 0; t < 2; ++t)
-      if (!issue_qk(t, it, nk == 1)) goto drain;
-    for (int j = 0; j < nk; ++j) {
-      const uint32_t vu = it + C::KSL, next = it + C::USES;
-      const bool more = j + 1 < nk;
-      if (!full(vu)) goto drain;
-      clear_tail(vu, item.keys, item.kv0 + j);
-      for (int t = 0; t < 2; ++t) {
-        if (!diff_wait(smem_u32(&bars->p_full[t]), pc & 1, bars, p)) goto drain;
+    for (int j = 0; j < nk; ++j, ++step, use += C::USES) {
+      if (!ring.full(use, p)) goto drain;
+      clear_tail(item.keys, item.kv0 + j);
+      // Each half's products as soon as its weights are written: the early half's run beside the
+      // late half's exponentials.
+      for (int u = 0; u < 4; ++u) {
+        const int t = u >> 1, half = u & 1;
+        if (!diff_wait(smem_u32(&bars->p_full[t][half]), step & 1, bars, p)) goto drain;
         tc_fence_after();
         if (elect_one()) {
-          diff_pv<C>(tmem + C::COL_O + t * C::DV, tmem + t * 128, at(vdesc0, vu), j > 0 ? 1u : 0u);
-          if (t == 1) tc_commit(empty(vu));
-          if (t == 1 && !more) tc_commit(smem_u32(&bars->o_full));
+          diff_pv<C>(tmem + C::COL_O + t * C::DV, tmem + t * 128 + half * 32,
+                     ring.at(vdesc0, use) + (half == 0 ? 0 : kChunkRows), j > 0 || half == 1 ? 1u : 0u);
+          if (half == 1) tc_commit(smem_u32(&bars->pv_done[t]));
+          if (u == 3) {
+            tc_commit(ring.empty(use));
+            if (j == nk - 1) tc_commit(smem_u32(&bars->o_full));
+          }
         }
         __syncwarp();
-        if (more && !issue_qk(t, next, j + 2 == nk)) goto drain;
       }
-      ++pc;
-      it += C::USES;
     }
   }
 drain:
-  // All MMAs issued must finish before Tensor Memory is released.
-  if (elect_one()) tc_commit(smem_u32(&bars->drain));
+  if (elect_one()) tc_commit(smem_u32(&bars->drain[1]));
   __syncwarp();
-  diff_drain(smem_u32(&bars->drain), 0);
+  diff_drain(smem_u32(&bars->drain[1]), 0);
 }
 
 // ------------------------------------------------------------------ softmax / epilogue
@@ -435,39 +515,36 @@ __device__ __forceinline__ float *stage_row(const DiffParams &p, int b, int h, i
   return p.stage + ((static_cast<long long>(b) * p.H + h) * p.Nq + n) * d;
 }
 
-// Maximum over 64 raw scores in 8 chains of 3-input max; `first` starts the chains.
-__device__ __forceinline__ void diff_max(const uint32_t (&a)[32], const uint32_t (&b)[32],
-                                         float (&mp)[8], bool first) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = __uint_as_float(a[i]), y = __uint_as_float(a[i + 8]);
-    mp[i] = first ? fmaxf(x, y) : max3(mp[i], x, y);
-  }
+// Maximum over 64 raw scores, in 8 chains of 3-input max.
+__device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (&b)[32]) {
+  float mp[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    mp[i] = max3(mp[i], __uint_as_float(a[i + 16]), __uint_as_float(a[i + 24]));
+    mp[i] = max3(__uint_as_float(a[i]), __uint_as_float(a[i + 8]), __uint_as_float(a[i + 16]));
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    mp[i] = max3(mp[i], __uint_as_float(b[i]), __uint_as_float(b[i + 8]));
+    mp[i] = max3(mp[i], __uint_as_float(a[i + 24]), __uint_as_float(b[i]));
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    mp[i] = max3(mp[i], __uint_as_float(b[i + 16]), __uint_as_float(b[i + 24]));
+    mp[i] = max3(mp[i], __uint_as_float(b[i + 8]), __uint_as_float(b[i + 16]));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mp[i] = fmaxf(mp[i], __uint_as_float(b[i + 24]));
+  return max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
 }
 
 // This thread's NX columns (from col0 of the unit's) of one finished row: norm, scale, store.
 // `ss` is the whole row's sum of squares.
 template <class C, int NX>
-__device__ __forceinline__ void finish_row(const DiffParams &p, const DItem &item, const DPlace &at,
-                                           int n, int col0, float (&x)[NX], float ss) {
+__device__ __forceinline__ void finish_row(const DiffParams &p, int b, const DPlace &at, int n, int col0, float (&x)[NX], float ss) {
   constexpr int D = C::DQ;
   if (!C::NORM && p.weight) {   // d = 256: the norm follows in a kernel of its own
-    float4 *dst = reinterpret_cast<float4 *>(stage_row(p, item.b, at.h, n, D) + at.vp * C::DV + col0);
+    float4 *dst = reinterpret_cast<float4 *>(stage_row(p, b, at.h, n, D) + at.vp * C::DV + col0);
 #pragma unroll
     for (int i = 0; i < NX / 4; ++i)
       dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     return;
   }
-  uint16_t *dst = out_row(p, item.b, at.h, n, D) + at.vp * C::DV + col0;
+  uint16_t *dst = out_row(p, b, at.h, n, D) + at.vp * C::DV + col0;
   if (C::NORM && p.weight) {
     const float r = rsqrtf(ss * (1.f / D) + p.eps) * p.out_scale;
 #pragma unroll
@@ -499,11 +576,13 @@ __device__ __forceinline__ float map_factor(int t, float lambda, float l) {
 }
 
 // One piece of a cut unit: leaves its partial result in the workspace; the CTA that counts the
-// last piece merges all of them. All eight softmax warps take part.
+// last piece merges all of them. All softmax warps take part; `l` is this thread's map's sum.
 template <class C>
-__device__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const DItem &item,
-                           const DPlace &at, uint32_t tmem, float m, float l, float lambda, bool dead) {
-  const int tid = threadIdx.x, t = tid / 128, row = tid & 127, lane = tid & 31;
+__device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const DItem item,
+                                        uint32_t tmem, float m, float l, bool dead) {
+  const int tid = threadIdx.x, t = tid >> 7, row = tid & 127, lane = tid & 31;
+  const DPlace at = place_of(p, item);
+  const float lambda = __ldg(p.lambda + at.h);
   const int rows = min(BM, p.Nq - at.q0);
   const long long T = bars->plan.total;
   const int G = bars->plan.grid;
@@ -523,24 +602,23 @@ __device__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const 
   };
   auto stat_of = [&](int k) { return reinterpret_cast<float4 *>(part(k) + 2 * C::DV * 128); };
   const int own = static_cast<int>(blockIdx.x) - c0;
-  if (row < rows && !dead) reinterpret_cast<float2 *>(stat_of(own) + row)[t] = make_float2(m, l);
-  {
-    // Columns as float4 groups, [col/4][row][4]: a warp instruction moves 512 bytes.
-    const uint32_t tO = tmem + (static_cast<uint32_t>((row & ~31)) << 16) + C::COL_O + t * C::DV;
-    float4 *o4 = reinterpret_cast<float4 *>(part(own) + t * C::DV * 128);
-    if ((row & ~31) < rows) {
+  if (row < rows && !dead)
+    __stcg(reinterpret_cast<float2 *>(stat_of(own) + row) + t, make_float2(m, l));
+  if ((row & ~31) < rows) {
+    // The columns as float4 groups [col/4][row][4]: a warp instruction moves 512 bytes.
+    const uint32_t tO = tmem + (static_cast<uint32_t>(row & ~31) << 16) + C::COL_O + t * C::DV;
+    float4 *o4 = reinterpret_cast<float4 *>(part(own)) + t * (C::DV / 4) * 128 + row;
 #pragma unroll 1
-      for (int c = 0; c < C::DV / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * c, o);
-        tmem_wait_ld_regs(o);
-        if (row < rows && !dead) {
+    for (int c = 0; c < C::DV / 32; ++c) {
+      uint32_t o[32];
+      tmem_ld32(tO + 32 * c, o);
+      tmem_wait_ld_regs(o);
+      if (row < rows && !dead) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            __stcg(o4 + (8 * c + i) * 128 + row,
-                   make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
-        }
+        for (int i = 0; i < 8; ++i)
+          __stcg(o4 + (8 * c + i) * 128,
+                 make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
       }
     }
   }
@@ -554,12 +632,12 @@ __device__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const 
     bars->last = last;
   }
   softmax_sync();
-  const int last = bars->last;
-  if (!last) return;   // the next write of `last` follows another meeting
+  if (!bars->last) return;   // its next write follows another meeting
   __threadfence();
   if (rows > kFewRows) {
     // A thread takes one row and half of the columns.
     constexpr int NX = C::DV / 2;
+    const int col0 = (tid >> 7) * NX;
     float x[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) x[i] = 0.f;
@@ -583,7 +661,7 @@ __device__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const 
       for (int k = 0; k < S; ++k) {
         const float4 s = __ldcg(stat_of(k) + row);
         const float g1 = f1 * ex2_approx(s.x - m1), g2 = f2 * ex2_approx(s.z - m2);
-        const float4 *a = reinterpret_cast<const float4 *>(part(k)) + (t * (NX / 4)) * 128 + row;
+        const float4 *a = reinterpret_cast<const float4 *>(part(k)) + (col0 / 4) * 128 + row;
         const float4 *b = a + C::DV / 4 * 128;
 #pragma unroll
         for (int i = 0; i < NX / 4; ++i) {
@@ -598,15 +676,16 @@ __device__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const 
       for (int i = 0; i < NX; ++i) ss = fmaf(x[i], x[i], ss);
     }
     if constexpr (C::NORM) {
-      exch[256 + tid] = ss;
+      float *sums = exch + kSoftThreads;
+      sums[tid] = ss;
       softmax_sync();
-      ss += exch[256 + (tid ^ 128)];
+      ss = sums[row] + sums[row + 128];
     }
-    if (row < rows) finish_row<C, NX>(p, item, at, at.q0 + row, t * NX, x, ss);
+    if (row < rows) finish_row<C, NX>(p, item.b, at, at.q0 + row, col0, x, ss);
     return;
   }
   // Few rows: row by row, a warp takes CW groups of four columns, and its lanes share the pieces.
-  constexpr int CW = C::DV / 4 / 8, PG = 32 / CW;
+  constexpr int CW = C::DV / 4 / kSoftWarps, PG = 32 / CW;
   const int c4 = (tid / 32) * CW + lane % CW, pg = lane / CW;
   for (int r = 0; r < rows; ++r) {
     float m1 = -INFINITY, m2 = -INFINITY, l1 = 0.f, l2 = 0.f;
@@ -656,169 +735,209 @@ __device__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const 
       softmax_sync();
       ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += bars->red[i];
+      for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
     }
-    if (pg == 0) finish_row<C, 4>(p, item, at, at.q0 + r, c4 * 4, x, ss);
+    if (pg == 0) finish_row<C, 4>(p, item.b, at, at.q0 + r, c4 * 4, x, ss);
   }
 }
 
+// 64 scores of a row to weights 2^(s * scale - m), packed to bf16 pairs in place of `pk`; their sum.
+__device__ __forceinline__ float weights64(const uint32_t (&s)[2][32], float scale, float m,
+                                           uint32_t (&pk)[2][16]) {
+  // Without any key m is -inf, and the weights are 2^(-inf - 0) = 0.
+  const float neg_m = m == -INFINITY ? 0.f : -m;
+  const uint64_t scale2 = f2_pack(scale, scale), negm2 = f2_pack(neg_m, neg_m);
+  uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint64_t x2 = f2_fma(
+          f2_pack(__uint_as_float(s[h][2 * i]), __uint_as_float(s[h][2 * i + 1])), scale2, negm2);
+      float x0, x1;
+      f2_unpack(x2, x0, x1);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+      pk[h][i] = pack_bf16x2(p0, p1);   // P goes to the tensor cores in bf16, as V does; the sum is fp32
+    }
+  float a, b;
+  f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+  return a + b;
+}
+__device__ __forceinline__ void mask64(uint32_t (&s)[2][32], int valid) {
+  if (valid < BC) {
+    asm volatile("");   // keeps this a branch
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * h + i >= valid) s[h][i] = 0xff800000u;   // -inf, whatever the score was
+  }
+}
+
+// The factor 2^(a - b) of a maximum that moved from a to b; 1 where it did not (-inf included).
+__device__ __forceinline__ float shrink(float a, float b) { return a == b ? 1.f : ex2_approx(a - b); }
+
+// Softmax of one map, a thread per row, in halves of 64 keys: the early half's exponentials run
+// while the tensor cores finish the last tile's products and compute the late half's scores.
+// The running maximum is kept rounded up to a whole number (log2 units), so that every rescaling
+// is by a power of two, exact for the early half's weights already rounded to bf16; it moves only
+// when it grew by more than 2^kDiffRescale.
 template <class C>
 __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem) {
-  const int t = threadIdx.x / 128, row = threadIdx.x & 127, wq = (threadIdx.x / 32) & 3;
+  const int tid = threadIdx.x, t = tid >> 7, row = tid & 127, wq = row >> 5;
   const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-  const uint32_t tS = tmem + lane_base + t * 128;
+  const uint32_t tS = tmem + lane_base + t * 128;   // late half and P [0, 64), early half [64, 128)
   const uint32_t tO = tmem + lane_base + C::COL_O + t * C::DV;
-  const uint32_t s_full = smem_u32(&bars->s_full[t]), p_full = smem_u32(&bars->p_full[t]);
+  const uint32_t e_full = smem_u32(&bars->e_full[t]), e_free = smem_u32(&bars->e_free[t]);
+  const uint32_t l_full = smem_u32(&bars->l_full[t]), p_full = smem_u32(&bars->p_full[t][0]);
   const uint32_t o_full = smem_u32(&bars->o_full);
   float *exch = reinterpret_cast<float *>(smem + C::OFF_EXCH);
   const float scale = p.scale_log2;
-  uint32_t sc = 0, items = 0;
+  uint32_t step = 0, items = 0;
   bool dead = false;   // a wait gave up: go on without waiting, store nothing
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!dead && !diff_wait(bar, parity, bars, p)) dead = true;
+    if (!dead && !diff_wait_inline(bar, parity, bars, p)) dead = true;
   };
-  DWalk &walk = bars->walk[threadIdx.x / 32];
-  DItem &item = bars->item[threadIdx.x / 32];
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) walk.start(p, bars->plan);
-  for (;; ++items) {
-    int more = 0;
-    if (lane == 0) more = walk.next(p, item);
-    if (!__shfl_sync(0xffffffffu, more, 0)) break;
-    __syncwarp();
-    // No query in this warp's rows: nothing to compute or store.
+  if (tid == 0) {
+    bars->walk.start(p, bars->plan);
+    bars->more[0] = bars->walk.next(p, bars->item[0]);
+  }
+  softmax_sync();
+  for (; bars->more[items & 1]; ++items) {
+    const DItem &item = bars->item[items & 1];
+    // No query in this warp's rows: nothing to compute or store, but the barriers' arrivals.
     const bool idle = place_of(p, item).q0 + wq * 32 >= p.Nq;
     const int nk = item.kv1 - item.kv0;
     int valid = item.keys - item.kv0 * BN;   // keys from this tile on that count
     float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < nk; ++j, ++sc, valid -= BN) {
-      wait(s_full, sc & 1);
+    for (int j = 0; j < nk; ++j, ++step, valid -= BN) {
+      wait(e_full, step & 1);
       if (idle) {
+        mbar_arrive(e_free);
+        wait(l_full, step & 1);
         mbar_arrive(p_full);
+        mbar_arrive(p_full + 8);
         continue;
       }
+      uint32_t pe[2][16], pl[2][16];
+      float alpha = 1.f, sum;
+      bool rescale;   // of O, by alpha, in some lane
       tc_fence_after();
-      uint32_t s[4][32];
+      {
+        uint32_t s[2][32];
+        tmem_ld32(tS + 64, s[0]);
+        tmem_ld32(tS + 96, s[1]);
+        tmem_wait_ld_regs(s[0]);
+        tmem_wait_ld_regs(s[1]);
+        tc_fence_before();
+        mbar_arrive(e_free);
+        mask64(s, valid);
+        const float mx = max64(s[0], s[1]) * scale, before = m;
+        if (j == 0 || mx > m + kDiffRescale) m = ceilf(mx);
+        sum = weights64(s, scale, m, pe);
+        rescale = j > 0 && __any_sync(0xffffffffu, m != before);
+        if (rescale) alpha = shrink(before, m);
+      }
+      wait(l_full, step & 1);
+      tc_fence_after();
+      uint32_t s[2][32];
       tmem_ld32(tS, s[0]);
       tmem_ld32(tS + 32, s[1]);
       tmem_wait_ld_regs(s[0]);
       tmem_wait_ld_regs(s[1]);
-      tmem_ld32(tS + 64, s[2]);
-      tmem_ld32(tS + 96, s[3]);
-      float mp[8];
-      if (valid < BN) {
-        tmem_wait_ld_regs(s[2]);
-        tmem_wait_ld_regs(s[3]);
+      mask64(s, valid - BC);
+      const float mx = max64(s[0], s[1]) * scale, before = m;
+      if (mx > m + kDiffRescale) m = ceilf(mx);
+      if (__any_sync(0xffffffffu, m != before)) {
+        const float a = shrink(before, m);   // a power of two: exact on the rounded weights
+        const uint32_t a2 = pack_bf16x2(a, a);
+        alpha *= a;
+        sum *= a;
+        rescale = j > 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= valid) s[c][i] = 0xff800000u;   // -inf, whatever the score was
-        diff_max(s[0], s[1], mp, true);
-      } else {
-        diff_max(s[0], s[1], mp, true);
-        tmem_wait_ld_regs(s[2]);
-        tmem_wait_ld_regs(s[3]);
+          for (int i = 0; i < 16; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(pe[h][i]) : "r"(a2));
       }
-      diff_max(s[2], s[3], mp, false);
-      const float mx = max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-      const float m_new = fmaxf(m, mx * scale);
-      float alpha = 1.f;
-      bool rescale = false;
-      if (j == 0) {
-        m = m_new;
-      } else {
-        const bool need = m_new > m + kDiffRescale;
-        if (__any_sync(0xffffffffu, need)) {
-          rescale = true;
-          if (need) {
-            alpha = ex2_approx(m - m_new);
-            m = m_new;
-          }
-        }
-      }
-      // A tile without any key has m = -inf; its weights are 2^(-inf - 0) = 0.
-      const float neg_m = m == -INFINITY ? 0.f : -m;
-      const uint64_t scale2 = f2_pack(scale, scale), negm2 = f2_pack(neg_m, neg_m);
-      float lsum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t x2 = f2_fma(
-              f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), scale2, negm2);
-          float x0, x1;
-          f2_unpack(x2, x0, x1);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          lsum[i & 3] += p0 + p1;
-          pk[i] = pack_bf16x2(p0, p1);   // P goes to the tensor cores in bf16, as V does; l sums it in fp32
-        }
-        tmem_st16(tS + 16 * c, pk);
-      }
-      l = fmaf(l, alpha, (lsum[0] + lsum[1]) + (lsum[2] + lsum[3]));
+      // The late half's scores came after the products of the last tile: P and O are free.
       if (rescale) {
 #pragma unroll 1
-        for (int c = 0; c < C::DV / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld_regs(o);
+        for (int h = 0; h < C::DV / 16; ++h) {
+          uint32_t o[16];
+          tmem_ld16(tO + 16 * h, o);
+          tmem_wait_ld16(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(tO + 32 * c, o);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(tO + 16 * h, o);
         }
       }
+      tmem_st16(tS, pe[0]);
+      tmem_st16(tS + 16, pe[1]);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_full);
+      sum += weights64(s, scale, m, pl);
+      tmem_st16(tS + 32, pl[0]);
+      tmem_st16(tS + 48, pl[1]);
+      l = fmaf(l, alpha, sum);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full + 8);
     }
     // Both maps' O are final once the unit's last product completes.
     wait(o_full, items & 1);
     tc_fence_after();
-    const DPlace at = place_of(p, item);
-    const float lambda = __ldg(p.lambda + at.h);
+    if (tid == 0) bars->more[(items + 1) & 1] = bars->walk.next(p, bars->item[(items + 1) & 1]);
+    __syncwarp();
     if (item.piece) {
-      diff_piece<C>(p, bars, exch, item, at, tmem, m, l, lambda, dead);
-      __syncwarp();
+      diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
       continue;
     }
-    exch[threadIdx.x] = map_factor(t, lambda, l);
+    exch[tid] = l;
     softmax_sync();
     constexpr int NX = C::DV / 2;
+    const DPlace at = place_of(p, item);
+    const int b = item.b;   // taken before the meeting that lets `item` be replaced
+    const int col0 = t * NX;
     float x[NX], ss = 0.f;
     if (!idle) {
-      const float f1 = exch[row], f2 = exch[128 + row];
-      const uint32_t o1 = tmem + lane_base + C::COL_O + t * NX;
+      const float lambda = __ldg(p.lambda + at.h);
+      const float f1 = map_factor(0, lambda, exch[row]);
+      const float f2 = map_factor(1, lambda, exch[row + 128]);
+      const uint32_t o1 = tmem + lane_base + C::COL_O + col0;
 #pragma unroll
-      for (int c = 0; c < NX / 32; ++c) {
-        uint32_t a[32], b[32];
-        tmem_ld32(o1 + 32 * c, a);
-        tmem_ld32(o1 + C::DV + 32 * c, b);
-        tmem_wait_ld_regs(a);
-        tmem_wait_ld_regs(b);
+      for (int c = 0; c < NX / 16; ++c) {
+        uint32_t a[16], v[16];
+        tmem_ld16(o1 + 16 * c, a);
+        tmem_ld16(o1 + C::DV + 16 * c, v);
+        tmem_wait_ld16(a);
+        tmem_wait_ld16(v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float v = fmaf(f1, __uint_as_float(a[i]), f2 * __uint_as_float(b[i]));
-          x[32 * c + i] = v;
-          ss = fmaf(v, v, ss);
+        for (int i = 0; i < 16; ++i) {
+          const float y = fmaf(f1, __uint_as_float(a[i]), f2 * __uint_as_float(v[i]));
+          x[16 * c + i] = y;
+          ss = fmaf(y, y, ss);
         }
       }
     }
     tc_fence_before();
-    if constexpr (C::NORM) exch[256 + threadIdx.x] = ss;
-    // Both groups have read O: a group's next P may let the next unit's products overwrite it.
+    float *sums = exch + kSoftThreads;
+    if constexpr (C::NORM) sums[tid] = ss;
+    // All have read O (and l): a map's next P may let the next unit's products overwrite it.
     softmax_sync();
-    if constexpr (C::NORM) ss += exch[256 + (threadIdx.x ^ 128)];
-    if (at.q0 + row < p.Nq && !dead) finish_row<C, NX>(p, item, at, at.q0 + row, t * NX, x, ss);
-    __syncwarp();   // `item` has been read
+    if constexpr (C::NORM) ss = sums[row] + sums[row + 128];
+    if (at.q0 + row < p.Nq && !dead) finish_row<C, NX>(p, b, at, at.q0 + row, col0, x, ss);
   }
 }
 
 template <class C>
 __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid_constant__ DiffParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle pattern repeats every 1024 bytes
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicExch(p.status, kDevBadPlan);
+    return;
+  }
   DBars *bars = reinterpret_cast<DBars *>(smem + C::OFF_BAR);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -829,17 +948,22 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
       mbar_init(smem_u32(&bars->kv_empty[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&bars->s_full[t]), 1);
-      mbar_init(smem_u32(&bars->p_full[t]), 128);
+      mbar_init(smem_u32(&bars->e_full[t]), 1);
+      mbar_init(smem_u32(&bars->e_free[t]), 128);
+      mbar_init(smem_u32(&bars->l_full[t]), 1);
+      mbar_init(smem_u32(&bars->p_full[t][0]), 128);
+      mbar_init(smem_u32(&bars->p_full[t][1]), 128);
+      mbar_init(smem_u32(&bars->pv_done[t]), 1);
     }
     mbar_init(smem_u32(&bars->o_full), 1);
-    mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->drain[0]), 1);
+    mbar_init(smem_u32(&bars->drain[1]), 1);
     bars->abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   if (warp == 1 && p.split) plan_split(p, bars);
-  if (warp == kDiffMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
@@ -855,15 +979,18 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
   if (warp == kDiffLoadWarp) {
     diff_loader<C>(p, smem, bars);
     __syncwarp();
-  } else if (warp == kDiffMmaWarp) {
-    diff_issuer<C>(p, smem, bars, tmem);
+  } else if (warp == kScoreWarp) {
+    diff_score_issuer<C>(p, smem, bars, tmem);
+    __syncwarp();
+  } else if (warp == kProductWarp) {
+    diff_product_issuer<C>(p, smem, bars, tmem);
     __syncwarp();
   } else {
     diff_softmax<C>(p, smem, bars, tmem);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kDiffMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
