@@ -54,8 +54,8 @@ namespace {
 constexpr int BM = kTileRows, BN = kTileRows;
 constexpr int BC = 64;                              // keys of half a KV tile
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kDiffThreads = kSoftThreads + 96;
-constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadWarp = kSoftWarps + 2;
+constexpr int kDiffThreads = kSoftThreads + 128;
+constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadWarp = kSoftWarps + 2, kThirdWarp = kSoftWarps + 3;
 constexpr int kDiffHalf = BM * 128;                 // one 64-column half of a 128-row tile
 constexpr uint32_t kDiffSleepNs = 100000;
 constexpr float kDiffRescale = 8.0f;                // log2 units: rescale O only past a growth of 2^8
@@ -67,14 +67,14 @@ struct DCfg {
   static constexpr int DH = DH_, DV = DV_, DQ = 2 * DH;
   static constexpr int SLOT = BN * DV * 2;          // a ring slot: the V tile, or DV columns of the K tile
   static constexpr int KSL = DQ / DV;               // slots of a K tile (2 at d = 256: one per map)
-  static constexpr int USES = KSL + 1;              // ring uses per KV step
   static constexpr int QB = BM * DQ * 2;
-  static constexpr int STAGES = DV == 64 ? 10 : 5;
+  static constexpr int KS = 3, VS = DV == 64 ? 3 : 2;   // slots of the K ring and of the V ring behind it
   static constexpr bool NORM = DQ == DV;            // the whole row is in one unit: the norm is fused
   static constexpr int OFF_RING = QB;
-  static constexpr int OFF_BAR = OFF_RING + STAGES * SLOT;
-  static constexpr int OFF_EXCH = OFF_BAR + 640;    // [512] words, twice where the norm is fused
-  static constexpr int SMEM = OFF_EXCH + (NORM ? 2 : 1) * 4 * kSoftThreads;
+  static constexpr int OFF_BAR = OFF_RING + (KS + VS) * SLOT;
+  static constexpr int OFF_STG = OFF_BAR + 512;   // a warp's 32 rows of half the columns, bf16
+  static constexpr int OFF_EXCH = OFF_STG + (NORM ? BM * DV * 2 : 0);    // sums; squares and the norm's weights
+  static constexpr int SMEM = OFF_EXCH + (NORM ? 8 * kSoftThreads + 4 * DV : 4 * kSoftThreads);
   static constexpr uint32_t COL_O = 256;
   static constexpr int PART = 2 * DV * 128 + 4 * 128;   // floats of one piece's partial result
   static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -158,23 +158,33 @@ struct DWalk {
   }
 };
 
+struct DPlace {
+  int h, q0, vp;
+};
+// What the softmax warps know of an item.
+struct DTask {
+  long long u0;
+  int b, keys, kv0, kv1, nk;
+  int h, q0;
+  short vp, kind;   // kind: 0 none (the list's end), 1 a whole unit, 2 a piece
+};
+
 struct DBars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[10], kv_empty[10];
+  uint64_t kv_full[6], kv_empty[6];
   uint64_t e_full[2], e_free[2];   // [map]: the early half's scores written; read into registers
   uint64_t l_full[2];              // the late half's scores written
   uint64_t p_full[2][2];           // [map][half]: the weights written
   uint64_t pv_done[2];             // the tile's products done
-  uint64_t o_full, drain[2];
+  uint64_t o_full, drain[3];
+  uint64_t item_full[4];
   DPlan plan;
-  DWalk walk;         // the softmax warps' place in the work list, their item and the one after it
-  DItem item[2];      // (written by one thread; here, as registers are short while scores are held)
-  int more[2];        // whether item[] holds one
+  DTask task[4];           // the softmax warps' items, published by the loader (task i mod 4)
   uint32_t tmem_base;
   int abort, last;
   float red[kSoftWarps];
 };
-static_assert(sizeof(DBars) <= 640, "barrier block too large");
+static_assert(sizeof(DBars) <= 512, "barrier block too large");
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
                                             int y, int z, int w) {
@@ -213,7 +223,7 @@ __device__ __noinline__ bool diff_wait_slow(uint32_t bar, uint32_t parity, DBars
                                             uint64_t limit) {
   volatile int *abort_flag = &bars->abort;
   const int warp = threadIdx.x / 32;
-  const bool sleepy = warp != kScoreWarp && warp != kProductWarp;   // the issuers poll
+  const bool sleepy = warp < kSoftWarps || warp == kDiffLoadWarp;   // the issuers poll
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (sleepy ? mbar_try_wait_sleep(bar, parity, kDiffSleepNs) : mbar_try_wait(bar, parity))
@@ -304,9 +314,6 @@ __device__ void plan_split(const DiffParams &p, DBars *bars) {
   if (lane == 0) bars->plan = DPlan{0, 0, 0, b0};
 }
 
-struct DPlace {
-  int h, q0, vp;
-};
 __device__ __forceinline__ DPlace place_of(const DiffParams &p, const DItem &it) {
   int u = it.unit - it.b * p.units_b;
   DPlace r;
@@ -320,15 +327,16 @@ __device__ __forceinline__ DPlace place_of(const DiffParams &p, const DItem &it)
 // ------------------------------------------------------------------ TMA loader
 template <class C>
 __device__ void diff_loader(const DiffParams &p, uint8_t *smem, DBars *bars) {
-  uint32_t it = 0, items = 0;   // ring uses, items
+  uint32_t k_use = 0, v_use = 0, items = 0;   // uses of the two rings, items
   const uint32_t q_full = smem_u32(&bars->q_full), q_empty = smem_u32(&bars->q_empty);
   DWalk walk;
   walk.start(p, bars->plan);
   DItem item;
   bool ok = true;
-  // One ring use: DV columns from x of rows [j*128, +128) of a K or V head.
-  auto load = [&](const CUtensorMap *m, int x, int j, int h, int b) {
-    const uint32_t slot = it % C::STAGES, ph = (it / C::STAGES) & 1;
+  // The next use of a ring (`first` slot, `n` slots): DV columns from x of rows [j*128, +128) of a
+  // K or V head.
+  auto load = [&](uint32_t &use, int first, int n, const CUtensorMap *m, int x, int j, int h, int b) {
+    const uint32_t slot = first + use % n, ph = (use / n) & 1;
     if (!diff_wait(smem_u32(&bars->kv_empty[slot]), ph ^ 1, bars, p)) return false;
     const uint32_t full = smem_u32(&bars->kv_full[slot]);
     if (elect_one()) {
@@ -338,13 +346,24 @@ __device__ void diff_loader(const DiffParams &p, uint8_t *smem, DBars *bars) {
                     x + hf * 64, j * BN, h, b);
     }
     __syncwarp();
-    ++it;
+    ++use;
     return true;
+  };
+  // Item i's record is written once the scores of item i - 1 are done: the softmax has then
+  // begun the last tile of item i - 2 at least, and four records are enough (the end's included).
+  auto publish = [&](const DTask &task) {
+    if (elect_one()) {
+      bars->task[items & 3] = task;
+      mbar_arrive(smem_u32(&bars->item_full[items & 3]));
+    }
+    __syncwarp();
   };
   for (; ok && walk.next(p, item); ++items) {
     const DPlace at = place_of(p, item);
     const int hk = at.h / p.group;
     if (items > 0 && !diff_wait(q_empty, (items - 1) & 1, bars, p)) break;
+    publish(DTask{item.u0, item.b, item.keys, item.kv0, item.kv1, item.nk, at.h, at.q0,
+                  static_cast<short>(at.vp), static_cast<short>(item.piece ? 2 : 1)});
     if (elect_one()) {
       mbar_arrive_expect_tx(q_full, C::QB);
       for (int hf = 0; hf < C::DQ / 64; ++hf)
@@ -352,14 +371,16 @@ __device__ void diff_loader(const DiffParams &p, uint8_t *smem, DBars *bars) {
     }
     __syncwarp();
     for (int j = item.kv0; ok && j < item.kv1; ++j) {
-      for (int ks = 0; ok && ks < C::KSL; ++ks) ok = load(&p.tm_k, ks * C::DV, j, hk, item.b);
-      ok = ok && load(&p.tm_v, at.vp * C::DV, j, hk, item.b);
+      for (int ks = 0; ok && ks < C::KSL; ++ks) ok = load(k_use, 0, C::KS, &p.tm_k, ks * C::DV, j, hk, item.b);
+      ok = ok && load(v_use, C::KS, C::VS, &p.tm_v, at.vp * C::DV, j, hk, item.b);
     }
   }
+  publish(DTask{0, 0, 0, 0, 0, 0, 0, 0, 0, 0});   // the end, also after a wait that gave up
   // Every load issued must land before the CTA releases its shared memory.
-  for (uint32_t s = 0; s < C::STAGES && s < it; ++s) {
-    const uint32_t last = s + ((it - 1 - s) / C::STAGES) * C::STAGES;
-    diff_drain(smem_u32(&bars->kv_full[s]), (last / C::STAGES) & 1);
+  for (uint32_t s = 0; s < C::KS + C::VS; ++s) {
+    const uint32_t n = s < C::KS ? C::KS : C::VS, first = s < C::KS ? s : s - C::KS;
+    const uint32_t uses = s < C::KS ? k_use : v_use;
+    if (uses > first) diff_drain(smem_u32(&bars->kv_full[s]), ((uses - 1 - first) / n) & 1);
   }
   if (items > 0) diff_drain(q_full, (items - 1) & 1);
 }
@@ -387,19 +408,20 @@ __device__ __forceinline__ void diff_pv(uint32_t dcol, uint32_t pcol, uint64_t v
     tc_mma_ts(dcol, pcol + kk * 8, vdesc + static_cast<uint64_t>((kk * 2048) >> 4), idesc,
               (kk > 0 || accumulate) ? 1u : 0u);
 }
-// The ring use of a step's K (map t) or V tile, its barriers and its place in a descriptor.
-template <class C>
+// A ring's slots as its consumers see them. K and V have a ring each, so that a consumer sees
+// every phase of the barriers it waits on: a parity wait that skips one could pass too early.
+template <int FIRST, int N, int BYTES>
 struct DRing {
   DBars *bars;
-  __device__ __forceinline__ uint32_t slot(uint32_t use) const { return use % C::STAGES; }
+  __device__ __forceinline__ uint32_t slot(uint32_t use) const { return FIRST + use % N; }
   __device__ __forceinline__ bool full(uint32_t use, const DiffParams &p) const {
-    return diff_wait(smem_u32(&bars->kv_full[slot(use)]), (use / C::STAGES) & 1, bars, p);
+    return diff_wait(smem_u32(&bars->kv_full[slot(use)]), (use / N) & 1, bars, p);
   }
   __device__ __forceinline__ uint32_t empty(uint32_t use) const {
     return smem_u32(&bars->kv_empty[slot(use)]);
   }
   __device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t use) const {
-    return desc + static_cast<uint64_t>(slot(use) * (C::SLOT >> 4));
+    return desc + static_cast<uint64_t>(slot(use) * (BYTES >> 4));
   }
 };
 constexpr uint64_t kChunkRows = (BC * 128) >> 4;   // descriptor step to a tile's second 64 keys
@@ -409,10 +431,10 @@ constexpr uint64_t kChunkRows = (BC * 128) >> 4;   // descriptor step to a tile'
 // columns with P, once the products of the tile before have read it (pv_done: a wait, as the
 // order of two threads' tcgen05 operations, or of two shapes, is not given).
 template <class C>
-__device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
+__device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in, const int half) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_in, 0);
   uint32_t use = 0, items = 0, step = 0;   // ring use of the tile's K, items, tiles
-  const DRing<C> ring{bars};
+  const DRing<0, C::KS, C::SLOT> ring{bars};
   const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
   DWalk walk;
@@ -421,11 +443,11 @@ __device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bar
   for (; walk.next(p, item); ++items) {
     const int nk = item.kv1 - item.kv0;
     if (!diff_wait(smem_u32(&bars->q_full), items & 1, bars, p)) goto drain;
-    for (int j = 0; j < nk; ++j, ++step, use += C::USES) {
-      for (int half = 0; half < 2; ++half)
+    for (int j = 0; j < nk; ++j, ++step, use += C::KSL) {
+      {
         for (int t = 0; t < 2; ++t) {
           const uint32_t ku = use + (C::KSL == 2 ? t : 0);
-          if (half == 0 && (C::KSL == 2 || t == 0) && !ring.full(ku, p)) goto drain;
+          if ((C::KSL == 2 || t == 0) && !ring.full(ku, p)) goto drain;
           const uint32_t ready = smem_u32(half == 0 ? &bars->e_free[t] : &bars->pv_done[t]);
           if (step >= 1 && !diff_wait(ready, (step - 1) & 1, bars, p)) goto drain;
           tc_fence_after();
@@ -433,26 +455,27 @@ __device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bar
             diff_qk<C>(tmem + t * 128 + (half == 0 ? BC : 0), qdesc,
                        ring.at(kdesc0, ku) + (half == 0 ? 0 : kChunkRows), t);
             tc_commit(smem_u32(half == 0 ? &bars->e_full[t] : &bars->l_full[t]));
-            if (half == 1 && (C::KSL == 2 || t == 1)) tc_commit(ring.empty(ku));
-            if (half == 1 && j == nk - 1 && t == 1) tc_commit(smem_u32(&bars->q_empty));
+            if (C::KSL == 2 || t == 1) tc_commit(ring.empty(ku));
+            if (j == nk - 1 && t == 1) tc_commit(smem_u32(&bars->q_empty));
           }
           __syncwarp();
         }
+      }
     }
   }
 drain:
   // All MMAs issued must finish before Tensor Memory is released.
-  if (elect_one()) tc_commit(smem_u32(&bars->drain[0]));
+  if (elect_one()) tc_commit(smem_u32(&bars->drain[half * 2]));
   __syncwarp();
-  diff_drain(smem_u32(&bars->drain[0]), 0);
+  diff_drain(smem_u32(&bars->drain[half * 2]), 0);
 }
 
 template <class C>
 __device__ void diff_product_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_in, 0);
   const int lane = threadIdx.x & 31;
-  uint32_t use = C::KSL, items = 0, step = 0;   // ring use of the tile's V
-  const DRing<C> ring{bars};
+  uint32_t use = 0, items = 0, step = 0;   // ring use of the tile's V
+  const DRing<C::KS, C::VS, C::SLOT> ring{bars};
   const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_RING), kDiffHalf, 1024);
   // A key past the batch entry's length has weight 0, but what lies in its row of V may not
   // be a number: the rows behind the last key are cleared before the products read them.
@@ -472,7 +495,7 @@ __device__ void diff_product_issuer(const DiffParams &p, uint8_t *smem, DBars *b
   DItem item;
   for (; walk.next(p, item); ++items) {
     const int nk = item.kv1 - item.kv0;
-    for (int j = 0; j < nk; ++j, ++step, use += C::USES) {
+    for (int j = 0; j < nk; ++j, ++step, ++use) {
       if (!ring.full(use, p)) goto drain;
       clear_tail(item.keys, item.kv0 + j);
       // Each half's products as soon as its weights are written: the early half's run beside the
@@ -486,6 +509,7 @@ __device__ void diff_product_issuer(const DiffParams &p, uint8_t *smem, DBars *b
                      ring.at(vdesc0, use) + (half == 0 ? 0 : kChunkRows), j > 0 || half == 1 ? 1u : 0u);
           if (half == 1) tc_commit(smem_u32(&bars->pv_done[t]));
           if (u == 3) {
+            tc_commit(ring.empty(use));
             tc_commit(ring.empty(use));
             if (j == nk - 1) tc_commit(smem_u32(&bars->o_full));
           }
@@ -532,24 +556,14 @@ __device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (
   return max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
 }
 
-// This thread's NX columns (from col0 of the unit's) of one finished row: norm, scale, store.
-// `ss` is the whole row's sum of squares.
+// The norm, from the whole row's sum of squares `ss`, and the output's factor on NX columns.
 template <class C, int NX>
-__device__ __forceinline__ void finish_row(const DiffParams &p, int b, const DPlace &at, int n, int col0, float (&x)[NX], float ss) {
-  constexpr int D = C::DQ;
-  if (!C::NORM && p.weight) {   // d = 256: the norm follows in a kernel of its own
-    float4 *dst = reinterpret_cast<float4 *>(stage_row(p, b, at.h, n, D) + at.vp * C::DV + col0);
-#pragma unroll
-    for (int i = 0; i < NX / 4; ++i)
-      dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    return;
-  }
-  uint16_t *dst = out_row(p, b, at.h, n, D) + at.vp * C::DV + col0;
+__device__ __forceinline__ void scale_row(const DiffParams &p, const float *weight, int col0, float (&x)[NX], float ss) {
   if (C::NORM && p.weight) {
-    const float r = rsqrtf(ss * (1.f / D) + p.eps) * p.out_scale;
+    const float r = rsqrtf(ss * (1.f / C::DQ) + p.eps) * p.out_scale;
 #pragma unroll
     for (int i = 0; i < NX / 4; ++i) {
-      const float4 w = __ldg(reinterpret_cast<const float4 *>(p.weight + col0) + i);
+      const float4 w = reinterpret_cast<const float4 *>(weight + col0)[i];
       x[4 * i] *= r * w.x;
       x[4 * i + 1] *= r * w.y;
       x[4 * i + 2] *= r * w.z;
@@ -559,6 +573,22 @@ __device__ __forceinline__ void finish_row(const DiffParams &p, int b, const DPl
 #pragma unroll
     for (int i = 0; i < NX; ++i) x[i] *= p.out_scale;
   }
+}
+
+// This thread's NX columns (from col0 of the unit's) of one finished row: norm, scale, store.
+// `ss` is the whole row's sum of squares.
+template <class C, int NX>
+__device__ __forceinline__ void finish_row(const DiffParams &p, const float *weight, int b, const DPlace &at, int n, int col0, float (&x)[NX], float ss) {
+  constexpr int D = C::DQ;
+  if (!C::NORM && p.weight) {   // d = 256: the norm follows in a kernel of its own
+    float4 *dst = reinterpret_cast<float4 *>(stage_row(p, b, at.h, n, D) + at.vp * C::DV + col0);
+#pragma unroll
+    for (int i = 0; i < NX / 4; ++i)
+      dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    return;
+  }
+  uint16_t *dst = out_row(p, b, at.h, n, D) + at.vp * C::DV + col0;
+  scale_row<C, NX>(p, weight, col0, x, ss);
   if constexpr (NX >= 8) {
 #pragma unroll
     for (int i = 0; i < NX / 8; ++i)
@@ -578,10 +608,10 @@ __device__ __forceinline__ float map_factor(int t, float lambda, float l) {
 // One piece of a cut unit: leaves its partial result in the workspace; the CTA that counts the
 // last piece merges all of them. All softmax warps take part; `l` is this thread's map's sum.
 template <class C>
-__device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const DItem item,
+__device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float *exch, const DTask item,
                                         uint32_t tmem, float m, float l, bool dead) {
   const int tid = threadIdx.x, t = tid >> 7, row = tid & 127, lane = tid & 31;
-  const DPlace at = place_of(p, item);
+  const DPlace at{item.h, item.q0, item.vp};
   const float lambda = __ldg(p.lambda + at.h);
   const int rows = min(BM, p.Nq - at.q0);
   const long long T = bars->plan.total;
@@ -681,7 +711,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       softmax_sync();
       ss = sums[row] + sums[row + 128];
     }
-    if (row < rows) finish_row<C, NX>(p, item.b, at, at.q0 + row, col0, x, ss);
+    if (row < rows) finish_row<C, NX>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + row, col0, x, ss);
     return;
   }
   // Few rows: row by row, a warp takes CW groups of four columns, and its lanes share the pieces.
@@ -737,42 +767,55 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
 #pragma unroll
       for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
     }
-    if (pg == 0) finish_row<C, 4>(p, item.b, at, at.q0 + r, c4 * 4, x, ss);
+    if (pg == 0) finish_row<C, 4>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, c4 * 4, x, ss);
   }
 }
 
-// 64 scores of a row to weights 2^(s * scale - m), packed to bf16 pairs in place of `pk`; their sum.
-__device__ __forceinline__ float weights64(const uint32_t (&s)[2][32], float scale, float m,
-                                           uint32_t (&pk)[2][16]) {
-  // Without any key m is -inf, and the weights are 2^(-inf - 0) = 0.
-  const float neg_m = m == -INFINITY ? 0.f : -m;
-  const uint64_t scale2 = f2_pack(scale, scale), negm2 = f2_pack(neg_m, neg_m);
-  uint64_t sum2[2] = {0ull, 0ull};
+// 32 scores of a row to weights 2^(s * scale - m), rounded to bf16 pairs: P goes to the tensor
+// cores in bf16, as V does; the sum stays fp32 (two packed chains).
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scale2, uint64_t negm2,
+                                          uint32_t (&pk)[16], uint64_t (&sum2)[2]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint64_t x2 = f2_fma(
-          f2_pack(__uint_as_float(s[h][2 * i]), __uint_as_float(s[h][2 * i + 1])), scale2, negm2);
-      float x0, x1;
-      f2_unpack(x2, x0, x1);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
-      pk[h][i] = pack_bf16x2(p0, p1);   // P goes to the tensor cores in bf16, as V does; the sum is fp32
-    }
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t x2 =
+        f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, negm2);
+    float x0, x1;
+    f2_unpack(x2, x0, x1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+    pk[i] = pack_bf16x2(p0, p1);
+  }
+}
+// Without any key the maximum is -inf, and the weights are 2^(-inf - 0) = 0.
+__device__ __forceinline__ uint64_t neg2(float m) {
+  const float n = m == -INFINITY ? 0.f : -m;
+  return f2_pack(n, n);
+}
+__device__ __forceinline__ float sum_of(const uint64_t (&sum2)[2]) {
   float a, b;
   f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
   return a + b;
 }
-__device__ __forceinline__ void mask64(uint32_t (&s)[2][32], int valid) {
-  if (valid < BC) {
-    asm volatile("");   // keeps this a branch
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (32 * h + i >= valid) s[h][i] = 0xff800000u;   // -inf, whatever the score was
-  }
+// Whether a barrier's phase is complete, without waiting; asked early, so that a phase that is
+// complete costs no wait (about 100 cycles) when it is needed.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The scores of keys from `valid` on, of 64 in Tensor Memory, become -inf, whatever they were. (In
+// place, one column at a time: selects on the registers would double the inner loop's code.)
+__device__ __noinline__ void mask64(uint32_t taddr, int valid) {
+  for (int c = max(valid, 0); c < BC; ++c)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr + c), "r"(0xff800000u)
+                 : "memory");
+  tmem_wait_st();
 }
 
 // The factor 2^(a - b) of a maximum that moved from a to b; 1 where it did not (-inf included).
@@ -799,20 +842,22 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (!dead && !diff_wait_inline(bar, parity, bars, p)) dead = true;
   };
-  if (tid == 0) {
-    bars->walk.start(p, bars->plan);
-    bars->more[0] = bars->walk.next(p, bars->item[0]);
-  }
-  softmax_sync();
-  for (; bars->more[items & 1]; ++items) {
-    const DItem &item = bars->item[items & 1];
+  for (;; ++items) {
+    const uint32_t item_full = smem_u32(&bars->item_full[items & 3]);
+    wait(item_full, (items >> 2) & 1);
+    if (dead) diff_drain(item_full, (items >> 2) & 1);   // every warp sees the same list to its end
+    const DTask &item = bars->task[items & 3];
+    if (item.kind == 0) break;
     // No query in this warp's rows: nothing to compute or store, but the barriers' arrivals.
-    const bool idle = place_of(p, item).q0 + wq * 32 >= p.Nq;
+    const bool idle = item.q0 + wq * 32 >= p.Nq;
+    const float lambda = __ldg(p.lambda + item.h);
     const int nk = item.kv1 - item.kv0;
     int valid = item.keys - item.kv0 * BN;   // keys from this tile on that count
     float m = -INFINITY, l = 0.f;
+    const uint64_t scale2 = f2_pack(scale, scale);
+    bool ready = false;   // this tile's early scores were seen complete
     for (int j = 0; j < nk; ++j, ++step, valid -= BN) {
-      wait(e_full, step & 1);
+      if (!__all_sync(0xffffffffu, ready)) wait(e_full, step & 1);
       if (idle) {
         mbar_arrive(e_free);
         wait(l_full, step & 1);
@@ -821,10 +866,12 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
         continue;
       }
       uint32_t pe[2][16], pl[2][16];
-      float alpha = 1.f, sum;
-      bool rescale;   // of O, by alpha, in some lane
+      uint64_t sum2[2] = {0ull, 0ull};
+      float alpha = 1.f, early;   // early: the early half's sum
+      bool rescale;               // of O, by alpha, in some lane
       tc_fence_after();
       {
+        if (valid < BC) mask64(tS + BC, valid);
         uint32_t s[2][32];
         tmem_ld32(tS + 64, s[0]);
         tmem_ld32(tS + 96, s[1]);
@@ -832,28 +879,31 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
         tmem_wait_ld_regs(s[1]);
         tc_fence_before();
         mbar_arrive(e_free);
-        mask64(s, valid);
         const float mx = max64(s[0], s[1]) * scale, before = m;
         if (j == 0 || mx > m + kDiffRescale) m = ceilf(mx);
-        sum = weights64(s, scale, m, pe);
+        const uint64_t negm2 = neg2(m);
+        weights32(s[0], scale2, negm2, pe[0], sum2);
+        ready = mbar_test(l_full, step & 1);
+        weights32(s[1], scale2, negm2, pe[1], sum2);
+        early = sum_of(sum2);
         rescale = j > 0 && __any_sync(0xffffffffu, m != before);
         if (rescale) alpha = shrink(before, m);
       }
-      wait(l_full, step & 1);
+      if (!__all_sync(0xffffffffu, ready)) wait(l_full, step & 1);
       tc_fence_after();
+      if (valid < BN) mask64(tS, valid - BC);
       uint32_t s[2][32];
       tmem_ld32(tS, s[0]);
       tmem_ld32(tS + 32, s[1]);
       tmem_wait_ld_regs(s[0]);
       tmem_wait_ld_regs(s[1]);
-      mask64(s, valid - BC);
       const float mx = max64(s[0], s[1]) * scale, before = m;
       if (mx > m + kDiffRescale) m = ceilf(mx);
       if (__any_sync(0xffffffffu, m != before)) {
         const float a = shrink(before, m);   // a power of two: exact on the rounded weights
         const uint32_t a2 = pack_bf16x2(a, a);
         alpha *= a;
-        sum *= a;
+        early *= a;
         rescale = j > 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -874,13 +924,18 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
       }
       tmem_st16(tS, pe[0]);
       tmem_st16(tS + 16, pe[1]);
+      // Some exponentials hide the store's latency.
+      const uint64_t negm2 = neg2(m);
+      sum2[0] = sum2[1] = 0ull;
+      weights32(s[0], scale2, negm2, pl[0], sum2);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_full);
-      sum += weights64(s, scale, m, pl);
+      weights32(s[1], scale2, negm2, pl[1], sum2);
       tmem_st16(tS + 32, pl[0]);
       tmem_st16(tS + 48, pl[1]);
-      l = fmaf(l, alpha, sum);
+      ready = j + 1 < nk && mbar_test(e_full, (step + 1) & 1);
+      l = fmaf(l, alpha, early + sum_of(sum2));
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_full + 8);
@@ -888,35 +943,32 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
     // Both maps' O are final once the unit's last product completes.
     wait(o_full, items & 1);
     tc_fence_after();
-    if (tid == 0) bars->more[(items + 1) & 1] = bars->walk.next(p, bars->item[(items + 1) & 1]);
-    __syncwarp();
-    if (item.piece) {
+    if (item.kind == 2) {
       diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
       continue;
     }
     exch[tid] = l;
     softmax_sync();
     constexpr int NX = C::DV / 2;
-    const DPlace at = place_of(p, item);
-    const int b = item.b;   // taken before the meeting that lets `item` be replaced
+    const DPlace at{item.h, item.q0, item.vp};
+    const int b = item.b;
     const int col0 = t * NX;
     float x[NX], ss = 0.f;
     if (!idle) {
-      const float lambda = __ldg(p.lambda + at.h);
       const float f1 = map_factor(0, lambda, exch[row]);
       const float f2 = map_factor(1, lambda, exch[row + 128]);
       const uint32_t o1 = tmem + lane_base + C::COL_O + col0;
 #pragma unroll
-      for (int c = 0; c < NX / 16; ++c) {
-        uint32_t a[16], v[16];
-        tmem_ld16(o1 + 16 * c, a);
-        tmem_ld16(o1 + C::DV + 16 * c, v);
-        tmem_wait_ld16(a);
-        tmem_wait_ld16(v);
+      for (int c = 0; c < NX / 32; ++c) {
+        uint32_t a[32], v[32];
+        tmem_ld32(o1 + 32 * c, a);
+        tmem_ld32(o1 + C::DV + 32 * c, v);
+        tmem_wait_ld_regs(a);
+        tmem_wait_ld_regs(v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 32; ++i) {
           const float y = fmaf(f1, __uint_as_float(a[i]), f2 * __uint_as_float(v[i]));
-          x[16 * c + i] = y;
+          x[32 * c + i] = y;
           ss = fmaf(y, y, ss);
         }
       }
@@ -927,7 +979,34 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
     // All have read O (and l): a map's next P may let the next unit's products overwrite it.
     softmax_sync();
     if constexpr (C::NORM) ss = sums[row] + sums[row + 128];
-    if (at.q0 + row < p.Nq && !dead) finish_row<C, NX>(p, b, at, at.q0 + row, col0, x, ss);
+    if (idle || dead) continue;
+    if constexpr (!C::NORM) {   // no room to stage the rows
+      if (at.q0 + row < p.Nq) finish_row<C, NX>(p, exch + 2 * kSoftThreads, b, at, at.q0 + row, col0, x, ss);
+      continue;
+    }
+    // Rows lie across the lanes: through shared memory (16-byte chunks, each row's permuted by
+    // its number against bank conflicts), so that NX / 8 lanes store one row's part together.
+    constexpr int CH = NX / 8, RPS = 32 / CH;   // chunks of a row's part; rows a warp stores at once
+    uint4 *stg = reinterpret_cast<uint4 *>(smem + C::OFF_STG) + (tid / 32) * 32 * CH;
+    const int lane = tid & 31;
+    scale_row<C, NX>(p, exch + 2 * kSoftThreads, col0, x, ss);
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      stg[lane * CH + (i ^ (lane & (CH - 1)))] =
+          make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                     pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+    unsigned long long dst = 0;
+    if (at.q0 + row < p.Nq)
+      dst = reinterpret_cast<unsigned long long>(out_row(p, b, at.h, at.q0 + row, C::DQ) + at.vp * C::DV + col0);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int r = k * RPS + lane / CH, ch = lane % CH;
+      const unsigned long long to = __shfl_sync(0xffffffffu, dst, r);
+      const uint4 v = stg[r * CH + (ch ^ (r & (CH - 1)))];
+      if (to) reinterpret_cast<uint4 *>(to)[ch] = v;
+    }
+    __syncwarp();   // the staged rows have been read
   }
 }
 
@@ -942,11 +1021,12 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_empty), 1);
-    for (int s = 0; s < C::STAGES; ++s) {
+    mbar_init(smem_u32(&bars->q_empty), 2);
+    for (int s = 0; s < (C::KS + C::VS); ++s) {
       mbar_init(smem_u32(&bars->kv_full[s]), 1);
-      mbar_init(smem_u32(&bars->kv_empty[s]), 1);
+      mbar_init(smem_u32(&bars->kv_empty[s]), 2);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->item_full[i]), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bars->e_full[t]), 1);
       mbar_init(smem_u32(&bars->e_free[t]), 128);
@@ -958,11 +1038,16 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
     mbar_init(smem_u32(&bars->o_full), 1);
     mbar_init(smem_u32(&bars->drain[0]), 1);
     mbar_init(smem_u32(&bars->drain[1]), 1);
+    mbar_init(smem_u32(&bars->drain[2]), 1);
     bars->abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   if (warp == 1 && p.split) plan_split(p, bars);
+  if (C::NORM && p.weight && warp >= 4 && warp < 4 + C::DV / 32) {   // the norm's weights
+    const int i = threadIdx.x - 128;
+    reinterpret_cast<float *>(smem + C::OFF_EXCH)[2 * kSoftThreads + i] = __ldg(p.weight + i);
+  }
   if (warp == kScoreWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
@@ -980,7 +1065,10 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
     diff_loader<C>(p, smem, bars);
     __syncwarp();
   } else if (warp == kScoreWarp) {
-    diff_score_issuer<C>(p, smem, bars, tmem);
+    diff_score_issuer<C>(p, smem, bars, tmem, 0);
+    __syncwarp();
+  } else if (warp == kThirdWarp) {
+    diff_score_issuer<C>(p, smem, bars, tmem, 1);
     __syncwarp();
   } else if (warp == kProductWarp) {
     diff_product_issuer<C>(p, smem, bars, tmem);
