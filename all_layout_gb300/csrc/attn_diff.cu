@@ -54,8 +54,7 @@ namespace {
 constexpr int BM = kTileRows, BN = kTileRows;
 constexpr int BC = 64;                              // keys of half a KV tile
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kDiffThreads = kSoftThreads + 128;
-constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadWarp = kSoftWarps + 2, kThirdWarp = kSoftWarps + 3;
+constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadWarp = kSoftWarps + 2;
 constexpr int kDiffHalf = BM * 128;                 // one 64-column half of a 128-row tile
 constexpr uint32_t kDiffSleepNs = 100000;
 constexpr float kDiffRescale = 8.0f;                // log2 units: rescale O only past a growth of 2^8
@@ -65,10 +64,13 @@ constexpr int kFewRows = 8;                         // rows of a tile up to whic
 template <int DH_, int DV_>
 struct DCfg {
   static constexpr int DH = DH_, DV = DV_, DQ = 2 * DH;
+  // With a twelfth warp, which does nothing, the compiler's schedule of the softmax came out 7%
+  // faster at DV = 128 (a KV tile 1.27 -> 1.19 us) and 2% slower at 64.
+  static constexpr int THREADS = kSoftThreads + (DV == 64 ? 96 : 128);
   static constexpr int SLOT = BN * DV * 2;          // a ring slot: the V tile, or DV columns of the K tile
   static constexpr int KSL = DQ / DV;               // slots of a K tile (2 at d = 256: one per map)
   static constexpr int QB = BM * DQ * 2;
-  static constexpr int KS = 3, VS = DV == 64 ? 3 : 2;   // slots of the K ring and of the V ring behind it
+  static constexpr int KS = 3, VS = DV == 64 ? 3 : 2;   // slots of the K ring, of the V ring behind it
   static constexpr bool NORM = DQ == DV;            // the whole row is in one unit: the norm is fused
   static constexpr int OFF_RING = QB;
   static constexpr int OFF_BAR = OFF_RING + (KS + VS) * SLOT;
@@ -170,13 +172,14 @@ struct DTask {
 };
 
 struct DBars {
+  static constexpr int kScore = kScoreWarp, kProduct = kProductWarp;   // warps
   uint64_t q_full, q_empty;
   uint64_t kv_full[6], kv_empty[6];
   uint64_t e_full[2], e_free[2];   // [map]: the early half's scores written; read into registers
   uint64_t l_full[2];              // the late half's scores written
   uint64_t p_full[2][2];           // [map][half]: the weights written
   uint64_t pv_done[2];             // the tile's products done
-  uint64_t o_full, drain[3];
+  uint64_t o_full, drain[2];
   uint64_t item_full[4];
   DPlan plan;
   DTask task[4];           // the softmax warps' items, published by the loader (task i mod 4)
@@ -219,11 +222,12 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
 }
 
 // Bounded wait on a barrier phase; false after a timeout here or elsewhere in the CTA.
-__device__ __noinline__ bool diff_wait_slow(uint32_t bar, uint32_t parity, DBars *bars, int *status,
+template <class B>
+__device__ __noinline__ bool diff_wait_slow(uint32_t bar, uint32_t parity, B *bars, int *status,
                                             uint64_t limit) {
   volatile int *abort_flag = &bars->abort;
   const int warp = threadIdx.x / 32;
-  const bool sleepy = warp < kSoftWarps || warp == kDiffLoadWarp;   // the issuers poll
+  const bool sleepy = warp != B::kScore && warp != B::kProduct;   // the issuers poll
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (sleepy ? mbar_try_wait_sleep(bar, parity, kDiffSleepNs) : mbar_try_wait(bar, parity))
@@ -238,14 +242,16 @@ __device__ __noinline__ bool diff_wait_slow(uint32_t bar, uint32_t parity, DBars
     }
   }
 }
-__device__ __forceinline__ bool diff_wait(uint32_t bar, uint32_t parity, DBars *bars,
+template <class B>
+__device__ __forceinline__ bool diff_wait(uint32_t bar, uint32_t parity, B *bars,
                                           const DiffParams &p) {
   const bool ok = mbar_try_wait(bar, parity) ||
                   diff_wait_slow(bar, parity, bars, p.status, p.wait_limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 // The same with no call, for waits made while most registers are live.
-__device__ __forceinline__ bool diff_wait_inline(uint32_t bar, uint32_t parity, DBars *bars,
+template <class B>
+__device__ __forceinline__ bool diff_wait_inline(uint32_t bar, uint32_t parity, B *bars,
                                                  const DiffParams &p) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
@@ -275,7 +281,8 @@ __device__ __noinline__ void diff_drain(uint32_t bar, uint32_t parity) {
 }
 
 // The split region's size and this CTA's place in it, by one warp.
-__device__ void plan_split(const DiffParams &p, DBars *bars) {
+template <class B>
+__device__ void plan_split(const DiffParams &p, B *bars) {
   const int lane = threadIdx.x & 31;
   const int first = p.waves * static_cast<int>(gridDim.x), b0 = first / p.units_b;
   auto size_of = [&](int b) -> long long {
@@ -312,6 +319,24 @@ __device__ void plan_split(const DiffParams &p, DBars *bars) {
     if (b + 32 >= p.B) break;
   }
   if (lane == 0) bars->plan = DPlan{0, 0, 0, b0};
+}
+
+// The consecutive CTAs that a cut unit's pieces run on.
+struct DSpan {
+  int first, pieces;
+};
+__device__ __forceinline__ DSpan span_of(const DPlan &plan, const DTask &item) {
+  const long long T = plan.total;
+  const int G = plan.grid;
+  auto start = [&](int c) { return static_cast<long long>(c) * T / G; };
+  auto owner = [&](long long pos) {
+    int c = static_cast<int>(pos * G / T);
+    while (c + 1 < G && start(c + 1) <= pos) ++c;
+    while (c > 0 && start(c) > pos) --c;
+    return c;
+  };
+  const int first = owner(item.u0);
+  return DSpan{first, owner(item.u0 + item.nk - 1) - first + 1};
 }
 
 __device__ __forceinline__ DPlace place_of(const DiffParams &p, const DItem &it) {
@@ -408,22 +433,33 @@ __device__ __forceinline__ void diff_pv(uint32_t dcol, uint32_t pcol, uint64_t v
     tc_mma_ts(dcol, pcol + kk * 8, vdesc + static_cast<uint64_t>((kk * 2048) >> 4), idesc,
               (kk > 0 || accumulate) ? 1u : 0u);
 }
-// A ring's slots as its consumers see them. K and V have a ring each, so that a consumer sees
-// every phase of the barriers it waits on: a parity wait that skips one could pass too early.
+// A ring's place as a consumer sees it: the slot (and its descriptor offset) and the parity of the
+// slot's use. K and V have a ring each, so that a consumer sees every phase of the barriers it
+// waits on: a parity wait that skips one could pass too early.
 template <int FIRST, int N, int BYTES>
 struct DRing {
-  DBars *bars;
-  __device__ __forceinline__ uint32_t slot(uint32_t use) const { return FIRST + use % N; }
-  __device__ __forceinline__ bool full(uint32_t use, const DiffParams &p) const {
-    return diff_wait(smem_u32(&bars->kv_full[slot(use)]), (use / N) & 1, bars, p);
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
   }
-  __device__ __forceinline__ uint32_t empty(uint32_t use) const {
-    return smem_u32(&bars->kv_empty[slot(use)]);
+  __device__ __forceinline__ bool full(DBars *bars, const DiffParams &p) const {
+    return diff_wait(smem_u32(&bars->kv_full[FIRST]) + slot * 8, parity, bars, p);
   }
-  __device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t use) const {
-    return desc + static_cast<uint64_t>(slot(use) * (BYTES >> 4));
+  __device__ __forceinline__ uint32_t empty(DBars *bars) const {
+    return smem_u32(&bars->kv_empty[FIRST]) + slot * 8;
+  }
+  __device__ __forceinline__ uint64_t offset() const {
+    return static_cast<uint64_t>((FIRST + slot) * (BYTES >> 4));
   }
 };
+// An item's tiles, as a value that the compiler knows to be the same in every lane: the issuers'
+// loops, and the addresses and descriptors they step, then stay in uniform registers. (An issuer
+// stands between every two halves of the softmax: with these in vector registers a tile took 5%
+// longer, with the loops below rolled up as well 35%.)
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 constexpr uint64_t kChunkRows = (BC * 128) >> 4;   // descriptor step to a tile's second 64 keys
 
 // The score issuer. The first 64 keys of a tile (the early half) go out as soon as the softmax
@@ -431,59 +467,67 @@ constexpr uint64_t kChunkRows = (BC * 128) >> 4;   // descriptor step to a tile'
 // columns with P, once the products of the tile before have read it (pv_done: a wait, as the
 // order of two threads' tcgen05 operations, or of two shapes, is not given).
 template <class C>
-__device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in, const int half) {
+__device__ void diff_score_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_in, 0);
-  uint32_t use = 0, items = 0, step = 0;   // ring use of the tile's K, items, tiles
-  const DRing<0, C::KS, C::SLOT> ring{bars};
+  uint32_t q_parity = 0, parity = 0;   // of the item, of the tile
+  DRing<0, C::KS, C::SLOT> ring;
   const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
+  const uint32_t q_full = smem_u32(&bars->q_full), q_empty = smem_u32(&bars->q_empty);
+  const uint32_t e_free = smem_u32(&bars->e_free[0]), e_full = smem_u32(&bars->e_full[0]);
+  const uint32_t l_full = smem_u32(&bars->l_full[0]), pv_done = smem_u32(&bars->pv_done[0]);
   DWalk walk;
   walk.start(p, bars->plan);
   DItem item;
-  for (; walk.next(p, item); ++items) {
-    const int nk = item.kv1 - item.kv0;
-    if (!diff_wait(smem_u32(&bars->q_full), items & 1, bars, p)) goto drain;
-    for (int j = 0; j < nk; ++j, ++step, use += C::KSL) {
-      {
+  for (; walk.next(p, item); q_parity ^= 1) {
+    const int nk = uniform(item.kv1 - item.kv0);
+    if (!diff_wait(q_full, q_parity, bars, p)) goto drain;
+    for (int j = 0; j < nk; ++j, parity ^= 1) {
+      // K of one map per slot at d = 256: its second slot is the next one.
+      DRing<0, C::KS, C::SLOT> kr[2] = {ring, ring};
+      if (C::KSL == 2) kr[1].advance();
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t ku = use + (C::KSL == 2 ? t : 0);
-          if ((C::KSL == 2 || t == 0) && !ring.full(ku, p)) goto drain;
-          const uint32_t ready = smem_u32(half == 0 ? &bars->e_free[t] : &bars->pv_done[t]);
-          if (step >= 1 && !diff_wait(ready, (step - 1) & 1, bars, p)) goto drain;
+          if (half == 0 && (C::KSL == 2 || t == 0) && !kr[t].full(bars, p)) goto drain;
+          // The phase before this tile's (none before the first tile: such a wait passes).
+          if (!diff_wait((half == 0 ? e_free : pv_done) + 8 * t, parity ^ 1, bars, p)) goto drain;
           tc_fence_after();
           if (elect_one()) {
             diff_qk<C>(tmem + t * 128 + (half == 0 ? BC : 0), qdesc,
-                       ring.at(kdesc0, ku) + (half == 0 ? 0 : kChunkRows), t);
-            tc_commit(smem_u32(half == 0 ? &bars->e_full[t] : &bars->l_full[t]));
-            if (C::KSL == 2 || t == 1) tc_commit(ring.empty(ku));
-            if (j == nk - 1 && t == 1) tc_commit(smem_u32(&bars->q_empty));
+                       kdesc0 + kr[t].offset() + (half == 0 ? 0 : kChunkRows), t);
+            tc_commit((half == 0 ? e_full : l_full) + 8 * t);
+            if (half == 1 && (C::KSL == 2 || t == 1)) tc_commit(kr[t].empty(bars));
+            if (half == 1 && t == 1 && j == nk - 1) tc_commit(q_empty);
           }
           __syncwarp();
         }
-      }
+      ring = kr[1];
+      ring.advance();
     }
   }
 drain:
   // All MMAs issued must finish before Tensor Memory is released.
-  if (elect_one()) tc_commit(smem_u32(&bars->drain[half * 2]));
+  if (elect_one()) tc_commit(smem_u32(&bars->drain[0]));
   __syncwarp();
-  diff_drain(smem_u32(&bars->drain[half * 2]), 0);
+  diff_drain(smem_u32(&bars->drain[0]), 0);
 }
 
 template <class C>
 __device__ void diff_product_issuer(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem_in) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_in, 0);
   const int lane = threadIdx.x & 31;
-  uint32_t use = 0, items = 0, step = 0;   // ring use of the tile's V
-  const DRing<C::KS, C::VS, C::SLOT> ring{bars};
+  uint32_t parity = 0;
+  DRing<C::KS, C::VS, C::SLOT> ring;
   const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_RING), kDiffHalf, 1024);
+  const uint32_t p_full = smem_u32(&bars->p_full[0][0]), pv_done = smem_u32(&bars->pv_done[0]);
+  const uint32_t o_full = smem_u32(&bars->o_full);
   // A key past the batch entry's length has weight 0, but what lies in its row of V may not
   // be a number: the rows behind the last key are cleared before the products read them.
   // (Rows past Nk were filled with zeros by the load.)
-  auto clear_tail = [&](int keys, int j) {
-    const int valid = keys - j * BN;
-    if (valid >= BN || keys >= p.Nk) return;
-    uint8_t *tile = smem + C::OFF_RING + ring.slot(use) * C::SLOT;
+  auto clear_tail = [&](int valid) {
+    uint8_t *tile = smem + C::OFF_RING + (C::KS + ring.slot) * C::SLOT;
     for (int hf = 0; hf < C::DV / 64; ++hf)
       for (int o = valid * 128 + lane * 16; o < kDiffHalf; o += 512)
         *reinterpret_cast<uint4 *>(tile + hf * kDiffHalf + o) = make_uint4(0, 0, 0, 0);
@@ -493,29 +537,32 @@ __device__ void diff_product_issuer(const DiffParams &p, uint8_t *smem, DBars *b
   DWalk walk;
   walk.start(p, bars->plan);
   DItem item;
-  for (; walk.next(p, item); ++items) {
-    const int nk = item.kv1 - item.kv0;
-    for (int j = 0; j < nk; ++j, ++step, ++use) {
-      if (!ring.full(use, p)) goto drain;
-      clear_tail(item.keys, item.kv0 + j);
+  while (walk.next(p, item)) {
+    const int nk = uniform(item.kv1 - item.kv0);
+    // Of the item's tiles only its batch entry's last one can hold such keys.
+    const int last_valid = uniform(item.keys >= p.Nk || item.kv1 < item.nk ? BN : item.keys - (item.nk - 1) * BN);
+    for (int j = 0; j < nk; ++j, parity ^= 1) {
+      if (!ring.full(bars, p)) goto drain;
+      if (j == nk - 1 && last_valid < BN) clear_tail(last_valid);
       // Each half's products as soon as its weights are written: the early half's run beside the
       // late half's exponentials.
+#pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int t = u >> 1, half = u & 1;
-        if (!diff_wait(smem_u32(&bars->p_full[t][half]), step & 1, bars, p)) goto drain;
+        if (!diff_wait(p_full + 8 * u, parity, bars, p)) goto drain;
         tc_fence_after();
         if (elect_one()) {
           diff_pv<C>(tmem + C::COL_O + t * C::DV, tmem + t * 128 + half * 32,
-                     ring.at(vdesc0, use) + (half == 0 ? 0 : kChunkRows), j > 0 || half == 1 ? 1u : 0u);
-          if (half == 1) tc_commit(smem_u32(&bars->pv_done[t]));
+                     vdesc0 + ring.offset() + (half == 0 ? 0 : kChunkRows), j > 0 || half == 1 ? 1u : 0u);
+          if (half == 1) tc_commit(pv_done + 8 * t);
           if (u == 3) {
-            tc_commit(ring.empty(use));
-            tc_commit(ring.empty(use));
-            if (j == nk - 1) tc_commit(smem_u32(&bars->o_full));
+            tc_commit(ring.empty(bars));
+            if (j == nk - 1) tc_commit(o_full);
           }
         }
         __syncwarp();
       }
+      ring.advance();
     }
   }
 drain:
@@ -525,8 +572,7 @@ drain:
 }
 
 // ------------------------------------------------------------------ softmax / epilogue
-// Where output row n of (b, h) begins (bf16), and where its fp32 form for a norm over both
-// column halves.
+// Where output row n of (b, h) begins.
 __device__ __forceinline__ uint16_t *out_row(const DiffParams &p, int b, int h, int n, int d) {
   if (p.shard_mode) {
     const int sh = n / p.rows_per_shard, i = n - sh * p.rows_per_shard;
@@ -535,10 +581,6 @@ __device__ __forceinline__ uint16_t *out_row(const DiffParams &p, int b, int h, 
   }
   return static_cast<uint16_t *>(p.o) + b * p.o_b + h * p.o_h + n * p.o_n;
 }
-__device__ __forceinline__ float *stage_row(const DiffParams &p, int b, int h, int n, int d) {
-  return p.stage + ((static_cast<long long>(b) * p.H + h) * p.Nq + n) * d;
-}
-
 // Maximum over 64 raw scores, in 8 chains of 3-input max.
 __device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (&b)[32]) {
   float mp[8];
@@ -580,13 +622,6 @@ __device__ __forceinline__ void scale_row(const DiffParams &p, const float *weig
 template <class C, int NX>
 __device__ __forceinline__ void finish_row(const DiffParams &p, const float *weight, int b, const DPlace &at, int n, int col0, float (&x)[NX], float ss) {
   constexpr int D = C::DQ;
-  if (!C::NORM && p.weight) {   // d = 256: the norm follows in a kernel of its own
-    float4 *dst = reinterpret_cast<float4 *>(stage_row(p, b, at.h, n, D) + at.vp * C::DV + col0);
-#pragma unroll
-    for (int i = 0; i < NX / 4; ++i)
-      dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    return;
-  }
   uint16_t *dst = out_row(p, b, at.h, n, D) + at.vp * C::DV + col0;
   scale_row<C, NX>(p, weight, col0, x, ss);
   if constexpr (NX >= 8) {
@@ -614,17 +649,8 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
   const DPlace at{item.h, item.q0, item.vp};
   const float lambda = __ldg(p.lambda + at.h);
   const int rows = min(BM, p.Nq - at.q0);
-  const long long T = bars->plan.total;
-  const int G = bars->plan.grid;
-  auto start = [&](int c) { return static_cast<long long>(c) * T / G; };
-  auto owner = [&](long long pos) {
-    int c = static_cast<int>(pos * G / T);
-    while (c + 1 < G && start(c + 1) <= pos) ++c;
-    while (c > 0 && start(c) > pos) --c;
-    return c;
-  };
-  const int c0 = owner(item.u0);
-  const int S = owner(item.u0 + item.nk - 1) - c0 + 1;
+  const DSpan span = span_of(bars->plan, item);
+  const int c0 = span.first, S = span.pieces;
   // Piece k ran on CTA c0 + k, as its first item (slot 0), but for the unit's first piece, which
   // is the last item of its CTA (slot 1).
   auto part = [&](int k) {
@@ -1011,20 +1037,20 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
 }
 
 template <class C>
-__global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid_constant__ DiffParams p) {
+__global__ void __launch_bounds__(C::THREADS, 1) attn_diff_kernel(const __grid_constant__ DiffParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle pattern repeats every 1024 bytes
   if ((smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicExch(p.status, kDevBadPlan);
     return;
   }
   DBars *bars = reinterpret_cast<DBars *>(smem + C::OFF_BAR);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_empty), 2);
+    mbar_init(smem_u32(&bars->q_empty), 1);
     for (int s = 0; s < (C::KS + C::VS); ++s) {
       mbar_init(smem_u32(&bars->kv_full[s]), 1);
-      mbar_init(smem_u32(&bars->kv_empty[s]), 2);
+      mbar_init(smem_u32(&bars->kv_empty[s]), 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->item_full[i]), 1);
     for (int t = 0; t < 2; ++t) {
@@ -1038,7 +1064,6 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
     mbar_init(smem_u32(&bars->o_full), 1);
     mbar_init(smem_u32(&bars->drain[0]), 1);
     mbar_init(smem_u32(&bars->drain[1]), 1);
-    mbar_init(smem_u32(&bars->drain[2]), 1);
     bars->abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -1065,15 +1090,12 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
     diff_loader<C>(p, smem, bars);
     __syncwarp();
   } else if (warp == kScoreWarp) {
-    diff_score_issuer<C>(p, smem, bars, tmem, 0);
-    __syncwarp();
-  } else if (warp == kThirdWarp) {
-    diff_score_issuer<C>(p, smem, bars, tmem, 1);
+    diff_score_issuer<C>(p, smem, bars, tmem);
     __syncwarp();
   } else if (warp == kProductWarp) {
     diff_product_issuer<C>(p, smem, bars, tmem);
     __syncwarp();
-  } else {
+  } else if (warp < kSoftWarps) {
     diff_softmax<C>(p, smem, bars, tmem);
   }
   tc_fence_before();
@@ -1084,29 +1106,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1) attn_diff_kernel(const __grid
   }
 }
 
-// d = 256: the norm of the staged fp32 rows (their columns come from two units), a warp per row.
-__global__ void __launch_bounds__(256) diff_norm_kernel(const __grid_constant__ DiffParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(p.B) * p.H * p.Nq;
-  const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * lane);
-  const float4 w1 = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * lane + 1);
-  for (long long r = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32; r < rows;
-       r += static_cast<long long>(gridDim.x) * 8) {
-    const float4 *src = reinterpret_cast<const float4 *>(p.stage + r * 256) + 2 * lane;
-    const float4 a = __ldcs(src), b = __ldcs(src + 1);
-    float ss = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y + b.z * b.z +
-               b.w * b.w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float f = rsqrtf(ss * (1.f / 256) + p.eps) * p.out_scale;
-    const long long bh = r / p.Nq;
-    const int n = static_cast<int>(r - bh * p.Nq), bb = static_cast<int>(bh / p.H);
-    uint16_t *dst = out_row(p, bb, static_cast<int>(bh - static_cast<long long>(bb) * p.H), n, 256);
-    reinterpret_cast<uint4 *>(dst)[lane] =
-        make_uint4(pack_bf16x2(a.x * f * w0.x, a.y * f * w0.y), pack_bf16x2(a.z * f * w0.z, a.w * f * w0.w),
-                   pack_bf16x2(b.x * f * w1.x, b.y * f * w1.y), pack_bf16x2(b.z * f * w1.z, b.w * f * w1.w));
-  }
-}
+#include "attn_diff_wide.cuh"
 
 // Every output row to zero, 16 bytes a thread.
 __global__ void __launch_bounds__(256) diff_zero_kernel(const __grid_constant__ DiffParams p, int d) {
@@ -1126,7 +1126,7 @@ cudaError_t launch_cfg(const DiffParams &p, int grid, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(attn_diff_kernel<C>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  attn_diff_kernel<C><<<grid, kDiffThreads, C::SMEM, s>>>(p);
+  attn_diff_kernel<C><<<grid, C::THREADS, C::SMEM, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1149,8 +1149,13 @@ cudaError_t launch_diff_zero(const DiffParams &p, int d, int grid, cudaStream_t 
   return cudaGetLastError();
 }
 
-cudaError_t launch_diff_norm(const DiffParams &p, int grid, cudaStream_t s) {
-  diff_norm_kernel<<<grid, 256, 0, s>>>(p);
+int diff_wide_part_floats(int rows) { return wide_part_floats(rows); }
+
+cudaError_t launch_attn_diff_wide(const DiffParams &p, int grid, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(attn_diff_wide_kernel,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, WideCfg::SMEM);
+  if (e != cudaSuccess) return e;
+  attn_diff_wide_kernel<<<grid, WideCfg::THREADS, WideCfg::SMEM, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -29,7 +29,10 @@ struct DiffParams {
   float scale_log2, eps, out_scale;
   float *parts;                       // split: [G][2 slots] partial results
   int *count;                         // split: pieces done of the unit that begins in CTA c's range
-  float *stage;                       // d = 256 with the norm: [B][H][Nq][256] fp32
+  // The d = 256 kernel: rows of a tile's partial results (Nq up to 128), and where map 1 of a whole
+  // unit waits for map 2: [G][256 columns][part_rows] fp32.
+  int part_rows;
+  float *stash;
   int *status;
   unsigned long long wait_limit_ns;
 };
@@ -37,6 +40,8 @@ struct DiffParams {
 int diff_part_floats(int d);          // fp32 values of one piece's partial result
 cudaError_t launch_attn_diff(const DiffParams &p, int d, int grid, cudaStream_t s);
 cudaError_t launch_diff_zero(const DiffParams &p, int d, int grid, cudaStream_t s);   // no keys at all
-cudaError_t launch_diff_norm(const DiffParams &p, int grid, cudaStream_t s);
+// d = 256 with a workspace.
+int diff_wide_part_floats(int rows);
+cudaError_t launch_attn_diff_wide(const DiffParams &p, int grid, cudaStream_t s);
 
 }  // namespace xs

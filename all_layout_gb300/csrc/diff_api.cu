@@ -19,15 +19,15 @@ bool aligned(const void *p, unsigned bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
-unsigned long long stage_bytes(int B, int H, int Nq, int d, bool norm) {
-  if (d != 256 || !norm) return 0;   // d <= 128: the norm is fused
-  const unsigned long long n = static_cast<unsigned long long>(B) * H * Nq * d * 4;
-  return (n + 255) / 256 * 256;
-}
-
 unsigned long long parts_bytes(int grid, int d) {
   return static_cast<unsigned long long>(grid) * 2 * diff_part_floats(d) * 4;
 }
+
+// The d = 256 kernel's workspace: rows of a tile's partial results, a CTA's place for map 1 of a
+// whole unit, and its two partial results.
+int wide_rows(int Nq) { return Nq < kTileRows ? (Nq + 7) / 8 * 8 : kTileRows; }
+unsigned long long wide_stash_bytes(int rows) { return 256ull * rows * 4; }
+unsigned long long wide_parts_bytes(int rows) { return 2ull * diff_wide_part_floats(rows) * 4; }
 
 // Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split
 // schedule. A cut unit costs about kMerge KV tiles more (its partial results are written and
@@ -37,7 +37,8 @@ struct Plan {
 };
 constexpr long kItem = 2, kMerge = 3, kMinTiles = 4;
 
-Plan plan(long long units, int sms, int nk, bool ragged, int d, unsigned long long room) {
+// `per_cta`: bytes of workspace that a CTA's partial results take.
+Plan plan(long long units, int sms, int nk, bool ragged, unsigned long long per_cta, unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
   const Plan whole{0, 0, grid0};
   if (nk < 2 || (units >= sms && units % sms == 0 && !ragged)) return whole;
@@ -49,7 +50,7 @@ Plan plan(long long units, int sms, int nk, bool ragged, int d, unsigned long lo
     if (per < kMinTiles) per = kMinTiles;
     grid = static_cast<int>((T + per - 1) / per);
   }
-  if (parts_bytes(grid, d) > room || grid > static_cast<int>(XS_WORKSPACE_HEADER_BYTES / sizeof(int)))
+  if (per_cta * grid > room || grid * 4 > static_cast<int>(XS_WORKSPACE_HEADER_BYTES / sizeof(int)))
     return whole;
   const long long items = (per + nk - 1) / nk + 1;
   const long long cost_split = waves * (nk + kItem) + per + items * kItem + 2 * kMerge;
@@ -113,8 +114,8 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   }
   if (d != 64 && d != 128 && d != 256) return XS_ERR_UNSUPPORTED;
   const long long qtiles = (static_cast<long long>(Nq) + kTileRows - 1) / kTileRows;
-  const int v_parts = d == 256 ? 2 : 1;
-  if (static_cast<double>(B) * H * static_cast<double>(qtiles) * v_parts > 2147483647.0 ||
+  const int most_parts = d == 256 ? 2 : 1;   // units of a query tile at most
+  if (static_cast<double>(B) * H * static_cast<double>(qtiles) * most_parts > 2147483647.0 ||
       Nk > 0x7fffff00 || Nq > 0x7fffff00)
     return XS_ERR_UNSUPPORTED;
   if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(o, 16) ||
@@ -129,9 +130,12 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
       (Nk > 0 && (!strides_aligned(a->k_stride, B, Hk, Nk) || !strides_aligned(a->v_stride, B, Hk, Nk))) ||
       (!shards && !strides_aligned(o_stride, B, H, Nq)))
     return XS_ERR_ALIGN;
-  const bool norm = a->norm_weight != nullptr;
-  const unsigned long long stage = stage_bytes(B, H, Nq, d, norm);
-  if (stage > 0 && Nk > 0 && ws_bytes < XS_WORKSPACE_HEADER_BYTES + stage) return XS_ERR_INVALID;
+  // d = 256: one map after the other with a workspace (the norm needs the whole row in one CTA),
+  // both at once on halves of v's columns without.
+  const unsigned long long room = ws && ws_bytes > XS_WORKSPACE_HEADER_BYTES ? ws_bytes - XS_WORKSPACE_HEADER_BYTES : 0;
+  const int rows = wide_rows(Nq);
+  const bool wide = d == 256 && room >= wide_stash_bytes(rows);
+  if (d == 256 && a->norm_weight && Nk > 0 && !wide) return XS_ERR_INVALID;
 
   DiffParams p;
   std::memset(&p, 0, sizeof(p));
@@ -162,28 +166,37 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   p.weight = a->norm_weight;
   p.kv_len = a->kv_len;
   p.n_qtiles = static_cast<int>(qtiles);
-  p.v_parts = v_parts;
-  p.units_b = H * p.n_qtiles * v_parts;
+  p.v_parts = d == 256 && !wide ? 2 : 1;
+  p.units_b = H * p.n_qtiles * p.v_parts;
   p.n_units = B * p.units_b;
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
   p.eps = a->eps;
   p.out_scale = a->out_scale;
   if (device_status_word(&p.status) != cudaSuccess) return XS_ERR_CUDA;
   p.wait_limit_ns = wait_limit_ns();
-  // Workspace: counters | fp32 rows (d = 256 with the norm) | partial results.
-  unsigned long long room = 0;
-  if (ws && ws_bytes >= XS_WORKSPACE_HEADER_BYTES + stage) {
-    p.count = static_cast<int *>(ws);
-    p.stage = reinterpret_cast<float *>(static_cast<char *>(ws) + XS_WORKSPACE_HEADER_BYTES);
-    p.parts = p.stage + stage / 4;
-    room = ws_bytes - XS_WORKSPACE_HEADER_BYTES - stage;
+  p.count = static_cast<int *>(ws);
+  float *area = ws ? reinterpret_cast<float *>(static_cast<char *>(ws) + XS_WORKSPACE_HEADER_BYTES) : nullptr;
+  const int nk = (Nk + kTileRows - 1) / kTileRows;
+  const bool ragged = a->kv_len != nullptr;
+  if (!wide) {
+    // Workspace: counters | partial results.
+    p.parts = area;
+    const Plan pl = plan(p.n_units, sms, nk, ragged, parts_bytes(1, d), d == 256 ? 0 : room);
+    p.split = pl.split;
+    p.waves = pl.waves;
+    return launch_attn_diff(p, d, pl.grid, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
   }
-  const Plan pl = plan(p.n_units, sms, (Nk + kTileRows - 1) / kTileRows, a->kv_len != nullptr, d, room);
+  // Workspace: counters | a CTA's place for map 1 each | partial results. A small one has places
+  // for fewer CTAs.
+  const unsigned long long places = room / wide_stash_bytes(rows);
+  const int ctas = places < static_cast<unsigned long long>(sms) ? static_cast<int>(places) : sms;
+  const Plan pl = plan(p.n_units, ctas, nk, ragged, wide_parts_bytes(rows), room - ctas * wide_stash_bytes(rows));
   p.split = pl.split;
   p.waves = pl.waves;
-  if (launch_attn_diff(p, d, pl.grid, s) != cudaSuccess) return XS_ERR_CUDA;
-  if (stage > 0 && launch_diff_norm(p, sms * 8, s) != cudaSuccess) return XS_ERR_CUDA;
-  return XS_OK;
+  p.part_rows = rows;
+  p.stash = area;
+  p.parts = area + ctas * wide_stash_bytes(rows) / 4;
+  return launch_attn_diff_wide(p, pl.grid, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
 }
 
 }  // namespace
@@ -201,12 +214,15 @@ XS_API xs_status xs_diff_attn_fused(const xs_diff_args *args, void *const *out_s
 
 XS_API xs_status xs_diff_workspace_bytes(int B, int H, int Nq, int Nk, int d, int norm,
                                          unsigned long long *bytes) {
+  (void)norm;   // no schedule depends on it so far
   if (!bytes || B < 0 || H < 0 || Nq < 0 || Nk < 0) return XS_ERR_INVALID;
   if (d != 64 && d != 128 && d != 256) return XS_ERR_UNSUPPORTED;
   *bytes = 0;
   if (B == 0 || H == 0 || Nq == 0 || Nk == 0) return XS_OK;
   const int sms = sm_count();
   if (sms <= 0) return XS_ERR_CUDA;
-  *bytes = XS_WORKSPACE_HEADER_BYTES + stage_bytes(B, H, Nq, d, norm != 0) + parts_bytes(sms, d);
+  const int rows = wide_rows(Nq);
+  *bytes = XS_WORKSPACE_HEADER_BYTES +
+           (d == 256 ? sms * (wide_stash_bytes(rows) + wide_parts_bytes(rows)) : parts_bytes(sms, d));
   return XS_OK;
 }
