@@ -14,13 +14,14 @@
 // the scores' issuer, warp 5 the products' issuer, warp 6 the TMA loader.
 // Tensor Memory: S of even tiles [0,128), of odd ones [128,256); P (bf16 pairs) overwrites the
 // first 64 columns of its S; O [256,512).
-// Shared memory: Q of map 1 | Q of map 2 | K ring (2 tiles of a map's 128 columns) | V ring (3
-// halves of 128 columns) | barriers | the norm's weights. 32 KiB a tile.
+// Shared memory: Q of the map | K ring (2 tiles of a map's 128 columns) | V ring (2 tiles, as 4
+// halves of 128 columns) | barriers | the norm's weights. (The other map's Q comes in while the
+// epilogue of the map before runs; a second place for it in V's stead left every tile waiting for V.)
 struct WideCfg {
   static constexpr int DH = 128, DV = 256, DQ = 256;
   static constexpr int SLOT = BN * 128 * 2;
-  static constexpr int KS = 2, VS = 3;
-  static constexpr int OFF_K = 2 * SLOT, OFF_V = OFF_K + KS * SLOT;
+  static constexpr int KS = 2, VS = 4;
+  static constexpr int OFF_K = SLOT, OFF_V = OFF_K + KS * SLOT;
   static constexpr int OFF_BAR = OFF_V + VS * SLOT, OFF_W = OFF_BAR + 768;
   static constexpr int SMEM = OFF_W + 4 * DV;
   static constexpr int THREADS = 224;
@@ -33,7 +34,7 @@ __host__ __device__ constexpr int wide_part_floats(int rows) { return 2 * WideCf
 
 struct WideBars {
   static constexpr int kScore = 4, kProduct = 5, kLoad = 6;   // warps
-  uint64_t q_full[2], q_empty[2];          // [map]
+  uint64_t q_full, q_empty;
   uint64_t k_full[WideCfg::KS], k_empty[WideCfg::KS], v_full[WideCfg::VS], v_empty[WideCfg::VS];
   uint64_t s_full[2], p_full[2][2], pv_done[2];   // [S buffer], P by halves of 64 keys
   uint64_t o_full, drain[2];
@@ -59,7 +60,7 @@ struct WideRing {
 
 __device__ void wide_loader(const DiffParams &p, uint8_t *smem, WideBars *bars) {
   using C = WideCfg;
-  uint32_t items = 0, q_armed[2] = {0, 0}, k_uses = 0, v_uses = 0;
+  uint32_t passes = 0, published = 0, k_uses = 0, v_uses = 0;   // passes: Q loads
   WideRing<C::KS> kr;
   WideRing<C::VS> vr;
   // 128 columns from x of 128 rows, as two 64-column halves.
@@ -71,14 +72,15 @@ __device__ void wide_loader(const DiffParams &p, uint8_t *smem, WideBars *bars) 
     }
     __syncwarp();
   };
-  // Item i's record is written once the scores of map 1 of item i - 1 are done: the softmax has
-  // then begun the last tile but one before them at least, and four records are enough.
+  // Item i's record is written once the scores of item i - 1 are done: the softmax has then begun
+  // the last tile but two of item i - 1 at least, and four records are enough.
   auto publish = [&](const DTask &task) {
     if (elect_one()) {
-      bars->task[items & 3] = task;
-      mbar_arrive(smem_u32(&bars->item_full[items & 3]));
+      bars->task[published & 3] = task;
+      mbar_arrive(smem_u32(&bars->item_full[published & 3]));
     }
     __syncwarp();
+    ++published;
   };
   DWalk walk;
   walk.start(p, bars->plan);
@@ -88,13 +90,13 @@ __device__ void wide_loader(const DiffParams &p, uint8_t *smem, WideBars *bars) 
     const DPlace at = place_of(p, item);
     const int hk = at.h / p.group;
     for (int t = 0; ok && t < 2; ++t) {
-      ok = diff_wait(smem_u32(&bars->q_empty[t]), (items & 1) ^ 1, bars, p);
+      ok = diff_wait(smem_u32(&bars->q_empty), (passes & 1) ^ 1, bars, p);
       if (!ok) break;
       if (t == 0)
         publish(DTask{item.u0, item.b, item.keys, item.kv0, item.kv1, item.nk, at.h, at.q0, 0,
                       static_cast<short>(item.piece ? 2 : 1)});
-      load(smem_u32(smem + t * C::SLOT), &p.tm_q, smem_u32(&bars->q_full[t]), t * C::DH, at.q0, at.h, item.b);
-      ++q_armed[t];
+      load(smem_u32(smem), &p.tm_q, smem_u32(&bars->q_full), t * C::DH, at.q0, at.h, item.b);
+      ++passes;
       // K runs a tile ahead of V: a K slot is free as soon as its scores are done, a V slot only
       // when the products are, and the scores behind them should not wait for a load.
       for (int j = item.kv0 - 1; ok && j < item.kv1; ++j) {
@@ -116,17 +118,14 @@ __device__ void wide_loader(const DiffParams &p, uint8_t *smem, WideBars *bars) 
         }
       }
     }
-    if (ok) ++items;
   }
-  if (!ok && q_armed[0] > items) ++items;   // the item that gave up has been published
   publish(DTask{0, 0, 0, 0, 0, 0, 0, 0, 0, 0});
   // Every load issued must land before the CTA releases its shared memory.
   for (uint32_t s = 0; s < C::KS; ++s)
     if (k_uses > s) diff_drain(smem_u32(&bars->k_full[s]), ((k_uses - 1 - s) / C::KS) & 1);
   for (uint32_t s = 0; s < C::VS; ++s)
     if (v_uses > s) diff_drain(smem_u32(&bars->v_full[s]), ((v_uses - 1 - s) / C::VS) & 1);
-  for (int t = 0; t < 2; ++t)
-    if (q_armed[t] > 0) diff_drain(smem_u32(&bars->q_full[t]), (q_armed[t] - 1) & 1);
+  if (passes > 0) diff_drain(smem_u32(&bars->q_full), (passes - 1) & 1);
 }
 
 // S of tile g into buffer g & 1, once the products of tile g - 2 have read P there.
@@ -141,27 +140,26 @@ __device__ void wide_score_issuer(const DiffParams &p, uint8_t *smem, WideBars *
   DWalk walk;
   walk.start(p, bars->plan);
   DItem item;
-  for (; walk.next(p, item); q_parity ^= 1) {
+  while (walk.next(p, item)) {
     const int nk = uniform(item.kv1 - item.kv0);
 #pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-      if (!diff_wait(smem_u32(&bars->q_full[0]) + 8 * t, q_parity, bars, p)) goto drain;
+    for (int t = 0; t < 2; ++t, q_parity ^= 1) {
+      if (!diff_wait(smem_u32(&bars->q_full), q_parity, bars, p)) goto drain;
 #pragma unroll 1
       for (int j = 0; j < nk; ++j) {
         if (!diff_wait(smem_u32(&bars->k_full[0]) + 8 * kr.slot, kr.parity, bars, p)) goto drain;
         if (!diff_wait(smem_u32(&bars->pv_done[0]) + 8 * buf, parity ^ 1, bars, p)) goto drain;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t qd = qdesc + static_cast<uint64_t>(t * (C::SLOT >> 4));
           const uint64_t kd = kdesc + static_cast<uint64_t>(kr.slot * (C::SLOT >> 4));
 #pragma unroll
           for (int kk = 0; kk < C::DH / 16; ++kk) {
             const uint64_t o = static_cast<uint64_t>(((kk / 4) * kDiffHalf + (kk % 4) * 32) >> 4);
-            tc_mma_ss(tmem + buf * 128, qd + o, kd + o, idesc, kk > 0 ? 1u : 0u);
+            tc_mma_ss(tmem + buf * 128, qdesc + o, kd + o, idesc, kk > 0 ? 1u : 0u);
           }
           tc_commit(smem_u32(&bars->s_full[0]) + 8 * buf);
           tc_commit(smem_u32(&bars->k_empty[0]) + 8 * kr.slot);
-          if (j == nk - 1) tc_commit(smem_u32(&bars->q_empty[0]) + 8 * t);
+          if (j == nk - 1) tc_commit(smem_u32(&bars->q_empty));
         }
         __syncwarp();
         kr.advance();
@@ -587,8 +585,6 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1) attn_diff_wide_kernel(con
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->q_full[i]), 1);
-      mbar_init(smem_u32(&bars->q_empty[i]), 1);
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       mbar_init(smem_u32(&bars->p_full[i][0]), 128);
       mbar_init(smem_u32(&bars->p_full[i][1]), 128);
@@ -604,6 +600,8 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1) attn_diff_wide_kernel(con
       mbar_init(smem_u32(&bars->v_empty[i]), 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->item_full[i]), 1);
+    mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_empty), 1);
     mbar_init(smem_u32(&bars->o_full), 1);
     bars->abort = 0;
     fence_mbar_init();
