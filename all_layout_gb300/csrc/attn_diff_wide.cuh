@@ -295,6 +295,14 @@ __device__ __forceinline__ void wide_leave(uint32_t tO, float4 *to, int stride, 
   }
 }
 
+// Four columns of a merged row: x += g1 O1 + g2 O2 of one piece.
+__device__ __forceinline__ void add_piece(float *x, float g1, const float4 &u, float g2, const float4 &v) {
+  x[0] = fmaf(g1, u.x, fmaf(g2, v.x, x[0]));
+  x[1] = fmaf(g1, u.y, fmaf(g2, v.y, x[1]));
+  x[2] = fmaf(g1, u.z, fmaf(g2, v.z, x[2]));
+  x[3] = fmaf(g1, u.w, fmaf(g2, v.w, x[3]));
+}
+
 // The end of a piece, per warp (its 32 rows): both maps' O, m and l are in the workspace. The
 // warp that counts the last piece of these rows merges all of them in piece order.
 __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bars, const float *weight,
@@ -339,18 +347,28 @@ __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bar
       float x[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] = 0.f;
+      // Two pieces' loads in flight at a time; the sum still runs in piece order.
 #pragma unroll 1
-      for (int k = 0; k < S; ++k) {
-        const float4 s = __ldcg(stat_of(k) + r);
-        const float g1 = f1 * ex2_approx(s.x - m1), g2 = f2 * ex2_approx(s.z - m2);
+      for (int k = 0; k < S; k += 2) {
+        const int k2 = k + 1 < S ? k + 1 : k;
+        const float4 s = __ldcg(stat_of(k) + r), s2 = __ldcg(stat_of(k2) + r);
         const float4 *a = reinterpret_cast<const float4 *>(part(k)) + 8 * c * R + r;
+        const float4 *b = reinterpret_cast<const float4 *>(part(k2)) + 8 * c * R + r;
+        float4 u[8], v[8], u2[8], v2[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 u = __ldcg(a + i * R), v = __ldcg(a + (C::DV / 4 + i) * R);
-          x[4 * i] = fmaf(g1, u.x, fmaf(g2, v.x, x[4 * i]));
-          x[4 * i + 1] = fmaf(g1, u.y, fmaf(g2, v.y, x[4 * i + 1]));
-          x[4 * i + 2] = fmaf(g1, u.z, fmaf(g2, v.z, x[4 * i + 2]));
-          x[4 * i + 3] = fmaf(g1, u.w, fmaf(g2, v.w, x[4 * i + 3]));
+          u[i] = __ldcg(a + i * R);
+          v[i] = __ldcg(a + (C::DV / 4 + i) * R);
+          u2[i] = __ldcg(b + i * R);
+          v2[i] = __ldcg(b + (C::DV / 4 + i) * R);
+        }
+        const float g1 = f1 * ex2_approx(s.x - m1), g2 = f2 * ex2_approx(s.z - m2);
+        const float h1 = k2 > k ? f1 * ex2_approx(s2.x - m1) : 0.f;
+        const float h2 = k2 > k ? f2 * ex2_approx(s2.z - m2) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          add_piece(x + 4 * i, g1, u[i], g2, v[i]);
+          if (k2 > k) add_piece(x + 4 * i, h1, u2[i], h2, v2[i]);
         }
       }
       uint32_t o[32];
@@ -399,10 +417,7 @@ __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bar
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float4 u = __ldcg(a + i * 32 * R), v = __ldcg(a + (C::DV / 4 + i * 32) * R);
-        x[4 * i] = fmaf(g1, u.x, fmaf(g2, v.x, x[4 * i]));
-        x[4 * i + 1] = fmaf(g1, u.y, fmaf(g2, v.y, x[4 * i + 1]));
-        x[4 * i + 2] = fmaf(g1, u.z, fmaf(g2, v.z, x[4 * i + 2]));
-        x[4 * i + 3] = fmaf(g1, u.w, fmaf(g2, v.w, x[4 * i + 3]));
+        add_piece(x + 4 * i, g1, u, g2, v);
       }
     }
     float f = p.out_scale;
