@@ -11,35 +11,52 @@
 // Flops per query/key pair and head: 2d for the two score maps (d/2 columns each) and 4d
 // for the two products with v.
 //
-// Work unit: one (batch, head) and one 128-row query tile (at d = 256 also one half of
-// v's columns, the scores being computed in both). The two maps of a unit ping-pong
-// through one MMA issuer exactly as two query tiles would: while the tensor pipe works on
-// one map, the other map's softmax runs.
+// Work unit: one (batch, head) and one 128-row query tile. This file has the schedule and
+// the kernel for d = 64 and 128, whose two maps of a unit run beside each other: 2 x 128
+// score columns and 2 x d of O fill Tensor Memory. d = 256 has a kernel of its own
+// (attn_diff_wide.cuh); only without a workspace does it run here, on halves of v's columns
+// (a unit is then a half, and the scores are computed in both).
 //
-// Roles (320 threads, one CTA per SM):
-//   warps 0-3  softmax warp group 0: map 1 (S1, P1, O1), row r of the tile = TMEM lane r
-//   warps 4-7  softmax warp group 1: map 2
-//   warp 8     MMA issuer and Tensor Memory allocation
-//   warp 9     TMA loader
+// Roles (352 or 384 threads, one CTA per SM):
+//   warps 0-3  softmax of map 1, row r of the tile = TMEM lane r
+//   warps 4-7  softmax of map 2
+//   warp 8     issues the scores; Tensor Memory allocation
+//   warp 9     issues the products with v
+//   warp 10    TMA loader; publishes the items of the list to the softmax warps
 // In the epilogue each group takes half of the columns and reads both maps' O for them.
 // Tensor Memory: S1 [0,128) S2 [128,256) O1 [256,256+DV) O2 [256+DV,256+2DV); P_t (bf16
 // pairs) overwrites the first 64 columns of S_t.
-// Shared memory: Q | ring of K and V tiles (64-column halves of 128 rows x 128 bytes,
-// 128-byte swizzle) | barriers | 128 rows x 2 exchange words (twice for the norm).
+// Shared memory: Q | ring of K tiles | ring of V tiles (64-column halves of 128 rows x 128
+// bytes, 128-byte swizzle) | barriers | staged output rows | sums and the norm's weights.
 //
-// Order per KV step j, t = 1, 2: O_t += P_t(j-1) V(j-1); S_t = Q_t K_t(j)^T. One thread's
-// tcgen05 operations execute in order, so S_t(j) cannot overwrite P_t(j-1) before it is
-// read, and the commit that signals S_t(j) also covers PV_t(j-1).
+// A tile of 128 keys goes in halves of 64. The early half's scores lie in columns 64-127 of
+// S_t, which P never covers: they are computed as soon as the softmax holds the tile
+// before's in registers, so its exponentials run while the tensor cores do the products of
+// the tile before. The late half's, in P's columns, follow those products. Each half's
+// weights go to the products as they are written.
+//
+// Bound: at d = 128 the tensor pipe has 1536 cycles of work a tile and both maps (512
+// scores, 1024 products), the softmax 2 x 128 x 128 exponentials, 1024 cycles of the
+// four special-function units and about as many issue slots again. A tile takes 1.19 us
+// (2460 cycles): the chain late scores - late softmax - products - late scores of a map is
+// what the other map's work does not hide. Measured (GB300, 2070 MHz): d = 128, 24 heads of
+// 4096 queries and keys 233 us (1320 TFLOP/s, 71% of the cuBLAS rate), of 16384 3.26 ms
+// (1517, 81%); one query of 8 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
+// 92% of the copy rate). A unit costs 3.7 us beside its tiles (first loads, epilogue).
+// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1,
+// late 1, early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34; sixteen
+// softmax warps on column halves no gain; whole tiles of 64 keys with S doubled 3.8 to 5.3 ms
+// at 16384 (several arrangements).
 //
 // Schedule: persistent CTAs take whole units, strided; with a workspace the units past the
 // last full wave but one are cut into equal contiguous ranges of KV tiles, and so are all
-// units when there are fewer than SMs (few queries, long keys). A cut unit's pieces leave
-// (m, l, O) of both maps in the workspace; the CTA that counts the last piece in merges
-// them in piece order, so the result does not depend on who was last.
+// units when there are fewer than SMs (few queries, long keys), where that is quicker. A cut
+// unit's pieces leave (m, l, O) of both maps in the workspace; the CTA that counts the last
+// piece in merges them in piece order, so the result does not depend on who was last.
 //
 // Waits are bounded: a role that gives up records a timeout; the softmax warps then run
 // their control flow to its end without waiting (so that they meet at the same named
-// barriers), the issuer and the loader drain what they issued.
+// barriers), the issuers and the loader drain what they issued.
 #include <cstdint>
 #include <cstring>
 
@@ -598,11 +615,16 @@ __device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (
   return max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
 }
 
+// 1 / sqrt(mean + eps) of a row of d columns. A row of zeros (no keys) stays one, also with eps = 0.
+__device__ __forceinline__ float norm_factor(float ss, int d, float eps) {
+  return ss == 0.f ? 0.f : rsqrtf(ss * (1.f / d) + eps);
+}
+
 // The norm, from the whole row's sum of squares `ss`, and the output's factor on NX columns.
 template <class C, int NX>
 __device__ __forceinline__ void scale_row(const DiffParams &p, const float *weight, int col0, float (&x)[NX], float ss) {
   if (C::NORM && p.weight) {
-    const float r = rsqrtf(ss * (1.f / C::DQ) + p.eps) * p.out_scale;
+    const float r = norm_factor(ss, C::DQ, p.eps) * p.out_scale;
 #pragma unroll
     for (int i = 0; i < NX / 4; ++i) {
       const float4 w = reinterpret_cast<const float4 *>(weight + col0)[i];

@@ -271,7 +271,7 @@ def qkv_rope(q_in, k_in, v_in, q, k, v, pos, axis_dims, *, theta: float = 10000.
     dev, src = q_in.get_device(), q_in.dtype
     dst = q.dtype if isinstance(q, torch.Tensor) else None
     _require(src in _TYPES and dst in _TYPES, "q_in and q must be bf16, fp16 or fp32")
-    dims, table, n_axes = _rope_axes(tuple(axis_dims), theta, None if freqs is None else tuple(freqs))
+    dims, table, n_axes = _rope_axes(tuple(axis_dims), theta, None if freqs is None else tuple(map(float, freqs)))
     _require(isinstance(pos, torch.Tensor), "pos must be [N, axes] or [B, N, axes]")
     shared = pos.dim() == 2
     ps = _operand("pos", pos, torch.int32, (N, n_axes) if shared else (B, N, n_axes), dev)
@@ -315,7 +315,7 @@ def _diff_args(q, k, v, lam, kv_len, norm_weight, eps, out_scale, scale):
                              _vector("lam", lam, torch.float32, H, dev),
                              _vector("norm_weight", norm_weight, torch.float32, d, dev),
                              _vector("kv_len", kv_len, torch.int32, B, dev),
-                             (d / 2) ** -0.5 if scale is None else scale, eps, out_scale, B, H, Hk, Nq, Nk, d)
+                             (max(d, 1) / 2) ** -0.5 if scale is None else scale, eps, out_scale, B, H, Hk, Nq, Nk, d)
     return packed, B, H, Nq, d, dev
 
 
@@ -333,7 +333,7 @@ def diff_attn(q, k, v, o, lam, *, kv_len=None, norm_weight=None, eps: float = 1e
     [B, H_kv, Nk, d]; o: [B, H, Nq, d]; bf16 views of any strides, d contiguous. The first d/2
     columns of q and k are the first map's. lam: fp32 [H]; norm_weight: fp32 [d] or None; kv_len:
     int32 [B] (keys that count) or None; scale: of the scores, 1/sqrt(d/2) if None; workspace:
-    from alloc_diff_workspace, or None."""
+    from alloc_diff_workspace, or None (at d = 256 a norm needs one). o must not overlap an input."""
     packed, B, H, Nq, d, dev = _diff_args(q, k, v, lam, kv_len, norm_weight, eps, out_scale, scale)
     os_ = _operand("o", o, torch.bfloat16, q.shape, dev)
     if os_[3] != 1 and d > 1:

@@ -324,8 +324,10 @@ typedef struct {
  *     o = x / sqrt(mean(x^2) + eps) * norm_weight * out_scale
  * (norm_weight NULL: o = x * out_scale), both softmaxes over the first kv_len[b] keys
  * (taken into [0, Nk]; what lies behind them is not used, NaN and infinity included),
- * non-causal. A batch entry without keys gives zeros. fp32 accumulation and statistics,
- * softmax weights rounded to bf16 for the product with v, output rounded to bf16.
+ * non-causal. A batch entry without keys gives zeros, and a row x of zeros stays one
+ * under the norm, with eps = 0 too. fp32 accumulation and statistics, softmax weights
+ * rounded to bf16 for the product with v, output rounded to bf16. Outputs must not
+ * overlap each other or an input.
  * lambda is taken as it is: a model computes it once from its learned vectors, for
  * example exp(a1.b1) - exp(a2.b2) + lambda_init, with out_scale = 1 - lambda_init.
  * Nq, Nk: any size, also 1 (one new token against a long sequence); not multiples of
@@ -338,8 +340,13 @@ typedef struct {
  *                leaves them zero), or NULL. With xs_diff_workspace_bytes of it a
  *                launch may cut units into ranges of keys over all SMs (few queries,
  *                a last wave that is not full, ragged lengths); with less it takes
- *                whole units. d = 256 with a norm needs it, for fp32 rows. Calls that
- *                share one workspace must not overlap on the GPU. After a timeout
+ *                whole units. At d = 256 a CTA also keeps the first map's rows in it
+ *                (fp32, 128 KB for 128 queries) while the second map's are computed:
+ *                with less than XS_WORKSPACE_HEADER_BYTES + 1024 * min(128, Nq rounded
+ *                up to 8) bytes a norm is refused, and without a norm both maps run at
+ *                once on each half of v's columns, their scores computed twice; with
+ *                less than all SMs' places fewer SMs work. Calls that share one
+ *                workspace must not overlap on the GPU. After a timeout
  *                (xs_last_device_status) zero the header again.
  * Results are the same from launch to launch on one GPU model; they differ in fp32
  * rounding between workspace and none.

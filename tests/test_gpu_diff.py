@@ -98,7 +98,7 @@ def done(xs, ws=None):
 SHAPES = [
     (1, 1, 1, 1, 1), (2, 3, 3, 1, 128), (1, 2, 1, 1, 129), (1, 1, 1, 128, 127), (1, 1, 1, 129, 128), (1, 2, 2, 127, 255),
     (2, 4, 2, 3, 700), (1, 2, 1, 300, 1), (3, 2, 2, 257, 385), (1, 6, 3, 640, 1025), (1, 1, 1, 9, 20000), (2, 24, 24, 1, 3000),
-    (1, 3, 1, 8, 9001), (1, 40, 40, 500, 640),
+    (1, 3, 1, 8, 9001), (1, 40, 40, 500, 640), (1, 2, 2, 200, 9000), (700, 2, 1, 1, 5),
 ]
 
 
@@ -146,10 +146,11 @@ def test_all_lengths_zero_and_no_keys(xs, d):
     q, k, v, lam, w = inputs(2, 2, 2, 140, 50, d, seed=d)
     ws = workspace()
     for kk, vv, kv_len in ((k, v, torch.zeros(2, dtype=torch.int32, device="cuda")), (k[:, :, :0], v[:, :, :0], None)):
-        o = torch.full_like(q, math.nan)
-        xs.diff_attn(q, kk, vv, o, lam, kv_len=kv_len, norm_weight=w, workspace=ws)
-        done(xs, ws)
-        assert not o.any()
+        for eps in (1e-5, 0.0):
+            o = torch.full_like(q, math.nan)
+            xs.diff_attn(q, kk, vv, o, lam, kv_len=kv_len, norm_weight=w, eps=eps, workspace=ws)
+            done(xs, ws)
+            assert not o.any()
 
 
 @pytest.mark.parametrize("use_ws", [False, True])
@@ -266,8 +267,8 @@ def test_workspace_that_is_just_enough_and_one_that_is_not(xs):
         full = xs.alloc_diff_workspace(1, 6, 900, 1100, d, norm=True)
         buf = torch.zeros(full.numel() + 4096, dtype=torch.uint8, device="cuda")
         buf[full.numel():] = 77
-        stage = 6 * 900 * d * 4 if d == 256 else 0
-        for n in (full.numel(), 16384 + stage):
+        place = 128 * 256 * 4 if d == 256 else 0   # of a CTA: one, some, and almost a second one
+        for n in (full.numel(), 16384 + place, 16384 + 2 * place - 256 * (d == 256), 16384 + 42 * place):
             o = torch.full_like(q, math.nan)
             xs.diff_attn(q, k, v, o, lam, norm_weight=w, workspace=buf[:n])
             done(xs, buf)
@@ -275,10 +276,11 @@ def test_workspace_that_is_just_enough_and_one_that_is_not(xs):
         assert bool((buf[full.numel():] == 77).all())
 
 
-def test_two_graphs_one_workspace_and_streams(xs):
+@pytest.mark.parametrize("d1,d2", [(128, 64), (256, 256)])
+def test_two_graphs_one_workspace_and_streams(xs, d1, d2):
     """Two captured calls of different shapes share a workspace, replayed one after the other; two
     streams with a workspace each run at once."""
-    cases = [inputs(1, 3, 3, 300, 2000, 128, seed=1), inputs(2, 2, 2, 1, 5000, 64, seed=2)]
+    cases = [inputs(1, 3, 3, 300, 2000, d1, seed=1), inputs(2, 2, 2, 1, 5000, d2, seed=2)]
     ws = [workspace(), workspace()]
     outs = [torch.empty_like(c[0]) for c in cases]
     refs = [reference(*c[:4], weight=c[4]) for c in cases]
