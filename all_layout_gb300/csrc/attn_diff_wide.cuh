@@ -501,10 +501,9 @@ __device__ void wide_softmax(const DiffParams &p, uint8_t *smem, WideBars *bars,
           const float before = m;
           if (j == 0 || mx > m + kDiffRescale) m = mx;
           const uint64_t negm2 = neg2(m);
-          uint64_t sum2[2] = {0ull, 0ull};
-          uint32_t pk[2][16];
-          weights32(s[0], scale2, negm2, pk[0], sum2);
-          weights32(s[1], scale2, negm2, pk[1], sum2);
+          uint32_t pk[4][16];
+          weights32(s[0], scale2, negm2, pk[0]);
+          weights32(s[1], scale2, negm2, pk[1]);
           tmem_st16(tS, pk[0]);
           tmem_st16(tS + 16, pk[1]);
           float alpha = 1.f;
@@ -529,14 +528,17 @@ __device__ void wide_softmax(const DiffParams &p, uint8_t *smem, WideBars *bars,
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_full + 16 * buf);
-          weights32(s[2], scale2, negm2, pk[0], sum2);
-          weights32(s[3], scale2, negm2, pk[1], sum2);
-          tmem_st16(tS + 32, pk[0]);
-          tmem_st16(tS + 48, pk[1]);
-          l = fmaf(l, alpha, sum_of(sum2));
+          weights32(s[2], scale2, negm2, pk[2]);
+          weights32(s[3], scale2, negm2, pk[3]);
+          tmem_st16(tS + 32, pk[2]);
+          tmem_st16(tS + 48, pk[3]);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_full + 16 * buf + 8);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) add_weights(pk[i], sum);
+          l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         } else {
           mbar_arrive(p_full + 16 * buf);
           mbar_arrive(p_full + 16 * buf + 8);
