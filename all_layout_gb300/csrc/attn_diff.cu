@@ -37,20 +37,20 @@
 //
 // Bound: at d = 128 the tensor pipe has 1536 cycles of work a tile and both maps (512
 // scores, 1024 products), the softmax 2 x 128 x 128 exponentials, 1024 cycles of the
-// four special-function units and about as many issue slots again. A tile takes 1.19 us
-// (2460 cycles): the chain late scores - late softmax - products - late scores of a map is
+// four special-function units and about as many issue slots again. A tile takes 1.26 us
+// (2610 cycles): the chain late scores - late softmax - products - late scores of a map is
 // what the other map's work does not hide. Measured (GB300, 2070 MHz): d = 128, 24 heads of
-// 4096 queries and keys 233 us (1320 TFLOP/s, 71% of the cuBLAS rate), of 16384 3.26 ms
-// (1517, 81%); one query of 8 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
+// 4096 queries and keys 244 us (1267 TFLOP/s, 68% of the cuBLAS rate), of 16384 3.43 ms
+// (1442, 77%); one query of 4 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
 // 92% of the copy rate). A unit costs 3.7 us beside its tiles (first loads, epilogue).
 // Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1,
-// late 1, early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34; sixteen
+// late 1, early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (1.23 then); sixteen
 // softmax warps on column halves no gain; whole tiles of 64 keys with S doubled 3.8 to 5.3 ms
 // at 16384 (several arrangements).
 //
 // Schedule: persistent CTAs take whole units, strided; with a workspace the units past the
-// last full wave but one are cut into equal contiguous ranges of KV tiles, and so are all
-// units when there are fewer than SMs (few queries, long keys), where that is quicker. A cut
+// last full wave but one are cut into contiguous ranges of KV tiles of equal cost, and so are
+// all units when there are fewer than SMs (few queries, long keys), where that is quicker. A cut
 // unit's pieces leave (m, l, O) of both maps in the workspace; the CTA that counts the last
 // piece in merges them in piece order, so the result does not depend on who was last.
 //
@@ -108,16 +108,17 @@ __device__ __forceinline__ int keys_of(const DiffParams &p, int b) {
 // KV tiles of a batch entry; one without keys keeps a tile, fully masked, that gives its zeros.
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + BN - 1) / BN); }
 
-// The split region: its KV tiles, the CTAs that share it, and where this CTA begins in it.
+// The split region: its places (kUnitCost for a unit and then one for each of its KV tiles), the
+// CTAs that share it, and where this CTA begins in it.
 struct DPlan {
-  long long total, bstart;   // bstart: first tile of batch entry b
+  long long total, bstart;   // bstart: first place of batch entry b
   int grid, b;
 };
 
 struct DItem {
   int unit, b, keys;       // unit, its batch entry and that entry's keys
   int kv0, kv1, nk;        // KV tiles to do, and the unit's
-  long long u0;            // a cut unit: its first tile in the split region
+  long long u0;            // a cut unit: its first tile's place in the split region
   bool piece;
 };
 
@@ -159,16 +160,21 @@ struct DWalk {
       it.keys = keys_of(p, b);
       it.nk = tiles_of(it.keys);
       const int skip = b == b0 ? first - b0 * p.units_b : 0;
-      const long long size = static_cast<long long>(p.units_b - skip) * it.nk;
+      const int places = it.nk + kUnitCost;
+      const long long size = static_cast<long long>(p.units_b - skip) * places;
       if (pos < bstart + size) {
-        const int ul = static_cast<int>((pos - bstart) / it.nk);
-        it.u0 = bstart + static_cast<long long>(ul) * it.nk;
-        it.kv0 = static_cast<int>(pos - it.u0);
-        it.kv1 = end - pos < it.nk - it.kv0 ? it.kv0 + static_cast<int>(end - pos) : it.nk;
+        const int ul = static_cast<int>((pos - bstart) / places);
+        it.u0 = bstart + static_cast<long long>(ul) * places + kUnitCost;
+        if (end <= it.u0) {   // the range ends before the unit's first tile
+          pos = end;
+          return false;
+        }
+        it.kv0 = pos > it.u0 ? static_cast<int>(pos - it.u0) : 0;
+        it.kv1 = end - it.u0 < it.nk ? static_cast<int>(end - it.u0) : it.nk;
         it.unit = b * p.units_b + skip + ul;
         it.b = b;
         it.piece = it.kv0 > 0 || it.kv1 < it.nk;
-        pos += it.kv1 - it.kv0;
+        pos = it.u0 + it.kv1;
         return true;
       }
       bstart += size;
@@ -305,7 +311,7 @@ __device__ void plan_split(const DiffParams &p, B *bars) {
   auto size_of = [&](int b) -> long long {
     if (b >= p.B) return 0;
     const int skip = b == b0 ? first - b0 * p.units_b : 0;
-    return static_cast<long long>(p.units_b - skip) * tiles_of(keys_of(p, b));
+    return static_cast<long long>(p.units_b - skip) * (tiles_of(keys_of(p, b)) + kUnitCost);
   };
   long long total = 0;
   for (int b = b0 + lane; b < p.B; b += 32) total += size_of(b);

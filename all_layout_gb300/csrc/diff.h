@@ -8,6 +8,10 @@
 
 namespace xs {
 
+// What a unit costs beside its KV tiles (its first loads and its epilogue), in tiles: 2 at d = 64, 3
+// to 4 at 128 and 256. In the split schedule a unit takes so many places more than it has tiles.
+constexpr int kUnitCost = 3;
+
 struct DiffParams {
   // q [B][H][Nq][d], k and v [B][Hk][Nk][d], any strides: 4-D maps {d, rows, heads, batch},
   // box {64, 128, 1, 1}, 128-byte swizzle.
@@ -23,8 +27,8 @@ struct DiffParams {
   int n_qtiles, v_parts;              // 128-row query tiles; halves of v's columns (2 at d = 256)
   int units_b, n_units;               // units of a batch entry (H * n_qtiles * v_parts), of all
   // Work list of a CTA (G = gridDim.x): units blockIdx.x + k*G, all of them (split = 0) or the
-  // first `waves` (split = 1); then the KV tiles of the remaining units, unit-major, in equal
-  // contiguous ranges.
+  // first `waves` (split = 1); then the KV tiles of the remaining units, unit-major, in contiguous
+  // ranges of equal cost.
   int split, waves;
   float scale_log2, eps, out_scale;
   float *parts;                       // split: [G][2 slots] partial results

@@ -30,39 +30,40 @@ unsigned long long wide_stash_bytes(int rows) { return 256ull * rows * 4; }
 unsigned long long wide_parts_bytes(int rows) { return 2ull * diff_wide_part_floats(rows) * 4; }
 
 // Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split
-// schedule. A cut unit costs about `merge` KV tiles more (its partial results are written and
-// merged), an item about kItem (its first loads and its epilogue).
+// schedule, whichever should end earlier. Times in KV tiles: a unit costs kUnitCost beside its own;
+// `merge` is what each of a CTA's two cut units costs more (partial results written and merged).
+// It follows from both schedules' measured times (GB300; heads x queries and keys, split / whole):
+//   d = 64   12 x 4096 112 / 116 us, 12 x 2048 44 / 44, 20 x 2048 58 / 63, 3 x 8192 108 / 147
+//   d = 128  12 x 4096 130 / 129 us, 12 x 2048 55 / 50, 20 x 2048 70 / 71, 3 x 8192 124 / 162
+//   d = 256  12 x 4096 220 / 214 us, 12 x 2048 94 / 82, 3 x 8192 227 / 287
+// Lengths that are on the device are taken as three quarters of Nk on average (8 entries of 8 heads,
+// 777 queries, up to 1101 keys at d = 64, lengths falling to none: split 45 us, whole 34).
 struct Plan {
   int split, waves, grid;
 };
-// Both schedules measured at d = 128, heads x queries and keys: 24 x 4096 split 233, whole 253 us;
-// 12 x 4096 130, 129; 20 x 2048 70, 71; 12 x 2048 55, 50; 3 x 8192 124, 162.
-constexpr long kItem = 2, kMerge = 5, kMinTiles = 4;
-// d = 256: 256 KB of partial results for 128 rows, written and read by four warps. Both schedules
-// measured, 12 heads of 4096 and of 2048 queries and keys, 3 heads of 8192: split 220, 94, 227 us,
-// whole units 214, 82, 287 us; a cut costs 17 to 18 tiles of both maps for a CTA's two pieces.
-constexpr long kMergeWide = 9;
+constexpr long kMinPlaces = 4;
+long merge_cost(int d, int rows) { return d == 64 ? 7 : d == 128 ? 8 : 6 + 4 * rows / kTileRows; }
 
 // `per_cta`: bytes of workspace that a CTA's partial results take.
 Plan plan(long long units, int sms, int nk, bool ragged, long merge, unsigned long long per_cta,
           unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
   const Plan whole{0, 0, grid0};
-  if (nk < 2 || (units >= sms && units % sms == 0 && !ragged)) return whole;
+  if (nk < 2) return whole;
   const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
-  const long long T = (units - static_cast<long long>(waves) * sms) * nk;
-  long long per = (T + sms - 1) / sms;
+  const long long left = units - static_cast<long long>(waves) * sms;
+  long long per = (left * (nk + kUnitCost) + sms - 1) / sms;
   int grid = sms;
   if (waves == 0) {
-    if (per < kMinTiles) per = kMinTiles;
-    grid = static_cast<int>((T + per - 1) / per);
+    if (per < kMinPlaces) per = kMinPlaces;
+    grid = static_cast<int>((left * (nk + kUnitCost) + per - 1) / per);
   }
   if (per_cta * grid > room || grid * 4 > static_cast<int>(XS_WORKSPACE_HEADER_BYTES / sizeof(int)))
     return whole;
-  const long long items = (per + nk - 1) / nk + 1;
-  const long long cost_split = waves * (nk + kItem) + per + items * kItem + 2 * merge;
-  const long long cost_whole = (units + grid0 - 1) / grid0 * (nk + kItem);
-  return cost_split < cost_whole || ragged ? Plan{1, waves, grid} : whole;
+  const long long mean = (ragged ? nk - nk / 4 : nk) + kUnitCost, rounds = (units + grid0 - 1) / grid0;
+  const long long cost_split = waves * mean + per * mean / (nk + kUnitCost) + 2 * merge;
+  const long long cost_whole = (rounds - 1) * mean + nk + kUnitCost;
+  return cost_split < cost_whole ? Plan{1, waves, grid} : whole;
 }
 
 // One operand as a 4-D map {d, rows, heads, batch}; strides of single extents do not matter.
@@ -188,7 +189,7 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   if (!wide) {
     // Workspace: counters | partial results.
     p.parts = area;
-    const Plan pl = plan(p.n_units, sms, nk, ragged, kMerge, parts_bytes(1, d), d == 256 ? 0 : room);
+    const Plan pl = plan(p.n_units, sms, nk, ragged, merge_cost(d, kTileRows), parts_bytes(1, d), d == 256 ? 0 : room);
     p.split = pl.split;
     p.waves = pl.waves;
     return launch_attn_diff(p, d, pl.grid, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
@@ -197,8 +198,7 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   // for fewer CTAs.
   const unsigned long long places = room / wide_stash_bytes(rows);
   const int ctas = places < static_cast<unsigned long long>(sms) ? static_cast<int>(places) : sms;
-  const long merge = kMerge + (kMergeWide - kMerge) * rows / kTileRows;
-  const Plan pl = plan(p.n_units, ctas, nk, ragged, merge, wide_parts_bytes(rows),
+  const Plan pl = plan(p.n_units, ctas, nk, ragged, merge_cost(d, rows), wide_parts_bytes(rows),
                        room - ctas * wide_stash_bytes(rows));
   p.split = pl.split;
   p.waves = pl.waves;

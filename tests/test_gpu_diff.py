@@ -120,6 +120,7 @@ def test_shapes(xs, B, H, Hk, Nq, Nk, d, use_ws):
 @pytest.mark.parametrize("B,H,Hk,Nq,Nk,lens", [
     (3, 2, 1, 150, 300, (300, 131, 0)), (4, 3, 3, 1, 5000, (4999, 1, 0, 128)), (2, 2, 2, 260, 129, (500, -3)),
     (70, 1, 1, 5, 400, tuple((37 * i) % 401 for i in range(70))), (40, 8, 4, 130, 520, tuple((129 * i) % 521 for i in range(40))),
+    (3, 2, 2, 200, 6000, (6000, 100, 0)), (60, 1, 1, 5, 3000, tuple((911 * i) % 3001 if i % 3 else i // 40 for i in range(60))),
 ])
 def test_lengths_and_what_lies_behind_them(xs, B, H, Hk, Nq, Nk, lens, d, use_ws):
     """Keys past an entry's length hold NaN and infinities in k and v; entries without keys give zeros."""
