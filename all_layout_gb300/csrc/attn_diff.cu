@@ -75,7 +75,6 @@ constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadW
 constexpr int kDiffHalf = BM * 128;                 // one 64-column half of a 128-row tile
 constexpr uint32_t kDiffSleepNs = 100000;
 constexpr float kDiffRescale = 8.0f;                // log2 units: rescale O only past a growth of 2^8
-constexpr int kFewRows = 8;                         // rows of a tile up to which a merge is spread over columns and pieces
 
 // DH: columns of one map's q and k; DV: columns of v that a unit takes.
 template <int DH_, int DV_>
@@ -316,7 +315,8 @@ __device__ void plan_split(const DiffParams &p, B *bars) {
   long long total = 0;
   for (int b = b0 + lane; b < p.B; b += 32) total += size_of(b);
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int grid = static_cast<int>(total < gridDim.x ? total : gridDim.x);
+  const long long most = max(1ll, total / p.min_places);
+  const int grid = static_cast<int>(most < gridDim.x ? most : gridDim.x);
   const long long pos = static_cast<int>(blockIdx.x) < grid
                             ? static_cast<long long>(blockIdx.x) * total / grid
                             : 0;
@@ -668,6 +668,14 @@ __device__ __forceinline__ float map_factor(int t, float lambda, float l) {
   return l == 0.f ? 0.f : (t == 0 ? 1.f : -lambda) / l;
 }
 
+// Four columns of a merged row: x += g1 O1 + g2 O2 of one piece.
+__device__ __forceinline__ void add_piece(float *x, float g1, const float4 &u, float g2, const float4 &v) {
+  x[0] = fmaf(g1, u.x, fmaf(g2, v.x, x[0]));
+  x[1] = fmaf(g1, u.y, fmaf(g2, v.y, x[1]));
+  x[2] = fmaf(g1, u.z, fmaf(g2, v.z, x[2]));
+  x[3] = fmaf(g1, u.w, fmaf(g2, v.w, x[3]));
+}
+
 // One piece of a cut unit: leaves its partial result in the workspace; the CTA that counts the
 // last piece merges all of them. All softmax warps take part; `l` is this thread's map's sum.
 template <class C>
@@ -718,7 +726,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
   softmax_sync();
   if (!bars->last) return;   // its next write follows another meeting
   __threadfence();
-  if (rows > kFewRows) {
+  if (rows > 64) {
     // A thread takes one row and half of the columns.
     constexpr int NX = C::DV / 2;
     const int col0 = (tid >> 7) * NX;
@@ -750,10 +758,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
 #pragma unroll
         for (int i = 0; i < NX / 4; ++i) {
           const float4 u = __ldcg(a + i * 128), v = __ldcg(b + i * 128);
-          x[4 * i] = fmaf(g1, u.x, fmaf(g2, v.x, x[4 * i]));
-          x[4 * i + 1] = fmaf(g1, u.y, fmaf(g2, v.y, x[4 * i + 1]));
-          x[4 * i + 2] = fmaf(g1, u.z, fmaf(g2, v.z, x[4 * i + 2]));
-          x[4 * i + 3] = fmaf(g1, u.w, fmaf(g2, v.w, x[4 * i + 3]));
+          add_piece(x + 4 * i, g1, u, g2, v);
         }
       }
 #pragma unroll
@@ -766,6 +771,83 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       ss = sums[row] + sums[row + 128];
     }
     if (row < rows) finish_row<C, NX>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + row, col0, x, ss);
+    return;
+  }
+  if (rows > kFewRows) {
+    // Up to 64 rows: a thread takes one row and every CG-th chunk of eight columns (with the mapping
+    // above 16 queries against 65536 keys took 92 us instead of 47). Four pieces' loads are in
+    // flight at a time, the sum runs in piece order. A row that is still to be normed waits in the
+    // first piece's place, each value for the thread that wrote it.
+    const int R = rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    const int r = min(tid & (R - 1), rows - 1), cg = tid / R, CG = kSoftThreads / R;
+    const bool live = (tid & (R - 1)) < rows;
+    float m1 = -INFINITY, m2 = -INFINITY, l1 = 0.f, l2 = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) {
+      const float4 s = __ldcg(stat_of(k) + r);
+      m1 = fmaxf(m1, s.x);
+      m2 = fmaxf(m2, s.z);
+    }
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) {
+      const float4 s = __ldcg(stat_of(k) + r);
+      l1 = fmaf(ex2_approx(s.x - m1), s.y, l1);
+      l2 = fmaf(ex2_approx(s.z - m2), s.w, l2);
+    }
+    const float f1 = map_factor(0, lambda, l1), f2 = map_factor(1, lambda, l2);
+    const bool normed = C::NORM && p.weight;
+    float4 *hold = reinterpret_cast<float4 *>(part(0)) + r;
+    float ss = 0.f;
+#pragma unroll 1
+    for (int c = cg; c < C::DV / 8; c += CG) {
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int k = 0; k < S; k += 4) {
+        float4 s[4], u[4][2], v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = min(k + i, S - 1);
+          s[i] = __ldcg(stat_of(kk) + r);
+          const float4 *a = reinterpret_cast<const float4 *>(part(kk)) + 2 * c * 128 + r;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            u[i][h] = __ldcg(a + h * 128);
+            v[i][h] = __ldcg(a + (C::DV / 4 + h) * 128);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (k + i >= S) break;
+          const float g1 = f1 * ex2_approx(s[i].x - m1), g2 = f2 * ex2_approx(s[i].z - m2);
+          add_piece(x, g1, u[i][0], g2, v[i][0]);
+          add_piece(x + 4, g1, u[i][1], g2, v[i][1]);
+        }
+      }
+      if (!live) continue;
+      if (normed) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        __stcg(hold + 2 * c * 128, make_float4(x[0], x[1], x[2], x[3]));
+        __stcg(hold + (2 * c + 1) * 128, make_float4(x[4], x[5], x[6], x[7]));
+      } else {
+        finish_row<C, 8>(p, nullptr, item.b, at, at.q0 + r, 8 * c, x, 0.f);
+      }
+    }
+    if constexpr (C::NORM) {
+      if (!p.weight) return;
+      float *sums = exch + kSoftThreads;
+      sums[tid] = ss;
+      softmax_sync();
+      if (!live) return;
+      ss = 0.f;
+      for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
+#pragma unroll 1
+      for (int c = cg; c < C::DV / 8; c += CG) {
+        const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
+        float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
+      }
+    }
     return;
   }
   // Few rows: row by row, a warp takes CW groups of four columns, and its lanes share the pieces.

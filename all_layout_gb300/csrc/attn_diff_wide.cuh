@@ -301,14 +301,6 @@ __device__ __forceinline__ void wide_leave(uint32_t tO, float4 *to, int stride, 
   }
 }
 
-// Four columns of a merged row: x += g1 O1 + g2 O2 of one piece.
-__device__ __forceinline__ void add_piece(float *x, float g1, const float4 &u, float g2, const float4 &v) {
-  x[0] = fmaf(g1, u.x, fmaf(g2, v.x, x[0]));
-  x[1] = fmaf(g1, u.y, fmaf(g2, v.y, x[1]));
-  x[2] = fmaf(g1, u.z, fmaf(g2, v.z, x[2]));
-  x[3] = fmaf(g1, u.w, fmaf(g2, v.w, x[3]));
-}
-
 // The end of a piece, per warp (its 32 rows): both maps' O, m and l are in the workspace. The
 // warp that counts the last piece of these rows merges all of them in piece order.
 __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bars, const float *weight,

@@ -11,6 +11,8 @@ namespace xs {
 // What a unit costs beside its KV tiles (its first loads and its epilogue), in tiles: 2 at d = 64, 3
 // to 4 at 128 and 256. In the split schedule a unit takes so many places more than it has tiles.
 constexpr int kUnitCost = 3;
+// Rows of a tile up to which a merge is spread over columns and pieces.
+constexpr int kFewRows = 8;
 
 struct DiffParams {
   // q [B][H][Nq][d], k and v [B][Hk][Nk][d], any strides: 4-D maps {d, rows, heads, batch},
@@ -30,6 +32,7 @@ struct DiffParams {
   // first `waves` (split = 1); then the KV tiles of the remaining units, unit-major, in contiguous
   // ranges of equal cost.
   int split, waves;
+  int min_places;                     // shortest range worth a CTA
   float scale_log2, eps, out_scale;
   float *parts;                       // split: [G][2 slots] partial results
   int *count;                         // split: pieces done of the unit that begins in CTA c's range

@@ -41,11 +41,21 @@ unsigned long long wide_parts_bytes(int rows) { return 2ull * diff_wide_part_flo
 struct Plan {
   int split, waves, grid;
 };
-constexpr long kMinPlaces = 4;
+// The shortest range worth a CTA. Merging a piece of more than a few rows takes the last CTA f KV
+// tiles' time, so n tiles in s pieces take n / s + f s, least at n / s = sqrt(f n). Measured f at 128
+// rows: 0.75, 2 and 1.6 at d = 64, 128 and 256. (With ranges of 4 at least, 128 queries of one head
+// against 65536 keys took 120, 353 and 425 us; so 55, 100 and 126.)
+int min_places(int d, int nk, int rows) {
+  int least = 4;
+  const int f4 = d == 64 || (d == 128 && rows <= 64) ? 3 : d == 128 ? 8 : 6;
+  if (rows > kFewRows)
+    while (4 * least * least < f4 * nk) ++least;
+  return least;
+}
 long merge_cost(int d, int rows) { return d == 64 ? 7 : d == 128 ? 8 : 6 + 4 * rows / kTileRows; }
 
 // `per_cta`: bytes of workspace that a CTA's partial results take.
-Plan plan(long long units, int sms, int nk, bool ragged, long merge, unsigned long long per_cta,
+Plan plan(long long units, int sms, int nk, bool ragged, int least, long merge, unsigned long long per_cta,
           unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
   const Plan whole{0, 0, grid0};
@@ -55,7 +65,7 @@ Plan plan(long long units, int sms, int nk, bool ragged, long merge, unsigned lo
   long long per = (left * (nk + kUnitCost) + sms - 1) / sms;
   int grid = sms;
   if (waves == 0) {
-    if (per < kMinPlaces) per = kMinPlaces;
+    if (per < least) per = least;
     grid = static_cast<int>((left * (nk + kUnitCost) + per - 1) / per);
   }
   if (per_cta * grid > room || grid * 4 > static_cast<int>(XS_WORKSPACE_HEADER_BYTES / sizeof(int)))
@@ -185,11 +195,12 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   p.count = static_cast<int *>(ws);
   float *area = ws ? reinterpret_cast<float *>(static_cast<char *>(ws) + XS_WORKSPACE_HEADER_BYTES) : nullptr;
   const int nk = (Nk + kTileRows - 1) / kTileRows;
+  p.min_places = min_places(d, nk, Nq < kTileRows ? Nq : kTileRows);
   const bool ragged = a->kv_len != nullptr;
   if (!wide) {
     // Workspace: counters | partial results.
     p.parts = area;
-    const Plan pl = plan(p.n_units, sms, nk, ragged, merge_cost(d, kTileRows), parts_bytes(1, d), d == 256 ? 0 : room);
+    const Plan pl = plan(p.n_units, sms, nk, ragged, p.min_places, merge_cost(d, kTileRows), parts_bytes(1, d), d == 256 ? 0 : room);
     p.split = pl.split;
     p.waves = pl.waves;
     return launch_attn_diff(p, d, pl.grid, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
@@ -198,7 +209,7 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   // for fewer CTAs.
   const unsigned long long places = room / wide_stash_bytes(rows);
   const int ctas = places < static_cast<unsigned long long>(sms) ? static_cast<int>(places) : sms;
-  const Plan pl = plan(p.n_units, ctas, nk, ragged, merge_cost(d, rows), wide_parts_bytes(rows),
+  const Plan pl = plan(p.n_units, ctas, nk, ragged, p.min_places, merge_cost(d, rows), wide_parts_bytes(rows),
                        room - ctas * wide_stash_bytes(rows));
   p.split = pl.split;
   p.waves = pl.waves;
