@@ -39,14 +39,18 @@
 // scores, 1024 products), the softmax 2 x 128 x 128 exponentials, 1024 cycles of the
 // four special-function units and about as many issue slots again. A tile takes 1.26 us
 // (2610 cycles): the chain late scores - late softmax - products - late scores of a map is
-// what the other map's work does not hide. Measured (GB300, 2070 MHz): d = 128, 24 heads of
-// 4096 queries and keys 244 us (1267 TFLOP/s, 68% of the cuBLAS rate), of 16384 3.43 ms
-// (1442, 77%); one query of 4 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
-// 92% of the copy rate). A unit costs 3.7 us beside its tiles (first loads, epilogue).
-// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1,
-// late 1, early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (1.23 then); sixteen
-// softmax warps on column halves no gain; whole tiles of 64 keys with S doubled 3.8 to 5.3 ms
-// at 16384 (several arrangements).
+// what the other map's work does not hide (tensor pipe busy 54% of the cycles, issue slots 52%).
+// At d = 64 (1.15 us a tile, 768 cycles of tensor work) it is the softmax itself, with two warps
+// a scheduler. Measured (GB300, 2070 MHz): d = 128, 24 heads of 4096 queries and keys 244 us
+// (1267 TFLOP/s, 68% of the cuBLAS rate), of 16384 3.43 ms (1442, 77%); one query of 4 x 24
+// heads against 16384 keys 129 us (6.2 TB/s of K and V, 92% of the copy rate). A unit costs
+// 3.7 us beside its tiles (first loads, epilogue).
+// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1, late 1,
+// early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (all three
+// against 1.23); sixteen softmax warps on column halves no gain; tiles of 64 keys with S
+// doubled 3.8 to 5.3 ms at 16384 (several arrangements); early weights without their maximum, asked for only by
+// weights of 2 and more, 247 us at 4096, late ones too 273. At d = 64, P in columns of its
+// own, so that late scores need not wait for the products: 1.30.
 //
 // Schedule: persistent CTAs take whole units, strided; with a workspace the units past the
 // last full wave but one are cut into contiguous ranges of KV tiles of equal cost, and so are
@@ -94,10 +98,13 @@ struct DCfg {
   static constexpr int OFF_EXCH = OFF_STG + (NORM ? BM * DV * 2 : 0);    // sums; squares and the norm's weights
   static constexpr int SMEM = OFF_EXCH + (NORM ? 8 * kSoftThreads + 4 * DV : 4 * kSoftThreads);
   static constexpr uint32_t COL_O = 256;
-  static constexpr int PART = 2 * DV * 128 + 4 * 128;   // floats of one piece's partial result
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(COL_O + 2 * DV <= 512, "Tensor Memory columns");
 };
+
+// Floats of one piece's partial result: O and (m, l) of both maps.
+template <int DV>
+constexpr int kPart = 2 * DV * 128 + 4 * 128;
 
 // ------------------------------------------------------------------ schedule
 __device__ __forceinline__ int keys_of(const DiffParams &p, int b) {
@@ -690,7 +697,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
   // Piece k ran on CTA c0 + k, as its first item (slot 0), but for the unit's first piece, which
   // is the last item of its CTA (slot 1).
   auto part = [&](int k) {
-    return p.parts + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::PART;
+    return p.parts + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPart<C::DV>;
   };
   auto stat_of = [&](int k) { return reinterpret_cast<float4 *>(part(k) + 2 * C::DV * 128); };
   const int own = static_cast<int>(blockIdx.x) - c0;
@@ -764,12 +771,10 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
 #pragma unroll
       for (int i = 0; i < NX; ++i) ss = fmaf(x[i], x[i], ss);
     }
-    if constexpr (C::NORM) {
-      float *sums = exch + kSoftThreads;
-      sums[tid] = ss;
-      softmax_sync();
-      ss = sums[row] + sums[row + 128];
-    }
+    float *sums = exch + kSoftThreads;
+    sums[tid] = ss;
+    softmax_sync();
+    ss = sums[row] + sums[row + 128];
     if (row < rows) finish_row<C, NX>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + row, col0, x, ss);
     return;
   }
@@ -795,7 +800,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       l2 = fmaf(ex2_approx(s.z - m2), s.w, l2);
     }
     const float f1 = map_factor(0, lambda, l1), f2 = map_factor(1, lambda, l2);
-    const bool normed = C::NORM && p.weight;
+    const bool normed = p.weight != nullptr;
     float4 *hold = reinterpret_cast<float4 *>(part(0)) + r;
     float ss = 0.f;
 #pragma unroll 1
@@ -833,20 +838,18 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
         finish_row<C, 8>(p, nullptr, item.b, at, at.q0 + r, 8 * c, x, 0.f);
       }
     }
-    if constexpr (C::NORM) {
-      if (!p.weight) return;
-      float *sums = exch + kSoftThreads;
-      sums[tid] = ss;
-      softmax_sync();
-      if (!live) return;
-      ss = 0.f;
-      for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
+    if (!normed) return;
+    float *sums = exch + kSoftThreads;
+    sums[tid] = ss;
+    softmax_sync();
+    if (!live) return;
+    ss = 0.f;
+    for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
 #pragma unroll 1
-      for (int c = cg; c < C::DV / 8; c += CG) {
-        const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
-        float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
-      }
+    for (int c = cg; c < C::DV / 8; c += CG) {
+      const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
+      float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
     }
     return;
   }
@@ -891,18 +894,15 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
     for (int o = CW; o < 32; o <<= 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-    float ss = 0.f;
-    if constexpr (C::NORM) {
-      ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+    float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
 #pragma unroll
-      for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      softmax_sync();   // the previous row's sums have been read
-      if (lane == 0) bars->red[tid / 32] = ss;
-      softmax_sync();
-      ss = 0.f;
+    for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    softmax_sync();   // the previous row's sums have been read
+    if (lane == 0) bars->red[tid / 32] = ss;
+    softmax_sync();
+    ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
-    }
+    for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
     if (pg == 0) finish_row<C, 4>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, c4 * 4, x, ss);
   }
 }
@@ -1095,9 +1095,11 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
     // Both maps' O are final once the unit's last product completes.
     wait(o_full, items & 1);
     tc_fence_after();
-    if (item.kind == 2) {
-      diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
-      continue;
+    if constexpr (C::NORM) {   // (the halves of v at d = 256 run without a workspace: no pieces)
+      if (item.kind == 2) {
+        diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
+        continue;
+      }
     }
     exch[tid] = l;
     softmax_sync();
@@ -1262,7 +1264,7 @@ using D256 = DCfg<128, 128>;
 
 }  // namespace
 
-int diff_part_floats(int d) { return d == 64 ? D64::PART : D128::PART; }
+int diff_part_floats(int d) { return d == 64 ? kPart<64> : kPart<128>; }
 
 cudaError_t launch_attn_diff(const DiffParams &p, int d, int grid, cudaStream_t s) {
   if (d == 64) return launch_cfg<D64>(p, grid, s);
