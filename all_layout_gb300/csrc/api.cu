@@ -164,9 +164,9 @@ xs_status validate(const void *const *ptrs, int nptrs, void *const *shards, int 
 struct MapKey {
   const void *base;
   int rank;
-  cuuint64_t dims[4];
-  cuuint64_t strides[3];
-  cuuint32_t box[4];
+  cuuint64_t dims[3];
+  cuuint64_t strides[2];
+  cuuint32_t box[3];
 };
 struct MapEntry {
   MapKey key;
@@ -177,6 +177,17 @@ constexpr int kMapCache = 96;
 std::mutex g_map_mu;
 MapEntry g_maps[kMapCache] = {};
 unsigned long long g_map_clock = 0;
+
+bool encode_now(CUtensorMap *m, void *base, int rank, const cuuint64_t *dims,
+                const cuuint64_t *strides_bytes, const cuuint32_t *box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), base, dims,
+            strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool encode(CUtensorMap *m, void *base, int rank, const cuuint64_t *dims,
             const cuuint64_t *strides_bytes, const cuuint32_t *box) {
@@ -198,14 +209,7 @@ bool encode(CUtensorMap *m, void *base, int rank, const cuuint64_t *dims,
         return true;
       }
   }
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
-  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), base, dims,
-         strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  if (!encode_now(m, base, rank, dims, strides_bytes, box)) return false;
   std::lock_guard<std::mutex> lock(g_map_mu);
   MapEntry *victim = &g_maps[0];
   for (MapEntry &e : g_maps)
@@ -369,7 +373,7 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const unsigned long 
     bx[i] = box[i];
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
-  return encode(m, const_cast<void *>(base), rank, d, st, bx);
+  return encode_now(m, const_cast<void *>(base), rank, d, st, bx);
 }
 
 }  // namespace xs

@@ -75,7 +75,7 @@ cudaError_t read_and_clear_status(cudaStream_t s, int *out);
 // What the other entry points share with api.cu.
 int sm_count();                          // of the current device; -1 on failure
 unsigned long long wait_limit_ns();      // xs_set_wait_limit_ns
-// A bf16 tensor map with 128-byte swizzle (up to 4 dimensions), from the cache of encoded maps.
+// A bf16 tensor map with 128-byte swizzle (up to 4 dimensions).
 bool encode_map(CUtensorMap *m, const void *base, int rank, const unsigned long long *dims,
                 const unsigned long long *strides_bytes, const unsigned *box);
 // Device address of the status word that xs_last_device_status reads.
