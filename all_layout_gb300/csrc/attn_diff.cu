@@ -39,18 +39,14 @@
 // scores, 1024 products), the softmax 2 x 128 x 128 exponentials, 1024 cycles of the
 // four special-function units and about as many issue slots again. A tile takes 1.26 us
 // (2610 cycles): the chain late scores - late softmax - products - late scores of a map is
-// what the other map's work does not hide (tensor pipe busy 54% of the cycles, issue slots 52%).
-// At d = 64 (1.15 us a tile, 768 cycles of tensor work) it is the softmax itself, with two warps
-// a scheduler. Measured (GB300, 2070 MHz): d = 128, 24 heads of 4096 queries and keys 244 us
-// (1267 TFLOP/s, 68% of the cuBLAS rate), of 16384 3.43 ms (1442, 77%); one query of 4 x 24
-// heads against 16384 keys 129 us (6.2 TB/s of K and V, 92% of the copy rate). A unit costs
-// 3.7 us beside its tiles (first loads, epilogue).
-// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1, late 1,
-// early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (all three
-// against 1.23); sixteen softmax warps on column halves no gain; tiles of 64 keys with S
-// doubled 3.8 to 5.3 ms at 16384 (several arrangements); early weights without their maximum, asked for only by
-// weights of 2 and more, 247 us at 4096, late ones too 273. At d = 64, P in columns of its
-// own, so that late scores need not wait for the products: 1.30.
+// what the other map's work does not hide. Measured (GB300, 2070 MHz): d = 128, 24 heads of
+// 4096 queries and keys 244 us (1267 TFLOP/s, 68% of the cuBLAS rate), of 16384 3.43 ms
+// (1442, 77%); one query of 4 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
+// 92% of the copy rate). A unit costs 3.7 us beside its tiles (first loads, epilogue).
+// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1,
+// late 1, early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (1.23 then); sixteen
+// softmax warps on column halves no gain; whole tiles of 64 keys with S doubled 3.8 to 5.3 ms
+// at 16384 (several arrangements).
 //
 // Schedule: persistent CTAs take whole units, strided; with a workspace the units past the
 // last full wave but one are cut into contiguous ranges of KV tiles of equal cost, and so are
@@ -78,7 +74,7 @@ constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
 constexpr int kScoreWarp = kSoftWarps, kProductWarp = kSoftWarps + 1, kDiffLoadWarp = kSoftWarps + 2;
 constexpr int kDiffHalf = BM * 128;                 // one 64-column half of a 128-row tile
 constexpr uint32_t kDiffSleepNs = 100000;
-constexpr float kDiffRescale = 8.0f;                // log2 units: rescale O only past a growth of 2^8
+constexpr float kDiffRescale = 8.0f;                // d = 256, log2 units: rescale O only past a growth of 2^8
 
 // DH: columns of one map's q and k; DV: columns of v that a unit takes.
 template <int DH_, int DV_>
@@ -98,13 +94,10 @@ struct DCfg {
   static constexpr int OFF_EXCH = OFF_STG + (NORM ? BM * DV * 2 : 0);    // sums; squares and the norm's weights
   static constexpr int SMEM = OFF_EXCH + (NORM ? 8 * kSoftThreads + 4 * DV : 4 * kSoftThreads);
   static constexpr uint32_t COL_O = 256;
+  static constexpr int PART = 2 * DV * 128 + 4 * 128;   // floats of one piece's partial result
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(COL_O + 2 * DV <= 512, "Tensor Memory columns");
 };
-
-// Floats of one piece's partial result: O and (m, l) of both maps.
-template <int DV>
-constexpr int kPart = 2 * DV * 128 + 4 * 128;
 
 // ------------------------------------------------------------------ schedule
 __device__ __forceinline__ int keys_of(const DiffParams &p, int b) {
@@ -697,7 +690,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
   // Piece k ran on CTA c0 + k, as its first item (slot 0), but for the unit's first piece, which
   // is the last item of its CTA (slot 1).
   auto part = [&](int k) {
-    return p.parts + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPart<C::DV>;
+    return p.parts + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::PART;
   };
   auto stat_of = [&](int k) { return reinterpret_cast<float4 *>(part(k) + 2 * C::DV * 128); };
   const int own = static_cast<int>(blockIdx.x) - c0;
@@ -771,10 +764,12 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
 #pragma unroll
       for (int i = 0; i < NX; ++i) ss = fmaf(x[i], x[i], ss);
     }
-    float *sums = exch + kSoftThreads;
-    sums[tid] = ss;
-    softmax_sync();
-    ss = sums[row] + sums[row + 128];
+    if constexpr (C::NORM) {
+      float *sums = exch + kSoftThreads;
+      sums[tid] = ss;
+      softmax_sync();
+      ss = sums[row] + sums[row + 128];
+    }
     if (row < rows) finish_row<C, NX>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + row, col0, x, ss);
     return;
   }
@@ -800,7 +795,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       l2 = fmaf(ex2_approx(s.z - m2), s.w, l2);
     }
     const float f1 = map_factor(0, lambda, l1), f2 = map_factor(1, lambda, l2);
-    const bool normed = p.weight != nullptr;
+    const bool normed = C::NORM && p.weight;
     float4 *hold = reinterpret_cast<float4 *>(part(0)) + r;
     float ss = 0.f;
 #pragma unroll 1
@@ -838,18 +833,20 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
         finish_row<C, 8>(p, nullptr, item.b, at, at.q0 + r, 8 * c, x, 0.f);
       }
     }
-    if (!normed) return;
-    float *sums = exch + kSoftThreads;
-    sums[tid] = ss;
-    softmax_sync();
-    if (!live) return;
-    ss = 0.f;
-    for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
+    if constexpr (C::NORM) {
+      if (!p.weight) return;
+      float *sums = exch + kSoftThreads;
+      sums[tid] = ss;
+      softmax_sync();
+      if (!live) return;
+      ss = 0.f;
+      for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
 #pragma unroll 1
-    for (int c = cg; c < C::DV / 8; c += CG) {
-      const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
-      float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
+      for (int c = cg; c < C::DV / 8; c += CG) {
+        const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
+        float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
+      }
     }
     return;
   }
@@ -894,15 +891,18 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
     for (int o = CW; o < 32; o <<= 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-    float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+    float ss = 0.f;
+    if constexpr (C::NORM) {
+      ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
 #pragma unroll
-    for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    softmax_sync();   // the previous row's sums have been read
-    if (lane == 0) bars->red[tid / 32] = ss;
-    softmax_sync();
-    ss = 0.f;
+      for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      softmax_sync();   // the previous row's sums have been read
+      if (lane == 0) bars->red[tid / 32] = ss;
+      softmax_sync();
+      ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
+      for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
+    }
     if (pg == 0) finish_row<C, 4>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, c4 * 4, x, ss);
   }
 }
@@ -932,6 +932,12 @@ __device__ __forceinline__ void add_weights(const uint32_t (&pk)[16], float (&su
         : "+f"(sum[2 * (i & 1)]), "+f"(sum[2 * (i & 1) + 1])
         : "r"(pk[i]));
 }
+__device__ __forceinline__ float sum_of(const uint32_t (&pk)[2][16]) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  add_weights(pk[0], sum);
+  add_weights(pk[1], sum);
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
 // Without any key the maximum is -inf, and the weights are 2^(-inf - 0) = 0.
 __device__ __forceinline__ uint64_t neg2(float m) {
   const float n = m == -INFINITY ? 0.f : -m;
@@ -959,19 +965,28 @@ __device__ __noinline__ void mask64(uint32_t taddr, int valid) {
   tmem_wait_st();
 }
 
-// A running maximum m that takes in a larger mx: by a whole number, but for the first one.
-__device__ __forceinline__ float grown(float m, float mx) { return m == -INFINITY ? mx : m + ceilf(mx - m); }
+// The reference m of a row's weights 2^(s - m): kHead above the maximum of its first keys, kNone while
+// all scores were -inf. A larger maximum mx moves it by a whole number.
+constexpr float kHead = 7.f, kMove = 1.f, kMany = 512.f, kNone = -1e30f;
+__device__ __forceinline__ float first_ref(float mx) { return mx == -INFINITY ? kNone : mx + kHead; }
+__device__ __forceinline__ float moved_ref(float m, float mx) {
+  return m == kNone ? mx + kHead : m + ceilf(mx + kHead - m);
+}
 
 // The factor 2^(a - b) of a maximum that moved from a to b; 1 where it did not (-inf included).
 __device__ __forceinline__ float shrink(float a, float b) { return a == b ? 1.f : ex2_approx(a - b); }
 
 // Softmax of one map, a thread per row, in halves of 64 keys: the early half's exponentials run
 // while the tensor cores finish the last tile's products and compute the late half's scores.
-// The running maximum begins as the first keys' own: the largest weight is then 1, which bf16 holds
-// exactly, and rows with few keys or one that stands out keep the formula's precision (rounded up
-// to a whole number, two keys' error against 64 bits was 0.0026 of the result instead of 0.0018).
-// It moves only when it grew by more than 2^kDiffRescale, and then by whole numbers (log2 units),
-// so that every rescaling is by a power of two, exact for the early half's weights already rounded.
+// The weights' reference begins 2^kHead above the first keys' own maximum: the largest weight is
+// then a power of two, which bf16 holds exactly, and rows with few keys or one that stands out keep
+// the formula's precision (with it rounded up to a whole number, two keys' error against 64 bits was
+// 0.0026 of the result instead of 0.0018). It moves only when it has to, and by whole numbers (log2
+// units), so that every rescaling is by a power of two, exact for weights already rounded: for the
+// late half when a score is 2^kMove above it; for the early half, which does not look for its
+// maximum, when its sum is kMany and more (a weight is 8 then at least). Nothing can overflow before
+// that shows: a weight that is infinite makes the sum so too, and the scores are still there. (With
+// the early half's maximum too 24 heads of 4096 took 244 us instead of 231.)
 template <class C>
 __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem) {
   const int tid = threadIdx.x, t = tid >> 7, row = tid & 127, wq = row >> 5;
@@ -1012,7 +1027,7 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
         continue;
       }
       uint32_t pe[2][16], pl[2][16];
-      float alpha = 1.f;
+      float alpha = 1.f, early;   // early: the sum of the early half's weights
       bool rescale;               // of O, by alpha, in some lane
       tc_fence_after();
       {
@@ -1022,21 +1037,30 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
         tmem_ld32(tS + 96, s[1]);
         tmem_wait_ld_regs(s[0]);
         tmem_wait_ld_regs(s[1]);
-        tc_fence_before();
-        mbar_arrive(e_free);
-        const float mx = max64(s[0], s[1]) * scale, before = m;
         rescale = false;
-        if (j == 0) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, mx > m + kDiffRescale)) {
-          if (mx > m + kDiffRescale) m = grown(m, mx);
-          alpha = shrink(before, m);
-          rescale = true;
-        }
-        const uint64_t negm2 = neg2(m);
+        if (j == 0) m = first_ref(max64(s[0], s[1]) * scale);
+        const uint64_t negm2 = f2_pack(-m, -m);
         weights32(s[0], scale2, negm2, pe[0]);
         ready = mbar_test(l_full, step & 1);
         weights32(s[1], scale2, negm2, pe[1]);
+        early = sum_of(pe);
+        // (Not a number asks too.)
+        if (__any_sync(0xffffffffu, !(early < kMany))) {
+          tmem_ld32(tS + 64, s[0]);
+          tmem_ld32(tS + 96, s[1]);
+          tmem_wait_ld_regs(s[0]);
+          tmem_wait_ld_regs(s[1]);
+          const float mx = max64(s[0], s[1]) * scale, before = m;
+          if (mx > m + kMove) m = moved_ref(m, mx);
+          alpha = shrink(before, m);
+          rescale = j > 0;
+          const uint64_t neg = f2_pack(-m, -m);
+          weights32(s[0], scale2, neg, pe[0]);
+          weights32(s[1], scale2, neg, pe[1]);
+          early = sum_of(pe);
+        }
+        tc_fence_before();
+        mbar_arrive(e_free);
       }
       if (!__all_sync(0xffffffffu, ready)) wait(l_full, step & 1);
       tc_fence_after();
@@ -1047,11 +1071,12 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
       tmem_wait_ld_regs(s[0]);
       tmem_wait_ld_regs(s[1]);
       const float mx = max64(s[0], s[1]) * scale, before = m;
-      if (__any_sync(0xffffffffu, mx > m + kDiffRescale)) {
-        if (mx > m + kDiffRescale) m = grown(m, mx);
+      if (__any_sync(0xffffffffu, mx > m + kMove)) {
+        if (mx > m + kMove) m = moved_ref(m, mx);
         const float a = shrink(before, m);   // in bf16 a power of two: exact on the rounded weights
         const uint32_t a2 = pack_bf16x2(a, a);
         alpha *= a;
+        early *= a;
         rescale = j > 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -1073,7 +1098,7 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
       tmem_st16(tS, pe[0]);
       tmem_st16(tS + 16, pe[1]);
       // Some exponentials hide the store's latency.
-      const uint64_t negm2 = neg2(m);
+      const uint64_t negm2 = f2_pack(-m, -m);
       weights32(s[0], scale2, negm2, pl[0]);
       tmem_wait_st();
       tc_fence_before();
@@ -1085,21 +1110,14 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(p_full + 8);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      add_weights(pe[0], sum);
-      add_weights(pe[1], sum);
-      add_weights(pl[0], sum);
-      add_weights(pl[1], sum);
-      l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      l = fmaf(l, alpha, early + sum_of(pl));
     }
     // Both maps' O are final once the unit's last product completes.
     wait(o_full, items & 1);
     tc_fence_after();
-    if constexpr (C::NORM) {   // (the halves of v at d = 256 run without a workspace: no pieces)
-      if (item.kind == 2) {
-        diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
-        continue;
-      }
+    if (item.kind == 2) {
+      diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
+      continue;
     }
     exch[tid] = l;
     softmax_sync();
@@ -1264,7 +1282,7 @@ using D256 = DCfg<128, 128>;
 
 }  // namespace
 
-int diff_part_floats(int d) { return d == 64 ? kPart<64> : kPart<128>; }
+int diff_part_floats(int d) { return d == 64 ? D64::PART : D128::PART; }
 
 cudaError_t launch_attn_diff(const DiffParams &p, int d, int grid, cudaStream_t s) {
   if (d == 64) return launch_cfg<D64>(p, grid, s);

@@ -226,6 +226,44 @@ def test_peaked_and_growing_scores(xs, d, use_ws):
     check(o, reference(q, k, v, lam, weight=w if use_ws else None), "o")
 
 
+@pytest.mark.parametrize("use_ws", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("grow", ["up", "down", "steps"])
+def test_scores_that_grow_past_every_range(xs, d, use_ws, grow):
+    """Whole-numbered q and k, whose products are exact, with scores from 0 to tens of thousands: a row's
+    weights would overflow or vanish if their reference did not move with them (or moved with the smallest)."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    H, Nq, Nk = 2, 140, 1500
+    size = {"up": torch.linspace(0, 120, Nk), "down": torch.linspace(120, 0, Nk),
+            "steps": torch.tensor([0.0, 100.0, 1.0, 120.0, 3.0, 60.0]).repeat_interleave(Nk // 6)}[grow].cuda()
+    q = torch.randint(-4, 5, (1, H, Nq, d), generator=g, device="cuda").to(BF)
+    k = (torch.randint(-2, 3, (1, H, Nk, d), generator=g, device="cuda") * size[:, None]).round().to(BF)
+    v = torch.randn(1, H, Nk, d, generator=g, device="cuda").to(BF)
+    lam = torch.rand(H, generator=g, device="cuda")
+    o = torch.full_like(q, math.nan)
+    xs.diff_attn(q, k, v, o, lam, workspace=workspace() if use_ws else None)
+    done(xs)
+    check(o, reference(q, k, v, lam), "o")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("below", [0, 6])
+def test_scores_of_minus_infinity(xs, d, below):
+    """The first keys' scores overflow to -inf (weight 0); those behind them are ordinary, or all low."""
+    q, k, v, lam, _ = inputs(1, 2, 2, 150, 900, d, seed=d)
+    q = (q.float().abs() + 0.5).to(BF).float() * 2.0 ** 64
+    kk = k.float()
+    kk[:, :, :200] = -(kk[:, :, :200].abs() + 0.5) * 2.0 ** 64 * 4.0
+    kk[:, :, 200:] = (kk[:, :, 200:] * 0.25 - below) * 2.0 ** -64
+    q, k = q.to(BF), kk.to(BF)
+    for ws in (None, workspace()):
+        o = torch.full_like(q, math.nan)
+        xs.diff_attn(q, k, v, o, lam, workspace=ws)
+        done(xs)
+        # The oracle leaves the keys of weight 0 out; scores of some hundreds add 2^-23 of their size.
+        check(o, reference(q, k[:, :, 200:].contiguous(), v[:, :, 200:].contiguous(), lam), "o")
+
+
 @pytest.mark.parametrize("lam_value", [0.0, 1.0, -0.5, 3.0])
 def test_lambda_and_scale(xs, lam_value):
     q, k, v, _, _ = inputs(1, 3, 3, 200, 300, 128, seed=11)
