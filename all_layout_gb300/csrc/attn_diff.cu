@@ -37,16 +37,21 @@
 //
 // Bound: at d = 128 the tensor pipe has 1536 cycles of work a tile and both maps (512
 // scores, 1024 products), the softmax 2 x 128 x 128 exponentials, 1024 cycles of the
-// four special-function units and about as many issue slots again. A tile takes 1.26 us
-// (2610 cycles): the chain late scores - late softmax - products - late scores of a map is
-// what the other map's work does not hide. Measured (GB300, 2070 MHz): d = 128, 24 heads of
-// 4096 queries and keys 244 us (1267 TFLOP/s, 68% of the cuBLAS rate), of 16384 3.43 ms
-// (1442, 77%); one query of 4 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
-// 92% of the copy rate). A unit costs 3.7 us beside its tiles (first loads, epilogue).
-// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1,
-// late 1, early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (1.23 then); sixteen
-// softmax warps on column halves no gain; whole tiles of 64 keys with S doubled 3.8 to 5.3 ms
-// at 16384 (several arrangements).
+// four special-function units and about as many issue slots again. A tile takes 1.17 us
+// (2420 cycles): the chain late scores - late softmax - products - late scores of a map is
+// what the other map's work does not hide, and the softmax warps' own instructions (without
+// the row sums a tile would take 7% less, with half of the exponentials no less).
+// At d = 64 (1.1 us a tile, 768 cycles of tensor work) it is the softmax itself, with two warps
+// a scheduler. Measured (GB300, 2070 MHz): d = 128, 24 heads of 4096 queries and keys 230 us
+// (1347 TFLOP/s, 72% of the cuBLAS rate), of 16384 3.25 ms (1522, 81%); one query of 4 x 24
+// heads against 16384 keys 128 us (6.3 TB/s of K and V, 93% of the copy rate). A unit costs
+// 3.8 us beside its tiles (first loads, epilogue).
+// Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1, late 1,
+// early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (all three
+// against 1.23); sixteen softmax warps on column halves no gain; tiles of 64 keys with S
+// doubled 3.8 to 5.3 ms at 16384 (several arrangements); late weights
+// without their maximum too, the early ones stored after them, 273 us at 4096. At d = 64, P in
+// columns of its own, so that late scores need not wait for the products: 1.30.
 //
 // Schedule: persistent CTAs take whole units, strided; with a workspace the units past the
 // last full wave but one are cut into contiguous ranges of KV tiles of equal cost, and so are
@@ -94,10 +99,13 @@ struct DCfg {
   static constexpr int OFF_EXCH = OFF_STG + (NORM ? BM * DV * 2 : 0);    // sums; squares and the norm's weights
   static constexpr int SMEM = OFF_EXCH + (NORM ? 8 * kSoftThreads + 4 * DV : 4 * kSoftThreads);
   static constexpr uint32_t COL_O = 256;
-  static constexpr int PART = 2 * DV * 128 + 4 * 128;   // floats of one piece's partial result
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(COL_O + 2 * DV <= 512, "Tensor Memory columns");
 };
+
+// Floats of one piece's partial result: O and (m, l) of both maps.
+template <int DV>
+constexpr int kPart = 2 * DV * 128 + 4 * 128;
 
 // ------------------------------------------------------------------ schedule
 __device__ __forceinline__ int keys_of(const DiffParams &p, int b) {
@@ -690,7 +698,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
   // Piece k ran on CTA c0 + k, as its first item (slot 0), but for the unit's first piece, which
   // is the last item of its CTA (slot 1).
   auto part = [&](int k) {
-    return p.parts + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::PART;
+    return p.parts + (static_cast<size_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPart<C::DV>;
   };
   auto stat_of = [&](int k) { return reinterpret_cast<float4 *>(part(k) + 2 * C::DV * 128); };
   const int own = static_cast<int>(blockIdx.x) - c0;
@@ -764,12 +772,10 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
 #pragma unroll
       for (int i = 0; i < NX; ++i) ss = fmaf(x[i], x[i], ss);
     }
-    if constexpr (C::NORM) {
-      float *sums = exch + kSoftThreads;
-      sums[tid] = ss;
-      softmax_sync();
-      ss = sums[row] + sums[row + 128];
-    }
+    float *sums = exch + kSoftThreads;
+    sums[tid] = ss;
+    softmax_sync();
+    ss = sums[row] + sums[row + 128];
     if (row < rows) finish_row<C, NX>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + row, col0, x, ss);
     return;
   }
@@ -795,7 +801,7 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       l2 = fmaf(ex2_approx(s.z - m2), s.w, l2);
     }
     const float f1 = map_factor(0, lambda, l1), f2 = map_factor(1, lambda, l2);
-    const bool normed = C::NORM && p.weight;
+    const bool normed = p.weight != nullptr;
     float4 *hold = reinterpret_cast<float4 *>(part(0)) + r;
     float ss = 0.f;
 #pragma unroll 1
@@ -833,20 +839,18 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
         finish_row<C, 8>(p, nullptr, item.b, at, at.q0 + r, 8 * c, x, 0.f);
       }
     }
-    if constexpr (C::NORM) {
-      if (!p.weight) return;
-      float *sums = exch + kSoftThreads;
-      sums[tid] = ss;
-      softmax_sync();
-      if (!live) return;
-      ss = 0.f;
-      for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
+    if (!normed) return;
+    float *sums = exch + kSoftThreads;
+    sums[tid] = ss;
+    softmax_sync();
+    if (!live) return;
+    ss = 0.f;
+    for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
 #pragma unroll 1
-      for (int c = cg; c < C::DV / 8; c += CG) {
-        const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
-        float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
-      }
+    for (int c = cg; c < C::DV / 8; c += CG) {
+      const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
+      float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      finish_row<C, 8>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, 8 * c, x, ss);
     }
     return;
   }
@@ -891,18 +895,15 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
     for (int o = CW; o < 32; o <<= 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-    float ss = 0.f;
-    if constexpr (C::NORM) {
-      ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+    float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
 #pragma unroll
-      for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      softmax_sync();   // the previous row's sums have been read
-      if (lane == 0) bars->red[tid / 32] = ss;
-      softmax_sync();
-      ss = 0.f;
+    for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    softmax_sync();   // the previous row's sums have been read
+    if (lane == 0) bars->red[tid / 32] = ss;
+    softmax_sync();
+    ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
-    }
+    for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
     if (pg == 0) finish_row<C, 4>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, c4 * 4, x, ss);
   }
 }
@@ -969,8 +970,14 @@ __device__ __noinline__ void mask64(uint32_t taddr, int valid) {
 // all scores were -inf. A larger maximum mx moves it by a whole number.
 constexpr float kHead = 7.f, kMove = 1.f, kMany = 512.f, kNone = -1e30f;
 __device__ __forceinline__ float first_ref(float mx) { return mx == -INFINITY ? kNone : mx + kHead; }
+// (Two forms of the same: from kNone the first step of the second ends at 0, and from anywhere else
+// its second step is 0. In the inner loop the compiler does better with the first at DV = 64, 722
+// against 753 us for 6 heads of 16384, and with the second at 128, 231 against 233 for 24 of 4096.)
+template <int DV>
 __device__ __forceinline__ float moved_ref(float m, float mx) {
-  return m == kNone ? mx + kHead : m + ceilf(mx + kHead - m);
+  if (DV == 64) return m == kNone ? mx + kHead : m + ceilf(mx + kHead - m);
+  m += ceilf(mx + kHead - m);
+  return m + ceilf(mx + kHead - m);
 }
 
 // The factor 2^(a - b) of a maximum that moved from a to b; 1 where it did not (-inf included).
@@ -986,7 +993,7 @@ __device__ __forceinline__ float shrink(float a, float b) { return a == b ? 1.f 
 // late half when a score is 2^kMove above it; for the early half, which does not look for its
 // maximum, when its sum is kMany and more (a weight is 8 then at least). Nothing can overflow before
 // that shows: a weight that is infinite makes the sum so too, and the scores are still there. (With
-// the early half's maximum too 24 heads of 4096 took 244 us instead of 231.)
+// the early half's maximum too 24 heads of 4096 took 244 us instead of 230.)
 template <class C>
 __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem) {
   const int tid = threadIdx.x, t = tid >> 7, row = tid & 127, wq = row >> 5;
@@ -1051,7 +1058,7 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
           tmem_wait_ld_regs(s[0]);
           tmem_wait_ld_regs(s[1]);
           const float mx = max64(s[0], s[1]) * scale, before = m;
-          if (mx > m + kMove) m = moved_ref(m, mx);
+          if (mx > m + kMove) m = moved_ref<C::DV>(m, mx);
           alpha = shrink(before, m);
           rescale = j > 0;
           const uint64_t neg = f2_pack(-m, -m);
@@ -1072,7 +1079,7 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
       tmem_wait_ld_regs(s[1]);
       const float mx = max64(s[0], s[1]) * scale, before = m;
       if (__any_sync(0xffffffffu, mx > m + kMove)) {
-        if (mx > m + kMove) m = moved_ref(m, mx);
+        if (mx > m + kMove) m = moved_ref<C::DV>(m, mx);
         const float a = shrink(before, m);   // in bf16 a power of two: exact on the rounded weights
         const uint32_t a2 = pack_bf16x2(a, a);
         alpha *= a;
@@ -1115,9 +1122,11 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
     // Both maps' O are final once the unit's last product completes.
     wait(o_full, items & 1);
     tc_fence_after();
-    if (item.kind == 2) {
-      diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
-      continue;
+    if constexpr (C::NORM) {   // (the halves of v at d = 256 run without a workspace: no pieces)
+      if (item.kind == 2) {
+        diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
+        continue;
+      }
     }
     exch[tid] = l;
     softmax_sync();
@@ -1282,7 +1291,7 @@ using D256 = DCfg<128, 128>;
 
 }  // namespace
 
-int diff_part_floats(int d) { return d == 64 ? D64::PART : D128::PART; }
+int diff_part_floats(int d) { return d == 64 ? kPart<64> : kPart<128>; }
 
 cudaError_t launch_attn_diff(const DiffParams &p, int d, int grid, cudaStream_t s) {
   if (d == 64) return launch_cfg<D64>(p, grid, s);
