@@ -85,8 +85,8 @@ constexpr float kDiffRescale = 8.0f;                // d = 256, log2 units: resc
 template <int DH_, int DV_>
 struct DCfg {
   static constexpr int DH = DH_, DV = DV_, DQ = 2 * DH;
-  // With a twelfth warp, which does nothing, the compiler's schedule of the softmax came out 7%
-  // faster at DV = 128 (a KV tile 1.27 -> 1.19 us) and 2% slower at 64.
+  // With a twelfth warp, which does nothing, the compiler's schedule of the softmax comes out faster
+  // at DV = 128 (a KV tile 1.20 -> 1.17 us) and slower at 64 (1.10 -> 1.20).
   static constexpr int THREADS = kSoftThreads + (DV == 64 ? 96 : 128);
   static constexpr int SLOT = BN * DV * 2;          // a ring slot: the V tile, or DV columns of the K tile
   static constexpr int KSL = DQ / DV;               // slots of a K tile (2 at d = 256: one per map)
@@ -985,13 +985,14 @@ __device__ __forceinline__ float shrink(float a, float b) { return a == b ? 1.f 
 
 // Softmax of one map, a thread per row, in halves of 64 keys: the early half's exponentials run
 // while the tensor cores finish the last tile's products and compute the late half's scores.
-// The weights' reference begins 2^kHead above the first keys' own maximum: the largest weight is
+// The weights' reference begins kHead above the first keys' own maximum: the largest weight is
 // then a power of two, which bf16 holds exactly, and rows with few keys or one that stands out keep
 // the formula's precision (with it rounded up to a whole number, two keys' error against 64 bits was
 // 0.0026 of the result instead of 0.0018). It moves only when it has to, and by whole numbers (log2
-// units), so that every rescaling is by a power of two, exact for weights already rounded: for the
-// late half when a score is 2^kMove above it; for the early half, which does not look for its
-// maximum, when its sum is kMany and more (a weight is 8 then at least). Nothing can overflow before
+// units), so that every rescaling is by a power of two, exact for weights already rounded (until
+// scores of 2^16, where fp32 no longer holds the reference's fraction: one more rounding then). For
+// the late half it moves when a score is kMove above it; for the early half, which does not look for
+// its maximum, when its sum is kMany and more (a weight is 8 then at least). Nothing can overflow before
 // that shows: a weight that is infinite makes the sum so too, and the scores are still there. (With
 // the early half's maximum too 24 heads of 4096 took 244 us instead of 230.)
 template <class C>
