@@ -301,6 +301,10 @@ __device__ __forceinline__ void wide_leave(uint32_t tO, float4 *to, int stride, 
   }
 }
 
+// The pieces' common reference: 0 where no piece has a score above -inf, whose factors 2^(-inf - 0)
+// are then 0 as the weights were (neg2), and the row's map gives 0 as it does in a whole unit.
+__device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
+
 // The end of a piece, per warp (its 32 rows): both maps' O, m and l are in the workspace. The
 // warp that counts the last piece of these rows merges all of them in piece order.
 __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bars, const float *weight,
@@ -332,6 +336,7 @@ __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bar
       m1 = fmaxf(m1, s.x);
       m2 = fmaxf(m2, s.z);
     }
+    m1 = finite_ref(m1), m2 = finite_ref(m2);
 #pragma unroll 4
     for (int k = 0; k < S; ++k) {
       const float4 s = __ldcg(stat_of(k) + r);
@@ -395,6 +400,7 @@ __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bar
       m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
       m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
     }
+    m1 = finite_ref(m1), m2 = finite_ref(m2);
     for (int k = lane; k < S; k += 32) {
       const float4 s = __ldcg(stat_of(k) + r);
       l1 = fmaf(ex2_approx(s.x - m1), s.y, l1);

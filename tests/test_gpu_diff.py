@@ -264,6 +264,37 @@ def test_scores_of_minus_infinity(xs, d, below):
         check(o, reference(q, k[:, :, 200:].contiguous(), v[:, :, 200:].contiguous(), lam), "o")
 
 
+@pytest.mark.parametrize("use_ws", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [3, 20, 150])
+def test_maps_without_a_finite_score(xs, Nq, d, use_ws):
+    """Every score of one map overflows to -inf: that map gives 0, the other its mean, in whole units and
+    in pieces; with both maps so the rows are zeros, under a norm too."""
+    H, Nk, half = 2, 6000, d // 2
+    ws = workspace() if use_ws else None
+    for gone in ((0,), (1,), (0, 1)):
+        q, k, v, lam, w = inputs(1, H, H, Nq, Nk, d, seed=Nq + d)
+        for t in gone:
+            part = slice(t * half, (t + 1) * half)
+            q[..., part] = (q[..., part].float().abs() + 0.5) * 2.0 ** 64
+            k[..., part] = -(k[..., part].float().abs() + 0.5) * 2.0 ** 66
+        o = torch.full_like(q, math.nan)
+        xs.diff_attn(q, k, v, o, lam, norm_weight=w if len(gone) == 2 and (use_ws or d != 256) else None, workspace=ws)
+        done(xs, ws)
+        if len(gone) == 2:
+            assert not o.any()
+            continue
+        # The map that is left, as a first map whose second has lambda 0; times -lambda where it is the second.
+        qq, kk = (q, k) if gone == (1,) else (x.roll(half, -1) for x in (q, k))
+        qq, kk = qq.clone(), kk.clone()
+        qq[..., half:] = 0
+        ref, tol, var = reference(qq, kk, v, torch.zeros_like(lam))
+        if gone == (0,):
+            f = -lam.double()[None, :, None, None]
+            ref, tol, var = ref * f, tol * f.abs(), var * f.square()
+        check(o, (ref, tol, var), f"map {gone[0]} gone")
+
+
 @pytest.mark.parametrize("lam_value", [0.0, 1.0, -0.5, 3.0])
 def test_lambda_and_scale(xs, lam_value):
     q, k, v, _, _ = inputs(1, 3, 3, 200, 300, 128, seed=11)
