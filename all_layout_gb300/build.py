@@ -21,7 +21,7 @@ SOURCES = ("attn.cu", "scatter.cu", "api.cu", "noalloc.cu", "probe.cu", "rope.cu
            "attn_diff.cu", "diff_api.cu")
 HEADERS = (os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "attn_wide.cuh"), os.path.join(CSRC, "diff.h"),
-           os.path.join(CSRC, "attn_diff_wide.cuh"),
+           os.path.join(CSRC, "attn_diff_wide.cuh"), os.path.join(CSRC, "turns.h"),
            os.path.join(ROOT, "include", "xs.h"))
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden"]

@@ -9,11 +9,11 @@
 // the pair's axis and frequency f: angle = pos[axis] * f,
 //     (a, b) <- (a cos - b sin, b cos + a sin).
 //
-// Angles. A frequency is held as a 64-bit fixed-point fraction of a turn, so
-// pos * f modulo one turn is one wrapping integer product: exact for every 32-bit
-// position, negative ones included, with no range reduction. Its top 32 bits, as a
-// signed fraction of a half turn, go to sincospif in fp32 (error below 2^-24 of a
-// turn plus sincospif's own).
+// Angles. A frequency is held as a 64-bit fixed-point fraction of a turn (turns.h: off by
+// 2^-65 of one at most), so pos * f modulo one turn is one wrapping integer product: off by
+// 2^-34 of a turn at most for every 32-bit position, negative ones included, with no range
+// reduction. Its top 32 bits, as a signed fraction of a half turn, go to sincospif in fp32
+// (in all below 2^-25 of a turn, plus sincospif's own error).
 //
 // Bound: HBM. Every value is read once and written once. A thread keeps one token
 // and eight columns and walks the heads, so the sines and cosines of its four pairs
@@ -37,6 +37,7 @@
 
 #include "../../include/xs.h"
 #include "internal.h"
+#include "turns.h"
 
 namespace xs {
 namespace {
@@ -333,9 +334,8 @@ extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
   for (int a = 0, pair = 0; a < n_axes; ++a)
     for (int i = 0; i < axis_dims[a] / 2; ++i, ++pair) {
       if (!std::isfinite(freqs[pair])) return XS_ERR_INVALID;
-      double turns = freqs[pair] / 6.283185307179586476925;
-      turns -= std::floor(turns);   // whole turns per step do not show at integer positions
-      p.freq[pair] = turns < 1.0 ? static_cast<unsigned long long>(turns * 0x1p64) : 0ull;
+      if (!turns_fit(freqs[pair])) return XS_ERR_UNSUPPORTED;
+      p.freq[pair] = turns_per_step(freqs[pair]);
       p.axis[pair] = static_cast<unsigned char>(a);
     }
   if (B == 0 || N == 0 || items == 0) return XS_OK;

@@ -281,8 +281,9 @@ typedef struct {
  *     (x_a, x_b) <- (x_a cos t - x_b sin t, x_b cos t + x_a sin t),  t = pos[axis] * f
  * for every pair of the first rot = sum(axis_dims) columns of a rotated tensor; the
  * other columns stay. Pair i (in the order of the axes) has frequency freqs[i] and
- * belongs to the axis whose axis_dims[a]/2 pairs hold it. t is exact modulo a turn
- * for every 32-bit position; negated positions undo a rotation.
+ * belongs to the axis whose axis_dims[a]/2 pairs hold it. t modulo a turn is off by
+ * 2^-25 of a turn at most, for every 32-bit position and every frequency; negated
+ * positions undo a rotation.
  *   pos               int32 (device), token n of batch entry b at
  *                     pos + b*pos_batch_stride + n*n_axes; stride 0 shares one list
  *   axis_dims, freqs  HOST arrays (n_axes entries; rot/2 radians per step), read
@@ -295,7 +296,7 @@ typedef struct {
  * types, output rows that overlap (a stride below d over more than one row), or
  * x == y with other strides or another type. XS_ERR_UNSUPPORTED for d not a multiple
  * of 8 in [8, 256], pairs i, i + rot/2 with rot not a multiple of 8, other type
- * pairs, B*N >= 2^31 or more than 65535 heads. XS_ERR_ALIGN unless x, y and weight are
+ * pairs, a frequency of 2^64 or more, B*N >= 2^31 or more than 65535 heads. XS_ERR_ALIGN unless x, y and weight are
  * 16-byte aligned and every stride over more than one row is a multiple of 16 bytes.
  * Empty problems return XS_OK. */
 xs_status xs_rope(const xs_rope_tensor *tensors, int n_tensors, const int *pos,

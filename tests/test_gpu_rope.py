@@ -9,6 +9,7 @@ to 2^-24 of a turn's half and cut at 2^-32 of a turn: pi * 2^-24 + 2^-30 in the 
 roundings of the rotation: 32 * 2^-24 * r in all. For far positions the table of exact angles
 itself is off by 2^-52 relative, at most 2^-21 of a radian at 2^31: added where |pos| is large."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -130,6 +131,26 @@ def test_custom_frequencies_above_a_turn(xs):
     x, pos, _, (q, _, _) = case(1, 40, 2, 1, 64, axes, FP, FP, False, seed=2, hi=300)
     xs.qkv_rope(x[:, :, :2].cuda(), None, None, q, None, None, pos.cuda(), axes, freqs=fr)
     check(q, formula(x[:, :, :2], pos, axes, fr, None, 0, True, True), "q")
+
+
+@pytest.mark.parametrize("freq", [0.3, 1.0, 7.25, -100.0, 1e4, 1e6, -2.5e15, 1.7e19])
+def test_angles_of_every_position_and_frequency(xs, freq):
+    """pos * freq modulo a turn from exact rationals, over the whole range of 32-bit positions: no allowance
+    for far positions or high frequencies beside the rounding of the angle's fraction of a turn."""
+    from test_rope_host import two_pi
+    g = torch.Generator().manual_seed(3)
+    pos = torch.randint(-(1 << 31), (1 << 31) - 1, (97, 1), generator=g, dtype=torch.int64).to(torch.int32)
+    pos[:6, 0] = torch.tensor([(1 << 31) - 1, -(1 << 31), -1, 1, 0, (1 << 31) - 2], dtype=torch.int32)
+    x = torch.randn(1, 97, 2, 8, generator=g)
+    q = torch.empty(1, 2, 97, 8, device="cuda")
+    xs.qkv_rope(x.cuda(), None, None, q, None, None, pos.cuda(), (2,), freqs=[freq])
+    turns = [float(Fraction(freq) * int(p) / two_pi() % 1) for p in pos[:, 0]]   # off by 2^-53 at most
+    ang = 2 * math.pi * torch.tensor(turns, dtype=torch.float64)[None, :, None]
+    a, b = x[..., 0].double(), x[..., 1].double()
+    want, size = x.double().clone(), x.double().abs()
+    want[..., 0], want[..., 1] = a * ang.cos() - b * ang.sin(), b * ang.cos() + a * ang.sin()
+    size[..., :2] = torch.hypot(a, b)[..., None]
+    check(q, (want.transpose(1, 2), size.transpose(1, 2)), f"freq {freq}")
 
 
 @pytest.mark.parametrize("adjacent", [True, False])

@@ -2,11 +2,15 @@
 of the binding, and the 64-bit turn arithmetic that the kernel uses, against exact rationals."""
 import ctypes
 import math
+import os
+import random
+import subprocess
 from fractions import Fraction
 
 import pytest
 import torch
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 0x10000   # a 16-byte aligned fake device address; never dereferenced
 
 
@@ -87,3 +91,52 @@ def test_turn_arithmetic(freq, pos):
     diff = (got - want) % 1
     diff = min(diff, 1 - diff)
     assert diff < Fraction(max(1, abs(pos)), 1 << 31) * Fraction(1, 1 << 20) + Fraction(1, 1 << 60)
+
+
+def two_pi():
+    """2 pi to 400 bits and more, from Machin's pi / 4 = 4 arctan(1/5) - arctan(1/239)."""
+    one = 1 << 440
+
+    def arctan_inverse(n):
+        term, total, k = one // n, 0, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+    return Fraction(8 * (4 * arctan_inverse(5) - arctan_inverse(239)), one)
+
+
+@pytest.fixture(scope="module")
+def turns(tmp_path_factory):
+    """turns_per_step of the library's header, built as host code."""
+    folder = tmp_path_factory.mktemp("turns")
+    (folder / "t.cpp").write_text(f'#include "{ROOT}/all_layout_gb300/csrc/turns.h"\n'
+                                  'extern "C" unsigned long long f(double x) { return xs::turns_per_step(x); }\n'
+                                  'extern "C" int fits(double x) { return xs::turns_fit(x); }\n')
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-o", folder / "t.so", folder / "t.cpp"], check=True)
+    lib = ctypes.CDLL(str(folder / "t.so"))
+    lib.f.restype, lib.f.argtypes = ctypes.c_ulonglong, [ctypes.c_double]
+    lib.fits.argtypes = [ctypes.c_double]
+    return lib
+
+
+def test_fraction_of_a_turn(turns):
+    """The 64-bit fraction of every frequency below 2^64 is the exact one, rounded to nearest (half a unit,
+    and 2^-60 of one for the 192 bits of 1 / (2 pi)): 2^-34 of a turn over 2^31 steps."""
+    rng, whole = random.Random(5), two_pi()
+    freqs = [1.0, 0.3, 7.25, 100.0, 1e4, 1e6, 2.0 ** 52, 2.0 ** 63, math.nextafter(2.0 ** 64, 0), 0.0, 5e-324, 2.0 ** -61, 2.0 ** -62,
+             2.0 ** -63, 2.0 ** -64, math.tau, 2 * math.tau, math.nextafter(math.tau, 7), 1e4 ** -0.25, 1e4 ** (-62 / 64)]
+    freqs += [rng.uniform(1, 2) * 2.0 ** rng.randint(-80, 63) for _ in range(3000)]
+    for f in freqs + [-f for f in freqs]:
+        want = Fraction(f) / whole * (1 << 64)
+        diff = (turns.f(f) - want) % (1 << 64)
+        assert min(diff, (1 << 64) - diff) <= Fraction(1, 2) + Fraction(1, 1 << 60), f
+
+
+def test_frequencies_out_of_range(turns, xs):
+    for f in (2.0 ** 64, -2.0 ** 64, 1e300):
+        assert not turns.fits(f)
+        assert _call(xs, freqs=[f] * 128) == xs.ERR_UNSUPPORTED
+    assert turns.fits(math.nextafter(2.0 ** 64, 0)) and turns.fits(0.0) and turns.fits(-1.0)
+    assert _call(xs, B=0, freqs=[math.nextafter(2.0 ** 64, 0)] * 128) == xs.OK
