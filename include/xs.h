@@ -280,10 +280,11 @@ typedef struct {
  *     x <- x / sqrt(mean(x^2) + eps) * weight            where weight is given
  *     (x_a, x_b) <- (x_a cos t - x_b sin t, x_b cos t + x_a sin t),  t = pos[axis] * f
  * for every pair of the first rot = sum(axis_dims) columns of a rotated tensor; the
- * other columns stay. Pair i (in the order of the axes) has frequency freqs[i] and
- * belongs to the axis whose axis_dims[a]/2 pairs hold it. t modulo a turn is off by
- * 2^-25 of a turn at most, for every 32-bit position and every frequency; negated
- * positions undo a rotation.
+ * other columns stay. The norm holds for rows of any finite values (squares past fp32's
+ * range included); a row of zeros stays one, with eps = 0 too. Pair i (in the order of
+ * the axes) has frequency freqs[i] and belongs to the axis whose axis_dims[a]/2 pairs
+ * hold it. t modulo a turn is off by 2^-25 of a turn at most, for every 32-bit position
+ * and every frequency; negated positions undo a rotation.
  *   pos               int32 (device), token n of batch entry b at
  *                     pos + b*pos_batch_stride + n*n_axes; stride 0 shares one list
  *   axis_dims, freqs  HOST arrays (n_axes entries; rot/2 radians per step), read

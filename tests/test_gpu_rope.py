@@ -219,6 +219,47 @@ def test_large_and_tiny_rows_under_the_norm(xs):
     check(q, formula(x, pos, (64,), freqs_of((64,)), w, 1e-6, True, True), "q")
 
 
+@pytest.mark.parametrize("adjacent", [True, False])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+@pytest.mark.parametrize("H,d,src,dst", [(3, 8, FP, FP), (70, 80, BF, BF), (3, 128, BF, BF), (34, 256, FP, FP), (3, 128, FP, BF), (3, 64, HF, HF)])
+def test_norm_over_the_whole_range_of_the_type(xs, H, d, src, dst, eps, adjacent):
+    """Rows whose squares leave fp32's range, both ways, beside ordinary ones; a row of zeros stays one, also
+    with eps = 0; a NaN stays in its row, and an infinity leaves zeros beside NaN. (Rows of subnormal numbers
+    are left out where the result would be one too.)"""
+    g = torch.Generator().manual_seed(d)
+    sizes = [1.0, 0.0, 1e-4, 1e4] if src is HF else [1.0, 0.0, 1e-25, 1e20, 1e-37, 3e37, 1e-20, 1e18, 1e-12, 1e10]
+    rows = torch.randn(len(sizes), H, d, generator=g).clamp(-4, 4) * torch.tensor(sizes)[:, None, None]
+    rows[:, H // 2, 1:] *= 2.0 ** -30   # one column far above the others
+    x = torch.cat([rows, torch.ones(2, H, d)])[None].to(src)
+    x[0, -2, :, 3], x[0, -1, :, 5] = math.nan, math.inf
+    N = x.shape[1]
+    w = 1 + 0.2 * torch.randn(d, generator=g)
+    pos = torch.zeros(N, 1, dtype=torch.int32)
+    q = torch.full((1, H, N, d), 7.0, dtype=dst, device="cuda")
+    xd = x.cuda()
+    xs.qkv_rope(xd, None, None, q, None, None, pos.cuda(), (8,), q_weight=w.cuda(), eps=eps, interleaved=adjacent)
+    want, size = formula(x[:, :-2], pos[:-2], (8,), freqs_of((8,)), w, eps, adjacent, True)
+    check(q[:, :, :-2], (want.nan_to_num(nan=0.0), size.nan_to_num(nan=0.0)), "q")   # 0 / 0: the row of zeros
+    assert not q[0, :, 1].any()
+    assert q[0, :, -2].isnan().all()
+    last = q[0, :, -1]
+    pair = [4, 5] if adjacent else [1, 5]
+    assert last[:, pair].isnan().any() and not last[:, [i for i in range(d) if i not in pair]].any()
+    if src is dst:
+        xs.qkv_rope(xd, None, None, xd.transpose(1, 2), None, None, pos.cuda(), (8,), q_weight=w.cuda(), eps=eps, interleaved=adjacent)
+        assert torch.equal(xd.transpose(1, 2).nan_to_num(nan=9.0), q.nan_to_num(nan=9.0))
+
+
+def test_norm_in_place_with_tiny_weights(xs):
+    """Rows that are tiny after the norm are not normed twice."""
+    x = torch.randn(1, 40, 37, 64, generator=torch.Generator().manual_seed(1))
+    x[:, ::3, ::2] *= 1e-25
+    w = torch.full((64,), 1e-27)
+    pos, xd = torch.arange(40, dtype=torch.int32)[:, None].contiguous(), x.cuda()
+    xs.qkv_rope(xd, None, None, xd.transpose(1, 2), None, None, pos.cuda(), (64,), q_weight=w.cuda(), eps=0.0)
+    check(xd.transpose(1, 2), formula(x, pos, (64,), freqs_of((64,)), w, 0.0, True, True), "in place")
+
+
 def test_offsets_past_32_bits(xs):
     """A head stride that puts the last rows more than 2^32 elements behind the first."""
     if torch.cuda.mem_get_info()[0] < 24 << 30:
