@@ -629,8 +629,63 @@ __device__ __forceinline__ float max64(const uint32_t (&a)[32], const uint32_t (
   return max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
 }
 
+// The sum of squares of a row, or of a part of one, as the norm passes it on: the sum, or, where squares
+// that count may have left fp32's range, minus its root. Rows with an infinity or NaN keep the sum.
+// (Below: scaled_squares and its like. Their code costs 24 heads of 4096 at d = 128 0.9%, at d = 64 nothing;
+// inlined, or with an eps in this test, which would spare rows that are small beside it, 1.3 to 1.6%.)
+__device__ __forceinline__ bool squares_fit(float ss) {   // in [2^-80, 2^120]
+  return __float_as_uint(ss) - __float_as_uint(0x1p-80f) <= __float_as_uint(0x1p120f) - __float_as_uint(0x1p-80f);
+}
+// The power of two that brings x near 1 (x > 0 and finite).
+__device__ __forceinline__ float near_one(float x) {
+  return __int_as_float((254 - min(max(__float_as_int(x) >> 23, 1), 253)) << 23);
+}
+// From the largest magnitude `big` and the sum `sum` of the squares times near_one(big)^2.
+__device__ __forceinline__ float minus_root(float sum, float big) { return -(sqrtf(sum) * near_one(near_one(big))); }
+__device__ __forceinline__ bool has_root(float big, float ss) { return big > 0.f && big < INFINITY && ss == ss; }
+template <int NX>
+__device__ __forceinline__ float scaled_squares(const float (&x)[NX], float ss) {
+  float big = 0.f, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NX; ++i) big = fmaxf(big, fabsf(x[i]));
+  if (!has_root(big, ss)) return ss;
+  const float s = near_one(big);
+#pragma unroll
+  for (int i = 0; i < NX; ++i) sum = fmaf(x[i] * s, x[i] * s, sum);
+  return minus_root(sum, big);
+}
+// Of two parts of a row (join_roots: one of them minus its root).
+__device__ __noinline__ float join_roots(float a, float b) {
+  const float ra = a < 0.f ? -a : sqrtf(a), rb = b < 0.f ? -b : sqrtf(b);
+  const float most = ra > rb ? ra : rb, q = (ra > rb ? rb : ra) / most;
+  return -(most * sqrtf(fmaf(q, q, 1.f)));
+}
+__device__ __forceinline__ float join_squares(float a, float b) {
+  return fminf(a, b) < 0.f ? join_roots(a, b) : a + b;
+}
+// The same of a row whose parts lie in N values of each of the first `lanes` lanes (a power of two),
+// repeated over the warp; `ss` is its sum.
+template <int N>
+__device__ __forceinline__ float lanes_squares(const float (&x)[N], float ss, int lanes) {
+  if (!__any_sync(0xffffffffu, !squares_fit(ss))) return ss;
+  float big = 0.f, sum = 0.f;
+  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(x[i]));
+  for (int o = 1; o < lanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+  const bool root = !squares_fit(ss) && has_root(big, ss);
+  const float s = root ? near_one(big) : 1.f;
+  for (int i = 0; i < N; ++i) sum = fmaf(x[i] * s, x[i] * s, sum);
+  for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return root ? minus_root(sum, big) : ss;
+}
+
+// norm_factor of a sum passed on as minus its root.
+__device__ __noinline__ float root_factor(float root, int d, float eps) {
+  const float s = near_one(fmaxf(fabsf(root), sqrtf(eps))), y = root * s;
+  return fminf(rsqrtf(y * y / d + eps * s * s) * s, 0x1p127f);
+}
 // 1 / sqrt(mean + eps) of a row of d columns. A row of zeros (no keys) stays one, also with eps = 0.
 __device__ __forceinline__ float norm_factor(float ss, int d, float eps) {
+  if (ss < 0.f) return root_factor(ss, d, eps);
   return ss == 0.f ? 0.f : rsqrtf(ss * (1.f / d) + eps);
 }
 
@@ -771,11 +826,12 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       }
 #pragma unroll
       for (int i = 0; i < NX; ++i) ss = fmaf(x[i], x[i], ss);
+      if (p.weight && !squares_fit(ss)) ss = scaled_squares(x, ss);
     }
     float *sums = exch + kSoftThreads;
     sums[tid] = ss;
     softmax_sync();
-    ss = sums[row] + sums[row + 128];
+    ss = join_squares(sums[row], sums[row + 128]);
     if (row < rows) finish_row<C, NX>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + row, col0, x, ss);
     return;
   }
@@ -840,12 +896,32 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
       }
     }
     if (!normed) return;
+    if (live && !squares_fit(ss)) {
+      float big = 0.f, sum = 0.f;
+      for (int c = cg; c < C::DV / 8; c += CG)
+        for (int i = 0; i < 2; ++i) {
+          const float4 a = __ldcg(hold + (2 * c + i) * 128);
+          big = fmaxf(big, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))));
+        }
+      if (has_root(big, ss)) {
+        const float s = near_one(big);
+        for (int c = cg; c < C::DV / 8; c += CG)
+          for (int i = 0; i < 2; ++i) {
+            const float4 a = __ldcg(hold + (2 * c + i) * 128);
+            sum = fmaf(a.x * s, a.x * s, sum);
+            sum = fmaf(a.y * s, a.y * s, sum);
+            sum = fmaf(a.z * s, a.z * s, sum);
+            sum = fmaf(a.w * s, a.w * s, sum);
+          }
+        ss = minus_root(sum, big);
+      }
+    }
     float *sums = exch + kSoftThreads;
     sums[tid] = ss;
     softmax_sync();
     if (!live) return;
-    ss = 0.f;
-    for (int g = 0; g < CG; ++g) ss += sums[g * R + r];
+    ss = sums[r];
+    for (int g = 1; g < CG; ++g) ss = join_squares(ss, sums[g * R + r]);
 #pragma unroll 1
     for (int c = cg; c < C::DV / 8; c += CG) {
       const float4 a = __ldcg(hold + 2 * c * 128), b = __ldcg(hold + (2 * c + 1) * 128);
@@ -898,14 +974,50 @@ __device__ __noinline__ void diff_piece(const DiffParams &p, DBars *bars, float 
     float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
 #pragma unroll
     for (int o = 1; o < CW; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (p.weight) ss = lanes_squares(x, ss, CW);
     softmax_sync();   // the previous row's sums have been read
     if (lane == 0) bars->red[tid / 32] = ss;
     softmax_sync();
     ss = 0.f;
+    float least = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSoftWarps; ++i) ss += bars->red[i];
+    for (int i = 0; i < kSoftWarps; ++i) {
+      ss += bars->red[i];
+      least = fminf(least, bars->red[i]);
+    }
+    if (least < 0.f) {
+      ss = bars->red[0];
+      for (int i = 1; i < kSoftWarps; ++i) ss = join_squares(ss, bars->red[i]);
+    }
     if (pg == 0) finish_row<C, 4>(p, exch + 2 * kSoftThreads, item.b, at, at.q0 + r, c4 * 4, x, ss);
   }
+}
+
+// scaled_squares of half a row's columns f1 O1 + f2 O2, read from Tensor Memory again; all lanes take part.
+template <int DV>
+__device__ __noinline__ float unit_squares(uint32_t o1, float f1, float f2, float ss) {
+  if (!__any_sync(0xffffffffu, f1 != 0.f || f2 != 0.f)) return ss;   // no keys: zeros
+  float big = 0.f, sum = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const float s = near_one(big);   // (2^126 in the first pass, which does not use the sum)
+    sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < DV / 32; ++c) {
+      uint32_t a[16], v[16];
+      tmem_ld16(o1 + 16 * c, a);
+      tmem_ld16(o1 + DV + 16 * c, v);
+      tmem_wait_ld16(a);
+      tmem_wait_ld16(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float y = fmaf(f1, __uint_as_float(a[i]), f2 * __uint_as_float(v[i]));
+        big = fmaxf(big, fabsf(y));
+        sum = fmaf(y * s, y * s, sum);
+      }
+    }
+  }
+  return !squares_fit(ss) && has_root(big, ss) ? minus_root(sum, big) : ss;
 }
 
 // 32 scores of a row to weights 2^(s * scale - m), rounded to bf16 pairs: P goes to the tensor
@@ -1154,13 +1266,15 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
           ss = fmaf(y, y, ss);
         }
       }
+      if (C::NORM && p.weight && __any_sync(0xffffffffu, !squares_fit(ss)))
+        ss = unit_squares<C::DV>(o1, f1, f2, ss);
     }
     tc_fence_before();
     float *sums = exch + kSoftThreads;
     if constexpr (C::NORM) sums[tid] = ss;
     // All have read O (and l): a map's next P may let the next unit's products overwrite it.
     softmax_sync();
-    if constexpr (C::NORM) ss = sums[row] + sums[row + 128];
+    if constexpr (C::NORM) ss = join_squares(sums[row], sums[row + 128]);
     if (idle || dead) continue;
     if constexpr (!C::NORM) {   // no room to stage the rows
       if (at.q0 + row < p.Nq) finish_row<C, NX>(p, exch + 2 * kSoftThreads, b, at, at.q0 + row, col0, x, ss);

@@ -251,12 +251,38 @@ drain:
   diff_drain(smem_u32(&bars->drain[1]), 0);
 }
 
+// scaled_squares of a row whose 256 combined columns lie in O's Tensor Memory columns; all lanes take part.
+__device__ __noinline__ float wide_squares(uint32_t tO, float ss) {
+  float big = 0.f, sum = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const float s = near_one(big);   // (2^126 in the first pass, which does not use the sum)
+    sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < WideCfg::DV / 32; ++c) {
+      uint32_t x[32];
+      tmem_ld32(tO + 32 * c, x);
+      tmem_wait_ld_regs(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float y = __uint_as_float(x[i]);
+        big = fmaxf(big, fabsf(y));
+        sum = fmaf(y * s, y * s, sum);
+      }
+    }
+  }
+  return !squares_fit(ss) && has_root(big, ss) ? minus_root(sum, big) : ss;
+}
+
 // The final row, whose 256 combined columns lie in O's Tensor Memory columns: norm, factor, store.
 __device__ __forceinline__ void wide_finish(const DiffParams &p, const float *weight, int b, int h, int n,
                                             bool live, uint32_t tO, float ss) {
   using C = WideCfg;
   float f = p.out_scale;
-  if (p.weight) f *= norm_factor(ss, C::DQ, p.eps);
+  if (p.weight) {
+    if (__any_sync(0xffffffffu, !squares_fit(ss))) ss = wide_squares(tO, ss);
+    f *= norm_factor(ss, C::DQ, p.eps);
+  }
   uint4 *dst = live ? reinterpret_cast<uint4 *>(out_row(p, b, h, n, C::DQ)) : nullptr;
 #pragma unroll 1
   for (int c = 0; c < C::DV / 32; ++c) {
@@ -431,6 +457,7 @@ __device__ __noinline__ void wide_merge(const DiffParams &p, const WideBars *bar
       for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      ss = lanes_squares(x, ss, 32);
       f *= norm_factor(ss, C::DQ, p.eps);
     }
     uint2 *dst = reinterpret_cast<uint2 *>(out_row(p, item.b, item.h, item.q0 + r, C::DQ));

@@ -328,7 +328,8 @@ typedef struct {
  * (taken into [0, Nk]; what lies behind them is not used, NaN and infinity included),
  * non-causal. A batch entry without keys gives zeros, a map whose scores of a row are
  * all -inf (they overflowed) gives 0 there, and a row x of zeros stays one under the
- * norm, with eps = 0 too. Scores times scale are taken below 2^30 in magnitude (beyond
+ * norm, with eps = 0 too; the norm holds for rows x of any finite values (squares past
+ * fp32's range included). Scores times scale are taken below 2^30 in magnitude (beyond
  * it fp32 no longer holds a weight's exponent, and a row may come out as zeros or not
  * a number). fp32 accumulation and statistics, softmax weights
  * rounded to bf16 for the product with v, output rounded to bf16. Outputs must not

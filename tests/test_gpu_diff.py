@@ -295,6 +295,23 @@ def test_maps_without_a_finite_score(xs, Nq, d, use_ws):
         check(o, (ref, tol, var), f"map {gone[0]} gone")
 
 
+@pytest.mark.parametrize("d,use_ws", [(64, False), (64, True), (128, False), (128, True), (256, True)])
+@pytest.mark.parametrize("Nq,Nk", [(3, 6000), (12, 6000), (40, 6000), (150, 6000), (150, 40)])
+@pytest.mark.parametrize("size,eps", [(1e-25, 0.0), (1e20, 1e-5), (1e-20, 1e-38), (1.0, 0.0)])
+def test_norm_of_rows_whose_squares_leave_the_range(xs, Nq, Nk, d, size, eps, use_ws):
+    """x / sqrt(mean x^2 + eps) of rows that fp32 holds but not their squares; one head has its values in one
+    half of the columns only, one in a single column."""
+    q, k, v, lam, w = inputs(1, 3, 3, Nq, Nk, d, seed=Nq + Nk + d)
+    v = (v.float() * size).to(BF)
+    v[:, 1, :, :d // 2] = 0
+    v[:, 2, :, 1:] = 0
+    ws = workspace() if use_ws else None
+    o = torch.full_like(q, math.nan)
+    xs.diff_attn(q, k, v, o, lam, norm_weight=w, eps=eps, workspace=ws)
+    done(xs, ws)
+    check(o, reference(q, k, v, lam, weight=w, eps=eps), "o")
+
+
 @pytest.mark.parametrize("lam_value", [0.0, 1.0, -0.5, 3.0])
 def test_lambda_and_scale(xs, lam_value):
     q, k, v, _, _ = inputs(1, 3, 3, 200, 300, 128, seed=11)
