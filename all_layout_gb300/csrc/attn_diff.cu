@@ -14,8 +14,9 @@
 // Work unit: one (batch, head) and one 128-row query tile. This file has the schedule and
 // the kernel for d = 64 and 128, whose two maps of a unit run beside each other: 2 x 128
 // score columns and 2 x d of O fill Tensor Memory. d = 256 has a kernel of its own
-// (attn_diff_wide.cuh); only without a workspace does it run here, on halves of v's columns
-// (a unit is then a half, and the scores are computed in both).
+// (attn_diff_wide.cuh); without a norm, where the workspace is missing or small or the call
+// short, it runs here, on halves of v's columns (a unit is then a half, and the scores are
+// computed in both).
 //
 // Roles (352 or 384 threads, one CTA per SM):
 //   warps 0-3  softmax of map 1, row r of the tile = TMEM lane r
@@ -1235,7 +1236,7 @@ __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, ui
     // Both maps' O are final once the unit's last product completes.
     wait(o_full, items & 1);
     tc_fence_after();
-    if constexpr (C::NORM) {   // (the halves of v at d = 256 run without a workspace: no pieces)
+    if constexpr (C::NORM) {   // (the halves of v at d = 256 have no pieces)
       if (item.kind == 2) {
         diff_piece<C>(p, bars, exch, item, tmem, m, l, dead);
         continue;

@@ -40,6 +40,7 @@ unsigned long long wide_parts_bytes(int rows) { return 2ull * diff_wide_part_flo
 // 777 queries, up to 1101 keys at d = 64, lengths falling to none: split 45 us, whole 34).
 struct Plan {
   int split, waves, grid;
+  long long cost, rounds;   // expected time in KV tiles; whole units a CTA takes
 };
 // The shortest range worth a CTA. Merging a piece of more than a few rows takes the last CTA f KV
 // tiles' time, so n tiles in s pieces take n / s + f s, least at n / s = sqrt(f n). Measured f at 128
@@ -58,7 +59,8 @@ long merge_cost(int d, int rows) { return d == 64 ? 7 : d == 128 ? 8 : 6 + 4 * r
 Plan plan(long long units, int sms, int nk, bool ragged, int least, long merge, unsigned long long per_cta,
           unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
-  const Plan whole{0, 0, grid0};
+  const long long mean = (ragged ? nk - nk / 4 : nk) + kUnitCost, rounds = (units + grid0 - 1) / grid0;
+  const Plan whole{0, 0, grid0, (rounds - 1) * mean + nk + kUnitCost, rounds};
   if (nk < 2) return whole;
   const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
   const long long left = units - static_cast<long long>(waves) * sms;
@@ -70,11 +72,21 @@ Plan plan(long long units, int sms, int nk, bool ragged, int least, long merge, 
   }
   if (per_cta * grid > room || grid * 4 > static_cast<int>(XS_WORKSPACE_HEADER_BYTES / sizeof(int)))
     return whole;
-  const long long mean = (ragged ? nk - nk / 4 : nk) + kUnitCost, rounds = (units + grid0 - 1) / grid0;
-  const long long cost_split = waves * mean + per * mean / (nk + kUnitCost) + 2 * merge;
-  const long long cost_whole = (rounds - 1) * mean + nk + kUnitCost;
-  return cost_split < cost_whole ? Plan{1, waves, grid} : whole;
+  const long long cost = waves * mean + per * mean / (nk + kUnitCost) + 2 * merge;
+  return cost < whole.cost ? Plan{1, waves, grid, cost, waves} : whole;
 }
+
+// Expected times at d = 256, of both maps one after the other and of both at once on half of v's columns
+// (two units then): a KV tile takes 1.95 or 1.55 us, a whole unit 9 or 4 us beside its own, of which the plan's
+// cost has kUnitCost tiles. Without a norm either will do, and the one that should end first is taken, so that a
+// workspace with places for a few SMs does not keep the others idle. Measured (GB300, no norm, us; one after the
+// other with places for 48 and for 80 SMs and with the whole workspace / halves; the first two lose to them):
+//   12 heads x 4096 queries and keys 550, 346, 215 / 315    12 x 1024 52, 52, 28 / 36
+//   8 heads x 256 queries, 16384 keys 254, 254, 116 / 201   24 x 4096, 1024 keys 381, 241, 148 / 174
+//   30 heads x 681 queries, 41 keys (whole) 27 / 21         20 x 3 queries, 685 keys (whole) 21 / 16
+// Over 200 random shapes and workspaces the choice was at most 12% from the better one.
+long long wide_ns(const Plan &p) { return 1950 * p.cost + 3000 * p.rounds; }
+long long halves_ns(const Plan &p) { return 1550 * p.cost - 600 * p.rounds; }
 
 // One operand as a 4-D map {d, rows, heads, batch}; strides of single extents do not matter.
 bool encode_operand(CUtensorMap *m, const void *base, int B, int H, int N, int d,
@@ -149,11 +161,11 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
       (!shards && !strides_aligned(o_stride, B, H, Nq)))
     return XS_ERR_ALIGN;
   // d = 256: one map after the other with a workspace (the norm needs the whole row in one CTA),
-  // both at once on halves of v's columns without.
+  // both at once on halves of v's columns without. A small workspace has places for fewer CTAs.
   const unsigned long long room = ws && ws_bytes > XS_WORKSPACE_HEADER_BYTES ? ws_bytes - XS_WORKSPACE_HEADER_BYTES : 0;
   const int rows = wide_rows(Nq);
-  const bool wide = d == 256 && room >= wide_stash_bytes(rows);
-  if (d == 256 && a->norm_weight && Nk > 0 && !wide) return XS_ERR_INVALID;
+  const bool fits = d == 256 && room >= wide_stash_bytes(rows);
+  if (d == 256 && a->norm_weight && Nk > 0 && !fits) return XS_ERR_INVALID;
 
   DiffParams p;
   std::memset(&p, 0, sizeof(p));
@@ -184,9 +196,30 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   p.weight = a->norm_weight;
   p.kv_len = a->kv_len;
   p.n_qtiles = static_cast<int>(qtiles);
+  const int nk = (Nk + kTileRows - 1) / kTileRows;
+  p.min_places = min_places(d, nk, Nq < kTileRows ? Nq : kTileRows);
+  const bool ragged = a->kv_len != nullptr;
+  const long long tiles = static_cast<long long>(B) * H * p.n_qtiles;
+  // Workspace of the d = 256 kernel: counters | a CTA's place for map 1 each | partial results.
+  const unsigned long long places = room / wide_stash_bytes(rows);
+  const int ctas = places < static_cast<unsigned long long>(sms) ? static_cast<int>(places) : sms;
+  Plan pl{0, 0, 0, 0, 0};
+  bool wide = fits;
+  if (fits)
+    pl = plan(tiles, ctas, nk, ragged, p.min_places, merge_cost(d, rows), wide_parts_bytes(rows),
+              room - ctas * wide_stash_bytes(rows));
+  if (!fits || !a->norm_weight) {
+    // Workspace of the others: counters | partial results (none on halves of v's columns).
+    const Plan other = plan(d == 256 ? 2 * tiles : tiles, sms, nk, ragged, p.min_places, merge_cost(d, kTileRows),
+                            parts_bytes(1, d), d == 256 ? 0 : room);
+    wide = fits && wide_ns(pl) <= halves_ns(other);
+    if (!wide) pl = other;
+  }
   p.v_parts = d == 256 && !wide ? 2 : 1;
   p.units_b = H * p.n_qtiles * p.v_parts;
   p.n_units = B * p.units_b;
+  p.split = pl.split;
+  p.waves = pl.waves;
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
   p.eps = a->eps;
   p.out_scale = a->out_scale;
@@ -194,25 +227,8 @@ xs_status diff_call(const xs_diff_args *a, void *o, const long long *o_stride, v
   p.wait_limit_ns = wait_limit_ns();
   p.count = static_cast<int *>(ws);
   float *area = ws ? reinterpret_cast<float *>(static_cast<char *>(ws) + XS_WORKSPACE_HEADER_BYTES) : nullptr;
-  const int nk = (Nk + kTileRows - 1) / kTileRows;
-  p.min_places = min_places(d, nk, Nq < kTileRows ? Nq : kTileRows);
-  const bool ragged = a->kv_len != nullptr;
-  if (!wide) {
-    // Workspace: counters | partial results.
-    p.parts = area;
-    const Plan pl = plan(p.n_units, sms, nk, ragged, p.min_places, merge_cost(d, kTileRows), parts_bytes(1, d), d == 256 ? 0 : room);
-    p.split = pl.split;
-    p.waves = pl.waves;
-    return launch_attn_diff(p, d, pl.grid, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
-  }
-  // Workspace: counters | a CTA's place for map 1 each | partial results. A small one has places
-  // for fewer CTAs.
-  const unsigned long long places = room / wide_stash_bytes(rows);
-  const int ctas = places < static_cast<unsigned long long>(sms) ? static_cast<int>(places) : sms;
-  const Plan pl = plan(p.n_units, ctas, nk, ragged, p.min_places, merge_cost(d, rows), wide_parts_bytes(rows),
-                       room - ctas * wide_stash_bytes(rows));
-  p.split = pl.split;
-  p.waves = pl.waves;
+  p.parts = area;
+  if (!wide) return launch_attn_diff(p, d, pl.grid, s) == cudaSuccess ? XS_OK : XS_ERR_CUDA;
   p.part_rows = rows;
   p.stash = area;
   p.parts = area + ctas * wide_stash_bytes(rows) / 4;

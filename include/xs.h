@@ -349,10 +349,11 @@ typedef struct {
  *                whole units. At d = 256 a CTA also keeps the first map's rows in it
  *                (fp32, 128 KB for 128 queries) while the second map's are computed:
  *                with less than XS_WORKSPACE_HEADER_BYTES + 1024 * min(128, Nq rounded
- *                up to 8) bytes a norm is refused, and without a norm both maps run at
- *                once on each half of v's columns, their scores computed twice; with
- *                less than all SMs' places fewer SMs work. Calls that share one
- *                workspace must not overlap on the GPU. After a timeout
+ *                up to 8) bytes a norm is refused, with places for fewer CTAs than SMs
+ *                fewer SMs work under a norm; without one a call may run both maps at
+ *                once on each half of v's columns (their scores computed twice), which
+ *                needs no workspace, and takes what should end first. Calls that
+ *                share one workspace must not overlap on the GPU. After a timeout
  *                (xs_last_device_status) zero the header again.
  * Results are the same from launch to launch on one GPU model; they differ in fp32
  * rounding between workspace and none.

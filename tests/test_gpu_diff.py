@@ -367,6 +367,28 @@ def test_workspace_that_is_just_enough_and_one_that_is_not(xs):
         assert bool((buf[full.numel():] == 77).all())
 
 
+def test_a_small_workspace_does_not_slow_a_call_without_a_norm(xs):
+    """d = 256, no norm: with places for a few SMs the call runs as without a workspace (bit for bit the same
+    result), with a place for every unit as with the whole workspace."""
+    B, H, Nq, Nk, d = 1, 12, 1024, 1024, 256
+    q, k, v, lam, w = inputs(B, H, H, Nq, Nk, d, seed=3)
+    full = xs.alloc_diff_workspace(B, H, Nq, Nk, d)
+    buf = torch.zeros(full.numel() + 4096, dtype=torch.uint8, device="cuda")
+    buf[full.numel():] = 77
+    ref, outs = reference(q, k, v, lam), {}
+    for places in (0, 1, 2, 40, 47, 96, "all"):
+        n = full.numel() if places == "all" else 16384 + places * 128 * 256 * 4
+        o = torch.full_like(q, math.nan)
+        xs.diff_attn(q, k, v, o, lam, workspace=buf[:n] if places else None)
+        done(xs, buf)
+        check(o, ref, f"{places} places")
+        outs[places] = o
+    for places in (1, 2, 40, 47):
+        assert torch.equal(outs[places], outs[0]), places
+    assert torch.equal(outs[96], outs["all"]) and not torch.equal(outs["all"], outs[0])
+    assert bool((buf[full.numel():] == 77).all())
+
+
 @pytest.mark.parametrize("d1,d2", [(128, 64), (256, 256)])
 def test_two_graphs_one_workspace_and_streams(xs, d1, d2):
     """Two captured calls of different shapes share a workspace, replayed one after the other; two
