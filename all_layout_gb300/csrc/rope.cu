@@ -390,7 +390,7 @@ extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
   auto has_rows = [&](const xs_rope_tensor &t) { return B > 0 && N > 0 && t.heads > 0; };
   for (int i = 0; i < n_tensors; ++i) {
     const xs_rope_tensor &t = tensors[i];
-    if (!t.x || !t.y || t.heads < 0) return XS_ERR_INVALID;
+    if (t.heads < 0 || (t.heads > 0 && (!t.x || !t.y))) return XS_ERR_INVALID;
     if (!has_rows(t)) {
       items += t.heads;
       continue;
@@ -413,6 +413,7 @@ extern "C" __attribute__((visibility("default"))) xs_status xs_rope(
   for (int i = 0; i < n_tensors; ++i) {
     const xs_rope_tensor &t = tensors[i];
     if (!aligned(t.x, 16) || !aligned(t.y, 16) || !aligned(t.weight, 16)) return XS_ERR_ALIGN;
+    if (!has_rows(t)) continue;
     const long long extent[3] = {B, N, t.heads};
     for (int k = 0; k < 3; ++k)
       if (extent[k] > 1 && (t.x_stride[k] % in_vec != 0 || t.y_stride[k] % out_vec != 0))

@@ -291,14 +291,16 @@ typedef struct {
  *                     during the call
  *   in_type, out_type XS_BF16, XS_FP16 or XS_FP32; equal, or out_type XS_BF16
  * Outputs must not overlap each other or another tensor's input.
- * XS_ERR_INVALID for NULL pointers (weight aside), n_tensors not in [1, 3], negative
- * sizes or strides, n_axes not in [1, 4], an axis width that is odd, below 2 or past
- * d, eps negative or not finite, a frequency that is not finite, unknown flags or
- * types, output rows that overlap (a stride below d over more than one row), or
- * x == y with other strides or another type. XS_ERR_UNSUPPORTED for d not a multiple
- * of 8 in [8, 256], pairs i, i + rot/2 with rot not a multiple of 8, other type
- * pairs, a frequency of 2^64 or more, B*N >= 2^31 or more than 65535 heads. XS_ERR_ALIGN unless x, y and weight are
- * 16-byte aligned and every stride over more than one row is a multiple of 16 bytes.
+ * XS_ERR_INVALID for NULL pointers (weight, and the pointers of a tensor of no heads,
+ * aside), n_tensors not in [1, 3], negative sizes or strides, n_axes not in [1, 4], an
+ * axis width that is odd, below 2 or past d, eps negative or not finite, a frequency
+ * that is not finite, unknown flags or types, output rows that overlap (a stride below d
+ * over more than one row), or x == y with other strides or another type.
+ * XS_ERR_UNSUPPORTED for d not a multiple of 8 in [8, 256], pairs i, i + rot/2 with rot
+ * not a multiple of 8, other type pairs, a frequency of 2^64 or more, B*N >= 2^31 or
+ * more than 65535 heads. XS_ERR_ALIGN unless x, y and weight are 16-byte aligned and
+ * every stride over more than one row is a multiple of 16 bytes. The strides of a tensor
+ * without rows are not looked at.
  * Empty problems return XS_OK. */
 xs_status xs_rope(const xs_rope_tensor *tensors, int n_tensors, const int *pos,
                   long long pos_batch_stride, const int *axis_dims, int n_axes,

@@ -300,6 +300,16 @@ def test_stream_and_graph(xs):
             check(q, formula(x2[:, :, :4], pos, (32, 48, 48), freqs_of((32, 48, 48)), w[0], 1e-6, True, True), "q")
 
 
+def test_tensors_without_heads(xs):
+    """k and v of no heads (no rows to write) leave the others as they are."""
+    x, pos, _, (q, k, v) = case(2, 9, 3, 0, 64, (64,), BF, BF, False, seed=1)
+    xd = x.cuda()
+    xs.qkv_rope(xd[:, :, :3], xd[:, :, 3:], xd[:, :, 3:], q, k, v, pos.cuda(), (64,))
+    check(q, formula(x, pos, (64,), freqs_of((64,)), None, 0, True, True), "q")
+    xs.qkv_rope(xd[:, :, 3:], xd[:, :, :3], None, k, q, None, pos.cuda(), (64,))
+    check(q, formula(x, pos, (64,), freqs_of((64,)), None, 0, True, True), "q as k")
+
+
 def test_empty(xs):
     z = torch.empty(1, 0, 4, 64, dtype=BF, device="cuda")
     xs.qkv_rope(z, None, None, z.transpose(1, 2), None, None, torch.empty(0, 1, dtype=torch.int32, device="cuda"), (64,))

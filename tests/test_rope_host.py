@@ -60,6 +60,12 @@ def test_strides_of_single_rows_do_not_matter(xs):
     assert _call(xs, B=1, N=0, xst=(3, 260, 64), yst=(1, 64, 512)) == 0
 
 
+def test_tensors_without_heads(xs):
+    assert _call(xs, heads=0, xst=(2048, 260, 64)) == 0
+    assert _call(xs, heads=0, yst=(2048, 3, 512)) == 0
+    assert _call(xs, heads=0, x=None, y=None) == 0
+
+
 def test_binding_refuses_before_the_library(xs):
     t = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
