@@ -327,6 +327,14 @@ def _diff_workspace(ws, index):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _diff_check(status, what, q, norm_weight, ws_bytes):
+    if status == ERR_INVALID and q.shape[3] == 256 and norm_weight is not None:
+        rows = min(128, (q.shape[2] + 7) // 8 * 8)
+        if ws_bytes < 16384 + 1024 * rows:
+            what += " (a norm at d = 256 needs a workspace: alloc_diff_workspace)"
+    _check(status, what)
+
+
 def diff_attn(q, k, v, o, lam, *, kv_len=None, norm_weight=None, eps: float = 1e-5,
               out_scale: float = 1.0, scale=None, workspace=None, stream=None):
     """Differential attention into o (see xs_diff_attn in xs.h). q: [B, H, Nq, d]; k, v:
@@ -341,7 +349,8 @@ def diff_attn(q, k, v, o, lam, *, kv_len=None, norm_weight=None, eps: float = 1e
     if o.numel() == 0:
         return
     ws, n = _diff_workspace(workspace, dev)
-    _check(_on(dev, stream, _lib.xs_diff_attn, packed, o.data_ptr(), _STRIDES.pack(*os_[:3]), ws, n), "xs_diff_attn")
+    _diff_check(_on(dev, stream, _lib.xs_diff_attn, packed, o.data_ptr(), _STRIDES.pack(*os_[:3]), ws, n),
+                "xs_diff_attn", q, norm_weight, n)
 
 
 def diff_attn_fused(q, k, v, shards, lam, *, kv_len=None, norm_weight=None, eps: float = 1e-5,
@@ -359,8 +368,8 @@ def diff_attn_fused(q, k, v, shards, lam, *, kv_len=None, norm_weight=None, eps:
     if q.numel() == 0:
         return
     ws, n = _diff_workspace(workspace, dev)
-    _check(_on(dev, stream, _lib.xs_diff_attn_fused, packed, (ctypes.c_void_p * P)(*pointers), P, ws, n),
-           "xs_diff_attn_fused")
+    _diff_check(_on(dev, stream, _lib.xs_diff_attn_fused, packed, (ctypes.c_void_p * P)(*pointers), P, ws, n),
+                "xs_diff_attn_fused", q, norm_weight, n)
 
 
 def alloc_diff_workspace(B: int, H: int, Nq: int, Nk: int, d: int, norm: bool = False, device="cuda"):

@@ -489,3 +489,21 @@ def test_binding_refusals(xs):
     with pytest.raises(ValueError):
         xs.diff_attn_fused(q, k, v, xs.alloc_shards(1, 16, 4, 64, 2) * 4 + [o], lam)
     done(xs)
+
+
+def test_refusal_of_a_norm_without_a_workspace(xs):
+    """At d = 256 the refusal names the workspace; other invalid arguments do not."""
+    q, k, v, lam, w = inputs(1, 2, 2, 20, 30, 256, seed=0)
+    o, shards = torch.empty_like(q), xs.alloc_shards(1, 20, 2, 256, 2)
+    small = workspace(16384 + 24 * 1024 - 256)
+    for ws in (None, small):
+        with pytest.raises(xs.XsError, match="needs a workspace") as e:
+            xs.diff_attn(q, k, v, o, lam, norm_weight=w, workspace=ws)
+        assert e.value.status == xs.ERR_INVALID
+        with pytest.raises(xs.XsError, match="needs a workspace"):
+            xs.diff_attn_fused(q, k, v, shards, lam, norm_weight=w, workspace=ws)
+    for bad in (dict(norm_weight=w, workspace=workspace(16384 + 24 * 1024)), dict()):
+        with pytest.raises(xs.XsError) as e:
+            xs.diff_attn(q, k, v, o, lam, scale=-1.0, **bad)
+        assert "workspace" not in str(e.value)
+    done(xs)
