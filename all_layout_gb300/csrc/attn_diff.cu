@@ -43,10 +43,12 @@
 // what the other map's work does not hide, and the softmax warps' own instructions (without
 // the row sums a tile would take 7% less, with half of the exponentials no less).
 // At d = 64 (1.1 us a tile, 768 cycles of tensor work) it is the softmax itself, with two warps
-// a scheduler. Measured (GB300, 2070 MHz): d = 128, 24 heads of 4096 queries and keys 230 us
-// (1347 TFLOP/s, 72% of the cuBLAS rate), of 16384 3.25 ms (1522, 81%); one query of 4 x 24
-// heads against 16384 keys 128 us (6.3 TB/s of K and V, 93% of the copy rate). A unit costs
-// 3.8 us beside its tiles (first loads, epilogue).
+// a scheduler: 6 heads of 16384 725 us (853 TFLOP/s, 46%). Measured (GB300, 2070 MHz): d = 128,
+// 24 heads of 4096 queries and keys 232 us (1331 TFLOP/s, 71% of the cuBLAS rate), of 16384
+// 3.34 ms (1482, 79%); one query of 4 x 24 heads against 16384 keys 129 us (6.2 TB/s of K and V,
+// 92% of the copy rate). A unit costs 3.8 us beside its tiles (first loads, epilogue). Few
+// queries: a 128-row tile holds those of one query head, also where heads share k and v, so
+// 24 heads on 8 k/v heads take as long as on 24.
 // Tried at d = 128, time of a tile: an issuer per map 1.37; scores in the order early 1, late 1,
 // early 2, late 2 1.76; registers moved from the issuers to the softmax 1.34 (all three
 // against 1.23); sixteen softmax warps on column halves no gain; tiles of 64 keys with S
@@ -1098,15 +1100,15 @@ __device__ __forceinline__ float shrink(float a, float b) { return a == b ? 1.f 
 
 // Softmax of one map, a thread per row, in halves of 64 keys: the early half's exponentials run
 // while the tensor cores finish the last tile's products and compute the late half's scores.
-// The weights' reference begins kHead above the first keys' own maximum: the largest weight is
-// then a power of two, which bf16 holds exactly, and rows with few keys or one that stands out keep
-// the formula's precision (with it rounded up to a whole number, two keys' error against 64 bits was
-// 0.0026 of the result instead of 0.0018). It moves only when it has to, and by whole numbers (log2
-// units), so that every rescaling is by a power of two, exact for weights already rounded (until
-// scores of 2^16, where fp32 no longer holds the reference's fraction: one more rounding then). For
-// the late half it moves when a score is kMove above it; for the early half, which does not look for
-// its maximum, when its sum is kMany and more (a weight is 8 then at least). Nothing can overflow before
-// that shows: a weight that is infinite makes the sum so too, and the scores are still there. (With
+// The weights' reference begins kHead above the first keys' own maximum: where that is the row's, the
+// largest weight is a power of two, which bf16 holds exactly, and rows with few keys, or one among the
+// first that stands out, keep the formula's precision (with it rounded up to a whole number, two keys'
+// error against 64 bits was 0.0026 of the result instead of 0.0018). It moves only when it has to, and by
+// whole numbers (log2 units), so that every rescaling is by a power of two, exact for weights already
+// rounded (until scores of 2^16, where fp32 no longer holds the reference's fraction: one more rounding
+// then). For the late half it moves when a score is kMove above it; for the early half, which does not
+// look for its maximum, when its sum is kMany and more (a weight is 8 then at least). Nothing can overflow
+// before that shows: a weight that is infinite makes the sum so too, and the scores are still there. (With
 // the early half's maximum too 24 heads of 4096 took 244 us instead of 230.)
 template <class C>
 __device__ void diff_softmax(const DiffParams &p, uint8_t *smem, DBars *bars, uint32_t tmem) {

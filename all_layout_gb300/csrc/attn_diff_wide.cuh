@@ -12,7 +12,9 @@
 // Bound: at 2.0 us a tile of both maps (2070 cycles a map) neither is full. Each SM reads 96 KB a
 // tile and map from L2, about as fast as it gives them, and a unit costs 7.4 us beside its tiles
 // (the loads of Q and the first K, O through the workspace, the stores). Measured (GB300): 12 heads
-// of 4096 queries and keys 218 us = 1418 TFLOP/s, 76% of the cuBLAS rate. Tried: both maps at once
+// of 4096 queries and keys 218 us = 1418 TFLOP/s, 76% of the cuBLAS rate. Map 2 reads V again: from L2
+// while query tiles of a head run side by side, from HBM with few queries and long keys (one query of
+// 8 heads against 65536 keys 136 us, 1.7 times what its bytes take once). Tried: both maps at once
 // on halves of v's columns (half of the scores' work twice) 317-331 us; two places for Q and one
 // tile of V 241 us.
 //

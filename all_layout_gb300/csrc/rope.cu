@@ -23,11 +23,13 @@
 // lanes. There is no shared memory and no barrier; UNROLL rows are loaded before the
 // first is used, and blocks of 128 threads at no more than 64 registers keep 32 warps
 // on an SM. Measured (GB300, device time): 65536 tokens x 72 heads x 128 with the norm
-// 378 us = 6.39 TB/s, 94% of the copy rate; 4096 tokens of the same 30.9 us (72%: one
-// wave, whose start and end show); 16384 tokens x 36 x 256 fp16 half pairs 105.9 us
-// (84%). Tried: blocks of 256 threads 381, 34.1 and 107.3 us; the weight and the
-// rotation as two factors per column (fewer operations, 72-90 registers) 402, 36 and
-// 174 us; the partner columns by shuffle 384, 32.6 and 119.7 us.
+// 377 us = 6.41 TB/s, 95% of the copy rate; 4096 tokens of the same 31.6 us (71%: one
+// wave, whose start and end show); 16384 tokens x 36 x 256 fp16 half pairs 105.7 us
+// (84%); 65536 x 25 x 80 fp32 to bf16 149 us (78%: a row takes the power of two of lanes
+// at or above d / 8, of whose 16 ten work). Tried at the first three sizes, then 378, 30.9
+// and 105.9 us: blocks of 256 threads 381, 34.1 and 107.3; the weight and the rotation as
+// two factors per column (fewer operations, 72-90 registers) 402, 36 and 174; the partner
+// columns by shuffle 384, 32.6 and 119.7.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
