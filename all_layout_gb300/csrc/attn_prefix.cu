@@ -1,0 +1,408 @@
+// Attention of a batch of requests that share a prefix, for sm_103a (tcgen05 tensor cores,
+// Tensor Memory, TMA).
+//
+// Per request b and query head h, whose k/v head is hk:
+//     o = softmax(q [K_p | K_b]^T s) [V_p | V_b],   s = 1/sqrt(d),
+// K_p, V_p [Np][d] the same for every request, K_b, V_b [kv_len[b]][d] its own; both in bf16
+// tensors or in pages of an e4m3 cache (cache.cu). A row without any key gives zeros.
+//
+// Rows. The queries of all requests and of all heads that share a k/v head are the rows of one
+// matrix, [entry][head of the group][query], cut into tiles: each key of the prefix is read
+// once for a whole tile of them, whatever requests they belong to.
+// Keys. The own keys of all requests are packed one after the other, each request's beginning
+// at a multiple of `grain`; 128 of them are a KV tile, which may hold several short requests'.
+// A unit (k/v head, tile of rows) goes over the prefix's tiles and then those that hold its
+// requests' own keys; a row sees the range [lo, hi) of the packed keys, and what lies outside
+// gets the score -inf.
+//
+// Schedule: persistent CTAs take whole units, strided; with a workspace the units past the last
+// full wave but one are cut into contiguous ranges of KV tiles of equal cost. A cut unit's
+// pieces leave (m, l, O) in the workspace, and a second launch joins them in piece order.
+// Lengths are on the device, so each CTA works out its range itself.
+//
+// Waits are bounded: a role that gives up records a timeout; the softmax warps then run their
+// control flow to its end without waiting, the others drain what they issued.
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/xs.h"
+#include "internal.h"
+#include "prefix.h"
+#include "ptx.cuh"
+
+namespace xs {
+namespace {
+
+constexpr int BM = kTileRows, BN = kTileRows;
+constexpr int kHalf = BM * 128;   // one 64-column half of a 128-row tile
+constexpr uint32_t kSleepNs = 100000;
+constexpr float kGrowth = 8.0f;   // log2 units: rescale O only when the maximum grows by more than 2^8
+
+// ------------------------------------------------------------------ schedule
+__device__ __forceinline__ int keys_of(const PrefixParams &p, int b) {
+  return p.kv_len ? min(max(__ldg(p.kv_len + b), 0), p.Nk) : p.Nk;
+}
+
+// Where each entry's own keys begin among the packed ones (start[B]: their end), by one warp.
+__device__ void pack_keys(const PrefixParams &p, int *start) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  for (int b = lane; b - lane < p.B; b += 32) {
+    const int mine = b < p.B ? (keys_of(p, b) + p.grain - 1) / p.grain * p.grain : 0;
+    int incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (b < p.B) start[b] = base + incl - mine;
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) start[p.B] = base;
+}
+
+struct PrefixUnit {
+  int unit, hk, row0;   // first row of the k/v head's rows
+  int b_lo, b_hi;       // entries of its rows
+  int t0, n;            // first own tile; tiles, the prefix's first
+};
+__device__ __forceinline__ PrefixUnit unit_of(const PrefixParams &p, const int *start, int unit) {
+  PrefixUnit u;
+  u.unit = unit;
+  u.hk = unit / p.n_tiles;
+  u.row0 = (unit - u.hk * p.n_tiles) * p.row_tile;
+  u.b_lo = u.row0 / p.entry_rows;
+  u.b_hi = (min(u.row0 + p.row_tile, p.rows) - 1) / p.entry_rows;
+  const int s = start[u.b_lo], e = start[u.b_hi + 1];
+  u.t0 = s / BN;
+  // (Rows without any key keep a tile, fully masked, that gives their zeros.)
+  u.n = max(1, p.n_prefix + (e > s ? (e + BN - 1) / BN - u.t0 : 0));
+  return u;
+}
+
+// The split region: its places (kPrefixCost for a unit and then one for each of its KV tiles), the
+// CTAs that share it, and the unit where this CTA begins in it.
+struct PrefixPlan {
+  long long total, begin;   // begin: first place of `unit`
+  int grid, unit;
+};
+
+struct PrefixItem : PrefixUnit {
+  int kv0, kv1;     // KV tiles to do
+  long long u0;     // a cut unit: its first tile's place in the split region
+  bool piece;
+};
+
+// Walks a CTA's work list; every role walks its own copy.
+struct PrefixWalk {
+  int k, unit;
+  long long pos, end, begin;
+
+  __device__ __forceinline__ void start(const PrefixParams &p, const PrefixPlan &plan) {
+    k = 0;
+    pos = end = 0;
+    if (p.split && static_cast<int>(blockIdx.x) < plan.grid) {
+      pos = static_cast<long long>(blockIdx.x) * plan.total / plan.grid;
+      end = static_cast<long long>(blockIdx.x + 1) * plan.total / plan.grid;
+    }
+    unit = plan.unit;
+    begin = plan.begin;
+  }
+  __device__ __forceinline__ bool next(const PrefixParams &p, const int *table, PrefixItem &it) {
+    if (!p.split || k < p.waves) {
+      const int u = static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x);
+      ++k;
+      if (u >= p.n_units) return false;
+      static_cast<PrefixUnit &>(it) = unit_of(p, table, u);
+      it.kv0 = 0;
+      it.kv1 = it.n;
+      it.u0 = 0;
+      it.piece = false;
+      return true;
+    }
+    while (pos < end) {
+      static_cast<PrefixUnit &>(it) = unit_of(p, table, unit);
+      if (pos < begin + it.n + kPrefixCost) {
+        it.u0 = begin + kPrefixCost;
+        if (end <= it.u0) break;   // the range ends before the unit's first tile
+        it.kv0 = pos > it.u0 ? static_cast<int>(pos - it.u0) : 0;
+        it.kv1 = end - it.u0 < it.n ? static_cast<int>(end - it.u0) : it.n;
+        it.piece = it.kv0 > 0 || it.kv1 < it.n;
+        pos = it.u0 + it.kv1;
+        return true;
+      }
+      begin += it.n + kPrefixCost;
+      ++unit;
+    }
+    pos = end;
+    return false;
+  }
+};
+
+// The split region's size and this CTA's place in it, by one warp.
+__device__ PrefixPlan plan_split(const PrefixParams &p, const int *table) {
+  const int lane = threadIdx.x & 31, first = p.waves * static_cast<int>(gridDim.x);
+  auto size_of = [&](int u) -> int { return u < p.n_units ? unit_of(p, table, u).n + kPrefixCost : 0; };
+  long long total = 0;
+  for (int u = first + lane; u < p.n_units; u += 32) total += size_of(u);
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const long long most = max(1ll, total / p.min_places);
+  PrefixPlan plan{total, 0, static_cast<int>(most < gridDim.x ? most : gridDim.x), first};
+  const long long pos = static_cast<int>(blockIdx.x) < plan.grid
+                            ? static_cast<long long>(blockIdx.x) * total / plan.grid : 0;
+  long long base = 0;
+  for (int u = first; u < p.n_units; u += 32) {   // the unit that holds pos
+    const int mine = size_of(u + lane);
+    int incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, pos < base + incl);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      plan.begin = base + __shfl_sync(0xffffffffu, incl - mine, at);
+      plan.unit = u + at;
+      return plan;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return plan;
+}
+
+// The consecutive CTAs that a cut unit's pieces run on.
+struct PrefixSpan {
+  int first, pieces;
+};
+__device__ __forceinline__ PrefixSpan span_of(const PrefixPlan &plan, long long u0, int n) {
+  const long long T = plan.total;
+  const int G = plan.grid;
+  auto start = [&](int c) { return static_cast<long long>(c) * T / G; };
+  auto owner = [&](long long pos) {
+    int c = static_cast<int>(pos * G / T);
+    while (c + 1 < G && start(c + 1) <= pos) ++c;
+    while (c > 0 && start(c) > pos) --c;
+    return c;
+  };
+  const int first = owner(u0);
+  return PrefixSpan{first, owner(u0 + n - 1) - first + 1};
+}
+
+// One row of a k/v head's rows; n >= Nq: padding.
+struct PrefixRow {
+  int b, h, n;
+};
+__device__ __forceinline__ PrefixRow row_of(const PrefixParams &p, int hk, int row) {
+  PrefixRow r;
+  r.b = row / p.entry_rows;
+  const int in = row - r.b * p.entry_rows, g = in / p.nq_rows;
+  r.h = hk * p.group + g;
+  r.n = in - g * p.nq_rows;
+  return r;
+}
+// Where a row's output begins; null for padding.
+__device__ __forceinline__ uint16_t *out_row(const PrefixParams &p, int hk, int row, int d) {
+  if (row >= p.rows) return nullptr;
+  const PrefixRow r = row_of(p, hk, row);
+  if (r.n >= p.Nq) return nullptr;
+  if (p.shard_mode) {
+    const int sh = r.n / p.rows_per_shard, i = r.n - sh * p.rows_per_shard;
+    return static_cast<uint16_t *>(p.shards[sh]) +
+           ((static_cast<long long>(p.b0 + r.b) * p.rows_per_shard + i) * p.H + r.h) * d;
+  }
+  return p.o + r.b * p.o_b + r.h * p.o_h + r.n * p.o_n;
+}
+// The range of keys that a row sees: of the prefix [0, Np), of the packed own ones [lo, hi).
+struct PrefixRange {
+  int lo, hi;
+};
+__device__ __forceinline__ PrefixRange range_of(const PrefixParams &p, const int *table, int row) {
+  if (row >= p.rows) return PrefixRange{0, 0};
+  const int b = row / p.entry_rows, s = table[b];
+  return PrefixRange{s, s + keys_of(p, b)};
+}
+
+// Partial result of a piece: O as float4 groups [column / 4][row], then the rows' maxima and sums.
+template <int D>
+__device__ __forceinline__ float *part_of(const PrefixParams &p, int cta, int slot, int rows) {
+  return p.parts + (static_cast<size_t>(cta) * 2 + slot) * ((D + 2) * rows);
+}
+
+// ------------------------------------------------------------------ waits
+// Bounded wait on a barrier phase; false after a timeout here or elsewhere in the CTA.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status,
+                                       uint64_t limit, bool sleepy) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (sleepy ? mbar_try_wait_sleep(bar, parity, kSleepNs) : mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > limit) {
+        *abort_flag = 1;
+        atomicExch(status, kDevTimeout);
+        return false;
+      }
+    }
+  }
+}
+template <bool SLEEPY>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                         const PrefixParams &p) {
+  const bool ok = mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, p.status, p.wait_limit_ns, SLEEPY);
+  return __all_sync(0xffffffffu, ok);
+}
+// Tear-down: waits for this thread's own copies or MMAs in flight, whatever the abort flag, still bounded.
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > 2000000000ull) return;
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// `bytes` (a multiple of 16) of memory into shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// The wait for tmem_ld16, naming its registers so that no use of them moves before it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// ------------------------------------------------------------------ MMAs
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t dcol, uint64_t qdesc, uint64_t kdesc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>(((kk / 4) * kHalf + (kk % 4) * 32) >> 4);
+    tc_mma_ss(dcol, qdesc + off, kdesc + off, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t dcol, uint32_t pcol, uint64_t vdesc, uint32_t accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, D, 1);
+#pragma unroll
+  for (int kk = 0; kk < BN / 16; ++kk)
+    tc_mma_ts(dcol, pcol + kk * 8, vdesc + static_cast<uint64_t>((kk * 2048) >> 4), idesc,
+              (kk > 0 || accumulate) ? 1u : 0u);
+}
+
+#include "attn_prefix_flat.cuh"
+
+// ------------------------------------------------------------------ joining pieces
+// The pieces of the unit that begins in CTA blockIdx.x's range: 32 rows (blockIdx.y) and 8 columns
+// (blockIdx.z) a block, a lane per row; the four warps take every fourth piece each, and their sums
+// are added in order, so the result does not depend on the order in which the pieces ended.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefixParams p) {
+  __shared__ float top[4][32];
+  __shared__ float sums[4][9][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 cut = __ldcg(p.cuts + blockIdx.x);   // unit, pieces, k/v head, first row
+  const int S = cut.y, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 32 + lane, c8 = blockIdx.z;
+  if (S == 0 || cut.w + static_cast<int>(blockIdx.y) * 32 >= p.rows) return;
+  const int R = p.row_tile > BM ? p.row_tile : BM;
+  auto part = [&](int k) { return part_of<D>(p, blockIdx.x + k, k == 0 ? 1 : 0, R); };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int k = warp; k < S; k += 4) m = fmaxf(m, __ldcg(part(k) + D * R + row));
+  top[warp][lane] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(top[0][lane], top[1][lane]), fmaxf(top[2][lane], top[3][lane]));
+  float x[9];
+#pragma unroll
+  for (int i = 0; i < 9; ++i) x[i] = 0.f;
+#pragma unroll 4
+  for (int k = warp; k < S; k += 4) {
+    const float *q = part(k);
+    const float mk = __ldcg(q + D * R + row), l = __ldcg(q + (D + 1) * R + row);
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8) * R + row);
+    const float4 b = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8 + 1) * R + row);
+    const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - m);
+    x[0] = fmaf(f, a.x, x[0]);
+    x[1] = fmaf(f, a.y, x[1]);
+    x[2] = fmaf(f, a.z, x[2]);
+    x[3] = fmaf(f, a.w, x[3]);
+    x[4] = fmaf(f, b.x, x[4]);
+    x[5] = fmaf(f, b.y, x[5]);
+    x[6] = fmaf(f, b.z, x[6]);
+    x[7] = fmaf(f, b.w, x[7]);
+    x[8] = fmaf(f, l, x[8]);
+  }
+#pragma unroll
+  for (int i = 0; i < 9; ++i) sums[warp][i][lane] = x[i];
+  __syncthreads();
+  if (warp != 0 || row >= p.row_tile) return;
+  uint16_t *dst = out_row(p, cut.z, cut.w + row, D);
+  if (!dst) return;
+#pragma unroll
+  for (int i = 0; i < 9; ++i) x[i] = (sums[0][i][lane] + sums[1][i][lane]) + (sums[2][i][lane] + sums[3][i][lane]);
+  const float f = x[8] == 0.f ? 0.f : 1.f / x[8];
+  reinterpret_cast<uint4 *>(dst)[c8] =
+      make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f), pack_bf16x2(x[4] * f, x[5] * f),
+                 pack_bf16x2(x[6] * f, x[7] * f));
+}
+
+template <int D>
+cudaError_t launch_flat(const PrefixParams &p, int grid, cudaStream_t s) {
+  using C = FlatCfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(prefix_flat_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  prefix_flat_kernel<D><<<grid, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_join(const PrefixParams &p, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, ((p.row_tile < p.rows ? p.row_tile : p.rows) + 31) / 32, D / 8);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+}
+
+}  // namespace
+
+int prefix_part_floats(int d, int rows) { return (d + 2) * (rows > BM ? rows : BM); }
+
+cudaError_t launch_prefix_flat(const PrefixParams &p, int d, int grid, cudaStream_t s) {
+  return d == 64 ? launch_flat<64>(p, grid, s) : launch_flat<128>(p, grid, s);
+}
+
+cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, cudaStream_t s) {
+  return d == 64 ? launch_join<64>(p, grid, s) : launch_join<128>(p, grid, s);
+}
+
+}  // namespace xs

@@ -1,0 +1,56 @@
+// Internal interface between the shared-prefix attention entry points (prefix_api.cu) and
+// their kernels (attn_prefix.cu).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "cache.h"
+#include "internal.h"
+
+namespace xs {
+
+// Batch entries of one launch: their places among the packed own keys lie in shared memory.
+constexpr int kPrefixEntries = 256;
+// What a unit costs beside its KV tiles (its queries' loads and its epilogue), in tiles. In the
+// split schedule a unit takes so many places more than it has tiles.
+constexpr int kPrefixCost = 2;
+
+struct PrefixParams {
+  // Keys and values that lie in tensors: the prefix [Hk][Np][d], the own ones [B][Hk][Nk][d], any
+  // strides: maps {d, rows, heads, batch} with boxes of 64 columns and 128 rows (prefix) or
+  // `grain` rows (own), 128-byte swizzle. The tall kernel's queries: boxes of 8 rows.
+  CUtensorMap tm_q, tm_pk, tm_pv, tm_k, tm_v;
+  // Those that lie in the cache.
+  PageLists prefix_pages, own_pages;
+  const uint8_t *codes[2], *scales[2];   // of k and v
+  int prefix_cached, own_cached;
+  const uint16_t *q;                     // [B][H][Nq][d], strides in elements
+  long long q_b, q_h, q_n;
+  void *shards[kMaxShards];              // shard_mode 1: [all batches][Nq/P][H][d] each
+  uint16_t *o;                           // shard_mode 0: strides in elements
+  long long o_b, o_h, o_n;
+  int shard_mode, rows_per_shard;
+  const int *kv_len;                     // [B] or null: Nk keys everywhere
+  int b0, B;                             // the launch's batch entries; q, o, kv_len and the own pages begin at b0
+  int H, Hk, group, Nq, Np, Nk;          // group: query heads per k/v head
+  // Rows of one k/v head: (entry, head of the group, query), queries padded to nq_rows.
+  int nq_rows, entry_rows, rows;         // entry_rows = group * nq_rows, rows = B * entry_rows
+  int row_tile, n_tiles, n_units;        // rows of a unit; units of a head, of all
+  int copies;                            // flat kernel: copies of a unit's rows in its 128 lanes
+  int grain;                             // own keys of an entry begin at multiples of this among the packed ones
+  int n_prefix;                          // 128-key tiles of the prefix
+  int split, waves, min_places;          // see PrefixWalk
+  float scale_log2;
+  float *parts;                          // split: [grid][2 slots] partial results
+  int4 *cuts;                            // split: the unit that begins in CTA c's range and does not end there
+  int *status;
+  unsigned long long wait_limit_ns;
+};
+
+int prefix_part_floats(int d, int rows);   // fp32 values of one piece's partial result
+// Few rows for each k/v head: one 128-lane tile of rows at a time, two KV tiles in turn.
+cudaError_t launch_prefix_flat(const PrefixParams &p, int d, int grid, cudaStream_t s);
+// Joins the pieces of cut units, after a launch that had split set.
+cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, cudaStream_t s);
+
+}  // namespace xs

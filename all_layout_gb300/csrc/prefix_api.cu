@@ -1,0 +1,237 @@
+// C-ABI entry points of shared-prefix attention (declared in include/xs.h): argument
+// validation, tensor maps, the schedule's plan and the launches. Host code only.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/xs.h"
+#include "prefix.h"
+
+#define XS_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace xs;
+
+constexpr int kMostLength = 1 << 30;
+constexpr unsigned long long kCutsBytes = 4096;   // one int4 for each CTA, at most 256 of them
+
+bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// A tensor's strides over more than one row: at least d, and aligned.
+bool strides_apart(const long long *stride, const long long *extent, int n, int d) {
+  for (int i = 0; i < n; ++i)
+    if (extent[i] > 1 && stride[i] < d) return false;
+  return true;
+}
+bool strides_aligned(const long long *stride, const long long *extent, int n) {
+  for (int i = 0; i < n; ++i)
+    if (extent[i] > 1 && (stride[i] % 8 != 0 || stride[i] >= (1LL << 38))) return false;
+  return true;
+}
+
+// [batch][heads][rows][d] with strides (batch, head, row) as a map {d, rows, heads, batch}.
+bool encode_operand(CUtensorMap *m, const void *base, long long B, int H, int N, int d, long long sb, long long sh,
+                    long long sn, unsigned box_rows) {
+  const unsigned long long dims[4] = {static_cast<unsigned long long>(d), static_cast<unsigned long long>(N),
+                                      static_cast<unsigned long long>(H), static_cast<unsigned long long>(B)};
+  unsigned long long st[3] = {static_cast<unsigned long long>(sn) * 2, static_cast<unsigned long long>(sh) * 2,
+                              static_cast<unsigned long long>(sb) * 2};
+  for (int i = 0; i < 3; ++i)
+    if (dims[i + 1] == 1) st[i] = static_cast<unsigned long long>(d) * 2;
+  const unsigned box[4] = {64, box_rows, 1, 1};
+  return encode_map(m, base, 4, dims, st, box);
+}
+
+// Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split schedule,
+// whichever should end earlier; costs in KV tiles.
+struct Plan {
+  int split, waves, grid;
+};
+Plan plan(long long units, int sms, long long tiles, int least, unsigned long long per_cta, unsigned long long room) {
+  const int grid0 = units < sms ? static_cast<int>(units) : sms;
+  const long long unit = tiles + kPrefixCost, rounds = (units + grid0 - 1) / grid0;
+  const Plan whole{0, 0, grid0};
+  if (tiles < 2 || static_cast<unsigned long long>(sms) * sizeof(int4) > kCutsBytes) return whole;
+  const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
+  const long long left = units - static_cast<long long>(waves) * sms;
+  long long per = (left * unit + sms - 1) / sms;
+  int grid = sms;
+  if (waves == 0) {
+    if (per < least) per = least;
+    grid = static_cast<int>((left * unit + per - 1) / per);
+  }
+  if (per_cta * grid > room) return whole;
+  constexpr int kJoin = 6;   // what pieces and the launch that joins them cost
+  return waves * unit + per + kJoin < rounds * unit ? Plan{1, waves, grid} : whole;
+}
+
+xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_stride, void *const *shards, int P,
+                      void *ws, unsigned long long ws_bytes, void *stream) {
+  if (!a || !a->q) return XS_ERR_INVALID;
+  const int B = a->B, H = a->H, Hk = a->H_kv, Nq = a->Nq, Np = a->Np, Nk = a->Nk, d = a->d;
+  if (B < 0 || H < 0 || Hk < 0 || Nq < 0 || Np < 0 || Nk < 0) return XS_ERR_INVALID;
+  if (H > 0 && (Hk < 1 || H % Hk != 0)) return XS_ERR_INVALID;
+  if (!(a->scale > 0.f) || std::isinf(a->scale)) return XS_ERR_INVALID;
+  const bool prefix_cached = Np > 0 && !a->prefix_k, own_cached = Nk > 0 && !a->k;
+  if (Np > 0 && a->prefix_k && !a->prefix_v) return XS_ERR_INVALID;
+  if (Nk > 0 && a->k && !a->v) return XS_ERR_INVALID;
+  xs_status st = XS_OK;
+  if (prefix_cached || own_cached) {
+    st = check_cache(&a->cache);
+    if (st == XS_ERR_INVALID) return st;
+    if (a->cache.H_kv != Hk || a->cache.d != d) return XS_ERR_INVALID;
+    if ((prefix_cached && check_pages(&a->prefix_pages, 1) == XS_ERR_INVALID) ||
+        (own_cached && check_pages(&a->pages, B) == XS_ERR_INVALID))
+      return XS_ERR_INVALID;
+  }
+  if (shards) {
+    if (P < 1 || P > kMaxShards || Nq % P != 0) return XS_ERR_INVALID;
+    for (int p = 0; p < P; ++p)
+      if (!shards[p]) return XS_ERR_INVALID;
+  } else if (!o || !o_stride) {
+    return XS_ERR_INVALID;
+  }
+  if (!ws && ws_bytes != 0) return XS_ERR_INVALID;
+  const bool empty = B == 0 || H == 0 || Nq == 0;
+  const long long q_extent[3] = {B, H, Nq}, k_extent[3] = {B, Hk, Nk}, p_extent[2] = {Hk, Np};
+  const bool dense_prefix = Np > 0 && !prefix_cached, dense_own = Nk > 0 && !own_cached;
+  if (!empty) {
+    if (!strides_apart(a->q_stride, q_extent, 3, d) || (!shards && !strides_apart(o_stride, q_extent, 3, d)) ||
+        (dense_prefix && (!strides_apart(a->prefix_k_stride, p_extent, 2, d) ||
+                          !strides_apart(a->prefix_v_stride, p_extent, 2, d))) ||
+        (dense_own && (!strides_apart(a->k_stride, k_extent, 3, d) || !strides_apart(a->v_stride, k_extent, 3, d))))
+      return XS_ERR_INVALID;
+  }
+  if (st == XS_ERR_UNSUPPORTED || (d != 64 && d != 128)) return XS_ERR_UNSUPPORTED;
+  if (Np > kMostLength || Nk > kMostLength || Nq > kMostLength) return XS_ERR_UNSUPPORTED;
+  // Entries of a launch: as many as the kernel's table holds, and as their packed keys stay below 2^30 for.
+  constexpr int grain = 16;
+  const long long padded = (static_cast<long long>(Nk) + grain - 1) / grain * grain;
+  int chunk = kPrefixEntries;
+  if (padded > 0 && kMostLength / padded < chunk) chunk = static_cast<int>(kMostLength / padded);
+  if (chunk < 1) chunk = 1;
+  if (chunk > B) chunk = B;
+  const int group = H > 0 ? H / Hk : 1;
+  if (!empty && (static_cast<double>(chunk) * group * Nq > 2147483647.0 - 256 ||
+                 (static_cast<double>(chunk) * group * Nq / 32 + 1) * Hk > 2147483647.0))
+    return XS_ERR_UNSUPPORTED;
+  if (st != XS_OK || !aligned(a->q, 16) || !aligned(a->prefix_k, 16) || !aligned(a->prefix_v, 16) ||
+      !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(o, 16) || !aligned(a->kv_len, 4) || !aligned(ws, 256) ||
+      (prefix_cached && !aligned(a->prefix_pages.pages, 4)) || (own_cached && !aligned(a->pages.pages, 4)))
+    return XS_ERR_ALIGN;
+  if (shards)
+    for (int p = 0; p < P; ++p)
+      if (!aligned(shards[p], 16)) return XS_ERR_ALIGN;
+  if (empty) return XS_OK;
+  if (!strides_aligned(a->q_stride, q_extent, 3) || (!shards && !strides_aligned(o_stride, q_extent, 3)) ||
+      (dense_prefix && (!strides_aligned(a->prefix_k_stride, p_extent, 2) ||
+                        !strides_aligned(a->prefix_v_stride, p_extent, 2))) ||
+      (dense_own && (!strides_aligned(a->k_stride, k_extent, 3) || !strides_aligned(a->v_stride, k_extent, 3))))
+    return XS_ERR_ALIGN;
+  PrefixParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (shards) {
+    for (int i = 0; i < P; ++i) p.shards[i] = shards[i];
+    p.shard_mode = 1;
+    p.rows_per_shard = Nq / P;
+  } else {
+    p.o_b = o_stride[0];
+    p.o_h = o_stride[1];
+    p.o_n = o_stride[2];
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return XS_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  p.H = H;
+  p.Hk = Hk;
+  p.group = group;
+  p.Nq = Nq;
+  p.Np = Np;
+  p.Nk = Nk;
+  p.q_b = a->q_stride[0];
+  p.q_h = a->q_stride[1];
+  p.q_n = a->q_stride[2];
+  p.prefix_cached = prefix_cached;
+  p.own_cached = own_cached;
+  if (prefix_cached || own_cached) {
+    p.prefix_pages = lists_of(a->cache, &a->prefix_pages);
+    p.own_pages = lists_of(a->cache, &a->pages);
+    p.codes[0] = static_cast<const uint8_t *>(a->cache.k);
+    p.codes[1] = static_cast<const uint8_t *>(a->cache.v);
+    p.scales[0] = a->cache.k_scale;
+    p.scales[1] = a->cache.v_scale;
+  }
+  if (dense_prefix &&
+      (!encode_operand(&p.tm_pk, a->prefix_k, 1, Hk, Np, d, 0, a->prefix_k_stride[0], a->prefix_k_stride[1], kTileRows) ||
+       !encode_operand(&p.tm_pv, a->prefix_v, 1, Hk, Np, d, 0, a->prefix_v_stride[0], a->prefix_v_stride[1], kTileRows)))
+    return XS_ERR_CUDA;
+  if (dense_own &&
+      (!encode_operand(&p.tm_k, a->k, B, Hk, Nk, d, a->k_stride[0], a->k_stride[1], a->k_stride[2], grain) ||
+       !encode_operand(&p.tm_v, a->v, B, Hk, Nk, d, a->v_stride[0], a->v_stride[1], a->v_stride[2], grain)))
+    return XS_ERR_CUDA;
+  p.grain = grain;
+  p.n_prefix = (Np + kTileRows - 1) / kTileRows;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
+  if (device_status_word(&p.status) != cudaSuccess) return XS_ERR_CUDA;
+  p.wait_limit_ns = wait_limit_ns();
+  unsigned long long room = 0;
+  if (ws && ws_bytes > kCutsBytes) {
+    room = ws_bytes - kCutsBytes;
+    p.cuts = static_cast<int4 *>(ws);
+    p.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + kCutsBytes);
+  }
+  for (int b0 = 0; b0 < B; b0 += chunk) {
+    p.b0 = b0;
+    p.B = B - b0 < chunk ? B - b0 : chunk;
+    p.q = static_cast<const uint16_t *>(a->q) + b0 * a->q_stride[0];
+    if (!shards) p.o = static_cast<uint16_t *>(o) + b0 * o_stride[0];
+    p.kv_len = a->kv_len ? a->kv_len + b0 : nullptr;
+    if (own_cached) p.own_pages.pages = a->pages.pages + b0 * a->pages.stride;
+    p.nq_rows = Nq;
+    p.entry_rows = group * Nq;
+    p.rows = p.B * p.entry_rows;
+    p.copies = p.rows <= 32 ? 4 : p.rows <= 64 ? 2 : 1;
+    p.row_tile = kTileRows / p.copies;
+    p.n_tiles = (p.rows + p.row_tile - 1) / p.row_tile;
+    p.n_units = Hk * p.n_tiles;
+    // Own tiles of a unit: those of the entries that its rows belong to.
+    const long long entries = p.entry_rows >= p.row_tile ? 1 : (p.row_tile < p.rows ? p.row_tile : p.rows) / p.entry_rows;
+    const long long keys = entries * padded, tiles = p.n_prefix + (keys - (a->kv_len ? keys / 4 : 0) + kTileRows - 1) / kTileRows;
+    p.min_places = 4;
+    const Plan pl = plan(p.n_units, sms, tiles, p.min_places, 2ull * prefix_part_floats(d, kTileRows) * 4, room);
+    p.split = pl.split;
+    p.waves = pl.waves;
+    if (launch_prefix_flat(p, d, pl.grid, s) != cudaSuccess) return XS_ERR_CUDA;
+    if (pl.split && launch_prefix_join(p, d, pl.grid, s) != cudaSuccess) return XS_ERR_CUDA;
+  }
+  return XS_OK;
+}
+
+}  // namespace
+
+XS_API xs_status xs_prefix_attn(const xs_prefix_args *args, void *o, const long long *o_stride, void *ws,
+                                unsigned long long ws_bytes, void *stream) {
+  return prefix_call(args, o, o_stride, nullptr, 0, ws, ws_bytes, stream);
+}
+
+XS_API xs_status xs_prefix_attn_fused(const xs_prefix_args *args, void *const *out_shards, int P, void *ws,
+                                      unsigned long long ws_bytes, void *stream) {
+  if (!out_shards) return XS_ERR_INVALID;
+  return prefix_call(args, nullptr, nullptr, out_shards, P, ws, ws_bytes, stream);
+}
+
+XS_API xs_status xs_prefix_workspace_bytes(int B, int H, int H_kv, int Nq, int Np, int Nk, int d,
+                                           unsigned long long *bytes) {
+  if (!bytes || B < 0 || H < 0 || H_kv < 0 || Nq < 0 || Np < 0 || Nk < 0) return XS_ERR_INVALID;
+  if (H > 0 && (H_kv < 1 || H % H_kv != 0)) return XS_ERR_INVALID;
+  if (d != 64 && d != 128) return XS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (B == 0 || H == 0 || Nq == 0) return XS_OK;
+  const int sms = sm_count();
+  if (sms <= 0) return XS_ERR_CUDA;
+  *bytes = kCutsBytes + 2ull * sms * prefix_part_floats(d, kTileRows) * 4;
+  return XS_OK;
+}

@@ -12,6 +12,7 @@ import functools
 import os
 import re
 import struct
+from typing import NamedTuple
 
 import torch
 
@@ -84,6 +85,21 @@ _lib.xs_diff_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, ctypes.POINTER(
 for _f in ("xs_diff_attn", "xs_diff_attn_fused", "xs_diff_workspace_bytes"):
     getattr(_lib, _f).restype = _i
 _STRIDES = struct.Struct("@3q")
+
+# struct xs_pages: pages, stride, count. struct xs_cache: k, v, k_scale, v_scale, n_pages, H_kv,
+# page_size, d. struct xs_prefix_args: q, prefix_k, prefix_v, k, v, kv_len, the strides of q (3),
+# prefix_k, prefix_v (2 each), k, v (3 each), prefix_pages, pages, cache, scale, B, H, H_kv, Nq, Np,
+# Nk, d.
+_PAGES = struct.Struct("@Pqi0q")
+_CACHE = struct.Struct("@4P4i0q")
+_PREFIX_ARGS = struct.Struct("@6P13qPqi0qPqi0q4P4if7i0q")
+_lib.xs_cache_write.argtypes = [_vp] * 8 + [_i, _i, _i, _vp]
+_lib.xs_cache_read.argtypes = [_vp] * 8 + [_i, _i, _i, _vp]
+_lib.xs_prefix_attn.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_ulonglong, _vp]
+_lib.xs_prefix_attn_fused.argtypes = [_vp, _vp, _i, _vp, ctypes.c_ulonglong, _vp]
+_lib.xs_prefix_workspace_bytes.argtypes = [_i] * 7 + [ctypes.POINTER(ctypes.c_ulonglong)]
+for _f in ("xs_cache_write", "xs_cache_read", "xs_prefix_attn", "xs_prefix_attn_fused", "xs_prefix_workspace_bytes"):
+    getattr(_lib, _f).restype = _i
 
 
 def library():
@@ -380,6 +396,180 @@ def alloc_diff_workspace(B: int, H: int, Nq: int, Nk: int, d: int, norm: bool = 
         _check(_lib.xs_diff_workspace_bytes(B, H, Nq, Nk, d, 1 if norm else 0, ctypes.byref(n)),
                "xs_diff_workspace_bytes")
         return torch.zeros(int(n.value), dtype=torch.uint8, device=device)
+
+
+class KVCache(NamedTuple):
+    """A quantised key/value cache (see xs_cache in xs.h): k, v float8_e4m3fn [n_pages, H_kv,
+    page_size, d]; k_scale, v_scale uint8 [n_pages, H_kv, page_size], a row's scale being
+    2**(byte - 127). All contiguous, on one device."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def alloc_cache(n_pages: int, H_kv: int, page_size: int, d: int, device="cuda") -> KVCache:
+    """A cache of zeros (through torch). page_size: a power of two from 16 to 1024."""
+    codes = [torch.zeros((n_pages, H_kv, page_size, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    return KVCache(*codes, *(torch.full((n_pages, H_kv, page_size), 127, dtype=torch.uint8, device=device)
+                             for _ in range(2)))
+
+
+def _cache_fields(cache, index):
+    """Fields of struct xs_cache of a checked cache."""
+    k, v, ks, vs = cache
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("cache.k must be a CUDA tensor [n_pages, H_kv, page_size, d]")
+    shape = k.shape
+    for name, t, dtype, want in (("k", k, torch.float8_e4m3fn, shape), ("v", v, torch.float8_e4m3fn, shape),
+                                 ("k_scale", ks, torch.uint8, shape[:3]), ("v_scale", vs, torch.uint8, shape[:3])):
+        _operand("cache." + name, t, dtype, want, index)
+        if not t.is_contiguous():
+            raise ValueError(f"cache.{name} must be contiguous")
+    return (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), *shape)
+
+
+def _page_list(name, pages, B, index):
+    """Fields of struct xs_pages: [n] (one list for all) or [B, n] int32."""
+    if not isinstance(pages, torch.Tensor) or pages.dim() not in (1, 2):
+        raise ValueError(f"{name} must be [n] or [B, n]")
+    n = pages.shape[-1]
+    st = _operand(name, pages, torch.int32, (n,) if pages.dim() == 1 else (B, n), index)
+    if st[-1] != 1 and n > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return pages.data_ptr() if pages.numel() else 0, st[0] if pages.dim() == 2 and B > 1 else 0, n
+
+
+def _cache_rows(call, what, k, v, cache, pages, start, lens, stream):
+    _require(isinstance(k, torch.Tensor) and k.is_cuda and k.dim() == 4, "k must be a CUDA tensor [B, H_kv, N, d]")
+    B, H, N, d = k.shape
+    dev, dtype = k.get_device(), k.dtype
+    _require(dtype in _TYPES, "k and v must be bf16, fp16 or fp32")
+    ks, vs = k.stride(), _operand("v", v, dtype, k.shape, dev)
+    if (ks[3] != 1 or vs[3] != 1) and d > 1:
+        raise ValueError("the last dimension of k and v must be contiguous")
+    fields = _cache_fields(cache, dev)
+    if fields[5] != H or fields[7] != d:
+        raise ValueError(f"the cache holds {fields[5]} heads of {fields[7]} columns, k {H} of {d}")
+    packed, lists = _CACHE.pack(*fields), _PAGES.pack(*_page_list("pages", pages, B, dev))
+    start, lens = _vector("start", start, torch.int32, B, dev), _vector("lens", lens, torch.int32, B, dev)
+    if k.numel() == 0:
+        return
+    _check(_on(dev, stream, call, packed, k.data_ptr(), v.data_ptr(), _STRIDES.pack(*ks[:3]), _STRIDES.pack(*vs[:3]),
+               lists, start, lens, B, N, _TYPES[dtype]), what)
+
+
+def cache_write(k, v, cache, pages, *, start=None, lens=None, stream=None):
+    """Quantises rows into a cache (see xs_cache_write in xs.h). k, v: [B, H_kv, N, d] views of any
+    strides, d contiguous (bf16, fp16 or fp32; a projection's [B, N, H_kv, d] transposed, too).
+    Token n of request b goes to place start[b] + n of its pages: place i is row i % page_size of
+    page pages[b, i // page_size]. pages: int32 [B, n], or [n] for one list; start, lens: int32 [B]
+    or None (0; every token). Tokens from lens[b] on, and those without a page, are not stored."""
+    _cache_rows(_lib.xs_cache_write, "xs_cache_write", k, v, cache, pages, start, lens, stream)
+
+
+def cache_read(cache, pages, k, v, *, start=None, lens=None, stream=None):
+    """The values that places start[b] + n of a cache stand for, into k and v [B, H_kv, N, d] (see
+    xs_cache_read in xs.h; arguments as in cache_write). Tokens from lens[b] on are left as they
+    were, those without a page become NaN."""
+    _cache_rows(_lib.xs_cache_read, "xs_cache_read", k, v, cache, pages, start, lens, stream)
+
+
+def _prefix_args(q, prefix_k, prefix_v, k, v, kv_len, cache, prefix_pages, prefix_len, pages, max_len, scale):
+    """(struct xs_prefix_args, B, H, Nq, d, device index) of checked operands."""
+    _require(isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 4, "q must be a CUDA tensor [B, H, Nq, d]")
+    B, H, Nq, d = q.shape
+    dev, bf16 = q.get_device(), torch.bfloat16
+    qs = _operand("q", q, bf16, q.shape, dev)
+    Hk = Np = Nk = 0
+    fields, lists, own_lists = (0,) * 8, (0, 0, 0), (0, 0, 0)
+    pointers, ps, ks = [0, 0, 0, 0], (0, 0, 0, 0), (0,) * 6
+    contiguous = qs[3] == 1
+    if cache is not None:
+        fields = _cache_fields(cache, dev)
+        Hk = fields[5]
+    if prefix_k is not None:
+        _require(isinstance(prefix_k, torch.Tensor) and prefix_k.dim() == 3, "prefix_k must be [H_kv, Np, d]")
+        _require(prefix_pages is None and prefix_len is None, "the prefix lies in prefix_k and prefix_v or in prefix_pages")
+        Hk, Np = Hk or prefix_k.shape[0], prefix_k.shape[1]
+        a, b = (_operand(n, t, bf16, (Hk, Np, d), dev) for n, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v)))
+        pointers[:2] = prefix_k.data_ptr(), prefix_v.data_ptr()
+        ps, contiguous = a[:2] + b[:2], contiguous and a[2] == 1 and b[2] == 1
+    elif prefix_pages is not None:
+        _require(cache is not None, "prefix_pages needs a cache")
+        _require(prefix_pages.dim() == 1, "prefix_pages must be [n]")
+        lists = _page_list("prefix_pages", prefix_pages, 1, dev)
+        Np = lists[2] * fields[6] if prefix_len is None else prefix_len
+        _require(0 <= Np <= lists[2] * fields[6], f"prefix_pages hold {lists[2] * fields[6]} keys, not {prefix_len}")
+    if k is not None:
+        _require(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be a CUDA tensor [B, H_kv, Nk, d]")
+        _require(pages is None and max_len is None, "the own keys lie in k and v or in pages")
+        Hk, Nk = Hk or k.shape[1], k.shape[2]
+        a, b = (_operand(n, t, bf16, (B, Hk, Nk, d), dev) for n, t in (("k", k), ("v", v)))
+        pointers[2:] = k.data_ptr(), v.data_ptr()
+        ks, contiguous = a[:3] + b[:3], contiguous and a[3] == 1 and b[3] == 1
+    elif pages is not None:
+        _require(cache is not None, "pages needs a cache")
+        own_lists = _page_list("pages", pages, B, dev)
+        Nk = own_lists[2] * fields[6] if max_len is None else max_len
+        _require(0 <= Nk <= own_lists[2] * fields[6], f"pages hold {own_lists[2] * fields[6]} keys, not {max_len}")
+    if not contiguous and d > 1:
+        raise ValueError("the last dimension of q, prefix_k, prefix_v, k and v must be contiguous")
+    packed = _PREFIX_ARGS.pack(q.data_ptr(), *(p if n else 0 for p, n in zip(pointers, (Np, Np, Nk, Nk))),
+                               _vector("kv_len", kv_len, torch.int32, B, dev), *qs[:3], *ps, *ks, *lists, *own_lists,
+                               *fields, max(d, 1) ** -0.5 if scale is None else scale, B, H, Hk or H, Nq, Np, Nk, d)
+    return packed, B, H, Nq, d, dev
+
+
+def prefix_attn(q, o, *, prefix_k=None, prefix_v=None, k=None, v=None, kv_len=None, cache=None, prefix_pages=None,
+                prefix_len=None, pages=None, max_len=None, scale=None, workspace=None, stream=None):
+    """Attention of a batch of requests that share a prefix, into o (see xs_prefix_attn in xs.h).
+    q, o: [B, H, Nq, d]. The prefix's keys and values: prefix_k, prefix_v [H_kv, Np, d], or the first
+    prefix_len places of prefix_pages (int32 [n]) of `cache`. The requests' own ones: k, v
+    [B, H_kv, Nk, d], or the first max_len places of pages (int32 [B, n]) of `cache`; of both the
+    first kv_len[b] count (int32 [B], or None: all). Tensors are bf16 views of any strides, d
+    contiguous (64 or 128). scale: of the scores, 1/sqrt(d) if None; workspace: from
+    alloc_prefix_workspace, or None. o must not overlap an input."""
+    packed, B, H, Nq, d, dev = _prefix_args(q, prefix_k, prefix_v, k, v, kv_len, cache, prefix_pages, prefix_len,
+                                            pages, max_len, scale)
+    os_ = _operand("o", o, torch.bfloat16, q.shape, dev)
+    if os_[3] != 1 and d > 1:
+        raise ValueError("the last dimension of o must be contiguous")
+    if o.numel() == 0:
+        return
+    ws, n = _diff_workspace(workspace, dev)
+    _check(_on(dev, stream, _lib.xs_prefix_attn, packed, o.data_ptr(), _STRIDES.pack(*os_[:3]), ws, n), "xs_prefix_attn")
+
+
+def prefix_attn_fused(q, shards, *, prefix_k=None, prefix_v=None, k=None, v=None, kv_len=None, cache=None,
+                      prefix_pages=None, prefix_len=None, pages=None, max_len=None, scale=None, workspace=None,
+                      stream=None):
+    """prefix_attn with the fused shard layout: shards are P tensors [B, Nq/P, H, d] bf16
+    (alloc_shards), as in attn_fused."""
+    packed, B, H, Nq, d, dev = _prefix_args(q, prefix_k, prefix_v, k, v, kv_len, cache, prefix_pages, prefix_len,
+                                            pages, max_len, scale)
+    P = len(shards)
+    _require(1 <= P <= MAX_SHARDS and Nq % P == 0, f"1 to {MAX_SHARDS} shards that divide Nq = {Nq} are needed, not {P}")
+    pointers = []
+    for s in shards:
+        _operand("shards", s, torch.bfloat16, (B, Nq // P, H, d), dev)
+        _require(s.is_contiguous(), "shards must be contiguous")
+        pointers.append(s.data_ptr())
+    if q.numel() == 0:
+        return
+    ws, n = _diff_workspace(workspace, dev)
+    _check(_on(dev, stream, _lib.xs_prefix_attn_fused, packed, (ctypes.c_void_p * P)(*pointers), P, ws, n),
+           "xs_prefix_attn_fused")
+
+
+def alloc_prefix_workspace(B: int, H: int, H_kv: int, Nq: int, Np: int, Nk: int, d: int, device="cuda"):
+    """A workspace (through torch) with which prefix_attn and prefix_attn_fused of this shape can take
+    every schedule; larger shapes' workspaces serve smaller ones."""
+    n = ctypes.c_ulonglong(0)
+    with torch.cuda.device(device):
+        _check(_lib.xs_prefix_workspace_bytes(B, H, H_kv, Nq, Np, Nk, d, ctypes.byref(n)), "xs_prefix_workspace_bytes")
+        return torch.empty(int(n.value), dtype=torch.uint8, device=device)
 
 
 def store_burst_probe(dst, K, burst_bytes, n_bursts, gap_ns, mode, times, stream=None):

@@ -379,6 +379,117 @@ xs_status xs_diff_attn_fused(const xs_diff_args *args, void *const *out_shards, 
 xs_status xs_diff_workspace_bytes(int B, int H, int Nq, int Nk, int d, int norm,
                                   unsigned long long *bytes);
 
+/* A quantised key/value cache: pages of rows (one token, one k/v head, d values) in
+ * e4m3, each row with a power of two as its scale. Row i of head h of a page is
+ * page * H_kv * page_size + h * page_size + i; its values are code * 2^(byte - 127),
+ * codes in k or v at row * d, the byte in k_scale or v_scale at row. A byte of 255
+ * makes the whole row NaN. The caller owns all four arrays (device). */
+typedef struct {
+  void *k, *v;                         /* [n_pages][H_kv][page_size][d] e4m3 */
+  unsigned char *k_scale, *v_scale;    /* [n_pages][H_kv][page_size] */
+  int n_pages, H_kv, page_size, d;     /* page_size: a power of two in [16, 1024] */
+} xs_cache;
+
+/* One list of pages for each request: place i of request b is row i % page_size of page
+ * pages[b * stride + i / page_size]. Lists may share pages. */
+typedef struct {
+  const int *pages;   /* device */
+  long long stride;   /* entries between requests; 0: one list for all */
+  int count;          /* entries of a list */
+} xs_pages;
+
+/* Quantises rows into a cache (this library's own addition: history that later steps of
+ * attention read, kept in half the memory of bf16). Token n < lens[b] of request b goes to
+ * place start[b] + n:
+ *     e = the least integer with max|x| <= 448 * 2^e, within [-120, 119] (0 for zeros),
+ *     codes = e4m3(x * 2^-e), to nearest even, at most 448; byte = e + 127.
+ * A row with a NaN or an infinity gets the byte 255. Nothing else of the cache changes:
+ * tokens from lens[b] on, and those whose place no page holds (negative, past the list, or
+ * a page that is not in [0, n_pages)), are not stored. Two tokens of one place in one call
+ * leave either's values.
+ *   k, v, strides   [B][H_kv][N][d] of in_type (device), rows of d contiguous values,
+ *                   strides in elements (batch, head, token)
+ *   start           [B] int32 (device), or NULL: 0
+ *   lens            [B] int32 (device), taken into [0, N], or NULL: N
+ * XS_ERR_INVALID for NULL cache, lists, k, v, strides or arrays of the cache (with
+ * pages), negative sizes or strides, page_size < 1 or an unknown type; XS_ERR_UNSUPPORTED
+ * for d not a multiple of 16 in [16, 256], a page_size that is not a power of two in
+ * [16, 1024] or H_kv * N >= 2^31; XS_ERR_ALIGN unless k, v and the cache's arrays are
+ * 16-byte aligned and every stride over more than one row is a multiple of 16 bytes.
+ * Empty problems return XS_OK. */
+xs_status xs_cache_write(const xs_cache *cache, const void *k, const void *v,
+                         const long long *k_stride, const long long *v_stride,
+                         const xs_pages *pages, const int *start, const int *lens, int B,
+                         int N, int in_type, void *stream);
+
+/* The rows that a cache stands for, back: arguments and refusals as xs_cache_write, with
+ * the outputs k and v of out_type (strides of at least d over more than one row). Values
+ * are exact in bf16 and fp32 and rounded to nearest even in fp16. Tokens from lens[b] on
+ * are left as they were; those whose place no page holds become NaN. Outputs must not
+ * overlap each other or the cache. */
+xs_status xs_cache_read(const xs_cache *cache, void *k, void *v, const long long *k_stride,
+                        const long long *v_stride, const xs_pages *pages, const int *start,
+                        const int *lens, int B, int N, int out_type, void *stream);
+
+/* Operands of attention over a shared prefix. The prefix's keys and values lie in tensors
+ * (prefix_k not NULL) or in the pages of `cache` that prefix_pages lists (one list); the
+ * requests' own ones in tensors (k not NULL) or in pages of the same cache. Tensors are
+ * bf16 (device), rows of d contiguous values, strides in elements. Head h reads k/v head
+ * h / (H / H_kv). */
+typedef struct {
+  const void *q;                        /* [B][H][Nq][d] */
+  const void *prefix_k, *prefix_v;      /* [H_kv][Np][d] */
+  const void *k, *v;                    /* [B][H_kv][Nk][d] */
+  const int *kv_len;                    /* [B] int32 (device), or NULL: Nk own keys everywhere */
+  long long q_stride[3];                /* batch, head, row; k and v alike */
+  long long prefix_k_stride[2], prefix_v_stride[2];   /* head, row */
+  long long k_stride[3], v_stride[3];
+  xs_pages prefix_pages, pages;
+  xs_cache cache;                       /* not looked at where nothing lies in it */
+  float scale;                          /* of the scores; 1/sqrt(d) is the usual one */
+  int B, H, H_kv, Nq, Np, Nk, d;        /* Np: keys of the prefix; Nk: own keys at most */
+} xs_prefix_args;
+
+/* Attention of a batch of requests that share a prefix (this library's own addition beside
+ * xs_attn: same element type and output layouts; several candidates of one prompt, guidance
+ * branches, continuations of one history):
+ *     o[b][h] = softmax(q[b][h] [K | K_b]^T * scale) [V | V_b]
+ * K, V the prefix's Np keys and values of the head, K_b, V_b the first kv_len[b] of the
+ * request's own (taken into [0, Nk]; what lies behind them is not used, NaN and infinity
+ * included), non-causal. The prefix's keys are read once for a whole tile of queries,
+ * whichever requests and heads of one k/v head they belong to. A request without any key
+ * gives zeros. fp32 accumulation and statistics, softmax weights rounded to bf16 for the
+ * product with v, output rounded to bf16; cached keys and values are exact in bf16. A cached
+ * key whose place no page holds counts as NaN. Outputs must not overlap each other or an
+ * input. Nq, Np, Nk: any size, also 0 or 1.
+ *   o, o_stride  [B][H][Nq][d] bf16 (device), strides in elements (batch, head, row)
+ *   out_shards   host array of P device pointers, shard p [B][Nq/P][H][d] bf16, as in
+ *                xs_attn_fused; the warps that finish a row store it in its shard
+ *   ws           caller-owned device memory, 256-byte aligned, of any content, or NULL. With
+ *                xs_prefix_workspace_bytes of it a launch may cut units into ranges of keys over
+ *                all SMs (few queries, a last wave that is not full); with less it takes whole
+ *                units. Calls that share one workspace must not overlap on the GPU.
+ * Results are the same from launch to launch on one GPU model; they differ in fp32
+ * rounding between workspace and none.
+ * XS_ERR_INVALID for NULL args, q, output or a NULL of a part that has keys; negative sizes;
+ * H not a multiple of H_kv; a cache whose H_kv or d differ; scale not positive and finite;
+ * P not in [1, 8], Nq % P != 0; a stride below d over more than one row; ws NULL with
+ * ws_bytes > 0. XS_ERR_UNSUPPORTED for d not in {64, 128}, a page_size as in xs_cache_write,
+ * a length past 2^30, or 2^31 and more rows of a k/v head or tiles of 128 of them.
+ * XS_ERR_ALIGN for a tensor that is not 16-byte aligned, strides over more than one row that
+ * are not multiples of 8, or a ws that is not 256-byte aligned. Empty problems return XS_OK. */
+xs_status xs_prefix_attn(const xs_prefix_args *args, void *o, const long long *o_stride,
+                         void *ws, unsigned long long ws_bytes, void *stream);
+xs_status xs_prefix_attn_fused(const xs_prefix_args *args, void *const *out_shards, int P,
+                               void *ws, unsigned long long ws_bytes, void *stream);
+
+/* *bytes = the workspace with which a call of this shape on the current device can take
+ * every schedule. XS_ERR_INVALID for a NULL bytes, negative sizes or H not a multiple of
+ * H_kv, XS_ERR_UNSUPPORTED for d not in {64, 128}, XS_ERR_CUDA if the device cannot be
+ * queried. */
+xs_status xs_prefix_workspace_bytes(int B, int H, int H_kv, int Nq, int Np, int Nk, int d,
+                                    unsigned long long *bytes);
+
 /* Static English text for a status code; never NULL. */
 const char *xs_status_string(xs_status s);
 
