@@ -24,6 +24,7 @@
 // control flow to its end without waiting, the others drain what they issued.
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/xs.h"
 #include "internal.h"

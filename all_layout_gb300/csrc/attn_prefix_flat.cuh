@@ -1,51 +1,51 @@
 // The flat kernel of shared-prefix attention (included by attn_prefix.cu): one tile of up to 128
 // rows at a time, for calls with few rows for each k/v head, where reading the keys is the bound.
 //
-// Two sets of Tensor Memory columns take the unit's KV tiles in turn (set t the tiles j = t mod 2
-// of the item, with its own running maximum, sum and O), so that one set's softmax runs beside
-// the other's matrix products; the epilogue joins them.
-//
 // Copies. The tensor cores always work on 128 rows. With 64 rows or fewer (or 32) the tile holds
 // the rows twice (four times), and each copy's softmax takes its half (quarter) of a KV tile's
 // keys, the weights of the others being zero: a tile's exponentials are then halved (quartered),
 // and the epilogue adds the copies' results, each with its own maximum and sum.
 //
 // Cached keys and values: the loader copies a tile's codes and scales into a ring of raw slots, and
-// four warps turn them into bf16 operands in the K and V rings. A code's bits moved to bf16's
+// four warps each turn K's and V's into bf16 operands in rings of their own. A code's bits moved to bf16's
 // place stand for code * 2^-120, so one product with 2^(120 + e) is exact (e > 7 takes two).
 //
-// Roles (512 threads of 128 registers):
-//   warps 0-3, 4-7  softmax of set 0 and 1, row r of the tile = TMEM lane r
-//   warps 8-11      queries to shared memory, codes to bf16, TMA loads of keys that are not cached
-//   warp 12         MMA issuer, Tensor Memory allocation
-//   warp 13         loads of codes and scales
-//   warps 14, 15    nothing
-// Tensor Memory: S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [256+d,256+2d); P_t over S_t's first 64.
-// The issuer's order is QK(i) after PV(i-2): both are set t's, so one thread's order keeps S_t(i)
-// from overwriting P_t(i-2) before its product, and the commit that signals S_t covers O_t.
+// Roles (448 threads, one CTA per SM):
+//   warps 0-3   softmax, row r of the tile = TMEM lane r
+//   warps 4-7   K: codes to bf16, TMA loads of tiles that are not cached
+//   warps 8-11  V, and the queries to Tensor Memory
+//   warp 12     MMA issuer, Tensor Memory allocation
+//   warp 13     loads of codes and scales
+// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) Q (bf16 pairs) [384,384+d/2); P_t over S_t's
+// first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax. The issuer's
+// order is QK(i), PV(i-1): QK(i) overwrites P(i-2), whose product went out before it.
+// Q is read from Tensor Memory because shared memory is what the SM has least of here: with cached
+// keys a tile's codes are written (256 cycles at d = 128) and read (256), its operands written (512)
+// and read (512), about as long as its 33 KB take from HBM at this SM's share of the bandwidth (1450).
 
 template <int D>
 struct FlatCfg {
-  static constexpr int THREADS = 512;
+  static constexpr int THREADS = 448;
   static constexpr int TILE = BN * D * 2, RAW = BN * D + BN;   // a bf16 tile; codes and scale bytes
-  static constexpr int KS = 2, VS = 2, FS = D == 128 ? 3 : 10;
-  static constexpr int OFF_K = TILE, OFF_V = OFF_K + KS * TILE, OFF_F = OFF_V + VS * TILE;
+  static constexpr int KS = 2, VS = 2, FK = D == 128 ? 3 : 5, FV = D == 128 ? 2 : 5, FS = FK + FV;
+  static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * TILE, OFF_F = OFF_V + VS * TILE;
   static constexpr int OFF_STG = OFF_F + FS * RAW;
-  static constexpr int OFF_FIN = OFF_STG + 2 * BM * 16 * 4;
+  static constexpr int OFF_FIN = OFF_STG + BM * 16 * 4;
   static constexpr int OFF_TAB = OFF_FIN + BM * 4;
   static constexpr int OFF_BAR = OFF_TAB + (kPrefixEntries + 4) * 4;
   static constexpr int SMEM = OFF_BAR + 512;
+  static constexpr uint32_t COL_O = 256, COL_Q = 384;
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(OFF_BAR % 16 == 0 && RAW % 16 == 0, "alignment");
 };
-constexpr int kFlatConvert = 8, kFlatMma = 12, kFlatLoad = 13;
+constexpr int kFlatKeys = 4, kFlatValues = 8, kFlatOperandWarps = 4, kFlatMma = 12, kFlatLoad = 13;   // warps
 
 struct FlatBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw[2];                   // V tiles whose rows behind a request's last key are still to be cleared
   uint64_t f_full[10], f_empty[10];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2], pv_done, o_full;
   uint64_t drain;
   PrefixPlan plan;
   uint32_t tmem_base;
@@ -88,40 +88,51 @@ __device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars
   using C = FlatCfg<D>;
   volatile int *abort_flag = &bars->abort;
   const int lane = threadIdx.x & 31;
-  uint32_t use = 0;
+  uint32_t use = 0, uses[2] = {0, 0};   // cached tiles so far; K and V slots filled
   PrefixWalk walk;
   walk.start(p, bars->plan);
   PrefixItem item;
   bool ok = true;
-  while (ok && walk.next(p, table, item)) {
-    for (int j = item.kv0; ok && j < item.kv1; ++j) {
-      if (!is_cached(p, j)) continue;
-      // This lane's rows of the tile: `rows` of them from `first` on, in `page` from row `at` on.
-      int first, rows = 0, page = -1, at = 0;
-      if (j < p.n_prefix) {
-        const int c = min(p.prefix_pages.page, BN), pos = j * BN + lane * c;
-        first = lane * c;
-        if (first < BN && pos < p.Np) {
-          rows = c;
-          page = page_of(p.prefix_pages, 0, pos);
-          at = pos & (p.prefix_pages.page - 1);
-        }
-      } else {
-        first = lane * 16;
-        if (first < BN) {
-          const Grain g = grain_of(p, table, item, own_pos(p, item, j) + first);
-          if (g.valid > 0) {
-            rows = 16;
-            page = page_of(p.own_pages, g.b, g.off);
-            at = g.off & (p.own_pages.page - 1);
-          }
+  // This lane's rows of a tile: `rows` of them from `first` on, in `page` from row `at` on.
+  struct Part {
+    int first, rows, page, at;
+  };
+  auto part_at = [&](int j) {
+    Part r{0, 0, -1, 0};
+    if (j >= item.kv1 || !is_cached(p, j)) return r;
+    if (j < p.n_prefix) {
+      const int c = min(p.prefix_pages.page, BN), pos = j * BN + lane * c;
+      r.first = lane * c;
+      if (r.first < BN && pos < p.Np) {
+        r.rows = c;
+        r.page = page_of(p.prefix_pages, 0, pos);
+        r.at = pos & (p.prefix_pages.page - 1);
+      }
+    } else {
+      r.first = lane * 16;
+      if (r.first < BN) {
+        const Grain g = grain_of(p, table, item, own_pos(p, item, j) + r.first);
+        if (g.valid > 0) {
+          r.rows = 16;
+          r.page = page_of(p.own_pages, g.b, g.off);
+          r.at = g.off & (p.own_pages.page - 1);
         }
       }
+    }
+    return r;
+  };
+  while (ok && walk.next(p, table, item)) {
+    Part ahead = part_at(item.kv0);
+    for (int j = item.kv0; ok && j < item.kv1; ++j) {
+      const Part r = ahead;
+      ahead = part_at(j + 1);   // (its page number is on its way while this tile's slots are waited for)
+      if (!is_cached(p, j)) continue;
+      const int first = r.first, rows = r.rows, page = r.page, at = r.at;
       const unsigned bytes = __reduce_add_sync(0xffffffffu, page >= 0 ? rows * (D + 1) : rows);
       const int psize = p.prefix_pages.page;   // one cache: all its pages have one size
       const long long row = (static_cast<long long>(page) * p.Hk + item.hk) * psize + at;
-      for (int kv = 0; ok && kv < 2; ++kv, ++use) {
-        const uint32_t slot = use % C::FS, ph = (use / C::FS) & 1;
+      for (int kv = 0; ok && kv < 2; ++kv) {   // K's and V's slots have a ring each
+        const uint32_t n = kv ? C::FV : C::FK, slot = (kv ? C::FK : 0) + use % n, ph = (use / n) & 1;
         ok = wait_for<true>(smem_u32(&bars->f_empty[slot]), ph ^ 1, abort_flag, p);
         if (!ok) break;
         const uint32_t full = smem_u32(&bars->f_full[slot]);
@@ -137,12 +148,16 @@ __device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars
           }
         }
         __syncwarp();
+        ++uses[kv];
       }
+      ++use;
     }
   }
   // Every load issued must land before the CTA releases its shared memory.
-  for (uint32_t s = 0; s < C::FS && s < use; ++s)
-    drain(smem_u32(&bars->f_full[s]), ((use - 1 - s) / C::FS) & 1);
+  for (uint32_t s = 0; s < C::FS; ++s) {
+    const uint32_t n = s < C::FK ? C::FK : C::FV, at = s < C::FK ? s : s - C::FK, last = uses[s < C::FK ? 0 : 1];
+    if (last > at) drain(smem_u32(&bars->f_full[s]), ((last - 1 - at) / n) & 1);
+  }
 }
 
 // ------------------------------------------------------------------ operands
@@ -155,43 +170,80 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t spread(uint32_t x) {
   return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
 }
-// Sixteen codes of a row with scale byte `byte` to bf16.
-__device__ __forceinline__ void to_bf16(const uint4 &c, int byte, uint4 (&out)[2]) {
+// Sixteen codes of a row with scale byte `byte` to bf16. PLAIN: the byte is at most 134.
+template <bool PLAIN>
+__device__ __forceinline__ void to_bf16(const uint4 &c, uint32_t byte, uint32_t (&r)[8]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t r[8];
   // 2^(120 + e) in bf16 for e = byte - 127 <= 7.
-  const uint32_t f = byte == kNanScale ? 0x7fffu : static_cast<uint32_t>(min(byte, 134) + 120) << 7;
-  const uint32_t f2 = f | f << 16;
+  uint32_t f = (PLAIN ? byte + 120u : min(byte, 134u) + 120u) << 7;
+  if (!PLAIN && byte == kNanScale) f = 0x7fffu;
+  const uint32_t f2 = __byte_perm(f, 0, 0x1010);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r[2 * i] = mul_bf16x2(spread(__byte_perm(w[i], 0, 0x1404)), f2);
     r[2 * i + 1] = mul_bf16x2(spread(__byte_perm(w[i], 0, 0x3424)), f2);
   }
-  if (byte > 134 && byte != kNanScale) {
-    const uint32_t g = static_cast<uint32_t>(byte - 134 + 127) << 7, g2 = g | g << 16;
+  if (!PLAIN && byte > 134 && byte != kNanScale) {
+    const uint32_t g2 = __byte_perm((byte - 134 + 127) << 7, 0, 0x1010);
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = mul_bf16x2(r[i], g2);
   }
-  out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  out[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
+// Codes and scale bytes of a raw slot to a bf16 tile, by four warps; `valid`: see valid_of. A thread has one
+// 16-byte group of every STEP-th row, so its place in the swizzle stays. One copy of short loops for K's and
+// V's warps: with all groups unrolled in each the warps waited for instructions.
 template <int D>
-__device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table) {
+__device__ __noinline__ void convert_tile(const uint8_t *src, uint8_t *dst, int valid) {
+  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR;   // groups of a row's codes
+  const uint32_t tid = threadIdx.x & 127, lane = tid & 31;
+  const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
+  const uint32_t bytes = *reinterpret_cast<const uint32_t *>(src + BN * D + lane * 4);
+  const uint8_t *scales = src + BN * D + row0;
+  src += tid * 16;
+  dst += (cc / 4) * kHalf + row0 * 128;
+  // (Of a group's two chunks the second half's lanes store the second one first, which spares conflicts.)
+  const uint32_t c0 = ((first + odd) ^ (row0 & 7)) * 16, c1 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
+  const bool clear = __any_sync(0xffffffffu, valid < 16);
+  if (!clear && !__any_sync(0xffffffffu, __vcmpgtu4(bytes, 0x86868686u) != 0)) {
+#pragma unroll 2
+    for (uint32_t i = 0; i < BN / STEP; ++i) {
+      uint32_t r[8];
+      to_bf16<true>(*reinterpret_cast<const uint4 *>(src + i * STEP * D), scales[i * STEP], r);
+      uint8_t *to = dst + i * STEP * 128;
+      *reinterpret_cast<uint4 *>(to + c0) = odd ? make_uint4(r[4], r[5], r[6], r[7]) : make_uint4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<uint4 *>(to + c1) = odd ? make_uint4(r[0], r[1], r[2], r[3]) : make_uint4(r[4], r[5], r[6], r[7]);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (uint32_t i = 0; i < BN / STEP; ++i) {
+    uint32_t r[8];
+    to_bf16<false>(*reinterpret_cast<const uint4 *>(src + i * STEP * D), scales[i * STEP], r);
+    const uint32_t row = row0 + i * STEP;
+    if (static_cast<int>(row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4))
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[k] = 0;
+    uint8_t *to = dst + i * STEP * 128;
+    *reinterpret_cast<uint4 *>(to + c0) = odd ? make_uint4(r[4], r[5], r[6], r[7]) : make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4 *>(to + c1) = odd ? make_uint4(r[0], r[1], r[2], r[3]) : make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+// The warps of K, or of V (which also bring the queries): each tile's operand, in order.
+template <int D, bool V>
+__device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem) {
   using C = FlatCfg<D>;
+  constexpr uint32_t S = V ? C::VS : C::KS, F = V ? C::FV : C::FK, F0 = V ? C::FK : 0;   // slots; raw slots, the first
   volatile int *abort_flag = &bars->abort;
-  const int tid = threadIdx.x - kFlatConvert * 32, lane = tid & 31;
+  const int tid = threadIdx.x & 127, lane = tid & 31;
   const bool issuer = tid < 32;
+  uint64_t *full_of = V ? bars->v_full : bars->k_full, *empty_of = V ? bars->v_empty : bars->k_empty;
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<true>(smem_u32(&bar), parity, abort_flag, p); };
-  auto arrive = [&](uint64_t &bar) {   // after this warp's writes to shared memory
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bar));
-  };
-  uint32_t base = 0, f_use = 0, items = 0;   // base: ring use of the item's first tile
-  uint32_t raw_parity = 0;                   // of the next wait, a bit a slot
-  // Loads of this warp that nobody may have waited for: a bit a slot of the K ring (0, 1), of the V ring
-  // (2, 3) and of `raw` (4, 5), with the phase that they complete.
+  uint32_t use = 0, f_use = 0, items = 0;   // uses of the ring, of the raw one
+  uint32_t raw_parity = 0;                  // of the next wait, a bit a slot
+  // Loads of this warp that nobody may have waited for: a bit a slot of the ring (0, 1) and of `raw`
+  // (2, 3), with the phase that they complete.
   uint32_t pending = 0, phase = 0;
   auto loading = [&](uint32_t bit, uint32_t parity) {
     pending |= 1u << bit;
@@ -207,136 +259,131 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     if (j < p.n_prefix) return min(max(p.Np - j * BN - lane * 16, 0), 16);
     return grain_of(p, table, item, own_pos(p, item, j) + lane * 16).valid;
   };
-  // TMA loads of the keys or the values (V) of a tile that is not cached; its V's rows are cleared by finish.
-  auto issue = [&](int j, bool V) {
+  // TMA loads of a tile that is not cached, use `u` of the ring.
+  auto issue = [&](int j, uint32_t u) {
     if (j >= item.kv1 || is_cached(p, j)) return true;
-    const uint32_t use = base + (j - item.kv0), slot = V ? use % C::VS : use % C::KS;
-    const uint32_t parity = (V ? use / C::VS : use / C::KS) & 1;
-    if (!wait(V ? bars->v_empty[slot] : bars->k_empty[slot], parity ^ 1)) return false;
+    const uint32_t slot = u % S, parity = u / S & 1;
+    if (!wait(empty_of[slot], parity ^ 1)) return false;
     const uint32_t dst = smem_u32(smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE);
-    uint32_t full = smem_u32(V ? &bars->v_full[slot] : &bars->k_full[slot]);
-    const bool prefix = j < p.n_prefix;
-    const CUtensorMap *map = prefix ? (V ? &p.tm_pv : &p.tm_pk) : (V ? &p.tm_v : &p.tm_k);
-    if (prefix) {   // (rows past Np come as zeros)
+    uint32_t full = smem_u32(full_of + slot);
+    if (j < p.n_prefix) {   // (rows past Np come as zeros)
       if (issuer && lane == 0) {
         mbar_arrive_expect_tx(full, C::TILE);
-        mbar_arrive_n(full, 3);
-        for (int hf = 0; hf < D / 64; ++hf) tma_load_4d(dst + hf * kHalf, map, full, hf * 64, j * BN, item.hk, 0);
+        mbar_arrive_n(full, kFlatOperandWarps - 1);
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_4d(dst + hf * kHalf, V ? &p.tm_pv : &p.tm_pk, full, hf * 64, j * BN, item.hk, 0);
       }
-      loading(V ? 2 + slot : slot, parity);
+      loading(slot, parity);
     } else {
       Grain g{0, 0, 0};
       if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
+      // V's rows behind a request's last key are still to be cleared then.
       const bool whole = !V || __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16;
       if (!whole) full = smem_u32(&bars->raw[slot]);
       if (issuer) {
         if (lane == 0) {
           mbar_arrive_expect_tx(full, bytes);
-          if (whole) mbar_arrive_n(full, 3);
+          if (whole) mbar_arrive_n(full, kFlatOperandWarps - 1);
         }
         __syncwarp();
         if (g.valid > 0)
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_4d(dst + hf * kHalf + lane * 2048, map, full, hf * 64, g.off, item.hk, p.b0 + g.b);
+            tma_load_4d(dst + hf * kHalf + lane * 2048, V ? &p.tm_v : &p.tm_k, full, hf * 64, g.off, item.hk, p.b0 + g.b);
       }
-      if (whole) {
-        loading(V ? 2 + slot : slot, parity);
-      } else {
-        pending &= ~(4u << slot);
-        loading(4 + slot, raw_parity >> slot & 1);
-      }
+      pending &= ~(1u << slot);
+      if (whole) loading(slot, parity); else loading(2 + slot, raw_parity >> slot & 1);
     }
     __syncwarp();
     return true;
   };
-  // Codes of a raw slot to a bf16 tile; rows that do not count to zeros (V) or to anything (K).
-  auto convert = [&](uint8_t *dst, bool clear, int valid) {
-    constexpr int CPR = D / 16;   // 16-byte chunks of a row's codes
-    const uint8_t *src = smem + C::OFF_F + (f_use % C::FS) * C::RAW;
-#pragma unroll 4
-    for (int i = 0; i < BN * CPR / 128; ++i) {
-      const int at = i * 128 + tid, row = at / CPR, cc = at % CPR;
-      uint4 out[2];
-      to_bf16(*reinterpret_cast<const uint4 *>(src + at * 16), src[BN * D + row], out);
-      if (clear && (row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4)) {
-        out[0] = make_uint4(0, 0, 0, 0);
-        out[1] = out[0];
-      }
-      uint8_t *half = dst + (cc / 4) * kHalf + row * 128;
-      const int first = (cc % 4) * 2, odd = (cc / 4) & 1;   // (the order spares bank conflicts between halves)
-      *reinterpret_cast<uint4 *>(half + (((first + odd) ^ (row & 7)) * 16)) = odd ? out[1] : out[0];
-      *reinterpret_cast<uint4 *>(half + (((first + 1 - odd) ^ (row & 7)) * 16)) = odd ? out[0] : out[1];
-    }
-  };
-  auto finish = [&](int j, bool V) {
-    const uint32_t use = base + (j - item.kv0), slot = V ? use % C::VS : use % C::KS;
-    if (is_cached(p, j)) {
-      const int valid = V ? valid_of(j) : 16;
-      if (!wait(bars->f_full[f_use % C::FS], f_use / C::FS & 1)) return false;
-      if (!wait(V ? bars->v_empty[slot] : bars->k_empty[slot], ((V ? use / C::VS : use / C::KS) & 1) ^ 1)) return false;
-      pending &= ~((V ? 4u : 1u) << slot);
-      convert(smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE, __any_sync(0xffffffffu, valid < 16), valid);
-      arrive(V ? bars->v_full[slot] : bars->k_full[slot]);
-      if (lane == 0) mbar_arrive(smem_u32(&bars->f_empty[f_use % C::FS]));
+  // A cached tile, or the rest of a V tile that is not.
+  auto finish = [&](int j) {
+    const uint32_t slot = use % S;
+    const bool cached = is_cached(p, j);
+    if (!cached && (!V || j < p.n_prefix)) return true;
+    const int valid = V ? valid_of(j) : 16;
+    const bool clear = __any_sync(0xffffffffu, valid < 16);
+    uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
+    const uint32_t f = F0 + f_use % F;
+    if (cached) {
+      if (!wait(bars->f_full[f], f_use / F & 1) || !wait(empty_of[slot], (use / S & 1) ^ 1)) return false;
+      pending &= ~(1u << slot);
+      convert_tile<D>(smem + C::OFF_F + f * C::RAW, dst, valid);
       ++f_use;
-    } else if (V && j >= p.n_prefix) {
-      const int valid = valid_of(j);
-      if (!__any_sync(0xffffffffu, valid < 16)) return true;
+    } else {
+      if (!clear) return true;
       if (!wait(bars->raw[slot], raw_parity >> slot & 1)) return false;
       raw_parity ^= 1u << slot;
-      pending &= ~(16u << slot);
-      uint8_t *v = smem + C::OFF_V + slot * C::TILE;
+      pending &= ~(4u << slot);
       if ((tid & 15) >= __shfl_sync(0xffffffffu, valid, tid >> 4))
         for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4 *>(v + (i / 8) * kHalf + tid * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
-      arrive(bars->v_full[slot]);
+          *reinterpret_cast<uint4 *>(dst + (i / 8) * kHalf + tid * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_u32(full_of + slot));
+      if (cached) mbar_arrive(smem_u32(&bars->f_empty[f]));
     }
     return true;
   };
 
   bool ok = true;
   for (; ok && walk.next(p, table, item); ++items) {
-    if (items > 0) ok = wait(bars->q_empty, (items - 1) & 1);
-    if (!ok) break;
-    {
-      const int in = tid % p.row_tile, row = item.row0 + in;   // (the copies begin at multiples of row_tile)
+    if (V) {   // the queries, a row a thread; the copies begin at multiples of row_tile
+      const int row = item.row0 + tid % p.row_tile;
       const uint16_t *src = nullptr;
       if (row < p.rows) {
         const PrefixRow r = row_of(p, item.hk, row);
         if (r.n < p.Nq) src = p.q + r.b * p.q_b + r.h * p.q_h + r.n * p.q_n;
       }
-#pragma unroll 4
+      const uint32_t to = tmem + (static_cast<uint32_t>(tid & ~31) << 16) + C::COL_Q;
+      uint32_t q[D / 2];
+#pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const uint4 v = src ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(smem + (c / 8) * kHalf + tid * 128 + (((c % 8) ^ (tid & 7)) * 16)) = v;
+        q[4 * c] = v.x;
+        q[4 * c + 1] = v.y;
+        q[4 * c + 2] = v.z;
+        q[4 * c + 3] = v.w;
       }
-      arrive(bars->q_full);
+      if (items > 0) ok = wait(bars->q_empty, (items - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();   // (the last item's scores, read from here, are done)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) tmem_st16(to + 16 * c, q + 16 * c);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bars->q_full));
     }
-    // A tile's TMA loads go out one tile ahead. (The next V's slot is free once the product with the last
-    // tile's V is done, which follows this tile's scores: its K has to be finished before that is waited for.)
-    ok = issue(item.kv0, false) && issue(item.kv0, true);
-    for (int j = item.kv0; ok && j < item.kv1; ++j)
-      ok = issue(j + 1, false) && finish(j, false) && finish(j, true) && issue(j + 1, true);
-    base += item.kv1 - item.kv0;
+    // TMA loads go out one tile ahead of the clearing that V's may need.
+    ok = issue(item.kv0, use);
+    for (int j = item.kv0; ok && j < item.kv1; ++j, ++use) ok = issue(j + 1, use + 1) && finish(j);
   }
   // Every load issued must land before the CTA releases its shared memory.
   if (issuer)
     for (int s = 0; s < 2; ++s) {
-      if (pending >> s & 1) drain(smem_u32(&bars->k_full[s]), phase >> s & 1);
-      if (pending >> (2 + s) & 1) drain(smem_u32(&bars->v_full[s]), phase >> (2 + s) & 1);
-      if (pending >> (4 + s) & 1) drain(smem_u32(&bars->raw[s]), phase >> (4 + s) & 1);
+      if (pending >> s & 1) drain(smem_u32(full_of + s), phase >> s & 1);
+      if (pending >> (2 + s) & 1) drain(smem_u32(&bars->raw[s]), phase >> (2 + s) & 1);
     }
 }
 
 // ------------------------------------------------------------------ MMA issuer
 template <int D>
+__device__ __forceinline__ void issue_qk_ts(uint32_t dcol, uint32_t qcol, uint64_t kdesc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    tc_mma_ts(dcol, qcol + kk * 8, kdesc + static_cast<uint64_t>(((kk / 4) * kHalf + (kk % 4) * 32) >> 4), idesc,
+              kk > 0 ? 1u : 0u);
+}
+template <int D>
 __device__ void flat_mma(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem_in) {
   using C = FlatCfg<D>;
   volatile int *abort_flag = &bars->abort;
   const uint32_t tmem = uniform(tmem_in);
-  uint32_t base = 0, items = 0, pc = 0;   // ring use of the item's first tile; items; parities of p_full, a bit a set
-  const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+  uint32_t base = 0, items = 0;   // tiles before the item; items
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
   const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), kHalf, 1024);
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
@@ -346,30 +393,29 @@ __device__ void flat_mma(const PrefixParams &p, uint8_t *smem, FlatBars *bars, c
   for (; walk.next(p, table, item); ++items) {
     const int n = uniform(item.kv1 - item.kv0);
     if (!wait(bars->q_full, items & 1)) goto done;
-    for (int i = 0; i < n + 2; ++i) {
-      const int t = i & 1;
-      if (i >= 2) {
-        const uint32_t use = base + i - 2, vs = use % C::VS;
-        if (!wait(bars->v_full[vs], use / C::VS & 1)) goto done;
-        if (!wait(bars->p_full[t], pc >> t & 1)) goto done;
-        pc ^= 1u << t;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_pv<D>(tmem + 256 + t * D, tmem + t * 128, vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), i >= 4 ? 1u : 0u);
-          tc_commit(smem_u32(&bars->v_empty[vs]));
-          if (i >= n) tc_commit(smem_u32(&bars->o_full[t]));   // the set's last tile
-        }
-        __syncwarp();
-      }
+    for (int i = 0; i <= n; ++i) {
       if (i < n) {
-        const uint32_t use = base + i, ks = use % C::KS;
-        if (!wait(bars->k_full[ks], use / C::KS & 1)) goto done;
+        const uint32_t g = base + i, t = g & 1, ks = g % C::KS;
+        if (!wait(bars->k_full[ks], g / C::KS & 1)) goto done;
         tc_fence_after();
         if (elect_one()) {
-          issue_qk<D>(tmem + t * 128, qdesc, kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)));
+          issue_qk_ts<D>(tmem + t * 128, tmem + C::COL_Q, kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)));
           tc_commit(smem_u32(&bars->s_full[t]));
           tc_commit(smem_u32(&bars->k_empty[ks]));
           if (i == n - 1) tc_commit(smem_u32(&bars->q_empty));
+        }
+        __syncwarp();
+      }
+      if (i > 0) {
+        const uint32_t g = base + i - 1, t = g & 1, vs = g % C::VS;
+        if (!wait(bars->v_full[vs], g / C::VS & 1)) goto done;
+        if (!wait(bars->p_full[t], g >> 1 & 1)) goto done;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_pv<D>(tmem + C::COL_O, tmem + t * 128, vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), i > 1 ? 1u : 0u);
+          tc_commit(smem_u32(&bars->v_empty[vs]));
+          tc_commit(smem_u32(&bars->pv_done));
+          if (i == n) tc_commit(smem_u32(&bars->o_full));
         }
         __syncwarp();
       }
@@ -384,8 +430,7 @@ done:
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
-__device__ __forceinline__ void both_sets_sync() { asm volatile("bar.sync 9, 256;" ::: "memory"); }
-__device__ __forceinline__ void one_set_sync(int t) { asm volatile("bar.sync %0, 128;" ::"r"(10 + t) : "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 9, 128;" ::: "memory"); }
 
 // Bits [lo, hi) of a 32-bit word, both limits taken into [0, 32].
 __device__ __forceinline__ uint32_t bits_of(int lo, int hi) {
@@ -431,36 +476,32 @@ template <int D, int NC>
 __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem) {
   using C = FlatCfg<D>;
   constexpr int COPIES = 4 / NC, RT = BM / COPIES;   // rows of a unit
-  const int tid = threadIdx.x, t = tid >> 7, lrow = tid & 127, wq = lrow >> 5;
-  const int in = lrow % RT, copy = lrow / RT;
-  const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-  const uint32_t tS = tmem + lane_base + t * 128, tO = tmem + lane_base + 256;
-  const uint32_t s_full = smem_u32(&bars->s_full[t]), p_full = smem_u32(&bars->p_full[t]);
-  const uint32_t o_full = smem_u32(&bars->o_full[t]);
+  const int tid = threadIdx.x, wq = tid >> 5;
+  const int in = tid % RT, copy = tid / RT;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16), tO = lanes + C::COL_O;
   volatile int *abort_flag = &bars->abort;
   float2 *exch = reinterpret_cast<float2 *>(smem + C::OFF_STG);
   float *fin = reinterpret_cast<float *>(smem + C::OFF_FIN);
   const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
-  uint32_t step = 0, outs = 0;
+  uint32_t step = 0, items = 0;   // tiles, items so far
   bool dead = false;   // a wait gave up: go on without waiting, store nothing
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!dead && !wait_for<true>(bar, parity, abort_flag, p)) dead = true;
+  auto wait = [&](uint64_t &bar, uint32_t parity) {
+    if (!dead && !wait_for<true>(smem_u32(&bar), parity, abort_flag, p)) dead = true;
   };
   PrefixWalk walk;
   walk.start(p, bars->plan);
   PrefixItem item;
   bool cut = false;   // a piece was this CTA's first of its unit
-  while (walk.next(p, table, item)) {
+  for (; walk.next(p, table, item); ++items) {
     const int row = item.row0 + in;
     const bool idle = item.row0 + (wq * 32) % RT >= p.rows;   // no row in this warp
     const PrefixRange own = range_of(p, table, row);
-    const int n = item.kv1 - item.kv0, mine = (n - t + 1) / 2;   // tiles of the item, of this set
     float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < mine; ++i, ++step) {
-      const int j = item.kv0 + 2 * i + t;
-      wait(s_full, step & 1);
+    for (int j = item.kv0; j < item.kv1; ++j, ++step) {
+      const uint32_t t = step & 1, tS = lanes + t * 128;
+      wait(bars->s_full[t], step >> 1 & 1);
       if (idle) {
-        mbar_arrive(p_full);
+        mbar_arrive(smem_u32(&bars->p_full[t]));
         continue;
       }
       tc_fence_after();
@@ -486,7 +527,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       const float m_new = fmaxf(m, mx * p.scale_log2);
       float alpha = 1.f;
       bool rescale = false;
-      if (i == 0) {
+      if (j == item.kv0) {
         m = m_new;
       } else {
         const bool need = m_new > m + kGrowth;
@@ -523,46 +564,47 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       }
       l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       if (rescale) {
+        // (The products before the last are done, as these scores followed them.)
+        wait(bars->pv_done, (step - 1) & 1);
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           uint32_t o[16];
-          tmem_ld16(tO + t * D + 16 * c, o);
+          tmem_ld16(tO + 16 * c, o);
           tmem_wait_ld16(o);
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st16(tO + t * D + 16 * c, o);
+          tmem_st16(tO + 16 * c, o);
         }
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(smem_u32(&bars->p_full[t]));
     }
-    if (mine > 0) {
-      wait(o_full, outs & 1);
-      ++outs;
-    }
-    // Both sets' and all copies' (m, l) of a row.
-    exch[tid] = make_float2(m, l);
-    both_sets_sync();
+    wait(bars->o_full, items & 1);
     tc_fence_after();
-    float top = -INFINITY, total = 0.f;
+    // (m, l) of all copies of a row.
+    float top = m, total = l, f = 1.f;
+    if constexpr (COPIES > 1) {
+      exch[tid] = make_float2(m, l);
+      softmax_sync();
 #pragma unroll
-    for (int k = 0; k < 2 * COPIES; ++k) top = fmaxf(top, exch[(k & 1) * 128 + (k >> 1) * RT + in].x);
+      for (int k = 0; k < COPIES; ++k) top = fmaxf(top, exch[k * RT + in].x);
+      total = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2 * COPIES; ++k) {
-      const float2 e = exch[(k & 1) * 128 + (k >> 1) * RT + in];
-      total = fmaf(shrink(e.x, top), e.y, total);
+      for (int k = 0; k < COPIES; ++k) {
+        const float2 e = exch[k * RT + in];
+        total = fmaf(shrink(e.x, top), e.y, total);
+      }
+      f = shrink(m, top);
     }
-    // (A set without tiles in the item has nothing in its O.)
-    const float f0 = shrink(exch[lrow].x, top), f1 = shrink(exch[128 + lrow].x, top);
-    const bool second = n > 1;
     // A piece leaves its sums as they are, a whole unit divides by them.
     const float norm = item.piece ? 1.f : total == 0.f ? 0.f : 1.f / total;
     float *part = nullptr;
     if (item.piece) {
       part = part_of<D>(p, blockIdx.x, item.kv0 == 0 ? 1 : 0, BM);
       if (item.kv0 == 0) cut = true;
-      if (t == 0 && copy == 0 && row < p.rows && !dead) {
+      if (copy == 0 && row < p.rows && !dead) {
         __stcg(part + D * BM + in, top);
         __stcg(part + (D + 1) * BM + in, total);
       }
@@ -571,73 +613,57 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         __stcg(p.cuts + blockIdx.x, make_int4(item.unit, dead ? 0 : span.pieces, item.hk, item.row0));
       }
     }
-    uint16_t *dst = item.piece || dead ? nullptr : out_row(p, item.hk, row, D);
     if constexpr (COPIES == 1) {
+      uint16_t *dst = item.piece || dead ? nullptr : out_row(p, item.hk, row, D);
       if (!idle) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t a[16], b[16];
-          const int col = t * (D / 2) + 16 * c;
-          tmem_ld16(tO + col, a);
-          if (second) tmem_ld16(tO + D + col, b);
-          tmem_wait_ld16(a);
-          tmem_wait_ld16(b);
-          float x[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            x[k] = f0 * __uint_as_float(a[k]);
-            if (second) x[k] = fmaf(f1, __uint_as_float(b[k]), x[k]);
-          }
+          uint32_t a[32];
+          tmem_ld32(tO + 32 * c, a);
+          tmem_wait_ld_regs(a);
           if (part) {
             if (row < p.rows && !dead)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                __stcg(reinterpret_cast<float4 *>(part) + (col / 4 + k) * BM + in,
-                       make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+              for (int k = 0; k < 8; ++k)
+                __stcg(reinterpret_cast<float4 *>(part) + (8 * c + k) * BM + in,
+                       make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
+                                   __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3])));
           } else if (dst) {
+            float x[32];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              reinterpret_cast<uint4 *>(dst + col)[k] =
-                  make_uint4(pack_bf16x2(x[8 * k] * norm, x[8 * k + 1] * norm),
-                             pack_bf16x2(x[8 * k + 2] * norm, x[8 * k + 3] * norm),
-                             pack_bf16x2(x[8 * k + 4] * norm, x[8 * k + 5] * norm),
-                             pack_bf16x2(x[8 * k + 6] * norm, x[8 * k + 7] * norm));
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(a[k]) * norm;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<uint4 *>(dst + 32 * c)[k] =
+                  make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
+                             pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
           }
         }
       }
       tc_fence_before();
-      both_sets_sync();   // O and exch have been read
     } else {
       // The copies of a row lie in other warps' lanes: 16 columns at a time through shared memory
       // (16-byte groups, moved by half the row's number against bank conflicts), then a thread adds the
       // copies of four columns.
-      if (t == 0 && copy == 0) fin[in] = norm;
-      both_sets_sync();   // exch has been read, fin is written
-      float4 *stg = reinterpret_cast<float4 *>(smem + C::OFF_STG) + t * (BM * 4);
+      if (copy == 0) fin[in] = norm;
+      softmax_sync();   // exch has been read, fin is written
+      float4 *stg = reinterpret_cast<float4 *>(smem + C::OFF_STG);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        const int col = t * (D / 2) + 16 * c;
+      for (int c = 0; c < D / 16; ++c) {
         if (!idle) {
-          uint32_t a[16], b[16];
-          tmem_ld16(tO + col, a);
-          if (second) tmem_ld16(tO + D + col, b);
+          uint32_t a[16];
+          tmem_ld16(tO + 16 * c, a);
           tmem_wait_ld16(a);
-          tmem_wait_ld16(b);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[e] = f0 * __uint_as_float(a[4 * k + e]);
-              if (second) x[e] = fmaf(f1, __uint_as_float(b[4 * k + e]), x[e]);
-            }
-            stg[lrow * 4 + (k ^ (lrow >> 1 & 3))] = make_float4(x[0], x[1], x[2], x[3]);
-          }
+          for (int k = 0; k < 4; ++k)
+            stg[tid * 4 + (k ^ (tid >> 1 & 3))] =
+                make_float4(f * __uint_as_float(a[4 * k]), f * __uint_as_float(a[4 * k + 1]),
+                            f * __uint_as_float(a[4 * k + 2]), f * __uint_as_float(a[4 * k + 3]));
         }
-        one_set_sync(t);
+        softmax_sync();
 #pragma unroll
         for (int k = 0; k < RT * 4 / 128; ++k) {
-          const int r = (lrow + 128 * k) / 4, q = lrow & 3;
+          const int r = (tid + 128 * k) / 4, q = tid & 3;
           if (item.row0 + r >= p.rows || dead) continue;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -650,24 +676,23 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
             x.w += y.w;
           }
           if (part) {
-            __stcg(reinterpret_cast<float4 *>(part) + (col / 4 + q) * BM + r, x);
+            __stcg(reinterpret_cast<float4 *>(part) + (4 * c + q) * BM + r, x);
           } else if (uint16_t *to = out_row(p, item.hk, item.row0 + r, D)) {
             const float g = fin[r];
-            *reinterpret_cast<uint2 *>(to + col + 4 * q) =
+            *reinterpret_cast<uint2 *>(to + 16 * c + 4 * q) =
                 make_uint2(pack_bf16x2(x.x * g, x.y * g), pack_bf16x2(x.z * g, x.w * g));
           }
         }
-        one_set_sync(t);
+        softmax_sync();
       }
       tc_fence_before();
-      both_sets_sync();   // O, fin and the staged columns have been read
     }
   }
   if (p.split && tid == 0 && !cut) __stcg(p.cuts + blockIdx.x, make_int4(0, 0, 0, 0));
 }
 
 template <int D>
-__global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(448, 1) prefix_flat_kernel(const __grid_constant__ PrefixParams p) {
   using C = FlatCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle pattern repeats every 1024 bytes
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -678,22 +703,23 @@ __global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_consta
   int *table = reinterpret_cast<int *>(smem + C::OFF_TAB);
   const int warp = uniform(threadIdx.x / 32);
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->q_full), 4);
+    mbar_init(smem_u32(&bars->q_full), BM);
     mbar_init(smem_u32(&bars->q_empty), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), 4);
+      mbar_init(smem_u32(&bars->k_full[s]), kFlatOperandWarps);
       mbar_init(smem_u32(&bars->k_empty[s]), 1);
-      mbar_init(smem_u32(&bars->v_full[s]), 4);
+      mbar_init(smem_u32(&bars->v_full[s]), kFlatOperandWarps);
       mbar_init(smem_u32(&bars->v_empty[s]), 1);
       mbar_init(smem_u32(&bars->raw[s]), 1);
       mbar_init(smem_u32(&bars->s_full[s]), 1);
       mbar_init(smem_u32(&bars->p_full[s]), 128);
-      mbar_init(smem_u32(&bars->o_full[s]), 1);
     }
     for (int s = 0; s < C::FS; ++s) {
       mbar_init(smem_u32(&bars->f_full[s]), 1);
-      mbar_init(smem_u32(&bars->f_empty[s]), 4);
+      mbar_init(smem_u32(&bars->f_empty[s]), kFlatOperandWarps);
     }
+    mbar_init(smem_u32(&bars->pv_done), 1);
+    mbar_init(smem_u32(&bars->o_full), 1);
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -714,20 +740,21 @@ __global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  if (warp < kFlatConvert) {
+  if (warp < kFlatKeys) {
     if (p.copies == 1)
       flat_softmax<D, 4>(p, smem, bars, table, tmem);
     else if (p.copies == 2)
       flat_softmax<D, 2>(p, smem, bars, table, tmem);
     else
       flat_softmax<D, 1>(p, smem, bars, table, tmem);
+  } else if (warp < kFlatValues) {
+    flat_operands<D, false>(p, smem, bars, table, tmem);
   } else if (warp < kFlatMma) {
-    flat_operands<D>(p, smem, bars, table);
+    flat_operands<D, true>(p, smem, bars, table, tmem);
+  } else if (warp == kFlatMma) {
+    flat_mma<D>(p, smem, bars, table, tmem);
   } else {
-    if (warp == kFlatMma)
-      flat_mma<D>(p, smem, bars, table, tmem);
-    else if (warp == kFlatLoad)
-      flat_loader<D>(p, smem, bars, table);
+    flat_loader<D>(p, smem, bars, table);
   }
   __syncwarp();
   tc_fence_before();
