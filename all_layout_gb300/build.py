@@ -23,7 +23,7 @@ HEADERS = (os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "attn_wide.cuh"), os.path.join(CSRC, "diff.h"),
            os.path.join(CSRC, "attn_diff_wide.cuh"), os.path.join(CSRC, "turns.h"),
            os.path.join(CSRC, "cache.h"), os.path.join(CSRC, "prefix.h"),
-           os.path.join(CSRC, "attn_prefix_flat.cuh"),
+           os.path.join(CSRC, "attn_prefix_flat.cuh"), os.path.join(CSRC, "attn_prefix_tall.cuh"),
            os.path.join(ROOT, "include", "xs.h"))
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden"]

@@ -315,6 +315,7 @@ __device__ __forceinline__ void issue_pv(uint32_t dcol, uint32_t pcol, uint64_t 
 }
 
 #include "attn_prefix_flat.cuh"
+#include "attn_prefix_tall.cuh"
 
 // ------------------------------------------------------------------ joining pieces
 // The pieces of the unit that begins in CTA blockIdx.x's range: 32 rows (blockIdx.y) and 8 columns
@@ -381,6 +382,15 @@ cudaError_t launch_flat(const PrefixParams &p, int grid, cudaStream_t s) {
 }
 
 template <int D>
+cudaError_t launch_tall(const PrefixParams &p, int grid, cudaStream_t s) {
+  using C = TallCfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(prefix_tall_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  prefix_tall_kernel<D><<<grid, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
 cudaError_t launch_join(const PrefixParams &p, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, ((p.row_tile < p.rows ? p.row_tile : p.rows) + 31) / 32, D / 8);
@@ -400,6 +410,10 @@ int prefix_part_floats(int d, int rows) { return (d + 2) * (rows > BM ? rows : B
 
 cudaError_t launch_prefix_flat(const PrefixParams &p, int d, int grid, cudaStream_t s) {
   return d == 64 ? launch_flat<64>(p, grid, s) : launch_flat<128>(p, grid, s);
+}
+
+cudaError_t launch_prefix_tall(const PrefixParams &p, int d, int grid, cudaStream_t s) {
+  return d == 64 ? launch_tall<64>(p, grid, s) : launch_tall<128>(p, grid, s);
 }
 
 cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, cudaStream_t s) {

@@ -50,6 +50,8 @@ struct PrefixParams {
 int prefix_part_floats(int d, int rows);   // fp32 values of one piece's partial result
 // Few rows for each k/v head: one 128-lane tile of rows at a time, two KV tiles in turn.
 cudaError_t launch_prefix_flat(const PrefixParams &p, int d, int grid, cudaStream_t s);
+// Many rows: pairs of 128-row tiles; keys and values in tensors.
+cudaError_t launch_prefix_tall(const PrefixParams &p, int d, int grid, cudaStream_t s);
 // Joins the pieces of cut units, after a launch that had split set.
 cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, cudaStream_t s);
 

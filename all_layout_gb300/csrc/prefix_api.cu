@@ -46,14 +46,16 @@ bool encode_operand(CUtensorMap *m, const void *base, long long B, int H, int N,
 }
 
 // Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split schedule,
-// whichever should end earlier; costs in KV tiles.
+// whichever should end earlier; costs in KV tiles. `join`: what pieces and the launch that joins them cost.
 struct Plan {
   int split, waves, grid;
+  long long cost;
 };
-Plan plan(long long units, int sms, long long tiles, int least, unsigned long long per_cta, unsigned long long room) {
+Plan plan(long long units, int sms, long long tiles, int least, int join, unsigned long long per_cta,
+          unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
   const long long unit = tiles + kPrefixCost, rounds = (units + grid0 - 1) / grid0;
-  const Plan whole{0, 0, grid0};
+  const Plan whole{0, 0, grid0, rounds * unit};
   if (tiles < 2 || static_cast<unsigned long long>(sms) * sizeof(int4) > kCutsBytes) return whole;
   const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
   const long long left = units - static_cast<long long>(waves) * sms;
@@ -64,9 +66,50 @@ Plan plan(long long units, int sms, long long tiles, int least, unsigned long lo
     grid = static_cast<int>((left * unit + per - 1) / per);
   }
   if (per_cta * grid > room) return whole;
-  constexpr int kJoin = 6;   // what pieces and the launch that joins them cost
-  return waves * unit + per + kJoin < rounds * unit ? Plan{1, waves, grid} : whole;
+  const long long cost = waves * unit + per + join;
+  return cost < whole.cost ? Plan{1, waves, grid, cost} : whole;
 }
+
+// What a launch is to do, of the batch entries of one launch.
+struct Shape {
+  int B, group, Hk, Nq, Np, Nk, d;
+  bool ragged;
+};
+struct Choice {
+  bool tall;
+  int grain, nq_rows, copies, row_tile, n_tiles;
+  long long rows;
+  Plan plan;
+  double us;
+};
+constexpr int kLeast = 4;   // the shortest range worth a CTA
+
+Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
+  Choice c;
+  c.tall = tall;
+  c.grain = tall ? kTileRows : 16;
+  c.nq_rows = tall ? (s.Nq + 7) / 8 * 8 : s.Nq;
+  const long long entry = static_cast<long long>(s.group) * c.nq_rows;
+  c.rows = s.B * entry;
+  c.copies = tall ? 1 : c.rows <= 32 ? 4 : c.rows <= 64 ? 2 : 1;
+  c.row_tile = tall ? 2 * kTileRows : kTileRows / c.copies;
+  c.n_tiles = static_cast<int>((c.rows + c.row_tile - 1) / c.row_tile);
+  // Own tiles of a unit: those of the entries that its rows belong to (three quarters of them where lengths
+  // are on the device).
+  const long long entries = entry >= c.row_tile ? 1 : (c.row_tile < c.rows ? c.row_tile : c.rows) / entry;
+  const long long padded = (static_cast<long long>(s.Nk) + c.grain - 1) / c.grain * c.grain, keys = entries * padded;
+  const long long tiles = (s.Np + kTileRows - 1) / kTileRows + (keys - (s.ragged ? keys / 4 : 0) + kTileRows - 1) / kTileRows;
+  c.plan = plan(static_cast<long long>(s.Hk) * c.n_tiles, sms, tiles, kLeast, tall ? 10 : 6,
+                2ull * prefix_part_floats(s.d, c.row_tile) * 4, room);
+  // Measured times of a KV tile: a pair of row tiles in the tall kernel, one in the flat kernel.
+  c.us = c.plan.cost * (tall ? (s.d == 128 ? 1.5 : 1.2) : (s.d == 128 ? 1.9 : 1.2));
+  return c;
+}
+
+// Bytes of the workspace that hold cached keys and values read back to bf16, K and V.
+unsigned long long unpacked(long long rows, int d) { return (4ull * rows * d + 511) / 512 * 512; }
+// Their time: half as much is read as is written.
+double unpack_us(unsigned long long bytes) { return bytes == 0 ? 0.0 : 3.0 + bytes * 1.5 / 5.0e6; }
 
 xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_stride, void *const *shards, int P,
                       void *ws, unsigned long long ws_bytes, void *stream) {
@@ -107,16 +150,15 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
   }
   if (st == XS_ERR_UNSUPPORTED || (d != 64 && d != 128)) return XS_ERR_UNSUPPORTED;
   if (Np > kMostLength || Nk > kMostLength || Nq > kMostLength) return XS_ERR_UNSUPPORTED;
-  // Entries of a launch: as many as the kernel's table holds, and as their packed keys stay below 2^30 for.
-  constexpr int grain = 16;
-  const long long padded = (static_cast<long long>(Nk) + grain - 1) / grain * grain;
+  // Entries of a launch: as many as the kernels' table holds, and as their packed keys stay below 2^30 for.
+  const long long padded = (static_cast<long long>(Nk) + kTileRows - 1) / kTileRows * kTileRows;
   int chunk = kPrefixEntries;
   if (padded > 0 && kMostLength / padded < chunk) chunk = static_cast<int>(kMostLength / padded);
   if (chunk < 1) chunk = 1;
   if (chunk > B) chunk = B;
   const int group = H > 0 ? H / Hk : 1;
-  if (!empty && (static_cast<double>(chunk) * group * Nq > 2147483647.0 - 256 ||
-                 (static_cast<double>(chunk) * group * Nq / 32 + 1) * Hk > 2147483647.0))
+  if (!empty && (static_cast<double>(chunk) * group * (Nq + 7.0) > 2147483647.0 - 256 ||
+                 (static_cast<double>(chunk) * group * (Nq + 7.0) / 32 + 1) * Hk > 2147483647.0))
     return XS_ERR_UNSUPPORTED;
   if (st != XS_OK || !aligned(a->q, 16) || !aligned(a->prefix_k, 16) || !aligned(a->prefix_v, 16) ||
       !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(o, 16) || !aligned(a->kv_len, 4) || !aligned(ws, 256) ||
@@ -154,58 +196,99 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
   p.q_b = a->q_stride[0];
   p.q_h = a->q_stride[1];
   p.q_n = a->q_stride[2];
-  p.prefix_cached = prefix_cached;
-  p.own_cached = own_cached;
-  if (prefix_cached || own_cached) {
-    p.prefix_pages = lists_of(a->cache, &a->prefix_pages);
-    p.own_pages = lists_of(a->cache, &a->pages);
-    p.codes[0] = static_cast<const uint8_t *>(a->cache.k);
-    p.codes[1] = static_cast<const uint8_t *>(a->cache.v);
-    p.scales[0] = a->cache.k_scale;
-    p.scales[1] = a->cache.v_scale;
+  const unsigned long long room = ws && ws_bytes > kCutsBytes ? ws_bytes - kCutsBytes : 0;
+  char *area = room > 0 ? static_cast<char *>(ws) + kCutsBytes : nullptr;
+  p.cuts = static_cast<int4 *>(ws);
+  // The kernel: with many rows the tall one, which wants cached keys and values in the workspace first.
+  Shape shape{chunk, group, Hk, Nq, Np, Nk, d, a->kv_len != nullptr};
+  const unsigned long long prefix_bytes = prefix_cached ? unpacked(static_cast<long long>(Hk) * Np, d) : 0;
+  const unsigned long long own_bytes = own_cached ? unpacked(static_cast<long long>(B) * Hk * Nk, d) : 0;
+  bool tall = false;
+  if (prefix_bytes + own_bytes <= room) {
+    const Choice x = choose(shape, true, sms, room - prefix_bytes - own_bytes), y = choose(shape, false, sms, room);
+    tall = static_cast<long long>(chunk) * group * Nq > kTileRows &&
+           x.us + unpack_us(prefix_bytes + own_bytes) / ((B + chunk - 1) / chunk) < y.us;
   }
-  if (dense_prefix &&
-      (!encode_operand(&p.tm_pk, a->prefix_k, 1, Hk, Np, d, 0, a->prefix_k_stride[0], a->prefix_k_stride[1], kTileRows) ||
-       !encode_operand(&p.tm_pv, a->prefix_v, 1, Hk, Np, d, 0, a->prefix_v_stride[0], a->prefix_v_stride[1], kTileRows)))
+  const void *prefix_k = a->prefix_k, *prefix_v = a->prefix_v, *own_k = a->k, *own_v = a->v;
+  long long pk_stride[2] = {a->prefix_k_stride[0], a->prefix_k_stride[1]};
+  long long pv_stride[2] = {a->prefix_v_stride[0], a->prefix_v_stride[1]};
+  long long k_stride[3], v_stride[3];
+  std::memcpy(k_stride, a->k_stride, sizeof(k_stride));
+  std::memcpy(v_stride, a->v_stride, sizeof(v_stride));
+  unsigned long long parts_room = room;
+  if (tall) {
+    if (prefix_cached) {
+      const long long st[3] = {0, static_cast<long long>(Np) * d, d};
+      char *v = area + prefix_bytes / 2;
+      if (xs_cache_read(&a->cache, area, v, st, st, &a->prefix_pages, nullptr, nullptr, 1, Np, XS_BF16, stream) != XS_OK)
+        return XS_ERR_CUDA;
+      prefix_k = area;
+      prefix_v = v;
+      pk_stride[0] = pv_stride[0] = st[1];
+      pk_stride[1] = pv_stride[1] = d;
+      area += prefix_bytes;
+    }
+    if (own_cached) {
+      const long long st[3] = {static_cast<long long>(Hk) * Nk * d, static_cast<long long>(Nk) * d, d};
+      char *v = area + own_bytes / 2;
+      if (xs_cache_read(&a->cache, area, v, st, st, &a->pages, nullptr, a->kv_len, B, Nk, XS_BF16, stream) != XS_OK)
+        return XS_ERR_CUDA;
+      own_k = area;
+      own_v = v;
+      std::memcpy(k_stride, st, sizeof(st));
+      std::memcpy(v_stride, st, sizeof(st));
+      area += own_bytes;
+    }
+    parts_room -= prefix_bytes + own_bytes;
+  } else {
+    p.prefix_cached = prefix_cached;
+    p.own_cached = own_cached;
+    if (prefix_cached || own_cached) {
+      p.prefix_pages = lists_of(a->cache, &a->prefix_pages);
+      p.own_pages = lists_of(a->cache, &a->pages);
+      p.codes[0] = static_cast<const uint8_t *>(a->cache.k);
+      p.codes[1] = static_cast<const uint8_t *>(a->cache.v);
+      p.scales[0] = a->cache.k_scale;
+      p.scales[1] = a->cache.v_scale;
+    }
+  }
+  p.parts = reinterpret_cast<float *>(area);
+  const unsigned box = tall ? kTileRows : 16;
+  if (Np > 0 && !p.prefix_cached &&
+      (!encode_operand(&p.tm_pk, prefix_k, 1, Hk, Np, d, 0, pk_stride[0], pk_stride[1], kTileRows) ||
+       !encode_operand(&p.tm_pv, prefix_v, 1, Hk, Np, d, 0, pv_stride[0], pv_stride[1], kTileRows)))
     return XS_ERR_CUDA;
-  if (dense_own &&
-      (!encode_operand(&p.tm_k, a->k, B, Hk, Nk, d, a->k_stride[0], a->k_stride[1], a->k_stride[2], grain) ||
-       !encode_operand(&p.tm_v, a->v, B, Hk, Nk, d, a->v_stride[0], a->v_stride[1], a->v_stride[2], grain)))
+  if (Nk > 0 && !p.own_cached &&
+      (!encode_operand(&p.tm_k, own_k, B, Hk, Nk, d, k_stride[0], k_stride[1], k_stride[2], box) ||
+       !encode_operand(&p.tm_v, own_v, B, Hk, Nk, d, v_stride[0], v_stride[1], v_stride[2], box)))
     return XS_ERR_CUDA;
-  p.grain = grain;
+  if (tall && !encode_operand(&p.tm_q, a->q, B, H, Nq, d, p.q_b, p.q_h, p.q_n, 8)) return XS_ERR_CUDA;
   p.n_prefix = (Np + kTileRows - 1) / kTileRows;
+  p.min_places = kLeast;
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
   if (device_status_word(&p.status) != cudaSuccess) return XS_ERR_CUDA;
   p.wait_limit_ns = wait_limit_ns();
-  unsigned long long room = 0;
-  if (ws && ws_bytes > kCutsBytes) {
-    room = ws_bytes - kCutsBytes;
-    p.cuts = static_cast<int4 *>(ws);
-    p.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + kCutsBytes);
-  }
   for (int b0 = 0; b0 < B; b0 += chunk) {
+    shape.B = B - b0 < chunk ? B - b0 : chunk;
+    const Choice c = choose(shape, tall, sms, parts_room);
     p.b0 = b0;
-    p.B = B - b0 < chunk ? B - b0 : chunk;
-    p.q = static_cast<const uint16_t *>(a->q) + b0 * a->q_stride[0];
-    if (!shards) p.o = static_cast<uint16_t *>(o) + b0 * o_stride[0];
+    p.B = shape.B;
+    p.q = static_cast<const uint16_t *>(a->q) + b0 * p.q_b;
+    if (!shards) p.o = static_cast<uint16_t *>(o) + b0 * p.o_b;
     p.kv_len = a->kv_len ? a->kv_len + b0 : nullptr;
-    if (own_cached) p.own_pages.pages = a->pages.pages + b0 * a->pages.stride;
-    p.nq_rows = Nq;
-    p.entry_rows = group * Nq;
-    p.rows = p.B * p.entry_rows;
-    p.copies = p.rows <= 32 ? 4 : p.rows <= 64 ? 2 : 1;
-    p.row_tile = kTileRows / p.copies;
-    p.n_tiles = (p.rows + p.row_tile - 1) / p.row_tile;
-    p.n_units = Hk * p.n_tiles;
-    // Own tiles of a unit: those of the entries that its rows belong to.
-    const long long entries = p.entry_rows >= p.row_tile ? 1 : (p.row_tile < p.rows ? p.row_tile : p.rows) / p.entry_rows;
-    const long long keys = entries * padded, tiles = p.n_prefix + (keys - (a->kv_len ? keys / 4 : 0) + kTileRows - 1) / kTileRows;
-    p.min_places = 4;
-    const Plan pl = plan(p.n_units, sms, tiles, p.min_places, 2ull * prefix_part_floats(d, kTileRows) * 4, room);
-    p.split = pl.split;
-    p.waves = pl.waves;
-    if (launch_prefix_flat(p, d, pl.grid, s) != cudaSuccess) return XS_ERR_CUDA;
-    if (pl.split && launch_prefix_join(p, d, pl.grid, s) != cudaSuccess) return XS_ERR_CUDA;
+    if (p.own_cached) p.own_pages.pages = a->pages.pages + b0 * a->pages.stride;
+    p.grain = c.grain;
+    p.nq_rows = c.nq_rows;
+    p.entry_rows = group * c.nq_rows;
+    p.rows = static_cast<int>(c.rows);
+    p.copies = c.copies;
+    p.row_tile = c.row_tile;
+    p.n_tiles = c.n_tiles;
+    p.n_units = Hk * c.n_tiles;
+    p.split = c.plan.split;
+    p.waves = c.plan.waves;
+    if ((tall ? launch_prefix_tall : launch_prefix_flat)(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;
+    if (p.split && launch_prefix_join(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;
   }
   return XS_OK;
 }
@@ -223,15 +306,22 @@ XS_API xs_status xs_prefix_attn_fused(const xs_prefix_args *args, void *const *o
   return prefix_call(args, nullptr, nullptr, out_shards, P, ws, ws_bytes, stream);
 }
 
-XS_API xs_status xs_prefix_workspace_bytes(int B, int H, int H_kv, int Nq, int Np, int Nk, int d,
+XS_API xs_status xs_prefix_workspace_bytes(int B, int H, int H_kv, int Nq, int Np, int Nk, int d, int cached,
                                            unsigned long long *bytes) {
-  if (!bytes || B < 0 || H < 0 || H_kv < 0 || Nq < 0 || Np < 0 || Nk < 0) return XS_ERR_INVALID;
+  if (!bytes || B < 0 || H < 0 || H_kv < 0 || Nq < 0 || Np < 0 || Nk < 0 ||
+      (cached & ~(XS_PREFIX_CACHED | XS_OWN_CACHED)) != 0)
+    return XS_ERR_INVALID;
   if (H > 0 && (H_kv < 1 || H % H_kv != 0)) return XS_ERR_INVALID;
   if (d != 64 && d != 128) return XS_ERR_UNSUPPORTED;
   *bytes = 0;
   if (B == 0 || H == 0 || Nq == 0) return XS_OK;
   const int sms = sm_count();
   if (sms <= 0) return XS_ERR_CUDA;
-  *bytes = kCutsBytes + 2ull * sms * prefix_part_floats(d, kTileRows) * 4;
+  *bytes = kCutsBytes + 2ull * sms * prefix_part_floats(d, 2 * kTileRows) * 4;
+  // Rows that one tile of the flat kernel holds never go to the tall one.
+  if (static_cast<double>(B) * (H / H_kv) * Nq > kTileRows) {
+    if (cached & XS_PREFIX_CACHED) *bytes += unpacked(static_cast<long long>(H_kv) * Np, d);
+    if (cached & XS_OWN_CACHED) *bytes += unpacked(static_cast<long long>(B) * H_kv * Nk, d);
+  }
   return XS_OK;
 }

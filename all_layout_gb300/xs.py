@@ -97,7 +97,7 @@ _lib.xs_cache_write.argtypes = [_vp] * 8 + [_i, _i, _i, _vp]
 _lib.xs_cache_read.argtypes = [_vp] * 8 + [_i, _i, _i, _vp]
 _lib.xs_prefix_attn.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_ulonglong, _vp]
 _lib.xs_prefix_attn_fused.argtypes = [_vp, _vp, _i, _vp, ctypes.c_ulonglong, _vp]
-_lib.xs_prefix_workspace_bytes.argtypes = [_i] * 7 + [ctypes.POINTER(ctypes.c_ulonglong)]
+_lib.xs_prefix_workspace_bytes.argtypes = [_i] * 8 + [ctypes.POINTER(ctypes.c_ulonglong)]
 for _f in ("xs_cache_write", "xs_cache_read", "xs_prefix_attn", "xs_prefix_attn_fused", "xs_prefix_workspace_bytes"):
     getattr(_lib, _f).restype = _i
 
@@ -563,12 +563,15 @@ def prefix_attn_fused(q, shards, *, prefix_k=None, prefix_v=None, k=None, v=None
            "xs_prefix_attn_fused")
 
 
-def alloc_prefix_workspace(B: int, H: int, H_kv: int, Nq: int, Np: int, Nk: int, d: int, device="cuda"):
+def alloc_prefix_workspace(B: int, H: int, H_kv: int, Nq: int, Np: int, Nk: int, d: int, prefix_cached: bool = False,
+                           own_cached: bool = False, device="cuda"):
     """A workspace (through torch) with which prefix_attn and prefix_attn_fused of this shape can take
-    every schedule; larger shapes' workspaces serve smaller ones."""
+    every schedule; larger shapes' workspaces serve smaller ones. prefix_cached, own_cached: which
+    keys and values lie in a cache."""
     n = ctypes.c_ulonglong(0)
     with torch.cuda.device(device):
-        _check(_lib.xs_prefix_workspace_bytes(B, H, H_kv, Nq, Np, Nk, d, ctypes.byref(n)), "xs_prefix_workspace_bytes")
+        _check(_lib.xs_prefix_workspace_bytes(B, H, H_kv, Nq, Np, Nk, d, (1 if prefix_cached else 0) | (2 if own_cached else 0),
+                                              ctypes.byref(n)), "xs_prefix_workspace_bytes")
         return torch.empty(int(n.value), dtype=torch.uint8, device=device)
 
 

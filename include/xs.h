@@ -483,12 +483,18 @@ xs_status xs_prefix_attn(const xs_prefix_args *args, void *o, const long long *o
 xs_status xs_prefix_attn_fused(const xs_prefix_args *args, void *const *out_shards, int P,
                                void *ws, unsigned long long ws_bytes, void *stream);
 
+/* Flags of xs_prefix_workspace_bytes: which part lies in the cache. */
+#define XS_PREFIX_CACHED 1
+#define XS_OWN_CACHED 2
+
 /* *bytes = the workspace with which a call of this shape on the current device can take
- * every schedule. XS_ERR_INVALID for a NULL bytes, negative sizes or H not a multiple of
- * H_kv, XS_ERR_UNSUPPORTED for d not in {64, 128}, XS_ERR_CUDA if the device cannot be
- * queried. */
+ * every schedule. With more than 128 queries for each k/v head (of all requests and of the
+ * heads that share it) that includes room for the cached keys and values in bf16, which such
+ * a call reads back first; with less a call reads them as they are, more slowly then.
+ * XS_ERR_INVALID for a NULL bytes, negative sizes, other flags or H not a multiple of H_kv,
+ * XS_ERR_UNSUPPORTED for d not in {64, 128}, XS_ERR_CUDA if the device cannot be queried. */
 xs_status xs_prefix_workspace_bytes(int B, int H, int H_kv, int Nq, int Np, int Nk, int d,
-                                    unsigned long long *bytes);
+                                    int cached, unsigned long long *bytes);
 
 /* Static English text for a status code; never NULL. */
 const char *xs_status_string(xs_status s);

@@ -76,7 +76,7 @@ class Problem:
 
     def workspace(self):
         B, H, Hk, d, Nq, Np, Nk = self.shape
-        ws = self.xs.alloc_prefix_workspace(B, H, Hk, Nq, Np, Nk, d)
+        ws = self.xs.alloc_prefix_workspace(B, H, Hk, Nq, Np, Nk, d, prefix_cached="prefix_pages" in self.kw, own_cached="pages" in self.kw)
         return ws.fill_(0xff)   # any content will do
 
     def want(self):
@@ -116,6 +116,12 @@ KINDS = [("bf16", "bf16"), ("cache", "bf16"), ("bf16", "cache"), ("cache", "cach
     (2, 2, 2, 128, 300, 0, 500, [500, 7]),
     (3, 2, 1, 128, 129, 300, 0, None),
     (40, 2, 2, 128, 1, 200, 60, [(7 * b) % 61 for b in range(40)]),
+    # Many rows: pairs of tiles, over several requests and heads, with requests between that have no keys.
+    (2, 4, 2, 128, 640, 700, 900, [900, 333]),
+    (3, 2, 1, 64, 500, 1000, 300, [1, 0, 300]),
+    (7, 4, 2, 128, 100, 300, 200, [200, 0, 0, 128, 129, 0, 1]),
+    (4, 3, 3, 64, 257, 0, 513, [0, 513, 512, 0]),
+    (2, 8, 1, 128, 321, 129, 0, None),
 ])
 def test_formula(xs, prefix, own, B, H, Hk, d, Nq, Np, Nk, lens):
     Problem(xs, B, H, Hk, d, Nq, Np, Nk, lens, prefix, own, seed=B + Nq).test()

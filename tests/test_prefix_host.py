@@ -67,11 +67,12 @@ def test_null_shard_array(xs):
 def test_workspace_refusals(xs):
     n = ctypes.c_ulonglong(7)
     call = lambda *a: xs.library().xs_prefix_workspace_bytes(*a, ctypes.byref(n))   # noqa: E731
-    assert xs.library().xs_prefix_workspace_bytes(1, 2, 2, 1, 8, 8, 64, None) == xs.ERR_INVALID
-    assert call(-1, 2, 2, 1, 8, 8, 64) == xs.ERR_INVALID
-    assert call(1, 3, 2, 1, 8, 8, 64) == xs.ERR_INVALID
-    assert call(1, 2, 2, 1, 8, 8, 256) == xs.ERR_UNSUPPORTED
-    assert call(0, 2, 2, 1, 8, 8, 64) == xs.OK and n.value == 0
+    assert xs.library().xs_prefix_workspace_bytes(1, 2, 2, 1, 8, 8, 64, 0, None) == xs.ERR_INVALID
+    assert call(-1, 2, 2, 1, 8, 8, 64, 0) == xs.ERR_INVALID
+    assert call(1, 3, 2, 1, 8, 8, 64, 0) == xs.ERR_INVALID
+    assert call(1, 2, 2, 1, 8, 8, 64, 4) == xs.ERR_INVALID
+    assert call(1, 2, 2, 1, 8, 8, 256, 0) == xs.ERR_UNSUPPORTED
+    assert call(0, 2, 2, 1, 8, 8, 64, 3) == xs.OK and n.value == 0
 
 
 def test_binding_refuses(xs):
