@@ -139,6 +139,11 @@ struct PrefixWalk {
   }
 };
 
+// One call in memory of its own, so that neither walk nor item takes registers between items.
+__device__ __noinline__ bool next_item(const PrefixParams &p, const int *table, PrefixWalk *walk, PrefixItem *item) {
+  return walk->next(p, table, *item);
+}
+
 // The split region's size and this CTA's place in it, by one warp.
 __device__ PrefixPlan plan_split(const PrefixParams &p, const int *table) {
   const int lane = threadIdx.x & 31, first = p.waves * static_cast<int>(gridDim.x);

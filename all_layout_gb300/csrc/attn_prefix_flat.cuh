@@ -121,7 +121,7 @@ __device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars
     }
     return r;
   };
-  while (ok && walk.next(p, table, item)) {
+  while (ok && next_item(p, table, &walk, &item)) {
     Part ahead = part_at(item.kv0);
     for (int j = item.kv0; ok && j < item.kv1; ++j) {
       const Part r = ahead;
@@ -330,7 +330,7 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
   };
 
   bool ok = true;
-  for (; ok && walk.next(p, table, item); ++items) {
+  for (; ok && next_item(p, table, &walk, &item); ++items) {
     if (V) {   // the queries, a row a thread; the copies begin at multiples of row_tile
       const int row = item.row0 + tid % p.row_tile;
       const uint16_t *src = nullptr;
@@ -390,7 +390,7 @@ __device__ void flat_mma(const PrefixParams &p, uint8_t *smem, FlatBars *bars, c
   PrefixWalk walk;
   walk.start(p, bars->plan);
   PrefixItem item;
-  for (; walk.next(p, table, item); ++items) {
+  for (; next_item(p, table, &walk, &item); ++items) {
     const int n = uniform(item.kv1 - item.kv0);
     if (!wait(bars->q_full, items & 1)) goto done;
     for (int i = 0; i <= n; ++i) {
@@ -492,7 +492,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
   walk.start(p, bars->plan);
   PrefixItem item;
   bool cut = false;   // a piece was this CTA's first of its unit
-  for (; walk.next(p, table, item); ++items) {
+  for (; next_item(p, table, &walk, &item); ++items) {
     const int row = item.row0 + in;
     const bool idle = item.row0 + (wq * 32) % RT >= p.rows;   // no row in this warp
     const PrefixRange own = range_of(p, table, row);

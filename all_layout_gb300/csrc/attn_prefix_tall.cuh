@@ -89,7 +89,7 @@ __device__ void tall_loader(const PrefixParams &p, uint8_t *smem, TallBars *bars
   walk.start(p, bars->plan);
   PrefixItem item;
   bool ok = true;
-  for (; ok && walk.next(p, table, item); ++items) {
+  for (; ok && next_item(p, table, &walk, &item); ++items) {
     if (items > 0) ok = wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p);
     if (!ok) break;
     {
@@ -163,7 +163,7 @@ __device__ void tall_mma(const PrefixParams &p, uint8_t *smem, TallBars *bars, c
   PrefixWalk walk;
   walk.start(p, bars->plan);
   PrefixItem item;
-  for (; walk.next(p, table, item); ++items) {
+  for (; next_item(p, table, &walk, &item); ++items) {
     const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
     TallTiles tiles[2];
 #pragma unroll
@@ -174,7 +174,43 @@ __device__ void tall_mma(const PrefixParams &p, uint8_t *smem, TallBars *bars, c
     int b = item.b_lo;
     if (!wait(bars->q_full, items & 1)) goto done;
     bool active[2] = {false, false}, fresh[2] = {true, true};   // at the tile before; no product of this item yet
+    // Tiles before `plain`: both row tiles take them, and no V but the last has rows to clear.
+    const int plain = uniform(item.row0 + BM >= p.rows ? 0 : item.b_lo == item.b_hi ? kv1 : min(kv1, p.n_prefix));
     for (int j = kv0; j <= kv1; ++j, ++use) {
+      // Between two of them both row tiles have a product and scores.
+      if (j > kv0 && j < plain) {
+        for (; j < plain; ++j, ++use) {
+          const uint32_t vs = (use - 1) % C::VS, ks = use % C::KS;
+          const uint64_t vd = vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), kd = kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4));
+          if (!wait(bars->v_full[vs], (use - 1) / C::VS & 1)) goto done;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!wait(bars->p_full[t], pc >> t & 1)) goto done;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_pv<D>(tmem + 256 + t * D, tmem + t * 128, vd, fresh[t] ? 0u : 1u);
+              if (t == 1) tc_commit(smem_u32(&bars->v_empty[vs]));
+            }
+            __syncwarp();
+            // (K is waited for after the first product, which does not need it.)
+            if (t == 0) {
+              if (!wait(bars->k_full[ks], use / C::KS & 1)) goto done;
+              tc_fence_after();
+            }
+            if (elect_one()) {
+              issue_qk<D>(tmem + t * 128, qdesc + static_cast<uint64_t>(t * (C::TILE >> 4)), kd);
+              tc_commit(smem_u32(&bars->s_full[t]));
+              if (t == 1) {
+                tc_commit(smem_u32(&bars->k_empty[ks]));
+                if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+              }
+            }
+            __syncwarp();
+            fresh[t] = false;
+          }
+          pc ^= 3u;
+        }
+      }
       const uint32_t vs = (use - 1) % C::VS, ks = use % C::KS;   // the last tile's V, this one's K
       const bool now[2] = {j < kv1 && tiles[0].has(j), j < kv1 && tiles[1].has(j)};
       if (j > kv0) {
@@ -184,39 +220,50 @@ __device__ void tall_mma(const PrefixParams &p, uint8_t *smem, TallBars *bars, c
           if (valid < BN) clear_tail(vs, valid);
         }
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (active[t]) {
-          if (!wait(bars->p_full[t], pc >> t & 1)) goto done;
-          pc ^= 1u << t;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_pv<D>(tmem + 256 + t * D, tmem + t * 128, vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), fresh[t] ? 0u : 1u);
-            if (j - 1 == tiles[t].last()) tc_commit(smem_u32(&bars->o_full[t]));
-          }
-          __syncwarp();
-          fresh[t] = false;
-        }
-        // (K is waited for after the first product, which does not need it.)
-        if (t == 0 && j < kv1) {
-          if (!wait(bars->k_full[ks], use / C::KS & 1)) goto done;
-          tc_fence_after();
-        }
-        if (now[t]) {
-          if (elect_one()) {
-            issue_qk<D>(tmem + t * 128, qdesc + static_cast<uint64_t>(t * (C::TILE >> 4)), kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)));
-            tc_commit(smem_u32(&bars->s_full[t]));
-          }
-          __syncwarp();
-        }
-        if (t == 1 && elect_one()) {
-          if (j > kv0) tc_commit(smem_u32(&bars->v_empty[vs]));
-          if (j < kv1) tc_commit(smem_u32(&bars->k_empty[ks]));
-          if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+      const uint64_t vd = vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), kd = kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4));
+      if (active[0]) {
+        if (!wait(bars->p_full[0], pc & 1)) goto done;
+        pc ^= 1u;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_pv<D>(tmem + 256, tmem, vd, fresh[0] ? 0u : 1u);
+          if (j - 1 == tiles[0].last()) tc_commit(smem_u32(&bars->o_full[0]));
         }
         __syncwarp();
-        active[t] = now[t];
+        fresh[0] = false;
       }
+      // (K is waited for after the first product, which does not need it.)
+      if (j < kv1) {
+        if (!wait(bars->k_full[ks], use / C::KS & 1)) goto done;
+        tc_fence_after();
+        if (now[0] && elect_one()) {
+          issue_qk<D>(tmem, qdesc, kd);
+          tc_commit(smem_u32(&bars->s_full[0]));
+        }
+        __syncwarp();
+      }
+      if (active[1]) {
+        if (!wait(bars->p_full[1], pc >> 1 & 1)) goto done;
+        pc ^= 2u;
+        tc_fence_after();
+      }
+      if (elect_one()) {
+        if (active[1]) {
+          issue_pv<D>(tmem + 256 + D, tmem + 128, vd, fresh[1] ? 0u : 1u);
+          if (j - 1 == tiles[1].last()) tc_commit(smem_u32(&bars->o_full[1]));
+        }
+        if (now[1]) {
+          issue_qk<D>(tmem + 128, qdesc + static_cast<uint64_t>(C::TILE >> 4), kd);
+          tc_commit(smem_u32(&bars->s_full[1]));
+        }
+        if (j > kv0) tc_commit(smem_u32(&bars->v_empty[vs]));
+        if (j < kv1) tc_commit(smem_u32(&bars->k_empty[ks]));
+        if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+      }
+      __syncwarp();
+      if (active[1]) fresh[1] = false;
+      active[0] = now[0];
+      active[1] = now[1];
     }
     --use;   // (the step past the last tile has no K)
   }
@@ -243,34 +290,46 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
   walk.start(p, bars->plan);
   PrefixItem item;
   bool cut = false, ok = true;   // a piece was this CTA's first of its unit
-  while (ok && walk.next(p, table, item)) {
+  while (ok && next_item(p, table, &walk, &item)) {
     const int row = item.row0 + t * BM + in;
     const TallTiles tiles = tiles_of(p, table, item, t);
     const PrefixRange own = range_of(p, table, row);
     const int n = tiles.count();
     float m = -INFINITY, l = 0.f;
-    int j = tiles.prefix > tiles.kv0 ? tiles.kv0 : tiles.own0;
-    for (int i = 0; i < n; ++i, ++step) {
-      const int lo = j < p.n_prefix ? 0 : own.lo - own_pos(p, item, j);
-      const int hi = j < p.n_prefix ? p.Np - j * BN : own.hi - own_pos(p, item, j);
-      if (++j == tiles.prefix) j = tiles.own0;
+    // The keys [lo, hi) of a tile that the row sees: first the prefix's tiles, then its own.
+    const int n_own = n - (tiles.own1 - tiles.own0), own_lo = own.lo - own_pos(p, item, tiles.own0), own_len = own.hi - own.lo;
+    int lo = -tiles.kv0 * BN, hi = p.Np - tiles.kv0 * BN;
+    for (int i = 0; i < n; ++i, ++step, lo -= BN, hi -= BN) {
+      if (i == n_own) {
+        lo = own_lo;
+        hi = own_lo + own_len;
+      }
+      const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < BN);
       if (!wait_for<true>(s_full, step & 1, abort_flag, p)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      // The first half's maximum beside the second half's load.
       uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
-      if (__any_sync(0xffffffffu, lo > 0 || hi < BN)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mask32(s[c], bits_of(lo - 32 * c, hi - 32 * c));
+      tmem_ld32(tS, s[0]);
+      tmem_ld32(tS + 32, s[1]);
+      tmem_wait_ld_regs(s[0]);
+      tmem_wait_ld_regs(s[1]);
+      tmem_ld32(tS + 64, s[2]);
+      tmem_ld32(tS + 96, s[3]);
+      if (masked) {
+        mask32(s[0], bits_of(lo, hi));
+        mask32(s[1], bits_of(lo - 32, hi - 32));
       }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mx = max32(s[c], mx);
+      float mx = max32(s[1], max32(s[0], -INFINITY));
+      tmem_wait_ld_regs(s[2]);
+      tmem_wait_ld_regs(s[3]);
+      if (masked) {
+        mask32(s[2], bits_of(lo - 64, hi - 64));
+        mask32(s[3], bits_of(lo - 96, hi - 96));
+      }
+      mx = max32(s[3], max32(s[2], mx));
       const float m_new = fmaxf(m, mx * scale);
       float alpha = 1.f;
       bool rescale = false;
