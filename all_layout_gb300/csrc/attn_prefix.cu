@@ -262,10 +262,6 @@ __device__ __noinline__ void drain(uint32_t bar, uint32_t parity) {
   while (!mbar_try_wait(bar, parity))
     if (globaltimer_ns() - t0 > 2000000000ull) return;
 }
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
-
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z,
                                             int w) {
   asm volatile(

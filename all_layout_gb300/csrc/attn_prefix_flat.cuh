@@ -259,7 +259,9 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     if (j < p.n_prefix) return min(max(p.Np - j * BN - lane * 16, 0), 16);
     return grain_of(p, table, item, own_pos(p, item, j) + lane * 16).valid;
   };
-  // TMA loads of a tile that is not cached, use `u` of the ring.
+  // TMA loads of a tile that is not cached, use `u` of the ring. All warps wait for the slot and arrive at its
+  // barrier, though one of them issues: a phase then cannot end before each has seen the one before it. (One
+  // that fell two phases behind would take the next for its own.)
   auto issue = [&](int j, uint32_t u) {
     if (j >= item.kv1 || is_cached(p, j)) return true;
     const uint32_t slot = u % S, parity = u / S & 1;
@@ -269,10 +271,10 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     if (j < p.n_prefix) {   // (rows past Np come as zeros)
       if (issuer && lane == 0) {
         mbar_arrive_expect_tx(full, C::TILE);
-        mbar_arrive_n(full, kFlatOperandWarps - 1);
         for (int hf = 0; hf < D / 64; ++hf)
           tma_load_4d(dst + hf * kHalf, V ? &p.tm_pv : &p.tm_pk, full, hf * 64, j * BN, item.hk, 0);
       }
+      if (!issuer && lane == 0) mbar_arrive(full);
       loading(slot, parity);
     } else {
       Grain g{0, 0, 0};
@@ -282,14 +284,13 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
       const bool whole = !V || __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16;
       if (!whole) full = smem_u32(&bars->raw[slot]);
       if (issuer) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full, bytes);
-          if (whole) mbar_arrive_n(full, kFlatOperandWarps - 1);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
         if (g.valid > 0)
           for (int hf = 0; hf < D / 64; ++hf)
             tma_load_4d(dst + hf * kHalf + lane * 2048, V ? &p.tm_v : &p.tm_k, full, hf * 64, g.off, item.hk, p.b0 + g.b);
+      } else if (whole && lane == 0) {
+        mbar_arrive(full);
       }
       pending &= ~(1u << slot);
       if (whole) loading(slot, parity); else loading(2 + slot, raw_parity >> slot & 1);
