@@ -7,15 +7,16 @@
 // and the epilogue adds the copies' results, each with its own maximum and sum.
 //
 // Cached keys and values: the loader copies a tile's codes and scales into a ring of raw slots, and
-// four warps each turn K's and V's into bf16 operands in rings of their own. A code's bits moved to bf16's
+// eight warps each turn K's and V's into bf16 operands in rings of their own. A code's bits moved to bf16's
 // place stand for code * 2^-120, so one product with 2^(120 + e) is exact (e > 7 takes two).
 //
-// Roles (448 threads, one CTA per SM):
+// Roles (768 threads, one CTA per SM):
 //   warps 0-3   softmax, row r of the tile = TMEM lane r
-//   warps 4-7   K: codes to bf16, TMA loads of tiles that are not cached
-//   warps 8-11  V, and the queries to Tensor Memory
-//   warp 12     MMA issuer, Tensor Memory allocation
-//   warp 13     loads of codes and scales
+//   warps 4-11  K: codes to bf16, TMA loads of tiles that are not cached
+//   warps 12-19 V, and the queries to Tensor Memory
+//   warp 20     MMA issuer, Tensor Memory allocation
+//   warp 21     loads of codes and scales
+//   warps 22-23 nothing
 // Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) Q (bf16 pairs) [384,384+d/2); P_t over S_t's
 // first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax. The issuer's
 // order is QK(i), PV(i-1): QK(i) overwrites P(i-2), whose product went out before it.
@@ -25,7 +26,7 @@
 
 template <int D>
 struct FlatCfg {
-  static constexpr int THREADS = 448;
+  static constexpr int THREADS = 768;
   static constexpr int TILE = BN * D * 2, RAW = BN * D + BN;   // a bf16 tile; codes and scale bytes
   static constexpr int KS = 2, VS = 2, FK = D == 128 ? 3 : 5, FV = D == 128 ? 2 : 5, FS = FK + FV;
   static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * TILE, OFF_F = OFF_V + VS * TILE;
@@ -38,7 +39,7 @@ struct FlatCfg {
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(OFF_BAR % 16 == 0 && RAW % 16 == 0, "alignment");
 };
-constexpr int kFlatKeys = 4, kFlatValues = 8, kFlatOperandWarps = 4, kFlatMma = 12, kFlatLoad = 13;   // warps
+constexpr int kFlatKeys = 4, kFlatValues = 12, kFlatOperandWarps = 8, kFlatMma = 20, kFlatLoad = 21;   // warps
 
 struct FlatBars {
   uint64_t q_full, q_empty;
@@ -166,67 +167,67 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Two e4m3 codes in bits 8-15 and 24-31 of x: the bf16 pair of their values times 2^-120.
-__device__ __forceinline__ uint32_t spread(uint32_t x) {
-  return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+// Bytes of x by selector; 8 to 11 are the sign bits of bytes 0 to 3, eight times each.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t prmt(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
+  return r;
 }
-// Sixteen codes of a row with scale byte `byte` to bf16. PLAIN: the byte is at most 134.
+// Two e4m3 codes as 16-bit integers with their signs extended: the bf16 pair of their values times 2^-120.
+__device__ __forceinline__ uint32_t spread(uint32_t z) { return z << 4 & 0x87f087f0u; }
+// Eight codes of a row with scale byte `byte` to bf16. PLAIN: the byte is at most 134.
 template <bool PLAIN>
-__device__ __forceinline__ void to_bf16(const uint4 &c, uint32_t byte, uint32_t (&r)[8]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  // 2^(120 + e) in bf16 for e = byte - 127 <= 7.
-  uint32_t f = (PLAIN ? byte + 120u : min(byte, 134u) + 120u) << 7;
-  if (!PLAIN && byte == kNanScale) f = 0x7fffu;
-  const uint32_t f2 = __byte_perm(f, 0, 0x1010);
+__device__ __forceinline__ uint4 to_bf16(uint32_t c0, uint32_t c1, uint32_t byte) {
+  // 2^(120 + e) in bf16, twice, for e = byte - 127 <= 7.
+  uint32_t f = (PLAIN ? byte : min(byte, 134u)) * 0x00800080u + 0x3c003c00u;
+  if (!PLAIN && byte == kNanScale) f = 0x7fff7fffu;
+  uint32_t r[4] = {spread(prmt<0x9180>(c0)), spread(prmt<0xb3a2>(c0)), spread(prmt<0x9180>(c1)), spread(prmt<0xb3a2>(c1))};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[2 * i] = mul_bf16x2(spread(__byte_perm(w[i], 0, 0x1404)), f2);
-    r[2 * i + 1] = mul_bf16x2(spread(__byte_perm(w[i], 0, 0x3424)), f2);
-  }
+  for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], f);
   if (!PLAIN && byte > 134 && byte != kNanScale) {
-    const uint32_t g2 = __byte_perm((byte - 134 + 127) << 7, 0, 0x1010);
+    const uint32_t g = (byte - 134 + 127) * 0x00800080u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = mul_bf16x2(r[i], g2);
+    for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], g);
   }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Codes and scale bytes of a raw slot to a bf16 tile, by four warps; `valid`: see valid_of. A thread has one
+// Codes and scale bytes of a raw slot to a bf16 tile, by eight warps; `valid`: see valid_of. A thread has one
 // 16-byte group of every STEP-th row, so its place in the swizzle stays. One copy of short loops for K's and
 // V's warps: with all groups unrolled in each the warps waited for instructions.
 template <int D>
-__device__ __noinline__ void convert_tile(const uint8_t *src, uint8_t *dst, int valid) {
+__device__ __noinline__ void convert_tile(const uint8_t *src, uint8_t *dst, int valid, uint32_t tid) {
   constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR;   // groups of a row's codes
-  const uint32_t tid = threadIdx.x & 127, lane = tid & 31;
+  const uint32_t lane = tid & 31;
   const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
   const uint32_t bytes = *reinterpret_cast<const uint32_t *>(src + BN * D + lane * 4);
   const uint8_t *scales = src + BN * D + row0;
   src += tid * 16;
   dst += (cc / 4) * kHalf + row0 * 128;
   // (Of a group's two chunks the second half's lanes store the second one first, which spares conflicts.)
-  const uint32_t c0 = ((first + odd) ^ (row0 & 7)) * 16, c1 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
+  const uint32_t first0 = ((first + odd) ^ (row0 & 7)) * 16, second0 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
   const bool clear = __any_sync(0xffffffffu, valid < 16);
   if (!clear && !__any_sync(0xffffffffu, __vcmpgtu4(bytes, 0x86868686u) != 0)) {
 #pragma unroll 2
     for (uint32_t i = 0; i < BN / STEP; ++i) {
-      uint32_t r[8];
-      to_bf16<true>(*reinterpret_cast<const uint4 *>(src + i * STEP * D), scales[i * STEP], r);
+      const uint4 c = *reinterpret_cast<const uint4 *>(src + i * STEP * D);
+      const uint32_t byte = scales[i * STEP];
       uint8_t *to = dst + i * STEP * 128;
-      *reinterpret_cast<uint4 *>(to + c0) = odd ? make_uint4(r[4], r[5], r[6], r[7]) : make_uint4(r[0], r[1], r[2], r[3]);
-      *reinterpret_cast<uint4 *>(to + c1) = odd ? make_uint4(r[0], r[1], r[2], r[3]) : make_uint4(r[4], r[5], r[6], r[7]);
+      *reinterpret_cast<uint4 *>(to + first0) = to_bf16<true>(odd ? c.z : c.x, odd ? c.w : c.y, byte);
+      *reinterpret_cast<uint4 *>(to + second0) = to_bf16<true>(odd ? c.x : c.z, odd ? c.y : c.w, byte);
     }
     return;
   }
 #pragma unroll 1
   for (uint32_t i = 0; i < BN / STEP; ++i) {
-    uint32_t r[8];
-    to_bf16<false>(*reinterpret_cast<const uint4 *>(src + i * STEP * D), scales[i * STEP], r);
-    const uint32_t row = row0 + i * STEP;
-    if (static_cast<int>(row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4))
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] = 0;
+    const uint4 c = *reinterpret_cast<const uint4 *>(src + i * STEP * D);
+    const uint32_t byte = scales[i * STEP], row = row0 + i * STEP;
+    uint4 x = to_bf16<false>(odd ? c.z : c.x, odd ? c.w : c.y, byte), y = to_bf16<false>(odd ? c.x : c.z, odd ? c.y : c.w, byte);
+    if (static_cast<int>(row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4)) x = y = make_uint4(0, 0, 0, 0);
     uint8_t *to = dst + i * STEP * 128;
-    *reinterpret_cast<uint4 *>(to + c0) = odd ? make_uint4(r[4], r[5], r[6], r[7]) : make_uint4(r[0], r[1], r[2], r[3]);
-    *reinterpret_cast<uint4 *>(to + c1) = odd ? make_uint4(r[0], r[1], r[2], r[3]) : make_uint4(r[4], r[5], r[6], r[7]);
+    *reinterpret_cast<uint4 *>(to + first0) = x;
+    *reinterpret_cast<uint4 *>(to + second0) = y;
   }
 }
 
@@ -236,7 +237,7 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
   using C = FlatCfg<D>;
   constexpr uint32_t S = V ? C::VS : C::KS, F = V ? C::FV : C::FK, F0 = V ? C::FK : 0;   // slots; raw slots, the first
   volatile int *abort_flag = &bars->abort;
-  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const int tid = threadIdx.x - 32 * (V ? kFlatValues : kFlatKeys), lane = tid & 31;
   const bool issuer = tid < 32;
   uint64_t *full_of = V ? bars->v_full : bars->k_full, *empty_of = V ? bars->v_empty : bars->k_empty;
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<true>(smem_u32(&bar), parity, abort_flag, p); };
@@ -310,16 +311,17 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     if (cached) {
       if (!wait(bars->f_full[f], f_use / F & 1) || !wait(empty_of[slot], (use / S & 1) ^ 1)) return false;
       pending &= ~(1u << slot);
-      convert_tile<D>(smem + C::OFF_F + f * C::RAW, dst, valid);
+      convert_tile<D>(smem + C::OFF_F + f * C::RAW, dst, valid, tid);
       ++f_use;
     } else {
       if (!clear) return true;
       if (!wait(bars->raw[slot], raw_parity >> slot & 1)) return false;
       raw_parity ^= 1u << slot;
       pending &= ~(4u << slot);
-      if ((tid & 15) >= __shfl_sync(0xffffffffu, valid, tid >> 4))
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4 *>(dst + (i / 8) * kHalf + tid * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+      const int row = tid & (BM - 1), part = tid / BM;   // two threads a row
+      if ((row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4))
+        for (int i = part * (D / 16); i < (part + 1) * (D / 16); ++i)
+          *reinterpret_cast<uint4 *>(dst + (i / 8) * kHalf + row * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -332,7 +334,7 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
 
   bool ok = true;
   for (; ok && next_item(p, table, &walk, &item); ++items) {
-    if (V) {   // the queries, a row a thread; the copies begin at multiples of row_tile
+    if (V && tid < BM) {   // the queries, a row a thread; the copies begin at multiples of row_tile
       const int row = item.row0 + tid % p.row_tile;
       const uint16_t *src = nullptr;
       if (row < p.rows) {
@@ -340,20 +342,22 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
         if (r.n < p.Nq) src = p.q + r.b * p.q_b + r.h * p.q_h + r.n * p.q_n;
       }
       const uint32_t to = tmem + (static_cast<uint32_t>(tid & ~31) << 16) + C::COL_Q;
-      uint32_t q[D / 2];
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = src ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
-        q[4 * c] = v.x;
-        q[4 * c + 1] = v.y;
-        q[4 * c + 2] = v.z;
-        q[4 * c + 3] = v.w;
-      }
       if (items > 0) ok = wait(bars->q_empty, (items - 1) & 1);
       if (!ok) break;
       tc_fence_after();   // (the last item's scores, read from here, are done)
+#pragma unroll 2
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t q[16];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) tmem_st16(to + 16 * c, q + 16 * c);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = src ? __ldg(reinterpret_cast<const uint4 *>(src) + 4 * c + i) : make_uint4(0, 0, 0, 0);
+          q[4 * i] = v.x;
+          q[4 * i + 1] = v.y;
+          q[4 * i + 2] = v.z;
+          q[4 * i + 3] = v.w;
+        }
+        tmem_st16(to + 16 * c, q);
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&bars->q_full));
@@ -508,22 +512,18 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       tc_fence_after();
       const int first = (j < p.n_prefix ? j * BN : own_pos(p, item, j)) + copy * (NC * 32);
       const int lo = (j < p.n_prefix ? 0 : own.lo) - first, hi = (j < p.n_prefix ? p.Np : own.hi) - first;
-      // Two passes over the scores, as 128 of them would not fit the registers beside the rest: the
-      // maximum, then the weights (each chunk of P covers scores that have been read).
+      // Two passes over the scores, 32 at a time (a thread has 80 registers): the maximum, then the
+      // weights (each chunk of P covers scores that have been read).
       const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < NC * 32);
       const uint32_t tC = tS + copy * (NC * 32);
-      uint32_t s[2][32];
+      uint32_t s[32];
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NC; c += 2) {
-        tmem_ld32(tC + 32 * c, s[0]);
-        if (NC > 1) tmem_ld32(tC + 32 * c + 32, s[1]);
-#pragma unroll
-        for (int k = 0; k < (NC > 1 ? 2 : 1); ++k) {
-          tmem_wait_ld_regs(s[k]);
-          if (masked) mask32(s[k], bits_of(lo - 32 * (c + k), hi - 32 * (c + k)));
-          mx = max32(s[k], mx);
-        }
+      for (int c = 0; c < NC; ++c) {
+        tmem_ld32(tC + 32 * c, s);
+        tmem_wait_ld_regs(s);
+        if (masked) mask32(s, bits_of(lo - 32 * c, hi - 32 * c));
+        mx = max32(s, mx);
       }
       const float m_new = fmaxf(m, mx * p.scale_log2);
       float alpha = 1.f;
@@ -546,13 +546,13 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        if constexpr (NC == 4) {
-          tmem_ld32(tC + 32 * c, s[c & 1]);
-          tmem_wait_ld_regs(s[c & 1]);
-          if (masked) mask32(s[c & 1], bits_of(lo - 32 * c, hi - 32 * c));
+        if constexpr (NC > 1) {
+          tmem_ld32(tC + 32 * c, s);
+          tmem_wait_ld_regs(s);
+          if (masked) mask32(s, bits_of(lo - 32 * c, hi - 32 * c));
         }
         uint32_t pk[16];
-        weights32(s[c & 1], scale2, negm2, pk, sum);
+        weights32(s, scale2, negm2, pk, sum);
         tmem_st16(tS + 16 * (copy * NC + c), pk);
       }
       if constexpr (NC < 4) {
@@ -693,7 +693,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
 }
 
 template <int D>
-__global__ void __launch_bounds__(448, 1) prefix_flat_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(768, 1) prefix_flat_kernel(const __grid_constant__ PrefixParams p) {
   using C = FlatCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle pattern repeats every 1024 bytes
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -748,14 +748,15 @@ __global__ void __launch_bounds__(448, 1) prefix_flat_kernel(const __grid_consta
       flat_softmax<D, 2>(p, smem, bars, table, tmem);
     else
       flat_softmax<D, 1>(p, smem, bars, table, tmem);
-  } else if (warp < kFlatValues) {
-    flat_operands<D, false>(p, smem, bars, table, tmem);
-  } else if (warp < kFlatMma) {
-    flat_operands<D, true>(p, smem, bars, table, tmem);
-  } else if (warp == kFlatMma) {
-    flat_mma<D>(p, smem, bars, table, tmem);
   } else {
-    flat_loader<D>(p, smem, bars, table);
+    if (warp < kFlatValues)
+      flat_operands<D, false>(p, smem, bars, table, tmem);
+    else if (warp < kFlatMma)
+      flat_operands<D, true>(p, smem, bars, table, tmem);
+    else if (warp == kFlatMma)
+      flat_mma<D>(p, smem, bars, table, tmem);
+    else if (warp == kFlatLoad)
+      flat_loader<D>(p, smem, bars, table);
   }
   __syncwarp();
   tc_fence_before();
