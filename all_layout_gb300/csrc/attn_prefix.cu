@@ -44,18 +44,26 @@ __device__ __forceinline__ int keys_of(const PrefixParams &p, int b) {
   return p.kv_len ? min(max(__ldg(p.kv_len + b), 0), p.Nk) : p.Nk;
 }
 
-// Where each entry's own keys begin among the packed ones (start[B]: their end), by one warp.
+// Table in shared memory: where each entry's own keys begin among the packed ones ([B]: their end), and
+// from kLens on how many each has.
+constexpr int kLens = kPrefixEntries + 4, kTable = 2 * kLens;
+__device__ __forceinline__ int len_of(const int *table, int b) { return table[kLens + b]; }
+
+// Fills the table, by one warp.
 __device__ void pack_keys(const PrefixParams &p, int *start) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   for (int b = lane; b - lane < p.B; b += 32) {
-    const int mine = b < p.B ? (keys_of(p, b) + p.grain - 1) / p.grain * p.grain : 0;
+    const int len = b < p.B ? keys_of(p, b) : 0, mine = (len + p.grain - 1) / p.grain * p.grain;
     int incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
-    if (b < p.B) start[b] = base + incl - mine;
+    if (b < p.B) {
+      start[b] = base + incl - mine;
+      start[kLens + b] = len;
+    }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
   if (lane == 0) start[p.B] = base;
@@ -66,13 +74,13 @@ struct PrefixUnit {
   int b_lo, b_hi;       // entries of its rows
   int t0, n;            // first own tile; tiles, the prefix's first
 };
-__device__ __forceinline__ PrefixUnit unit_of(const PrefixParams &p, const int *start, int unit) {
+__device__ __forceinline__ PrefixUnit unit_of(const PrefixGeo &p, const int *start, int unit) {
   PrefixUnit u;
   u.unit = unit;
-  u.hk = unit / p.n_tiles;
+  u.hk = p.by_tiles.of(unit);
   u.row0 = (unit - u.hk * p.n_tiles) * p.row_tile;
-  u.b_lo = u.row0 / p.entry_rows;
-  u.b_hi = (min(u.row0 + p.row_tile, p.rows) - 1) / p.entry_rows;
+  u.b_lo = p.by_entry.of(u.row0);
+  u.b_hi = p.by_entry.of(min(u.row0 + p.row_tile, p.rows) - 1);
   const int s = start[u.b_lo], e = start[u.b_hi + 1];
   u.t0 = s / BN;
   // (Rows without any key keep a tile, fully masked, that gives their zeros.)
@@ -83,32 +91,33 @@ __device__ __forceinline__ PrefixUnit unit_of(const PrefixParams &p, const int *
 // The split region: its places (kPrefixCost for a unit and then one for each of its KV tiles), the
 // CTAs that share it, and the unit where this CTA begins in it.
 struct PrefixPlan {
-  long long total, begin;   // begin: first place of `unit`
-  int grid, unit;
+  unsigned total, per;   // places; of a CTA
+  unsigned begin;        // first place of `unit`
+  int unit;
 };
 
 struct PrefixItem : PrefixUnit {
   int kv0, kv1;     // KV tiles to do
-  long long u0;     // a cut unit: its first tile's place in the split region
+  unsigned u0;      // a cut unit: its first tile's place in the split region
   bool piece;
 };
 
 // Walks a CTA's work list; every role walks its own copy.
 struct PrefixWalk {
   int k, unit;
-  long long pos, end, begin;
+  unsigned pos, end, begin;
 
-  __device__ __forceinline__ void start(const PrefixParams &p, const PrefixPlan &plan) {
+  __device__ __forceinline__ void start(const PrefixGeo &p, const PrefixPlan &plan) {
     k = 0;
     pos = end = 0;
-    if (p.split && static_cast<int>(blockIdx.x) < plan.grid) {
-      pos = static_cast<long long>(blockIdx.x) * plan.total / plan.grid;
-      end = static_cast<long long>(blockIdx.x + 1) * plan.total / plan.grid;
+    if (p.split) {
+      pos = min(blockIdx.x * plan.per, plan.total);
+      end = min(pos + plan.per, plan.total);
     }
     unit = plan.unit;
     begin = plan.begin;
   }
-  __device__ __forceinline__ bool next(const PrefixParams &p, const int *table, PrefixItem &it) {
+  __device__ __forceinline__ bool next(const PrefixGeo &p, const int *table, PrefixItem &it) {
     if (!p.split || k < p.waves) {
       const int u = static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x);
       ++k;
@@ -139,28 +148,37 @@ struct PrefixWalk {
   }
 };
 
-// One call in memory of its own, so that neither walk nor item takes registers between items.
-__device__ __noinline__ bool next_item(const PrefixParams &p, const int *table, PrefixWalk *walk, PrefixItem *item) {
-  return walk->next(p, table, *item);
+// The schedule in shared memory: its geometry, and where a CTA begins, which one warp works out for all.
+struct PrefixStart {
+  PrefixGeo geo;
+  PrefixPlan plan;
+  PrefixWalk walk;    // past `item`
+  PrefixItem item;
+  int any;            // whether there is an item
+};
+static_assert(sizeof(PrefixStart) <= 192, "room in shared memory");
+// A call with memory of its own, so that neither walk nor item takes registers between items.
+__device__ __noinline__ bool next_item(const PrefixStart *start, const int *table, PrefixWalk *walk, PrefixItem *item) {
+  return walk->next(start->geo, table, *item);
 }
 
 // The split region's size and this CTA's place in it, by one warp.
 __device__ PrefixPlan plan_split(const PrefixParams &p, const int *table) {
   const int lane = threadIdx.x & 31, first = p.waves * static_cast<int>(gridDim.x);
-  auto size_of = [&](int u) -> int { return u < p.n_units ? unit_of(p, table, u).n + kPrefixCost : 0; };
-  long long total = 0;
+  auto size_of = [&](int u) -> unsigned { return u < p.n_units ? unit_of(p, table, u).n + kPrefixCost : 0; };
+  unsigned total = 0;
   for (int u = first + lane; u < p.n_units; u += 32) total += size_of(u);
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const long long most = max(1ll, total / p.min_places);
-  PrefixPlan plan{total, 0, static_cast<int>(most < gridDim.x ? most : gridDim.x), first};
-  const long long pos = static_cast<int>(blockIdx.x) < plan.grid
-                            ? static_cast<long long>(blockIdx.x) * total / plan.grid : 0;
-  long long base = 0;
-  for (int u = first; u < p.n_units; u += 32) {   // the unit that holds pos
-    const int mine = size_of(u + lane);
-    int incl = mine;
+  total = __reduce_add_sync(0xffffffffu, total);
+  // (blockIdx.x * per stays below total + per * gridDim.x, far from 2^32 for lengths up to 2^29.)
+  PrefixPlan plan{total, max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(p.min_places)), 0, first};
+  const unsigned pos = blockIdx.x * plan.per;
+  if (pos >= total) return plan;
+  unsigned base = 0;
+  for (int u = first;; u += 32) {   // the unit that holds pos; ends, as pos < total
+    const unsigned mine = size_of(u + lane);
+    unsigned incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
     const unsigned past = __ballot_sync(0xffffffffu, pos < base + incl);
@@ -172,25 +190,29 @@ __device__ PrefixPlan plan_split(const PrefixParams &p, const int *table) {
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return plan;
 }
 
-// The consecutive CTAs that a cut unit's pieces run on.
-struct PrefixSpan {
-  int first, pieces;
-};
-__device__ __forceinline__ PrefixSpan span_of(const PrefixPlan &plan, long long u0, int n) {
-  const long long T = plan.total;
-  const int G = plan.grid;
-  auto start = [&](int c) { return static_cast<long long>(c) * T / G; };
-  auto owner = [&](long long pos) {
-    int c = static_cast<int>(pos * G / T);
-    while (c + 1 < G && start(c + 1) <= pos) ++c;
-    while (c > 0 && start(c) > pos) --c;
-    return c;
-  };
-  const int first = owner(u0);
-  return PrefixSpan{first, owner(u0 + n - 1) - first + 1};
+// Fills the table and the start, by one warp.
+__device__ __forceinline__ void begin_schedule(const PrefixParams &p, int *table, PrefixStart *start) {
+  pack_keys(p, table);
+  __syncwarp();
+  PrefixPlan plan{0, 1, 0, 0};
+  if (p.split) plan = plan_split(p, table);
+  if ((threadIdx.x & 31) == 0) {
+    start->geo = p;
+    start->plan = plan;
+    PrefixWalk walk;
+    PrefixItem item = {};
+    walk.start(p, plan);
+    start->any = walk.next(p, table, item);
+    start->walk = walk;
+    start->item = item;
+  }
+}
+
+// How many consecutive CTAs, from the one that begins the unit, its pieces run on.
+__device__ __forceinline__ int pieces_of(const PrefixPlan &plan, unsigned u0, int n) {
+  return static_cast<int>((u0 + n - 1) / plan.per - u0 / plan.per) + 1;
 }
 
 // One row of a k/v head's rows; n >= Nq: padding.
@@ -199,8 +221,8 @@ struct PrefixRow {
 };
 __device__ __forceinline__ PrefixRow row_of(const PrefixParams &p, int hk, int row) {
   PrefixRow r;
-  r.b = row / p.entry_rows;
-  const int in = row - r.b * p.entry_rows, g = in / p.nq_rows;
+  r.b = p.by_entry.of(row);
+  const int in = row - r.b * p.entry_rows, g = p.by_nq.of(in);
   r.h = hk * p.group + g;
   r.n = in - g * p.nq_rows;
   return r;
@@ -211,7 +233,7 @@ __device__ __forceinline__ uint16_t *out_row(const PrefixParams &p, int hk, int 
   const PrefixRow r = row_of(p, hk, row);
   if (r.n >= p.Nq) return nullptr;
   if (p.shard_mode) {
-    const int sh = r.n / p.rows_per_shard, i = r.n - sh * p.rows_per_shard;
+    const int sh = p.by_shard.of(r.n), i = r.n - sh * p.rows_per_shard;
     return static_cast<uint16_t *>(p.shards[sh]) +
            ((static_cast<long long>(p.b0 + r.b) * p.rows_per_shard + i) * p.H + r.h) * d;
   }
@@ -223,11 +245,12 @@ struct PrefixRange {
 };
 __device__ __forceinline__ PrefixRange range_of(const PrefixParams &p, const int *table, int row) {
   if (row >= p.rows) return PrefixRange{0, 0};
-  const int b = row / p.entry_rows, s = table[b];
-  return PrefixRange{s, s + keys_of(p, b)};
+  const int b = p.by_entry.of(row), s = table[b];
+  return PrefixRange{s, s + len_of(table, b)};
 }
 
-// Partial result of a piece: O as float4 groups [column / 4][row], then the rows' maxima and sums.
+// Partial result of a piece: O as float4 groups [column / 4][lane], then the lanes' maxima and sums. (A lane is
+// a row, or one copy of it.)
 template <int D>
 __device__ __forceinline__ float *part_of(const PrefixParams &p, int cta, int slot, int rows) {
   return p.parts + (static_cast<size_t>(cta) * 2 + slot) * ((D + 2) * rows);
@@ -320,53 +343,79 @@ __device__ __forceinline__ void issue_pv(uint32_t dcol, uint32_t pcol, uint64_t 
 
 // ------------------------------------------------------------------ joining pieces
 // The pieces of the unit that begins in CTA blockIdx.x's range: 32 rows (blockIdx.y) and 8 columns
-// (blockIdx.z) a block, a lane per row; the four warps take every fourth piece each, and their sums
-// are added in order, so the result does not depend on the order in which the pieces ended.
+// (blockIdx.z) a block, a lane per row. The eight warps take every eighth part each, four of them under way at
+// a time and joined with a running maximum, and their sums are joined in order, so the result does not depend
+// on the order in which the pieces ended.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PrefixParams p) {
-  __shared__ float top[4][32];
-  __shared__ float sums[4][9][32];
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PrefixParams p) {
+  __shared__ float sums[kJoinWarps][10][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 32 + lane, c8 = blockIdx.z;
+  const int R = p.row_tile > BM ? p.row_tile : BM;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 cut = __ldcg(p.cuts + blockIdx.x);   // unit, pieces, k/v head, first row
-  const int S = cut.y, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 32 + lane, c8 = blockIdx.z;
-  if (S == 0 || cut.w + static_cast<int>(blockIdx.y) * 32 >= p.rows) return;
-  const int R = p.row_tile > BM ? p.row_tile : BM;
-  auto part = [&](int k) { return part_of<D>(p, blockIdx.x + k, k == 0 ? 1 : 0, R); };
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int k = warp; k < S; k += 4) m = fmaxf(m, __ldcg(part(k) + D * R + row));
-  top[warp][lane] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(top[0][lane], top[1][lane]), fmaxf(top[2][lane], top[3][lane]));
-  float x[9];
+  if (cut.y == 0 || cut.w + static_cast<int>(blockIdx.y) * 32 >= p.rows) return;
+  // Part k: copy k mod copies of piece k / copies.
+  const int step = p.copies == 4 ? 2 : p.copies - 1, parts = cut.y << step;
+  float m = -INFINITY, x[9];
 #pragma unroll
   for (int i = 0; i < 9; ++i) x[i] = 0.f;
-#pragma unroll 4
-  for (int k = warp; k < S; k += 4) {
-    const float *q = part(k);
-    const float mk = __ldcg(q + D * R + row), l = __ldcg(q + (D + 1) * R + row);
-    const float4 a = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8) * R + row);
-    const float4 b = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8 + 1) * R + row);
-    const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - m);
-    x[0] = fmaf(f, a.x, x[0]);
-    x[1] = fmaf(f, a.y, x[1]);
-    x[2] = fmaf(f, a.z, x[2]);
-    x[3] = fmaf(f, a.w, x[3]);
-    x[4] = fmaf(f, b.x, x[4]);
-    x[5] = fmaf(f, b.y, x[5]);
-    x[6] = fmaf(f, b.z, x[6]);
-    x[7] = fmaf(f, b.w, x[7]);
-    x[8] = fmaf(f, l, x[8]);
+#pragma unroll 1
+  for (int k0 = warp; k0 < parts; k0 += 4 * kJoinWarps) {
+    float mk[4], l[4];
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = min(k0 + i * kJoinWarps, parts - 1);
+      const float *q = part_of<D>(p, blockIdx.x + (k >> step), k >> step == 0 ? 1 : 0, R);
+      const int at = (k & (p.copies - 1)) * p.row_tile + row;
+      mk[i] = __ldcg(q + D * R + at);
+      l[i] = __ldcg(q + (D + 1) * R + at);
+      a[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8) * R + at);
+      b[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8 + 1) * R + at);
+    }
+    const float before = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + i * kJoinWarps >= parts) mk[i] = -INFINITY;
+      m = fmaxf(m, mk[i]);
+    }
+    const float keep = shrink(before, m);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) x[i] *= keep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + i * kJoinWarps >= parts) break;
+      const float f = shrink(mk[i], m);
+      x[0] = fmaf(f, a[i].x, x[0]);
+      x[1] = fmaf(f, a[i].y, x[1]);
+      x[2] = fmaf(f, a[i].z, x[2]);
+      x[3] = fmaf(f, a[i].w, x[3]);
+      x[4] = fmaf(f, b[i].x, x[4]);
+      x[5] = fmaf(f, b[i].y, x[5]);
+      x[6] = fmaf(f, b[i].z, x[6]);
+      x[7] = fmaf(f, b[i].w, x[7]);
+      x[8] = fmaf(f, l[i], x[8]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 9; ++i) sums[warp][i][lane] = x[i];
+  sums[warp][9][lane] = m;
   __syncthreads();
   if (warp != 0 || row >= p.row_tile) return;
   uint16_t *dst = out_row(p, cut.z, cut.w + row, D);
   if (!dst) return;
 #pragma unroll
-  for (int i = 0; i < 9; ++i) x[i] = (sums[0][i][lane] + sums[1][i][lane]) + (sums[2][i][lane] + sums[3][i][lane]);
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sums[w][9][lane]);
+#pragma unroll
+  for (int i = 0; i < 9; ++i) x[i] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = shrink(sums[w][9][lane], m);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) x[i] = fmaf(f, sums[w][i][lane], x[i]);
+  }
   const float f = x[8] == 0.f ? 0.f : 1.f / x[8];
   reinterpret_cast<uint4 *>(dst)[c8] =
       make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f), pack_bf16x2(x[4] * f, x[5] * f),
@@ -395,7 +444,7 @@ template <int D>
 cudaError_t launch_join(const PrefixParams &p, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, ((p.row_tile < p.rows ? p.row_tile : p.rows) + 31) / 32, D / 8);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

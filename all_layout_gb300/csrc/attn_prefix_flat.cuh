@@ -7,52 +7,56 @@
 // and the epilogue adds the copies' results, each with its own maximum and sum.
 //
 // Cached keys and values: the loader copies a tile's codes and scales into a ring of raw slots, and
-// eight warps each turn K's and V's into bf16 operands in rings of their own. A code's bits moved to bf16's
-// place stand for code * 2^-120, so one product with 2^(120 + e) is exact (e > 7 takes two).
+// four warps each turn K's and V's into operands in rings of their own. K's codes become fp16 as they
+// are, and the scores are multiplied by the keys' scales; the queries that meet them are in fp16 too,
+// each row times a power of two. V's become bf16 (what it is multiplied with, the weights, needs
+// bf16's range): a code's bits moved to bf16's place stand for code * 2^-120, so one product with
+// 2^(120 + e) is exact (e > 7 takes two).
 //
-// Roles (768 threads, one CTA per SM):
+// Roles (512 threads, one CTA per SM):
 //   warps 0-3   softmax, row r of the tile = TMEM lane r
-//   warps 4-11  K: codes to bf16, TMA loads of tiles that are not cached
-//   warps 12-19 V, and the queries to Tensor Memory
-//   warp 20     MMA issuer, Tensor Memory allocation
-//   warp 21     loads of codes and scales
-//   warps 22-23 nothing
-// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) Q (bf16 pairs) [384,384+d/2); P_t over S_t's
-// first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax. The issuer's
-// order is QK(i), PV(i-1): QK(i) overwrites P(i-2), whose product went out before it.
+//   warps 4-7   K: codes to fp16, TMA loads of tiles that are not cached
+//   warps 8-11  V: codes to bf16, TMA loads, and the queries to Tensor Memory
+//   warp 12     issues the scores; Tensor Memory allocation
+//   warp 13     issues the products with V
+//   warps 14-15 load K's and V's codes and scales
+// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) Q in fp16 [384,384+d/2), in bf16 [448,448+d/2);
+// P_t over S_t's first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax.
 // Q is read from Tensor Memory because shared memory is what the SM has least of here: with cached
 // keys a tile's codes are written (256 cycles at d = 128) and read (256), its operands written (512)
 // and read (512), about as long as its 33 KB take from HBM at this SM's share of the bandwidth (1450).
 
 template <int D>
 struct FlatCfg {
-  static constexpr int THREADS = 768;
+  static constexpr int THREADS = 512;
   static constexpr int TILE = BN * D * 2, RAW = BN * D + BN;   // a bf16 tile; codes and scale bytes
-  static constexpr int KS = 2, VS = 2, FK = D == 128 ? 3 : 5, FV = D == 128 ? 2 : 5, FS = FK + FV;
+  static constexpr int KS = 2, VS = 2, FK = D == 128 ? 2 : 5, FV = D == 128 ? 3 : 5, FS = FK + FV;
   static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * TILE, OFF_F = OFF_V + VS * TILE;
   static constexpr int OFF_STG = OFF_F + FS * RAW;
   static constexpr int OFF_FIN = OFF_STG + BM * 16 * 4;
-  static constexpr int OFF_TAB = OFF_FIN + BM * 4;
-  static constexpr int OFF_BAR = OFF_TAB + (kPrefixEntries + 4) * 4;
-  static constexpr int SMEM = OFF_BAR + 512;
-  static constexpr uint32_t COL_O = 256, COL_Q = 384;
+  static constexpr int OFF_FAC = OFF_FIN + BM * 4;             // scales of cached keys, of four tiles
+  static constexpr int OFF_QF = OFF_FAC + 4 * BN * 4;          // factors of the rows
+  static constexpr int OFF_TAB = OFF_QF + BM * 4;
+  static constexpr int OFF_BAR = OFF_TAB + kTable * 4;
+  static constexpr int SMEM = OFF_BAR + 768;
+  static constexpr uint32_t COL_O = 256, COL_QH = 384, COL_Q = 448;
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(OFF_BAR % 16 == 0 && RAW % 16 == 0, "alignment");
 };
-constexpr int kFlatKeys = 4, kFlatValues = 12, kFlatOperandWarps = 8, kFlatMma = 20, kFlatLoad = 21;   // warps
+constexpr int kFlatOperands = 4, kFlatValues = 8, kFlatOperandWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
 
 struct FlatBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw[2];                   // V tiles whose rows behind a request's last key are still to be cleared
   uint64_t f_full[10], f_empty[10];
-  uint64_t s_full[2], p_full[2], pv_done, o_full;
-  uint64_t drain;
-  PrefixPlan plan;
+  uint64_t s_full[2], p_full[2], pv_done[2], o_full;
+  uint64_t drain, q_seen;
+  PrefixStart start;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(FlatBars) <= 512, "barrier block too large");
+static_assert(sizeof(FlatBars) <= 768, "barrier block too large");
 
 // The scale bytes of a place that no page holds.
 __device__ __align__(16) const unsigned g_nan_scales[32] = {
@@ -72,7 +76,7 @@ __device__ __forceinline__ Grain grain_of(const PrefixParams &p, const int *tabl
     if (table[mid] <= pos) lo = mid; else hi = mid - 1;
   }
   const int off = pos - table[lo];
-  return Grain{lo, off, min(max(keys_of(p, lo) - off, 0), 16)};
+  return Grain{lo, off, min(max(len_of(table, lo) - off, 0), 16)};
 }
 
 // Whether tile j of a unit lies in the cache, and the first packed own key of an own tile.
@@ -84,81 +88,85 @@ __device__ __forceinline__ int own_pos(const PrefixParams &p, const PrefixUnit &
 }
 
 // ------------------------------------------------------------------ loader of codes
-template <int D>
+// Sixteen bytes to shared memory, and an arrival when this thread's copies so far have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A warp of its own each for K and V: at the others' pace a tile's copies take one about 1000 cycles to issue.
+template <int D, bool V>
 __device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table) {
   using C = FlatCfg<D>;
+  constexpr uint32_t F = V ? C::FV : C::FK, F0 = V ? C::FK : 0;   // slots, the first
   volatile int *abort_flag = &bars->abort;
   const int lane = threadIdx.x & 31;
-  uint32_t use = 0, uses[2] = {0, 0};   // cached tiles so far; K and V slots filled
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
+  uint32_t use = 0;   // cached tiles so far
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
   bool ok = true;
-  // This lane's rows of a tile: `rows` of them from `first` on, in `page` from row `at` on.
+  const int psize = p.prefix_pages.page;   // one cache: all its pages have one size
+  // Lanes 0-7: sixteen rows of a tile each, in page number `page` (as it was read: nothing looks at it before
+  // the tile's turn, so that the load has a tile's time) from row `at` on; none: at < 0.
   struct Part {
-    int first, rows, page, at;
+    int page, at;
   };
   auto part_at = [&](int j) {
-    Part r{0, 0, -1, 0};
-    if (j >= item.kv1 || !is_cached(p, j)) return r;
-    if (j < p.n_prefix) {
-      const int c = min(p.prefix_pages.page, BN), pos = j * BN + lane * c;
-      r.first = lane * c;
-      if (r.first < BN && pos < p.Np) {
-        r.rows = c;
-        r.page = page_of(p.prefix_pages, 0, pos);
-        r.at = pos & (p.prefix_pages.page - 1);
-      }
-    } else {
-      r.first = lane * 16;
-      if (r.first < BN) {
-        const Grain g = grain_of(p, table, item, own_pos(p, item, j) + r.first);
-        if (g.valid > 0) {
-          r.rows = 16;
-          r.page = page_of(p.own_pages, g.b, g.off);
-          r.at = g.off & (p.own_pages.page - 1);
-        }
-      }
+    Part r{0, -1};
+    if (j >= item.kv1 || !is_cached(p, j) || lane >= BN / 16) return r;
+    const bool prefix = j < p.n_prefix;
+    const PageLists &list = prefix ? p.prefix_pages : p.own_pages;
+    int b = 0, place = j * BN + lane * 16;
+    bool live = place < p.Np;
+    if (!prefix) {
+      const Grain g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+      b = g.b;
+      place = g.off;
+      live = g.valid > 0;
     }
+    if (!live) return r;
+    r.at = place & (psize - 1);
+    r.page = -1;
+    if ((place >> list.shift) < list.count) r.page = __ldg(list.pages + b * list.stride + (place >> list.shift));
     return r;
   };
-  while (ok && next_item(p, table, &walk, &item)) {
+  for (; ok && more; more = next_item(&bars->start, table, &walk, &item)) {
     Part ahead = part_at(item.kv0);
     for (int j = item.kv0; ok && j < item.kv1; ++j) {
       const Part r = ahead;
-      ahead = part_at(j + 1);   // (its page number is on its way while this tile's slots are waited for)
+      ahead = part_at(j + 1);
       if (!is_cached(p, j)) continue;
-      const int first = r.first, rows = r.rows, page = r.page, at = r.at;
-      const unsigned bytes = __reduce_add_sync(0xffffffffu, page >= 0 ? rows * (D + 1) : rows);
-      const int psize = p.prefix_pages.page;   // one cache: all its pages have one size
-      const long long row = (static_cast<long long>(page) * p.Hk + item.hk) * psize + at;
-      for (int kv = 0; ok && kv < 2; ++kv) {   // K's and V's slots have a ring each
-        const uint32_t n = kv ? C::FV : C::FK, slot = (kv ? C::FK : 0) + use % n, ph = (use / n) & 1;
-        ok = wait_for<true>(smem_u32(&bars->f_empty[slot]), ph ^ 1, abort_flag, p);
-        if (!ok) break;
-        const uint32_t full = smem_u32(&bars->f_full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-        if (rows > 0) {
-          const uint32_t dst = smem_u32(smem + C::OFF_F + slot * C::RAW);
-          if (page >= 0) {
-            bulk_load(dst + first * D, p.codes[kv] + row * D, rows * D, full);
-            bulk_load(dst + BN * D + first, p.scales[kv] + row, rows, full);
-          } else {
-            bulk_load(dst + BN * D + first, g_nan_scales, rows, full);
-          }
-        }
-        __syncwarp();
-        ++uses[kv];
+      // Rows that follow each other in a page go in one copy, issued by the first one's lane.
+      const bool held = r.at >= 0 && static_cast<unsigned>(r.page) < static_cast<unsigned>(p.prefix_pages.n_pages);
+      const int last_page = __shfl_up_sync(0xffffffffu, held ? r.page : -1, 1);
+      const int last_at = __shfl_up_sync(0xffffffffu, r.at, 1);
+      const bool first = held && (lane == 0 || last_page != r.page || last_at + 16 != r.at);
+      const unsigned heads = __ballot_sync(0xffffffffu, first || !held);   // (lanes 8 to 31 hold nothing)
+      const unsigned bytes = __popc(__ballot_sync(0xffffffffu, held)) * 16u * D;
+      const long long row = (static_cast<long long>(r.page) * p.Hk + item.hk) * psize + r.at;
+      const uint32_t slot = F0 + use % F;
+      ok = wait_for<true>(smem_u32(&bars->f_empty[slot]), (use / F & 1) ^ 1, abort_flag, p);
+      if (!ok) break;
+      const uint32_t full = smem_u32(&bars->f_full[slot]), dst = smem_u32(smem + C::OFF_F + slot * C::RAW);
+      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+      __syncwarp();
+      if (first)
+        bulk_load(dst + lane * 16 * D, p.codes[V ? 1 : 0] + row * D, (__ffs(heads >> (lane + 1)) * 16) * D, full);
+      // The scales by the load/store unit, sixteen a lane: a bulk copy takes the copy engine about 300 cycles,
+      // however small.
+      if (lane < BN / 16) {
+        if (r.at >= 0)
+          copy16(dst + BN * D + lane * 16, held ? static_cast<const void *>(p.scales[V ? 1 : 0] + row) : g_nan_scales);
+        copies_arrive(full);
       }
+      __syncwarp();
       ++use;
     }
   }
   // Every load issued must land before the CTA releases its shared memory.
-  for (uint32_t s = 0; s < C::FS; ++s) {
-    const uint32_t n = s < C::FK ? C::FK : C::FV, at = s < C::FK ? s : s - C::FK, last = uses[s < C::FK ? 0 : 1];
-    if (last > at) drain(smem_u32(&bars->f_full[s]), ((last - 1 - at) / n) & 1);
-  }
+  for (uint32_t s = 0; s < F && s < use; ++s) drain(smem_u32(&bars->f_full[F0 + s]), ((use - 1 - s) / F) & 1);
 }
 
 // ------------------------------------------------------------------ operands
@@ -193,12 +201,57 @@ __device__ __forceinline__ uint4 to_bf16(uint32_t c0, uint32_t c1, uint32_t byte
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Codes and scale bytes of a raw slot to a bf16 tile, by eight warps; `valid`: see valid_of. A thread has one
-// 16-byte group of every STEP-th row, so its place in the swizzle stays. One copy of short loops for K's and
-// V's warps: with all groups unrolled in each the warps waited for instructions.
+// This warp has read a raw slot: its arrival at the slot's barrier.
+__device__ __forceinline__ void slot_read(uint32_t empty) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
+}
+
+// Codes of K's raw slot to a tile in fp16, which holds every code exactly; the keys' scales go to the scores.
+// A thread has one 16-byte group of every STEP-th row, so its place in the swizzle stays. Short loops: with all
+// groups unrolled the warps waited for instructions.
 template <int D>
-__device__ __noinline__ void convert_tile(const uint8_t *src, uint8_t *dst, int valid, uint32_t tid) {
-  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR;   // groups of a row's codes
+__device__ __noinline__ void convert_keys(const uint8_t *src, uint8_t *dst, uint32_t tid, uint32_t empty) {
+  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR, U = BN / STEP;   // groups of a row's codes
+  const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
+  src += tid * 16;
+  dst += (cc / 4) * kHalf + row0 * 128;
+  // (Of a group's two chunks the second half's lanes store the second one first, which spares conflicts.)
+  const uint32_t first0 = ((first + odd) ^ (row0 & 7)) * 16, second0 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
+  auto halves = [](uint32_t a, uint32_t b) {
+    uint4 r;
+    asm("{.reg .b16 t, u;\n\t"
+        "mov.b32 {t, u}, %4;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t"
+        "mov.b32 {t, u}, %5;\n\tcvt.rn.f16x2.e4m3x2 %2, t;\n\tcvt.rn.f16x2.e4m3x2 %3, u;}"
+        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+        : "r"(a), "r"(b));
+    return r;
+  };
+  // (Two groups at a time, the next two's loads before their stores.)
+  uint4 c[2], next[2];
+#pragma unroll
+  for (uint32_t k = 0; k < 2; ++k) c[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
+#pragma unroll 1
+  for (uint32_t i = 0; i < U; i += 2, dst += 2 * STEP * 128) {
+    src += 2 * STEP * D;
+    if (i + 2 < U)
+#pragma unroll
+      for (uint32_t k = 0; k < 2; ++k) next[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+      uint8_t *to = dst + k * STEP * 128;
+      *reinterpret_cast<uint4 *>(to + first0) = halves(odd ? c[k].z : c[k].x, odd ? c[k].w : c[k].y);
+      *reinterpret_cast<uint4 *>(to + second0) = halves(odd ? c[k].x : c[k].z, odd ? c[k].y : c[k].w);
+      c[k] = next[k];
+    }
+  }
+  slot_read(empty);
+}
+
+// Codes and scale bytes of V's raw slot to a bf16 tile; `valid`: see valid_of.
+template <int D>
+__device__ __noinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, uint32_t tid, uint32_t empty) {
+  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR, U = BN / STEP;   // groups of a row's codes
   const uint32_t lane = tid & 31;
   const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
   const uint32_t bytes = *reinterpret_cast<const uint32_t *>(src + BN * D + lane * 4);
@@ -209,14 +262,33 @@ __device__ __noinline__ void convert_tile(const uint8_t *src, uint8_t *dst, int 
   const uint32_t first0 = ((first + odd) ^ (row0 & 7)) * 16, second0 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
   const bool clear = __any_sync(0xffffffffu, valid < 16);
   if (!clear && !__any_sync(0xffffffffu, __vcmpgtu4(bytes, 0x86868686u) != 0)) {
-#pragma unroll 2
-    for (uint32_t i = 0; i < BN / STEP; ++i) {
-      const uint4 c = *reinterpret_cast<const uint4 *>(src + i * STEP * D);
-      const uint32_t byte = scales[i * STEP];
-      uint8_t *to = dst + i * STEP * 128;
-      *reinterpret_cast<uint4 *>(to + first0) = to_bf16<true>(odd ? c.z : c.x, odd ? c.w : c.y, byte);
-      *reinterpret_cast<uint4 *>(to + second0) = to_bf16<true>(odd ? c.x : c.z, odd ? c.y : c.w, byte);
+    uint4 c[2], next[2];
+    uint32_t byte[2], next_byte[2];
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+      c[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
+      byte[k] = scales[k * STEP];
     }
+#pragma unroll 1
+    for (uint32_t i = 0; i < U; i += 2, dst += 2 * STEP * 128) {
+      src += 2 * STEP * D;
+      scales += 2 * STEP;
+      if (i + 2 < U)
+#pragma unroll
+        for (uint32_t k = 0; k < 2; ++k) {
+          next[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
+          next_byte[k] = scales[k * STEP];
+        }
+#pragma unroll
+      for (uint32_t k = 0; k < 2; ++k) {
+        uint8_t *to = dst + k * STEP * 128;
+        *reinterpret_cast<uint4 *>(to + first0) = to_bf16<true>(odd ? c[k].z : c[k].x, odd ? c[k].w : c[k].y, byte[k]);
+        *reinterpret_cast<uint4 *>(to + second0) = to_bf16<true>(odd ? c[k].x : c[k].z, odd ? c[k].y : c[k].w, byte[k]);
+        c[k] = next[k];
+        byte[k] = next_byte[k];
+      }
+    }
+    slot_read(empty);
     return;
   }
 #pragma unroll 1
@@ -229,15 +301,91 @@ __device__ __noinline__ void convert_tile(const uint8_t *src, uint8_t *dst, int 
     *reinterpret_cast<uint4 *>(to + first0) = x;
     *reinterpret_cast<uint4 *>(to + second0) = y;
   }
+  slot_read(empty);
 }
 
-// The warps of K, or of V (which also bring the queries): each tile's operand, in order.
+// An item's queries to Tensor Memory by four warps of different lane quarters, a row a thread (the copies begin
+// at multiples of row_tile).
+template <int D>
+__device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const PrefixItem &item,
+                                          uint32_t items, uint32_t tmem) {
+  using C = FlatCfg<D>;
+  volatile int *abort_flag = &bars->abort;
+  const int tid = threadIdx.x & 127;
+  const int row = item.row0 + tid % p.row_tile;
+  const uint16_t *src = nullptr;
+  if (row < p.rows) {
+    const PrefixRow r = row_of(p, item.hk, row);
+    if (r.n < p.Nq) src = p.q + r.b * p.q_b + r.h * p.q_h + r.n * p.q_n;
+  }
+  const uint32_t to = tmem + (static_cast<uint32_t>(tid & ~31) << 16);
+  // (The row is read twice, the second time out of L1: held in registers, its conversion would be long code.)
+  auto part = [&](int i) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (src)
+      asm volatile("ld.global.ca.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src + 8 * i));
+    return v;
+  };
+  const bool cached = p.prefix_cached || p.own_cached;
+  float s = 1.f;
+  if (cached) {
+    // fp16 for cached keys: times the power of two that brings the row's largest magnitude to [2^14, 2^15).
+    // Exact then for values down to 2^-31 of that, and off by 2^-40 of it at most below. (Of a row whose
+    // largest is an infinity or NaN, and of zeros, nothing is asked.)
+    uint32_t big = 0;   // largest magnitudes, as bits, of the even and of the odd columns
+    uint4 x[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) x[i] = part(i);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 v = x[i];
+      big = __vmaxu2(__vmaxu2(big, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    }
+    const int e = min(max(static_cast<int>(max(big & 0xffffu, big >> 16) >> 7), 1), 254);
+    const int up = min(268 - e, 253);   // 2^(up - 127), 2^(141 - e) mostly
+    s = __int_as_float(up << 23);
+    big = (254 - up) << 23;
+    if (items > 0 && (!wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p) ||
+                      !wait_for<true>(smem_u32(&bars->q_seen), (items - 1) & 1, abort_flag, p)))
+      return false;
+    reinterpret_cast<float *>(smem + C::OFF_QF)[tid] = __int_as_float(big);
+  } else if (items > 0 && (!wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p) ||
+                           !wait_for<true>(smem_u32(&bars->q_seen), (items - 1) & 1, abort_flag, p))) {
+    return false;
+  }
+  tc_fence_after();   // (the last item's scores, read from here, are done)
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t q[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = part(4 * c + i);
+      q[4 * i] = v.x;
+      q[4 * i + 1] = v.y;
+      q[4 * i + 2] = v.z;
+      q[4 * i + 3] = v.w;
+    }
+    if (!p.prefix_cached || !p.own_cached) tmem_st16(to + C::COL_Q + 16 * c, q);
+    if (cached) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(__uint_as_float(q[i] & 0xffff0000u) * s), "f"(__uint_as_float(q[i] << 16) * s));
+      tmem_st16(to + C::COL_QH + 16 * c, q);
+    }
+  }
+  tmem_wait_st();
+  tc_fence_before();
+  mbar_arrive(smem_u32(&bars->q_full));
+  return true;
+}
+
+// The warps of K, or of V: each tile's operand, in order.
 template <int D, bool V>
 __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem) {
   using C = FlatCfg<D>;
   constexpr uint32_t S = V ? C::VS : C::KS, F = V ? C::FV : C::FK, F0 = V ? C::FK : 0;   // slots; raw slots, the first
   volatile int *abort_flag = &bars->abort;
-  const int tid = threadIdx.x - 32 * (V ? kFlatValues : kFlatKeys), lane = tid & 31;
+  const int tid = threadIdx.x & 127, lane = tid & 31;
   const bool issuer = tid < 32;
   uint64_t *full_of = V ? bars->v_full : bars->k_full, *empty_of = V ? bars->v_empty : bars->k_empty;
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<true>(smem_u32(&bar), parity, abort_flag, p); };
@@ -250,9 +398,9 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     pending |= 1u << bit;
     phase = (phase & ~(1u << bit)) | parity << bit;
   };
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
 
   // Rows of V behind a request's last key: their weights are 0, but what lies there may not be a number.
   auto valid_of = [&](int j) {   // of the lane's sixteen keys, in lanes 0-7
@@ -307,61 +455,37 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     const int valid = V ? valid_of(j) : 16;
     const bool clear = __any_sync(0xffffffffu, valid < 16);
     uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
-    const uint32_t f = F0 + f_use % F;
     if (cached) {
+      const uint32_t f = F0 + f_use % F, empty = smem_u32(&bars->f_empty[f]);
       if (!wait(bars->f_full[f], f_use / F & 1) || !wait(empty_of[slot], (use / S & 1) ^ 1)) return false;
       pending &= ~(1u << slot);
-      convert_tile<D>(smem + C::OFF_F + f * C::RAW, dst, valid, tid);
+      const uint8_t *raw = smem + C::OFF_F + f * C::RAW;
+      if (V) {
+        convert_values<D>(raw, dst, valid, tid, empty);
+      } else {
+        reinterpret_cast<float *>(smem + C::OFF_FAC)[(use & 3) * BN + tid] = power_of(raw[BN * D + tid]) * p.scale_log2;
+        convert_keys<D>(raw, dst, tid, empty);
+      }
       ++f_use;
     } else {
       if (!clear) return true;
       if (!wait(bars->raw[slot], raw_parity >> slot & 1)) return false;
       raw_parity ^= 1u << slot;
       pending &= ~(4u << slot);
-      const int row = tid & (BM - 1), part = tid / BM;   // two threads a row
-      if ((row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4))
-        for (int i = part * (D / 16); i < (part + 1) * (D / 16); ++i)
-          *reinterpret_cast<uint4 *>(dst + (i / 8) * kHalf + row * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+      if ((tid & 15) >= __shfl_sync(0xffffffffu, valid, tid >> 4))
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint4 *>(dst + (i / 8) * kHalf + tid * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(smem_u32(full_of + slot));
-      if (cached) mbar_arrive(smem_u32(&bars->f_empty[f]));
-    }
+    if (lane == 0) mbar_arrive(smem_u32(full_of + slot));
     return true;
   };
 
   bool ok = true;
-  for (; ok && next_item(p, table, &walk, &item); ++items) {
-    if (V && tid < BM) {   // the queries, a row a thread; the copies begin at multiples of row_tile
-      const int row = item.row0 + tid % p.row_tile;
-      const uint16_t *src = nullptr;
-      if (row < p.rows) {
-        const PrefixRow r = row_of(p, item.hk, row);
-        if (r.n < p.Nq) src = p.q + r.b * p.q_b + r.h * p.q_h + r.n * p.q_n;
-      }
-      const uint32_t to = tmem + (static_cast<uint32_t>(tid & ~31) << 16) + C::COL_Q;
-      if (items > 0) ok = wait(bars->q_empty, (items - 1) & 1);
-      if (!ok) break;
-      tc_fence_after();   // (the last item's scores, read from here, are done)
-#pragma unroll 2
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t q[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = src ? __ldg(reinterpret_cast<const uint4 *>(src) + 4 * c + i) : make_uint4(0, 0, 0, 0);
-          q[4 * i] = v.x;
-          q[4 * i + 1] = v.y;
-          q[4 * i + 2] = v.z;
-          q[4 * i + 3] = v.w;
-        }
-        tmem_st16(to + 16 * c, q);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&bars->q_full));
-    }
+  for (; ok && more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
+    if (V) ok = flat_queries<D>(p, smem, bars, item, items, tmem);
+    if (!ok) break;
     // TMA loads go out one tile ahead of the clearing that V's may need.
     ok = issue(item.kv0, use);
     for (int j = item.kv0; ok && j < item.kv1; ++j, ++use) ok = issue(j + 1, use + 1) && finish(j);
@@ -376,59 +500,80 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
 
 // ------------------------------------------------------------------ MMA issuer
 template <int D>
-__device__ __forceinline__ void issue_qk_ts(uint32_t dcol, uint32_t qcol, uint64_t kdesc) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0);
+__device__ __forceinline__ void issue_qk_ts(uint32_t dcol, uint32_t qcol, uint64_t kdesc, bool half) {
+  // (Formats of A and B in bits 7-9 and 10-12: 1 bf16, 0 fp16.)
+  const uint32_t idesc = idesc_bf16_f32(128, 128, 0) & (half ? ~(9u << 7) : ~0u);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
     tc_mma_ts(dcol, qcol + kk * 8, kdesc + static_cast<uint64_t>(((kk / 4) * kHalf + (kk % 4) * 32) >> 4), idesc,
               kk > 0 ? 1u : 0u);
 }
+// Scores and products have a warp each: a thread is held for about as long as the MMAs run that it issues.
+// QK(i) overwrites P(i-2), so it waits until that product is done.
 template <int D>
-__device__ void flat_mma(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem_in) {
+__device__ void flat_scores(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem_in) {
   using C = FlatCfg<D>;
   volatile int *abort_flag = &bars->abort;
   const uint32_t tmem = uniform(tmem_in);
-  uint32_t base = 0, items = 0;   // tiles before the item; items
+  uint32_t g = 0, items = 0;   // tiles, items so far
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), kHalf, 1024);
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
-  for (; next_item(p, table, &walk, &item); ++items) {
-    const int n = uniform(item.kv1 - item.kv0);
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
+  for (; more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
+    const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
     if (!wait(bars->q_full, items & 1)) goto done;
-    for (int i = 0; i <= n; ++i) {
-      if (i < n) {
-        const uint32_t g = base + i, t = g & 1, ks = g % C::KS;
-        if (!wait(bars->k_full[ks], g / C::KS & 1)) goto done;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_qk_ts<D>(tmem + t * 128, tmem + C::COL_Q, kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)));
-          tc_commit(smem_u32(&bars->s_full[t]));
-          tc_commit(smem_u32(&bars->k_empty[ks]));
-          if (i == n - 1) tc_commit(smem_u32(&bars->q_empty));
-        }
-        __syncwarp();
+    for (int j = kv0; j < kv1; ++j, ++g) {
+      const uint32_t t = g & 1, ks = g % C::KS;
+      const bool half = uniform(is_cached(p, j));   // cached keys are in fp16, others in bf16
+      if (g >= 2 && !wait(bars->pv_done[t], (g >> 1 & 1) ^ 1)) goto done;   // of tile g - 2
+      if (!wait(bars->k_full[ks], g / C::KS & 1)) goto done;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_qk_ts<D>(tmem + t * 128, tmem + (half ? C::COL_QH : C::COL_Q), kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)), half);
+        tc_commit(smem_u32(&bars->s_full[t]));
+        tc_commit(smem_u32(&bars->k_empty[ks]));
+        if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
       }
-      if (i > 0) {
-        const uint32_t g = base + i - 1, t = g & 1, vs = g % C::VS;
-        if (!wait(bars->v_full[vs], g / C::VS & 1)) goto done;
-        if (!wait(bars->p_full[t], g >> 1 & 1)) goto done;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_pv<D>(tmem + C::COL_O, tmem + t * 128, vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), i > 1 ? 1u : 0u);
-          tc_commit(smem_u32(&bars->v_empty[vs]));
-          tc_commit(smem_u32(&bars->pv_done));
-          if (i == n) tc_commit(smem_u32(&bars->o_full));
-        }
-        __syncwarp();
-      }
+      __syncwarp();
     }
-    base += n;
   }
 done:
   // All MMAs issued must finish before Tensor Memory is released.
+  if (elect_one()) tc_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  drain(smem_u32(&bars->drain), 0);
+}
+
+template <int D>
+__device__ void flat_products(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem_in) {
+  using C = FlatCfg<D>;
+  volatile int *abort_flag = &bars->abort;
+  const uint32_t tmem = uniform(tmem_in);
+  uint32_t g = 0;
+  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), kHalf, 1024);
+  auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
+  for (; more; more = next_item(&bars->start, table, &walk, &item)) {
+    const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
+    for (int j = kv0; j < kv1; ++j, ++g) {
+      const uint32_t t = g & 1, vs = g % C::VS;
+      if (!wait(bars->v_full[vs], g / C::VS & 1)) goto done;
+      if (!wait(bars->p_full[t], g >> 1 & 1)) goto done;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_pv<D>(tmem + C::COL_O, tmem + t * 128, vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), j > kv0 ? 1u : 0u);
+        tc_commit(smem_u32(&bars->v_empty[vs]));
+        tc_commit(smem_u32(&bars->pv_done[t]));
+        if (j == kv1 - 1) tc_commit(smem_u32(&bars->o_full));
+      }
+      __syncwarp();
+    }
+  }
+done:
   if (elect_one()) tc_commit(smem_u32(&bars->drain));
   __syncwarp();
   drain(smem_u32(&bars->drain), 0);
@@ -454,10 +599,24 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
   m = max3(m, __uint_as_float(s[30]), __uint_as_float(s[31]));
   return max3(m, mp[0], mp[1]);
 }
-// The scores of keys outside `keep` become -inf, whatever they were.
-__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t keep) {
+// Scores of N times 32 keys in Tensor Memory, times fac where given, with those outside [lo, hi) -inf, whatever
+// they were. (In place and out of line: the softmax's loop stays short.)
+template <int N>
+__device__ __noinline__ void mask_scores(uint32_t taddr, const float *fac, int lo, int hi) {
+#pragma unroll 1
+  for (int c = 0; c < N; ++c) {
+    uint32_t s[32];
+    tmem_ld32(taddr + 32 * c, s);
+    tmem_wait_ld_regs(s);
+    const uint32_t keep = bits_of(lo - 32 * c, hi - 32 * c);
 #pragma unroll
-  for (int k = 0; k < 32; ++k) s[k] = keep >> k & 1 ? s[k] : 0xff800000u;
+    for (int k = 0; k < 32; ++k) {
+      if (fac) s[k] = __float_as_uint(__uint_as_float(s[k]) * fac[32 * c + k]);
+      s[k] = keep >> k & 1 ? s[k] : 0xff800000u;
+    }
+    tmem_st32(taddr + 32 * c, s);
+  }
+  tmem_wait_st();
 }
 // Weights 2^(s * scale - m) of 32 scores as bf16 pairs, and their sum added to `sum`.
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scale2, uint64_t negm2, uint32_t (&pk)[16],
@@ -487,20 +646,22 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
   volatile int *abort_flag = &bars->abort;
   float2 *exch = reinterpret_cast<float2 *>(smem + C::OFF_STG);
   float *fin = reinterpret_cast<float *>(smem + C::OFF_FIN);
-  const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
   uint32_t step = 0, items = 0;   // tiles, items so far
   bool dead = false;   // a wait gave up: go on without waiting, store nothing
   auto wait = [&](uint64_t &bar, uint32_t parity) {
     if (!dead && !wait_for<true>(smem_u32(&bar), parity, abort_flag, p)) dead = true;
   };
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
   bool cut = false;   // a piece was this CTA's first of its unit
-  for (; next_item(p, table, &walk, &item); ++items) {
+  for (; more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
     const int row = item.row0 + in;
     const bool idle = item.row0 + (wq * 32) % RT >= p.rows;   // no row in this warp
     const PrefixRange own = range_of(p, table, row);
+    wait(bars->q_full, items & 1);
+    const float row_factor = reinterpret_cast<const float *>(smem + C::OFF_QF)[tid];   // (of rows in fp16)
+    mbar_arrive(smem_u32(&bars->q_seen));
     float m = -INFINITY, l = 0.f;
     for (int j = item.kv0; j < item.kv1; ++j, ++step) {
       const uint32_t t = step & 1, tS = lanes + t * 128;
@@ -512,20 +673,46 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       tc_fence_after();
       const int first = (j < p.n_prefix ? j * BN : own_pos(p, item, j)) + copy * (NC * 32);
       const int lo = (j < p.n_prefix ? 0 : own.lo) - first, hi = (j < p.n_prefix ? p.Np : own.hi) - first;
-      // Two passes over the scores, 32 at a time (a thread has 80 registers): the maximum, then the
-      // weights (each chunk of P covers scores that have been read).
-      const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < NC * 32);
+      // Two passes over the scores, as 128 of them would not fit the registers beside the rest: the
+      // maximum, then the weights (each chunk of P covers scores that have been read).
       const uint32_t tC = tS + copy * (NC * 32);
-      uint32_t s[32];
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        tmem_ld32(tC + 32 * c, s);
-        tmem_wait_ld_regs(s);
-        if (masked) mask32(s, bits_of(lo - 32 * c, hi - 32 * c));
-        mx = max32(s, mx);
+      // Scores of cached keys are times the key's scale (and scale_log2) times the row's factor.
+      bool times = is_cached(p, j);
+      const float scale = times ? row_factor : p.scale_log2;
+      const float4 *fac = reinterpret_cast<const float4 *>(smem + C::OFF_FAC) + (step & 3) * (BN / 4) + copy * NC * 8;
+      if (__any_sync(0xffffffffu, lo > 0 || hi < NC * 32)) {
+        mask_scores<NC>(tC, times ? reinterpret_cast<const float *>(fac) : nullptr, lo, hi);
+        times = false;
       }
-      const float m_new = fmaxf(m, mx * p.scale_log2);
+      constexpr int W = NC > 1 ? 2 : 1;   // chunks loaded at a time
+      uint32_t s[W][32];
+      auto finish = [&](int c, int k0) {
+        uint32_t (&x)[32] = s[k0];
+        tmem_wait_ld_regs(x);
+        if (times)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 f = fac[8 * c + k];
+            const uint64_t a = f2_mul(f2_pack(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])), f2_pack(f.x, f.y));
+            const uint64_t b = f2_mul(f2_pack(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), f2_pack(f.z, f.w));
+            x[4 * k] = static_cast<uint32_t>(a);
+            x[4 * k + 1] = static_cast<uint32_t>(a >> 32);
+            x[4 * k + 2] = static_cast<uint32_t>(b);
+            x[4 * k + 3] = static_cast<uint32_t>(b >> 32);
+          }
+      };
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < NC; c += W) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) tmem_ld32(tC + 32 * (c + k), s[k]);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          finish(c + k, k);
+          mx = max32(s[k], mx);
+        }
+      }
+      const float m_new = fmaxf(m, mx * scale);
       float alpha = 1.f;
       bool rescale = false;
       if (j == item.kv0) {
@@ -542,18 +729,21 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       }
       // (Without any key so far the weights are 2^(-inf - 0) = 0.)
       const float neg = m == -INFINITY ? 0.f : -m;
-      const uint64_t negm2 = f2_pack(neg, neg);
+      const uint64_t scale2 = f2_pack(scale, scale), negm2 = f2_pack(neg, neg);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int c = 0; c < NC; c += W) {
+        if constexpr (NC == 4) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if constexpr (NC > 1) {
-          tmem_ld32(tC + 32 * c, s);
-          tmem_wait_ld_regs(s);
-          if (masked) mask32(s, bits_of(lo - 32 * c, hi - 32 * c));
+          for (int k = 0; k < W; ++k) tmem_ld32(tC + 32 * (c + k), s[k]);
         }
-        uint32_t pk[16];
-        weights32(s, scale2, negm2, pk, sum);
-        tmem_st16(tS + 16 * (copy * NC + c), pk);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          if constexpr (NC == 4) finish(c + k, k);
+          uint32_t pk[16];
+          weights32(s[k], scale2, negm2, pk, sum);
+          tmem_st16(tS + 16 * (copy * NC + c + k), pk);
+        }
       }
       if constexpr (NC < 4) {
         uint32_t zero[16];
@@ -566,7 +756,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       if (rescale) {
         // (The products before the last are done, as these scores followed them.)
-        wait(bars->pv_done, (step - 1) & 1);
+        wait(bars->pv_done[t ^ 1], (step - 1) >> 1 & 1);
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
@@ -584,6 +774,34 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
     }
     wait(bars->o_full, items & 1);
     tc_fence_after();
+    if (item.piece) {
+      // Every copy's sums as they are; the join adds the copies with the pieces.
+      float *part = part_of<D>(p, blockIdx.x, item.kv0 == 0 ? 1 : 0, BM);
+      if (item.kv0 == 0) cut = true;
+      const bool live = row < p.rows && !dead;
+      if (live) {
+        __stcg(part + D * BM + tid, m);
+        __stcg(part + (D + 1) * BM + tid, l);
+      }
+      if (tid == 0 && item.kv0 == 0)
+        __stcg(p.cuts + blockIdx.x, make_int4(item.unit, dead ? 0 : pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
+      if (!idle) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t a[32];
+          tmem_ld32(tO + 32 * c, a);
+          tmem_wait_ld_regs(a);
+          if (live)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              __stcg(reinterpret_cast<float4 *>(part) + (8 * c + k) * BM + tid,
+                     make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
+                                 __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3])));
+        }
+      }
+      tc_fence_before();
+      continue;
+    }
     // (m, l) of all copies of a row.
     float top = m, total = l, f = 1.f;
     if constexpr (COPIES > 1) {
@@ -599,37 +817,16 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       }
       f = shrink(m, top);
     }
-    // A piece leaves its sums as they are, a whole unit divides by them.
-    const float norm = item.piece ? 1.f : total == 0.f ? 0.f : 1.f / total;
-    float *part = nullptr;
-    if (item.piece) {
-      part = part_of<D>(p, blockIdx.x, item.kv0 == 0 ? 1 : 0, BM);
-      if (item.kv0 == 0) cut = true;
-      if (copy == 0 && row < p.rows && !dead) {
-        __stcg(part + D * BM + in, top);
-        __stcg(part + (D + 1) * BM + in, total);
-      }
-      if (tid == 0 && item.kv0 == 0) {
-        const PrefixSpan span = span_of(bars->plan, item.u0, item.n);
-        __stcg(p.cuts + blockIdx.x, make_int4(item.unit, dead ? 0 : span.pieces, item.hk, item.row0));
-      }
-    }
+    const float norm = total == 0.f ? 0.f : 1.f / total;
     if constexpr (COPIES == 1) {
-      uint16_t *dst = item.piece || dead ? nullptr : out_row(p, item.hk, row, D);
+      uint16_t *dst = dead ? nullptr : out_row(p, item.hk, row, D);
       if (!idle) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t a[32];
           tmem_ld32(tO + 32 * c, a);
           tmem_wait_ld_regs(a);
-          if (part) {
-            if (row < p.rows && !dead)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                __stcg(reinterpret_cast<float4 *>(part) + (8 * c + k) * BM + in,
-                       make_float4(__uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]),
-                                   __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3])));
-          } else if (dst) {
+          if (dst) {
             float x[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(a[k]) * norm;
@@ -676,9 +873,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
             x.z += y.z;
             x.w += y.w;
           }
-          if (part) {
-            __stcg(reinterpret_cast<float4 *>(part) + (4 * c + q) * BM + r, x);
-          } else if (uint16_t *to = out_row(p, item.hk, item.row0 + r, D)) {
+          if (uint16_t *to = out_row(p, item.hk, item.row0 + r, D)) {
             const float g = fin[r];
             *reinterpret_cast<uint2 *>(to + 16 * c + 4 * q) =
                 make_uint2(pack_bf16x2(x.x * g, x.y * g), pack_bf16x2(x.z * g, x.w * g));
@@ -693,7 +888,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
 }
 
 template <int D>
-__global__ void __launch_bounds__(768, 1) prefix_flat_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_constant__ PrefixParams p) {
   using C = FlatCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle pattern repeats every 1024 bytes
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -716,52 +911,53 @@ __global__ void __launch_bounds__(768, 1) prefix_flat_kernel(const __grid_consta
       mbar_init(smem_u32(&bars->p_full[s]), 128);
     }
     for (int s = 0; s < C::FS; ++s) {
-      mbar_init(smem_u32(&bars->f_full[s]), 1);
+      mbar_init(smem_u32(&bars->f_full[s]), 1 + BN / 16);   // the codes, and the lanes with scales
       mbar_init(smem_u32(&bars->f_empty[s]), kFlatOperandWarps);
     }
-    mbar_init(smem_u32(&bars->pv_done), 1);
+    mbar_init(smem_u32(&bars->pv_done[0]), 1);
+    mbar_init(smem_u32(&bars->pv_done[1]), 1);
     mbar_init(smem_u32(&bars->o_full), 1);
-    mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->drain), 2);   // one commit of each issuer
+    mbar_init(smem_u32(&bars->q_seen), BM);
     bars->abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
-    pack_keys(p, table);
-    __syncwarp();
-    PrefixPlan plan{0, 0, 0, 0};
-    if (p.split) plan = plan_split(p, table);
-    if ((threadIdx.x & 31) == 0) bars->plan = plan;
-  }
-  if (warp == kFlatMma) {
+  if (warp == 1) begin_schedule(p, table, &bars->start);
+  if (warp == kFlatScores) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits for this grid's end itself
   const uint32_t tmem = bars->tmem_base;
-  if (warp < kFlatKeys) {
+  if (warp < kFlatOperands) {
     if (p.copies == 1)
       flat_softmax<D, 4>(p, smem, bars, table, tmem);
     else if (p.copies == 2)
       flat_softmax<D, 2>(p, smem, bars, table, tmem);
     else
       flat_softmax<D, 1>(p, smem, bars, table, tmem);
-  } else {
-    if (warp < kFlatValues)
-      flat_operands<D, false>(p, smem, bars, table, tmem);
-    else if (warp < kFlatMma)
+  } else if (warp < kFlatScores) {
+    if (warp >= kFlatValues)
       flat_operands<D, true>(p, smem, bars, table, tmem);
-    else if (warp == kFlatMma)
-      flat_mma<D>(p, smem, bars, table, tmem);
-    else if (warp == kFlatLoad)
-      flat_loader<D>(p, smem, bars, table);
+    else
+      flat_operands<D, false>(p, smem, bars, table, tmem);
+  } else if (warp == kFlatScores) {
+    flat_scores<D>(p, smem, bars, table, tmem);
+  } else if (warp == kFlatProducts) {
+    flat_products<D>(p, smem, bars, table, tmem);
+  } else if (warp == kFlatLoadKeys) {
+    flat_loader<D, false>(p, smem, bars, table);
+  } else {
+    flat_loader<D, true>(p, smem, bars, table);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kFlatMma) {
+  if (warp == kFlatScores) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -24,8 +24,8 @@ struct TallCfg {
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE;
   static constexpr int OFF_STG = OFF_V + VS * TILE;            // a warp's 32 rows of 64 columns, bf16
   static constexpr int OFF_TAB = OFF_STG + 8 * 32 * 128;
-  static constexpr int OFF_BAR = OFF_TAB + (kPrefixEntries + 4) * 4;
-  static constexpr int SMEM = OFF_BAR + 512;
+  static constexpr int OFF_BAR = OFF_TAB + kTable * 4;
+  static constexpr int SMEM = OFF_BAR + 416;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 constexpr int kTallMma = 8, kTallLoad = 9;
@@ -35,11 +35,11 @@ struct TallBars {
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;
-  PrefixPlan plan;
+  PrefixStart start;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(TallBars) <= 512, "barrier block too large");
+static_assert(sizeof(TallBars) <= 416, "barrier block too large");
 
 // The KV tiles of an item that row tile t of it takes: [kv0, prefix) and [own0, own1), the prefix's and
 // those of its rows' requests.
@@ -55,8 +55,8 @@ __device__ __forceinline__ TallTiles tiles_of(const PrefixParams &p, const int *
   TallTiles r;
   r.kv0 = it.kv0;
   r.prefix = min(it.kv1, p.n_prefix);
-  int a = table[row0 / p.entry_rows] / BN - it.t0 + p.n_prefix;
-  int e = table[(min(row0 + BM, p.rows) - 1) / p.entry_rows + 1] / BN - it.t0 + p.n_prefix;
+  int a = table[p.by_entry.of(row0)] / BN - it.t0 + p.n_prefix;
+  int e = table[p.by_entry.of(min(row0 + BM, p.rows) - 1) + 1] / BN - it.t0 + p.n_prefix;
   if (p.n_prefix == 0 && table[it.b_hi + 1] == table[it.b_lo]) {   // no key in the unit: the masked tile
     a = 0;
     e = 1;
@@ -74,7 +74,7 @@ __device__ __forceinline__ TallOwn own_tile(const PrefixParams &p, const int *ta
   const int pos = own_pos(p, it, j);
   while (b < it.b_hi && table[b + 1] <= pos) ++b;
   const int off = pos - table[b];
-  return TallOwn{off, min(max(keys_of(p, b) - off, 0), BN)};
+  return TallOwn{off, min(max(len_of(table, b) - off, 0), BN)};
 }
 
 // ------------------------------------------------------------------ TMA loader
@@ -85,11 +85,11 @@ __device__ void tall_loader(const PrefixParams &p, uint8_t *smem, TallBars *bars
   const int lane = threadIdx.x & 31;
   uint32_t use = 0, items = 0, uses[2] = {0, 0};
   const uint32_t q_full = smem_u32(&bars->q_full);
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
   bool ok = true;
-  for (; ok && next_item(p, table, &walk, &item); ++items) {
+  for (; ok && more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
     if (items > 0) ok = wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p);
     if (!ok) break;
     {
@@ -160,10 +160,10 @@ __device__ void tall_mma(const PrefixParams &p, uint8_t *smem, TallBars *bars, c
     fence_proxy_async_smem();
     __syncwarp();
   };
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
-  for (; next_item(p, table, &walk, &item); ++items) {
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
+  for (; more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
     const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
     TallTiles tiles[2];
 #pragma unroll
@@ -286,11 +286,11 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
   volatile int *abort_flag = &bars->abort;
   const float scale = p.scale_log2;
   uint32_t step = 0, outs = 0;
-  PrefixWalk walk;
-  walk.start(p, bars->plan);
-  PrefixItem item;
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
   bool cut = false, ok = true;   // a piece was this CTA's first of its unit
-  while (ok && next_item(p, table, &walk, &item)) {
+  for (; ok && more; more = next_item(&bars->start, table, &walk, &item)) {
     const int row = item.row0 + t * BM + in;
     const TallTiles tiles = tiles_of(p, table, item, t);
     const PrefixRange own = range_of(p, table, row);
@@ -310,6 +310,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
         break;
       }
       tc_fence_after();
+      if (masked) mask_scores<4>(tS, nullptr, lo, hi);
       // The first half's maximum beside the second half's load.
       uint32_t s[4][32];
       tmem_ld32(tS, s[0]);
@@ -318,17 +319,9 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
       tmem_wait_ld_regs(s[1]);
       tmem_ld32(tS + 64, s[2]);
       tmem_ld32(tS + 96, s[3]);
-      if (masked) {
-        mask32(s[0], bits_of(lo, hi));
-        mask32(s[1], bits_of(lo - 32, hi - 32));
-      }
       float mx = max32(s[1], max32(s[0], -INFINITY));
       tmem_wait_ld_regs(s[2]);
       tmem_wait_ld_regs(s[3]);
-      if (masked) {
-        mask32(s[2], bits_of(lo - 64, hi - 64));
-        mask32(s[3], bits_of(lo - 96, hi - 96));
-      }
       mx = max32(s[3], max32(s[2], mx));
       const float m_new = fmaxf(m, mx * scale);
       float alpha = 1.f;
@@ -386,8 +379,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
         __stcg(part + (D + 1) * 2 * BM + at, l);
       }
       if (tid == 0 && item.kv0 == 0) {
-        const PrefixSpan span = span_of(bars->plan, item.u0, item.n);
-        __stcg(p.cuts + blockIdx.x, make_int4(item.unit, span.pieces, item.hk, item.row0));
+        __stcg(p.cuts + blockIdx.x, make_int4(item.unit, pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
       }
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -471,13 +463,7 @@ __global__ void __launch_bounds__(320, 1) prefix_tall_kernel(const __grid_consta
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 1) {
-    pack_keys(p, table);
-    __syncwarp();
-    PrefixPlan plan{0, 0, 0, 0};
-    if (p.split) plan = plan_split(p, table);
-    if ((threadIdx.x & 31) == 0) bars->plan = plan;
-  }
+  if (warp == 1) begin_schedule(p, table, &bars->start);
   if (warp == kTallMma) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
@@ -485,6 +471,7 @@ __global__ void __launch_bounds__(320, 1) prefix_tall_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits for this grid's end itself
   const uint32_t tmem = bars->tmem_base;
   if (warp < kTallMma)
     tall_softmax<D>(p, smem, bars, table, tmem);

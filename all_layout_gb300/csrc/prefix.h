@@ -15,7 +15,34 @@ constexpr int kPrefixEntries = 256;
 // split schedule a unit takes so many places more than it has tiles.
 constexpr int kPrefixCost = 2;
 
-struct PrefixParams {
+// Division of n in [0, 2^31) by a fixed d: with l the least l for which d <= 2^l, n m >> (31 + l) for
+// m = ceil(2^(31 + l) / d). (A plain division is some forty instructions, and a launch's first ones wait
+// for instructions more than for anything else.)
+struct Divisor {
+  unsigned m, shift;   // m = 0: d = 1
+  void set(unsigned d) {
+    unsigned l = 0;
+    while ((1ull << l) < d) ++l;
+    m = d > 1 ? static_cast<unsigned>(((1ull << (31 + l)) + d - 1) / d) : 0;
+    shift = l > 0 ? l - 1 : 0;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int of(int n) const {
+    return m ? static_cast<int>(__umulhi(static_cast<unsigned>(n), m) >> shift) : n;
+  }
+#endif
+};
+
+// What the schedule goes by; the kernels keep a copy in shared memory for the calls that walk it.
+struct PrefixGeo {
+  int rows, entry_rows;                  // rows of a k/v head: (entry, head of the group, query padded to nq_rows)
+  int row_tile, n_tiles, n_units;        // rows of a unit; units of a head, of all
+  int n_prefix;                          // 128-key tiles of the prefix
+  int split, waves, min_places;          // see PrefixWalk
+  Divisor by_entry, by_tiles;            // entry_rows, n_tiles
+};
+
+struct PrefixParams : PrefixGeo {
   // Keys and values that lie in tensors: the prefix [Hk][Np][d], the own ones [B][Hk][Nk][d], any
   // strides: maps {d, rows, heads, batch} with boxes of 64 columns and 128 rows (prefix) or
   // `grain` rows (own), 128-byte swizzle. The tall kernel's queries: boxes of 8 rows.
@@ -33,13 +60,10 @@ struct PrefixParams {
   const int *kv_len;                     // [B] or null: Nk keys everywhere
   int b0, B;                             // the launch's batch entries; q, o, kv_len and the own pages begin at b0
   int H, Hk, group, Nq, Np, Nk;          // group: query heads per k/v head
-  // Rows of one k/v head: (entry, head of the group, query), queries padded to nq_rows.
-  int nq_rows, entry_rows, rows;         // entry_rows = group * nq_rows, rows = B * entry_rows
-  int row_tile, n_tiles, n_units;        // rows of a unit; units of a head, of all
+  int nq_rows;                           // entry_rows = group * nq_rows, rows = B * entry_rows
+  Divisor by_nq, by_shard;               // nq_rows, rows_per_shard
   int copies;                            // flat kernel: copies of a unit's rows in its 128 lanes
   int grain;                             // own keys of an entry begin at multiples of this among the packed ones
-  int n_prefix;                          // 128-key tiles of the prefix
-  int split, waves, min_places;          // see PrefixWalk
   float scale_log2;
   float *parts;                          // split: [grid][2 slots] partial results
   int4 *cuts;                            // split: the unit that begins in CTA c's range and does not end there

@@ -15,7 +15,7 @@ namespace {
 
 using namespace xs;
 
-constexpr int kMostLength = 1 << 30;
+constexpr int kMostLength = 1 << 29;   // (places of a split region then fit 32 bits)
 constexpr unsigned long long kCutsBytes = 4096;   // one int4 for each CTA, at most 256 of them
 
 bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -285,6 +285,10 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
     p.row_tile = c.row_tile;
     p.n_tiles = c.n_tiles;
     p.n_units = Hk * c.n_tiles;
+    p.by_nq.set(p.nq_rows);
+    p.by_entry.set(p.entry_rows);
+    p.by_tiles.set(p.n_tiles);
+    p.by_shard.set(p.rows_per_shard > 0 ? p.rows_per_shard : 1);
     p.split = c.plan.split;
     p.waves = c.plan.waves;
     if ((tall ? launch_prefix_tall : launch_prefix_flat)(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;

@@ -475,7 +475,7 @@ typedef struct {
  * H not a multiple of H_kv; a cache whose H_kv or d differ; scale not positive and finite;
  * P not in [1, 8], Nq % P != 0; a stride below d over more than one row; ws NULL with
  * ws_bytes > 0. XS_ERR_UNSUPPORTED for d not in {64, 128}, a page_size as in xs_cache_write,
- * a length past 2^30, or 2^31 and more rows of a k/v head or tiles of 128 of them.
+ * a length past 2^29, or 2^31 and more rows of a k/v head or tiles of 128 of them.
  * XS_ERR_ALIGN for a tensor that is not 16-byte aligned, strides over more than one row that
  * are not multiples of 8, or a ws that is not 256-byte aligned. Empty problems return XS_OK. */
 xs_status xs_prefix_attn(const xs_prefix_args *args, void *o, const long long *o_stride,

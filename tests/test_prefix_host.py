@@ -49,7 +49,7 @@ CACHED = dict(pk=None, pv=None, k=None, v=None, ppages=A, pcount=1, pages=A, cou
     (dict(CACHED, cache=(A, 0, A, A, 8, 2, 64, 64)), 1), (dict(CACHED, ppages=None), 1), (dict(CACHED, pages=None), 1),
     (dict(CACHED, pcount=-1), 1),
     (dict(d=32), 2), (dict(d=256), 2), (dict(d=96), 2), (dict(CACHED, cache=(A, A, A, A, 8, 2, 48, 64)), 2),
-    (dict(Np=(1 << 30) + 1), 2), (dict(H=1 << 24, Hk=1, Nq=1 << 20, qst=(1 << 38, 1 << 34, 64), ost=(1 << 38, 1 << 34, 64)), 2),
+    (dict(Np=(1 << 29) + 1), 2), (dict(H=1 << 24, Hk=1, Nq=1 << 20, qst=(1 << 38, 1 << 34, 64), ost=(1 << 38, 1 << 34, 64)), 2),
     (dict(q=A + 8), 3), (dict(pk=A + 2), 3), (dict(v=A + 4), 3), (dict(o=A + 8), 3), (dict(kv_len=A + 2), 3),
     (dict(ws=A + 16, ws_bytes=1 << 20), 3), (dict(shards=(A, A + 8)), 3), (dict(qst=(2048, 516, 64)), 3),
     (dict(pst=(2564, 64)), 3), (dict(kst=(3084, 1536, 64)), 3), (dict(ost=(2048, 512, 68)), 3),
