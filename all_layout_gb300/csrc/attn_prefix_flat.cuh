@@ -486,9 +486,39 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
   for (; ok && more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
     if (V) ok = flat_queries<D>(p, smem, bars, item, items, tmem);
     if (!ok) break;
+    int j = item.kv0;
+    if (p.prefix_cached) {
+      // The prefix's whole tiles, in a loop of few instructions.
+      const int whole = min(item.kv1, p.Np / BN);
+      uint32_t slot = use % S, parity = (use / S & 1) ^ 1, f = f_use % F, f_parity = f_use / F & 1;
+      if (j < whole) {
+        use += whole - j;
+        f_use += whole - j;
+        pending &= ~3u;
+      }
+#pragma unroll 1
+      for (; j < whole; ++j) {
+        if (!(ok = wait(bars->f_full[F0 + f], f_parity) && wait(empty_of[slot], parity))) break;
+        const uint8_t *raw = smem + C::OFF_F + (F0 + f) * C::RAW;
+        uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
+        const uint32_t empty = smem_u32(&bars->f_empty[F0 + f]);
+        if (V) {
+          convert_values<D>(raw, dst, 16, tid, empty);
+        } else {
+          // (The scores' slot of the scales: tile `use` modulo four.)
+          reinterpret_cast<float *>(smem + C::OFF_FAC)[((use - (whole - j)) & 3) * BN + tid] = power_of(raw[BN * D + tid]) * p.scale_log2;
+          convert_keys<D>(raw, dst, tid, empty);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(full_of + slot));
+        if (++slot == S) slot = 0, parity ^= 1;
+        if (++f == F) f = 0, f_parity ^= 1;
+      }
+    }
     // TMA loads go out one tile ahead of the clearing that V's may need.
-    ok = issue(item.kv0, use);
-    for (int j = item.kv0; ok && j < item.kv1; ++j, ++use) ok = issue(j + 1, use + 1) && finish(j);
+    ok = ok && issue(j, use);
+    for (; ok && j < item.kv1; ++j, ++use) ok = issue(j + 1, use + 1) && finish(j);
   }
   // Every load issued must land before the CTA releases its shared memory.
   if (issuer)
