@@ -133,8 +133,44 @@ __device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars
     return r;
   };
   for (; ok && more; more = next_item(&bars->start, table, &walk, &item)) {
-    Part ahead = part_at(item.kv0);
-    for (int j = item.kv0; ok && j < item.kv1; ++j) {
+    int j = item.kv0;
+    if (p.prefix_cached && psize >= BN) {
+      // The prefix's whole tiles, each in one page: a loop of few instructions.
+      const int whole = min(item.kv1, p.Np / BN);
+      const uint8_t *codes = p.codes[V ? 1 : 0], *scales = p.scales[V ? 1 : 0] + lane * 16;
+      uint32_t slot = use % F, parity = (use / F & 1) ^ 1;
+      const int shift = p.prefix_pages.shift, n_pages = p.prefix_pages.n_pages, count = p.prefix_pages.count;
+      auto page_at = [&](int t) {
+        const int i = t * BN >> shift;
+        return t < whole && i < count ? __ldg(p.prefix_pages.pages + i) : -1;
+      };
+      if (j < whole) use += whole - j;
+      int next = page_at(j);
+#pragma unroll 1
+      for (; j < whole; ++j) {
+        const int page = next;
+        next = page_at(j + 1);   // (not looked at before its turn)
+        const bool held = static_cast<unsigned>(page) < static_cast<unsigned>(n_pages);
+        const long long row = (static_cast<long long>(page) * p.Hk + item.hk) * psize + (j * BN & (psize - 1));
+        const uint32_t full = smem_u32(&bars->f_full[F0 + slot]), dst = smem_u32(smem + C::OFF_F + (F0 + slot) * C::RAW);
+        if (!(ok = wait_for<true>(smem_u32(&bars->f_empty[F0 + slot]), parity, abort_flag, p))) {
+          use -= whole - j;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, held ? BN * D : 0);
+          if (held) bulk_load(dst, codes + row * D, BN * D, full);
+        }
+        if (lane < BN / 16) {
+          copy16(dst + BN * D + lane * 16, held ? static_cast<const void *>(scales + row) : g_nan_scales);
+          copies_arrive(full);
+        }
+        __syncwarp();
+        if (++slot == F) slot = 0, parity ^= 1;
+      }
+    }
+    Part ahead = part_at(j);
+    for (; ok && j < item.kv1; ++j) {
       const Part r = ahead;
       ahead = part_at(j + 1);
       if (!is_cached(p, j)) continue;
@@ -428,16 +464,21 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     } else {
       Grain g{0, 0, 0};
       if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
+      // Keys of one request lie one after the other: a box of 128 rows, which may reach past its last.
+      const int first_b = __shfl_sync(0xffffffffu, g.b, 0), first_off = __shfl_sync(0xffffffffu, g.off, 0);
+      const bool one = __shfl_sync(0xffffffffu, g.valid, 0) > 0 &&
+                       __all_sync(0xffffffffu, g.valid == 0 || (g.b == first_b && g.off == first_off + 16 * lane));
+      const uint32_t bytes = one ? C::TILE : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
       // V's rows behind a request's last key are still to be cleared then.
       const bool whole = !V || __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16;
       if (!whole) full = smem_u32(&bars->raw[slot]);
       if (issuer) {
         if (lane == 0) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
-        if (g.valid > 0)
+        if (one ? lane == 0 : g.valid > 0)
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_4d(dst + hf * kHalf + lane * 2048, V ? &p.tm_v : &p.tm_k, full, hf * 64, g.off, item.hk, p.b0 + g.b);
+            tma_load_4d(dst + hf * kHalf + lane * 2048, one ? (V ? &p.tm_v : &p.tm_k) : V ? &p.tm_v16 : &p.tm_k16, full,
+                        hf * 64, g.off, item.hk, p.b0 + g.b);
       } else if (whole && lane == 0) {
         mbar_arrive(full);
       }
@@ -648,6 +689,14 @@ __device__ __noinline__ void mask_scores(uint32_t taddr, const float *fac, int l
   }
   tmem_wait_st();
 }
+// P of a tile to zeros.
+__device__ __noinline__ void zero_weights(uint32_t taddr) {
+  uint32_t zero[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) zero[k] = 0;
+  tmem_st32(taddr, zero);
+  tmem_st32(taddr + 32, zero);
+}
 // Weights 2^(s * scale - m) of 32 scores as bf16 pairs, and their sum added to `sum`.
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scale2, uint64_t negm2, uint32_t (&pk)[16],
                                           float (&sum)[4]) {
@@ -706,6 +755,13 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       // Two passes over the scores, as 128 of them would not fit the registers beside the rest: the
       // maximum, then the weights (each chunk of P covers scores that have been read).
       const uint32_t tC = tS + copy * (NC * 32);
+      if (__all_sync(0xffffffffu, lo >= NC * 32 || hi <= 0)) {   // nothing for any row: no weight
+        zero_weights(tS);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bars->p_full[t]));
+        continue;
+      }
       // Scores of cached keys are times the key's scale (and scale_log2) times the row's factor.
       bool times = is_cached(p, j);
       const float scale = times ? row_factor : p.scale_log2;

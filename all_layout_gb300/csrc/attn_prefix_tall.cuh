@@ -310,7 +310,16 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
         break;
       }
       tc_fence_after();
-      if (masked) mask_scores<4>(tS, nullptr, lo, hi);
+      if (masked) {
+        if (__all_sync(0xffffffffu, lo >= BN || hi <= 0)) {   // nothing for any row: no weight
+          zero_weights(tS);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_full);
+          continue;
+        }
+        mask_scores<4>(tS, nullptr, lo, hi);
+      }
       // The first half's maximum beside the second half's load.
       uint32_t s[4][32];
       tmem_ld32(tS, s[0]);

@@ -44,9 +44,9 @@ struct PrefixGeo {
 
 struct PrefixParams : PrefixGeo {
   // Keys and values that lie in tensors: the prefix [Hk][Np][d], the own ones [B][Hk][Nk][d], any
-  // strides: maps {d, rows, heads, batch} with boxes of 64 columns and 128 rows (prefix) or
-  // `grain` rows (own), 128-byte swizzle. The tall kernel's queries: boxes of 8 rows.
-  CUtensorMap tm_q, tm_pk, tm_pv, tm_k, tm_v;
+  // strides: maps {d, rows, heads, batch} with boxes of 64 columns and 128 rows, 128-byte swizzle; the flat
+  // kernel's own ones also with boxes of 16 rows. The tall kernel's queries: boxes of 8 rows.
+  CUtensorMap tm_q, tm_pk, tm_pv, tm_k, tm_v, tm_k16, tm_v16;
   // Those that lie in the cache.
   PageLists prefix_pages, own_pages;
   const uint8_t *codes[2], *scales[2];   // of k and v

@@ -46,34 +46,37 @@ bool encode_operand(CUtensorMap *m, const void *base, long long B, int H, int N,
 }
 
 // Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split schedule,
-// whichever should end earlier; costs in KV tiles. `join`: what pieces and the launch that joins them cost.
+// whichever should end earlier; costs in KV tiles. `mean`, `most`: tiles of a unit; `join`: what pieces and
+// the launch that joins them cost.
 struct Plan {
   int split, waves, grid;
-  long long cost;
+  double cost;
 };
-Plan plan(long long units, int sms, long long tiles, int least, int join, unsigned long long per_cta,
+Plan plan(long long units, int sms, double mean, double most, int least, double join, unsigned long long per_cta,
           unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
-  const long long unit = tiles + kPrefixCost, rounds = (units + grid0 - 1) / grid0;
-  const Plan whole{0, 0, grid0, rounds * unit};
-  if (tiles < 2 || static_cast<unsigned long long>(sms) * sizeof(int4) > kCutsBytes) return whole;
+  const long long rounds = (units + grid0 - 1) / grid0;
+  const double unit = mean + kPrefixCost;
+  const Plan whole{0, 0, grid0, (rounds - 1) * unit + most + kPrefixCost};
+  if (most < 2 || static_cast<unsigned long long>(sms) * sizeof(int4) > kCutsBytes) return whole;
   const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
   const long long left = units - static_cast<long long>(waves) * sms;
-  long long per = (left * unit + sms - 1) / sms;
+  double per = left * unit / sms;
   int grid = sms;
-  if (waves == 0) {
-    if (per < least) per = least;
-    grid = static_cast<int>((left * unit + per - 1) / per);
+  if (per < least) {
+    per = least;
+    grid = static_cast<int>(left * unit / per) + 1;
+    if (grid > sms) grid = sms;
   }
   if (per_cta * grid > room) return whole;
-  const long long cost = waves * unit + per + join;
+  const double cost = waves * unit + per + join;
   return cost < whole.cost ? Plan{1, waves, grid, cost} : whole;
 }
 
 // What a launch is to do, of the batch entries of one launch.
 struct Shape {
   int B, group, Hk, Nq, Np, Nk, d;
-  bool ragged;
+  bool ragged, cached;   // lengths on the device; keys in the cache
 };
 struct Choice {
   bool tall;
@@ -94,15 +97,23 @@ Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
   c.copies = tall ? 1 : c.rows <= 32 ? 4 : c.rows <= 64 ? 2 : 1;
   c.row_tile = tall ? 2 * kTileRows : kTileRows / c.copies;
   c.n_tiles = static_cast<int>((c.rows + c.row_tile - 1) / c.row_tile);
-  // Own tiles of a unit: those of the entries that its rows belong to (three quarters of them where lengths
-  // are on the device).
-  const long long entries = entry >= c.row_tile ? 1 : (c.row_tile < c.rows ? c.row_tile : c.rows) / entry;
-  const long long padded = (static_cast<long long>(s.Nk) + c.grain - 1) / c.grain * c.grain, keys = entries * padded;
-  const long long tiles = (s.Np + kTileRows - 1) / kTileRows + (keys - (s.ragged ? keys / 4 : 0) + kTileRows - 1) / kTileRows;
-  c.plan = plan(static_cast<long long>(s.Hk) * c.n_tiles, sms, tiles, kLeast, tall ? 10 : 6,
-                2ull * prefix_part_floats(s.d, c.row_tile) * 4, room);
-  // Measured times of a KV tile: a pair of row tiles in the tall kernel, one in the flat kernel.
-  c.us = c.plan.cost * (tall ? (s.d == 128 ? 1.5 : 1.2) : (s.d == 128 ? 1.9 : 1.2));
+  // Own tiles of a unit: those of the entries that its rows belong to, two entries' where a unit's rows cross
+  // from one to the next (lengths on the device are three quarters of Nk on average).
+  const double own = (static_cast<double>((static_cast<long long>(s.Nk) + c.grain - 1) / c.grain * c.grain)) / kTileRows;
+  const long long met = c.n_tiles + (entry % c.row_tile == 0 || c.row_tile % entry == 0 ? 0 : s.B - 1);
+  const double here = entry >= c.row_tile ? static_cast<double>(met) / c.n_tiles : static_cast<double>(s.B) / c.n_tiles;
+  const double top = entry >= c.row_tile ? (met > c.n_tiles ? 2 : 1)
+                                         : std::fmin(s.B, (c.row_tile + entry - 1) / entry + (c.row_tile % entry == 0 ? 0 : 1));
+  const double prefix = (s.Np + kTileRows - 1) / kTileRows;
+  // Times of a KV tile (GB300, us; 64 tiles a CTA, 128, 64 and 32 rows): the flat kernel at d = 128 1.67, 1.5
+  // and 1.5 with keys in tensors, 1.8, 1.2 and 1.15 with cached ones; at d = 64 1.06, 0.8 and 0.8, 1.55, 0.9 and
+  // 0.75. The tall kernel's, for a pair of row tiles: 1.46 and 1.27. The join: 6 us, in the tall kernel 10.
+  const bool half = s.d == 64, one = c.copies == 1;
+  const double us = tall ? (half ? 1.27 : 1.46)
+                         : s.cached ? (half ? (one ? 1.55 : 0.85) : one ? 1.8 : 1.2) : half ? (one ? 1.06 : 0.8) : one ? 1.67 : 1.5;
+  c.plan = plan(static_cast<long long>(s.Hk) * c.n_tiles, sms, prefix + own * here * (s.ragged ? 0.75 : 1.0), prefix + own * top,
+                kLeast, (tall ? 10 : 6) / us, 2ull * prefix_part_floats(s.d, c.row_tile) * 4, room);
+  c.us = c.plan.cost * us;
   return c;
 }
 
@@ -200,7 +211,7 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
   char *area = room > 0 ? static_cast<char *>(ws) + kCutsBytes : nullptr;
   p.cuts = static_cast<int4 *>(ws);
   // The kernel: with many rows the tall one, which wants cached keys and values in the workspace first.
-  Shape shape{chunk, group, Hk, Nq, Np, Nk, d, a->kv_len != nullptr};
+  Shape shape{chunk, group, Hk, Nq, Np, Nk, d, a->kv_len != nullptr, Np >= Nk ? prefix_cached : own_cached};
   const unsigned long long prefix_bytes = prefix_cached ? unpacked(static_cast<long long>(Hk) * Np, d) : 0;
   const unsigned long long own_bytes = own_cached ? unpacked(static_cast<long long>(B) * Hk * Nk, d) : 0;
   bool tall = false;
@@ -253,14 +264,15 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
     }
   }
   p.parts = reinterpret_cast<float *>(area);
-  const unsigned box = tall ? kTileRows : 16;
   if (Np > 0 && !p.prefix_cached &&
       (!encode_operand(&p.tm_pk, prefix_k, 1, Hk, Np, d, 0, pk_stride[0], pk_stride[1], kTileRows) ||
        !encode_operand(&p.tm_pv, prefix_v, 1, Hk, Np, d, 0, pv_stride[0], pv_stride[1], kTileRows)))
     return XS_ERR_CUDA;
   if (Nk > 0 && !p.own_cached &&
-      (!encode_operand(&p.tm_k, own_k, B, Hk, Nk, d, k_stride[0], k_stride[1], k_stride[2], box) ||
-       !encode_operand(&p.tm_v, own_v, B, Hk, Nk, d, v_stride[0], v_stride[1], v_stride[2], box)))
+      (!encode_operand(&p.tm_k, own_k, B, Hk, Nk, d, k_stride[0], k_stride[1], k_stride[2], kTileRows) ||
+       !encode_operand(&p.tm_v, own_v, B, Hk, Nk, d, v_stride[0], v_stride[1], v_stride[2], kTileRows) ||
+       (!tall && (!encode_operand(&p.tm_k16, own_k, B, Hk, Nk, d, k_stride[0], k_stride[1], k_stride[2], 16) ||
+                  !encode_operand(&p.tm_v16, own_v, B, Hk, Nk, d, v_stride[0], v_stride[1], v_stride[2], 16)))))
     return XS_ERR_CUDA;
   if (tall && !encode_operand(&p.tm_q, a->q, B, H, Nq, d, p.q_b, p.q_h, p.q_n, 8)) return XS_ERR_CUDA;
   p.n_prefix = (Np + kTileRows - 1) / kTileRows;

@@ -125,3 +125,11 @@ KINDS = [("bf16", "bf16"), ("cache", "bf16"), ("bf16", "cache"), ("cache", "cach
 ])
 def test_formula(xs, prefix, own, B, H, Hk, d, Nq, Np, Nk, lens):
     Problem(xs, B, H, Hk, d, Nq, Np, Nk, lens, prefix, own, seed=B + Nq).test()
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 256, 1024])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_pages(xs, page, d, Nq):
+    """Pages smaller and larger than a tile, ends inside a tile."""
+    Problem(xs, 3, 4, 2, d, Nq, 1500, 333, [333, 16, 0], "cache", "cache", page=page, seed=page).test()
