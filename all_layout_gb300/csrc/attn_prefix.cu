@@ -210,12 +210,20 @@ __device__ __forceinline__ void begin_schedule(const PrefixParams &p, int *table
   }
 }
 
+// Where the join finds the unit that begins in this CTA's range: with no more units than CTAs in the split
+// region a place for each unit (the join is then launched for so many), else one for each CTA.
+__device__ __forceinline__ bool cut_by_unit(const PrefixGeo &p) {
+  return p.n_units - p.waves * static_cast<int>(gridDim.x) <= static_cast<int>(gridDim.x);
+}
+__device__ __forceinline__ int4 *cut_place(const PrefixParams &p, int unit) {
+  return p.cuts + (cut_by_unit(p) ? unit - p.waves * static_cast<int>(gridDim.x) : static_cast<int>(blockIdx.x));
+}
 // How many consecutive CTAs, from the one that begins the unit, its pieces run on.
 __device__ __forceinline__ int pieces_of(const PrefixPlan &plan, unsigned u0, int n) {
   return static_cast<int>((u0 + n - 1) / plan.per - u0 / plan.per) + 1;
 }
 
-// One row of a k/v head's rows; n >= Nq: padding.
+// One row of a k/v head's rows; n >= Nq or h past the k/v head's: padding.
 struct PrefixRow {
   int b, h, n;
 };
@@ -231,7 +239,7 @@ __device__ __forceinline__ PrefixRow row_of(const PrefixParams &p, int hk, int r
 __device__ __forceinline__ uint16_t *out_row(const PrefixParams &p, int hk, int row, int d) {
   if (row >= p.rows) return nullptr;
   const PrefixRow r = row_of(p, hk, row);
-  if (r.n >= p.Nq) return nullptr;
+  if (r.n >= p.Nq || r.h >= (hk + 1) * p.group) return nullptr;
   if (p.shard_mode) {
     const int sh = p.by_shard.of(r.n), i = r.n - sh * p.rows_per_shard;
     return static_cast<uint16_t *>(p.shards[sh]) +
@@ -342,84 +350,100 @@ __device__ __forceinline__ void issue_pv(uint32_t dcol, uint32_t pcol, uint64_t 
 #include "attn_prefix_tall.cuh"
 
 // ------------------------------------------------------------------ joining pieces
-// The pieces of the unit that begins in CTA blockIdx.x's range: 32 rows (blockIdx.y) and 8 columns
-// (blockIdx.z) a block, a lane per row. The eight warps take every eighth part each, four of them under way at
-// a time and joined with a running maximum, and their sums are joined in order, so the result does not depend
-// on the order in which the pieces ended.
+// The pieces of the unit that begins in CTA blockIdx.x's range: 32 rows (blockIdx.y) and a slice of the columns
+// (blockIdx.z of gridDim.z) a block, a lane per row. The eight warps share the parts and the groups of eight
+// columns between them: with few parts a warp takes all of them, with many each takes every eighth. Six parts
+// are under way at a time and joined with a running maximum, the warps' sums in order, so the result does not
+// depend on the order in which the pieces ended.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PrefixParams p) {
+  constexpr int U = 6;   // parts under way
   __shared__ float sums[kJoinWarps][10][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 32 + lane, c8 = blockIdx.z;
+  const int row = blockIdx.y * 32 + lane;
   const int R = p.row_tile > BM ? p.row_tile : BM;
+  const int groups = D / 8 / gridDim.z;   // of columns
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 cut = __ldcg(p.cuts + blockIdx.x);   // unit, pieces, k/v head, first row
-  if (cut.y == 0 || cut.w + static_cast<int>(blockIdx.y) * 32 >= p.rows) return;
+  const int4 cut = __ldcg(p.cuts + blockIdx.x);   // first CTA, pieces (0: not cut), k/v head, first row
+  // (The places are of the launch before, but for a CTA that gave up: nothing is taken on trust.)
+  if (cut.y <= 0 || cut.x < 0 || cut.y > p.grid - cut.x || cut.z < 0 || cut.z >= p.Hk || cut.w < 0 ||
+      cut.w + static_cast<int>(blockIdx.y) * 32 >= p.rows)
+    return;
   // Part k: copy k mod copies of piece k / copies.
   const int step = p.copies == 4 ? 2 : p.copies - 1, parts = cut.y << step;
-  float m = -INFINITY, x[9];
-#pragma unroll
-  for (int i = 0; i < 9; ++i) x[i] = 0.f;
+  int shared = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;   // warps that share the parts of a group
+  if (shared * groups < kJoinWarps) shared = kJoinWarps / groups;
+  const int pw = warp & (shared - 1), others = kJoinWarps / shared;
+  uint16_t *dst = row < p.row_tile ? out_row(p, cut.z, cut.w + row, D) : nullptr;
 #pragma unroll 1
-  for (int k0 = warp; k0 < parts; k0 += 4 * kJoinWarps) {
-    float mk[4], l[4];
-    float4 a[4], b[4];
+  for (int g = warp / shared; g < groups; g += others) {   // (as many turns for each warp)
+    const int c8 = blockIdx.z * groups + g;
+    float m = -INFINITY, x[9];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = min(k0 + i * kJoinWarps, parts - 1);
-      const float *q = part_of<D>(p, blockIdx.x + (k >> step), k >> step == 0 ? 1 : 0, R);
-      const int at = (k & (p.copies - 1)) * p.row_tile + row;
-      mk[i] = __ldcg(q + D * R + at);
-      l[i] = __ldcg(q + (D + 1) * R + at);
-      a[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8) * R + at);
-      b[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8 + 1) * R + at);
+    for (int i = 0; i < 9; ++i) x[i] = 0.f;
+#pragma unroll 1
+    for (int k0 = pw; k0 < parts; k0 += U * shared) {
+      float mk[U], l[U];
+      float4 a[U], b[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int k = min(k0 + i * shared, parts - 1);
+        const float *q = part_of<D>(p, cut.x + (k >> step), k >> step == 0 ? 1 : 0, R);
+        const int at = (k & (p.copies - 1)) * p.row_tile + row;
+        mk[i] = __ldcg(q + D * R + at);
+        l[i] = __ldcg(q + (D + 1) * R + at);
+        a[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8) * R + at);
+        b[i] = __ldcg(reinterpret_cast<const float4 *>(q) + (2 * c8 + 1) * R + at);
+      }
+      const float before = m;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (k0 + i * shared >= parts) mk[i] = -INFINITY;
+        m = fmaxf(m, mk[i]);
+      }
+      const float keep = shrink(before, m);
+#pragma unroll
+      for (int i = 0; i < 9; ++i) x[i] *= keep;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (k0 + i * shared >= parts) break;
+        const float f = shrink(mk[i], m);
+        x[0] = fmaf(f, a[i].x, x[0]);
+        x[1] = fmaf(f, a[i].y, x[1]);
+        x[2] = fmaf(f, a[i].z, x[2]);
+        x[3] = fmaf(f, a[i].w, x[3]);
+        x[4] = fmaf(f, b[i].x, x[4]);
+        x[5] = fmaf(f, b[i].y, x[5]);
+        x[6] = fmaf(f, b[i].z, x[6]);
+        x[7] = fmaf(f, b[i].w, x[7]);
+        x[8] = fmaf(f, l[i], x[8]);
+      }
     }
-    const float before = m;
+    if (shared > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (k0 + i * kJoinWarps >= parts) mk[i] = -INFINITY;
-      m = fmaxf(m, mk[i]);
+      for (int i = 0; i < 9; ++i) sums[warp][i][lane] = x[i];
+      sums[warp][9][lane] = m;
+      __syncthreads();
+      if (pw == 0) {
+        for (int w = warp; w < warp + shared; ++w) m = fmaxf(m, sums[w][9][lane]);
+#pragma unroll
+        for (int i = 0; i < 9; ++i) x[i] = 0.f;
+        for (int w = warp; w < warp + shared; ++w) {
+          const float f = shrink(sums[w][9][lane], m);
+#pragma unroll
+          for (int i = 0; i < 9; ++i) x[i] = fmaf(f, sums[w][i][lane], x[i]);
+        }
+      }
+      __syncthreads();
     }
-    const float keep = shrink(before, m);
-#pragma unroll
-    for (int i = 0; i < 9; ++i) x[i] *= keep;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (k0 + i * kJoinWarps >= parts) break;
-      const float f = shrink(mk[i], m);
-      x[0] = fmaf(f, a[i].x, x[0]);
-      x[1] = fmaf(f, a[i].y, x[1]);
-      x[2] = fmaf(f, a[i].z, x[2]);
-      x[3] = fmaf(f, a[i].w, x[3]);
-      x[4] = fmaf(f, b[i].x, x[4]);
-      x[5] = fmaf(f, b[i].y, x[5]);
-      x[6] = fmaf(f, b[i].z, x[6]);
-      x[7] = fmaf(f, b[i].w, x[7]);
-      x[8] = fmaf(f, l[i], x[8]);
+    if (pw == 0 && dst) {
+      const float f = x[8] == 0.f ? 0.f : 1.f / x[8];
+      reinterpret_cast<uint4 *>(dst)[c8] =
+          make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f), pack_bf16x2(x[4] * f, x[5] * f),
+                     pack_bf16x2(x[6] * f, x[7] * f));
     }
   }
-#pragma unroll
-  for (int i = 0; i < 9; ++i) sums[warp][i][lane] = x[i];
-  sums[warp][9][lane] = m;
-  __syncthreads();
-  if (warp != 0 || row >= p.row_tile) return;
-  uint16_t *dst = out_row(p, cut.z, cut.w + row, D);
-  if (!dst) return;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sums[w][9][lane]);
-#pragma unroll
-  for (int i = 0; i < 9; ++i) x[i] = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float f = shrink(sums[w][9][lane], m);
-#pragma unroll
-    for (int i = 0; i < 9; ++i) x[i] = fmaf(f, sums[w][i][lane], x[i]);
-  }
-  const float f = x[8] == 0.f ? 0.f : 1.f / x[8];
-  reinterpret_cast<uint4 *>(dst)[c8] =
-      make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f), pack_bf16x2(x[4] * f, x[5] * f),
-                 pack_bf16x2(x[6] * f, x[7] * f));
 }
 
 template <int D>
@@ -443,7 +467,12 @@ cudaError_t launch_tall(const PrefixParams &p, int grid, cudaStream_t s) {
 template <int D>
 cudaError_t launch_join(const PrefixParams &p, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, ((p.row_tile < p.rows ? p.row_tile : p.rows) + 31) / 32, D / 8);
+  // Slices of the columns: about eight blocks an SM at most, of the units that may be cut.
+  const int rows = ((p.row_tile < p.rows ? p.row_tile : p.rows) + 31) / 32;
+  const long long cut = static_cast<long long>(p.n_units) - static_cast<long long>(p.waves) * grid;
+  int slices = D / 8;
+  while (slices > 1 && (cut < grid ? cut : grid) * rows * slices > 8 * 152) slices /= 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(cut < grid ? cut : grid), rows, slices);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -26,6 +26,12 @@
 // keys a tile's codes are written (256 cycles at d = 128) and read (256), its operands written (512)
 // and read (512), about as long as its 33 KB take from HBM at this SM's share of the bandwidth (1450).
 
+constexpr int kFlatOperands = 4, kFlatValues = 8, kFlatOperandWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
+// Requests whose values are not numbers, a bit each and one (kPrefixEntries) for the prefix: by item modulo two
+// and warp of V. A row of V that is not a number must not meet the zero weights of other requests' rows, so its
+// place in the operand is cleared, and the rows that see it become NaN at the end.
+constexpr int kBadWords = kPrefixEntries / 32 + 1;
+
 template <int D>
 struct FlatCfg {
   static constexpr int THREADS = 512;
@@ -36,14 +42,14 @@ struct FlatCfg {
   static constexpr int OFF_FIN = OFF_STG + BM * 16 * 4;
   static constexpr int OFF_FAC = OFF_FIN + BM * 4;             // scales of cached keys, of four tiles
   static constexpr int OFF_QF = OFF_FAC + 4 * BN * 4;          // factors of the rows
-  static constexpr int OFF_TAB = OFF_QF + BM * 4;
+  static constexpr int OFF_BAD = OFF_QF + BM * 4;              // see poison_words
+  static constexpr int OFF_TAB = OFF_BAD + 2 * kFlatOperandWarps * kBadWords * 4;
   static constexpr int OFF_BAR = OFF_TAB + kTable * 4;
   static constexpr int SMEM = OFF_BAR + 768;
   static constexpr uint32_t COL_O = 256, COL_QH = 384, COL_Q = 448;
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(OFF_BAR % 16 == 0 && RAW % 16 == 0, "alignment");
 };
-constexpr int kFlatOperands = 4, kFlatValues = 8, kFlatOperandWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
 
 struct FlatBars {
   uint64_t q_full, q_empty;
@@ -284,9 +290,11 @@ __device__ __noinline__ void convert_keys(const uint8_t *src, uint8_t *dst, uint
   slot_read(empty);
 }
 
-// Codes and scale bytes of V's raw slot to a bf16 tile; `valid`: see valid_of.
+// Codes and scale bytes of V's raw slot to a bf16 tile; `valid`, `entry`: of the sixteen rows of lanes 0-7
+// (valid_of); `bad`: this warp's words for requests whose values are not numbers.
 template <int D>
-__device__ __noinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, uint32_t tid, uint32_t empty) {
+__device__ __noinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, int entry, uint32_t *bad, uint32_t tid,
+                                           uint32_t empty) {
   constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR, U = BN / STEP;   // groups of a row's codes
   const uint32_t lane = tid & 31;
   const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
@@ -332,12 +340,35 @@ __device__ __noinline__ void convert_values(const uint8_t *src, uint8_t *dst, in
     const uint4 c = *reinterpret_cast<const uint4 *>(src + i * STEP * D);
     const uint32_t byte = scales[i * STEP], row = row0 + i * STEP;
     uint4 x = to_bf16<false>(odd ? c.z : c.x, odd ? c.w : c.y, byte), y = to_bf16<false>(odd ? c.x : c.z, odd ? c.y : c.w, byte);
-    if (static_cast<int>(row & 15) >= __shfl_sync(0xffffffffu, valid, row >> 4)) x = y = make_uint4(0, 0, 0, 0);
+    const bool counts = static_cast<int>(row & 15) < __shfl_sync(0xffffffffu, valid, row >> 4);
+    const int b = __shfl_sync(0xffffffffu, entry, row >> 4);
+    if (!counts || byte == kNanScale) x = y = make_uint4(0, 0, 0, 0);
+    if (counts && byte == kNanScale) atomicOr(bad + (b >> 5), 1u << (b & 31));
     uint8_t *to = dst + i * STEP * 128;
     *reinterpret_cast<uint4 *>(to + first0) = x;
     *reinterpret_cast<uint4 *>(to + second0) = y;
   }
   slot_read(empty);
+}
+
+// Rows of a bf16 tile of V that do not count to zeros, as well as what is not a finite number in those that do,
+// which is noted. By four warps; lanes 0-7 know of sixteen rows each whose they are and how many count.
+template <int D>
+__device__ __noinline__ void clear_rows(uint8_t *tile, int valid, int entry, uint32_t *bad, int tid) {
+#pragma unroll 1
+  for (int i = 0; i < BN * D / 8 / 128; ++i) {
+    const int at = i * 128 + tid, row = at / 8 % BN;   // 16-byte chunks of the halves, one after the other
+    uint4 *chunk = reinterpret_cast<uint4 *>(tile) + at;
+    const bool counts = (row & 15) < __shfl_sync(0xffffffffu, valid, row >> 4);
+    const int b = __shfl_sync(0xffffffffu, entry, row >> 4);
+    uint4 v = *chunk;
+    auto odd = [](uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); };   // exponents of infinities and NaN
+    const uint32_t x = odd(v.x), y = odd(v.y), z = odd(v.z), w = odd(v.w);
+    if (counts && (x | y | z | w) == 0) continue;
+    if (counts) atomicOr(bad + (b >> 5), 1u << (b & 31));
+    v = counts ? make_uint4(v.x & ~x, v.y & ~y, v.z & ~z, v.w & ~w) : make_uint4(0, 0, 0, 0);
+    *chunk = v;
+  }
 }
 
 // An item's queries to Tensor Memory by four warps of different lane quarters, a row a thread (the copies begin
@@ -438,11 +469,13 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
   PrefixItem item = bars->start.item;
   bool more = bars->start.any != 0;
 
-  // Rows of V behind a request's last key: their weights are 0, but what lies there may not be a number.
-  auto valid_of = [&](int j) {   // of the lane's sixteen keys, in lanes 0-7
-    if (lane >= BN / 16) return 16;
-    if (j < p.n_prefix) return min(max(p.Np - j * BN - lane * 16, 0), 16);
-    return grain_of(p, table, item, own_pos(p, item, j) + lane * 16).valid;
+  uint32_t *bad = nullptr;   // V: the item's words
+  // Lanes 0-7: of sixteen keys each, whose they are and how many count. (Rows of V behind a request's last key
+  // have the weight 0, but what lies there may not be a number.)
+  auto valid_of = [&](int j) {
+    if (lane >= BN / 16) return Grain{0, 0, 16};
+    if (j < p.n_prefix) return Grain{kPrefixEntries, 0, min(max(p.Np - j * BN - lane * 16, 0), 16)};
+    return grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
   };
   // TMA loads of a tile that is not cached, use `u` of the ring. All warps wait for the slot and arrive at its
   // barrier, though one of them issues: a phase then cannot end before each has seen the one before it. (One
@@ -469,8 +502,9 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
       const bool one = __shfl_sync(0xffffffffu, g.valid, 0) > 0 &&
                        __all_sync(0xffffffffu, g.valid == 0 || (g.b == first_b && g.off == first_off + 16 * lane));
       const uint32_t bytes = one ? C::TILE : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
-      // V's rows behind a request's last key are still to be cleared then.
-      const bool whole = !V || __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16;
+      // V's rows behind a request's last key are still to be cleared then, and those of an item of several
+      // requests to be looked through.
+      const bool whole = !V || (item.b_lo == item.b_hi && __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16);
       if (!whole) full = smem_u32(&bars->raw[slot]);
       if (issuer) {
         if (lane == 0) mbar_arrive_expect_tx(full, bytes);
@@ -493,8 +527,9 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     const uint32_t slot = use % S;
     const bool cached = is_cached(p, j);
     if (!cached && (!V || j < p.n_prefix)) return true;
-    const int valid = V ? valid_of(j) : 16;
-    const bool clear = __any_sync(0xffffffffu, valid < 16);
+    Grain g{0, 0, 16};
+    if (V) g = valid_of(j);
+    const int valid = g.valid;
     uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
     if (cached) {
       const uint32_t f = F0 + f_use % F, empty = smem_u32(&bars->f_empty[f]);
@@ -502,20 +537,18 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
       pending &= ~(1u << slot);
       const uint8_t *raw = smem + C::OFF_F + f * C::RAW;
       if (V) {
-        convert_values<D>(raw, dst, valid, tid, empty);
+        convert_values<D>(raw, dst, valid, g.b, bad, tid, empty);
       } else {
         reinterpret_cast<float *>(smem + C::OFF_FAC)[(use & 3) * BN + tid] = power_of(raw[BN * D + tid]) * p.scale_log2;
         convert_keys<D>(raw, dst, tid, empty);
       }
       ++f_use;
     } else {
-      if (!clear) return true;
+      if (item.b_lo == item.b_hi && !__any_sync(0xffffffffu, valid < 16)) return true;
       if (!wait(bars->raw[slot], raw_parity >> slot & 1)) return false;
       raw_parity ^= 1u << slot;
       pending &= ~(4u << slot);
-      if ((tid & 15) >= __shfl_sync(0xffffffffu, valid, tid >> 4))
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4 *>(dst + (i / 8) * kHalf + tid * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+      clear_rows<D>(dst, valid, g.b, bad, tid);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -527,6 +560,11 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
   for (; ok && more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
     if (V) ok = flat_queries<D>(p, smem, bars, item, items, tmem);
     if (!ok) break;
+    if (V) {   // (the softmax is done with the item before last, as it has begun the last one)
+      bad = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD) + ((items & 1) * kFlatOperandWarps + tid / 32) * kBadWords;
+      if (lane < kBadWords) bad[lane] = 0;
+      __syncwarp();
+    }
     int j = item.kv0;
     if (p.prefix_cached) {
       // The prefix's whole tiles, in a loop of few instructions.
@@ -544,7 +582,7 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
         uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
         const uint32_t empty = smem_u32(&bars->f_empty[F0 + f]);
         if (V) {
-          convert_values<D>(raw, dst, 16, tid, empty);
+          convert_values<D>(raw, dst, 16, kPrefixEntries, bad, tid, empty);
         } else {
           // (The scores' slot of the scales: tile `use` modulo four.)
           reinterpret_cast<float *>(smem + C::OFF_FAC)[((use - (whole - j)) & 3) * BN + tid] = power_of(raw[BN * D + tid]) * p.scale_log2;
@@ -860,6 +898,15 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
     }
     wait(bars->o_full, items & 1);
     tc_fence_after();
+    {
+      const uint32_t *bad = reinterpret_cast<const uint32_t *>(smem + C::OFF_BAD) + (items & 1) * kFlatOperandWarps * kBadWords;
+      const int b = p.by_entry.of(min(row, p.rows - 1));
+      uint32_t any = 0;
+#pragma unroll
+      for (int w = 0; w < kFlatOperandWarps; ++w)
+        any |= bad[w * kBadWords + (b >> 5)] >> (b & 31) | bad[w * kBadWords + kPrefixEntries / 32];
+      if (any & 1) l = NAN;
+    }
     if (item.piece) {
       // Every copy's sums as they are; the join adds the copies with the pieces.
       float *part = part_of<D>(p, blockIdx.x, item.kv0 == 0 ? 1 : 0, BM);
@@ -870,7 +917,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         __stcg(part + (D + 1) * BM + tid, l);
       }
       if (tid == 0 && item.kv0 == 0)
-        __stcg(p.cuts + blockIdx.x, make_int4(item.unit, dead ? 0 : pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
+        __stcg(cut_place(p, item.unit), make_int4(blockIdx.x, dead ? 0 : pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
       if (!idle) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -888,6 +935,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       tc_fence_before();
       continue;
     }
+    if (tid == 0 && item.u0 > 0 && cut_by_unit(p)) __stcg(cut_place(p, item.unit), make_int4(0, 0, 0, 0));
     // (m, l) of all copies of a row.
     float top = m, total = l, f = 1.f;
     if constexpr (COPIES > 1) {
@@ -970,7 +1018,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       tc_fence_before();
     }
   }
-  if (p.split && tid == 0 && !cut) __stcg(p.cuts + blockIdx.x, make_int4(0, 0, 0, 0));
+  if (p.split && tid == 0 && !cut && !cut_by_unit(p)) __stcg(p.cuts + blockIdx.x, make_int4(0, 0, 0, 0));
 }
 
 template <int D>

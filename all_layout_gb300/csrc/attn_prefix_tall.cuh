@@ -4,8 +4,9 @@
 // 6 bytes a value, against 4 flops for every row that meets it.)
 //
 // Both tiles of a unit go over the same KV tiles, each KV tile loaded once for the pair. Own keys
-// are packed at multiples of 128, so a KV tile has keys of one request only; a tile of rows skips
-// those of requests that it has no row of.
+// and a request's rows are padded to multiples of 128, so a tile of rows and a KV tile are of one request
+// each; a tile of rows takes the prefix and its own request's keys. (Its zero weights never meet another
+// request's values, which might not be numbers.)
 //
 // Roles (320 threads, one CTA per SM):
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, row r of the tile = TMEM lane r
@@ -95,12 +96,12 @@ __device__ void tall_loader(const PrefixParams &p, uint8_t *smem, TallBars *bars
     {
       // Eight rows a lane (queries are padded to multiples of eight, so they are one head's).
       const int row = item.row0 + lane * 8;
-      const bool live = row < p.rows;
+      const PrefixRow r = row_of(p, item.hk, min(row, p.rows - 1));
+      const bool live = row < p.rows && r.n < p.Nq && r.h < (item.hk + 1) * p.group;
       const unsigned bytes = __popc(__ballot_sync(0xffffffffu, live)) * 8u * D * 2;
       if (lane == 0) mbar_arrive_expect_tx(q_full, bytes);
       __syncwarp();
       if (live) {
-        const PrefixRow r = row_of(p, item.hk, row);
         const uint32_t dst = smem_u32(smem) + (lane / 16) * C::TILE + (lane % 16) * 1024;
         for (int hf = 0; hf < D / 64; ++hf) tma_load_4d(dst + hf * kHalf, &p.tm_q, q_full, hf * 64, r.n, r.h, p.b0 + r.b);
       }
@@ -388,7 +389,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
         __stcg(part + (D + 1) * 2 * BM + at, l);
       }
       if (tid == 0 && item.kv0 == 0) {
-        __stcg(p.cuts + blockIdx.x, make_int4(item.unit, pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
+        __stcg(cut_place(p, item.unit), make_int4(blockIdx.x, pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
       }
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -406,6 +407,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
       tc_fence_before();
       continue;
     }
+    if (tid == 0 && item.u0 > 0 && cut_by_unit(p)) __stcg(cut_place(p, item.unit), make_int4(0, 0, 0, 0));
     // Rows lie across the lanes: through shared memory, 64 columns at a time (16-byte chunks, each row's
     // permuted by its number against bank conflicts), so that eight lanes store a row's 128 bytes together.
     const float norm = l == 0.f ? 0.f : 1.f / l;
@@ -439,7 +441,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
     }
     tc_fence_before();
   }
-  if (p.split && tid == 0 && !cut) __stcg(p.cuts + blockIdx.x, make_int4(0, 0, 0, 0));
+  if (p.split && tid == 0 && !cut && !cut_by_unit(p)) __stcg(p.cuts + blockIdx.x, make_int4(0, 0, 0, 0));
 }
 
 template <int D>

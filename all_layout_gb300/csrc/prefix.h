@@ -60,13 +60,14 @@ struct PrefixParams : PrefixGeo {
   const int *kv_len;                     // [B] or null: Nk keys everywhere
   int b0, B;                             // the launch's batch entries; q, o, kv_len and the own pages begin at b0
   int H, Hk, group, Nq, Np, Nk;          // group: query heads per k/v head
-  int nq_rows;                           // entry_rows = group * nq_rows, rows = B * entry_rows
+  int nq_rows;                           // entry_rows >= group * nq_rows, rows = B * entry_rows
   Divisor by_nq, by_shard;               // nq_rows, rows_per_shard
   int copies;                            // flat kernel: copies of a unit's rows in its 128 lanes
   int grain;                             // own keys of an entry begin at multiples of this among the packed ones
   float scale_log2;
   float *parts;                          // split: [grid][2 slots] partial results
-  int4 *cuts;                            // split: the unit that begins in CTA c's range and does not end there
+  int4 *cuts;                            // split: what the join is to do (cut_place)
+  int grid;                              // CTAs of the launch
   int *status;
   unsigned long long wait_limit_ns;
 };

@@ -80,7 +80,7 @@ struct Shape {
 };
 struct Choice {
   bool tall;
-  int grain, nq_rows, copies, row_tile, n_tiles;
+  int grain, nq_rows, entry_rows, copies, row_tile, n_tiles;
   long long rows;
   Plan plan;
   double us;
@@ -92,7 +92,10 @@ Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
   c.tall = tall;
   c.grain = tall ? kTileRows : 16;
   c.nq_rows = tall ? (s.Nq + 7) / 8 * 8 : s.Nq;
-  const long long entry = static_cast<long long>(s.group) * c.nq_rows;
+  // (In the tall kernel a tile of 128 rows belongs to one request.)
+  long long entry = static_cast<long long>(s.group) * c.nq_rows;
+  if (tall) entry = (entry + kTileRows - 1) / kTileRows * kTileRows;
+  c.entry_rows = static_cast<int>(entry);
   c.rows = s.B * entry;
   c.copies = tall ? 1 : c.rows <= 32 ? 4 : c.rows <= 64 ? 2 : 1;
   c.row_tile = tall ? 2 * kTileRows : kTileRows / c.copies;
@@ -168,8 +171,8 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
   if (chunk < 1) chunk = 1;
   if (chunk > B) chunk = B;
   const int group = H > 0 ? H / Hk : 1;
-  if (!empty && (static_cast<double>(chunk) * group * (Nq + 7.0) > 2147483647.0 - 256 ||
-                 (static_cast<double>(chunk) * group * (Nq + 7.0) / 32 + 1) * Hk > 2147483647.0))
+  if (!empty && (static_cast<double>(chunk) * group * (Nq + 135.0) > 2147483647.0 - 256 ||
+                 (static_cast<double>(chunk) * group * (Nq + 135.0) / 32 + 1) * Hk > 2147483647.0))
     return XS_ERR_UNSUPPORTED;
   if (st != XS_OK || !aligned(a->q, 16) || !aligned(a->prefix_k, 16) || !aligned(a->prefix_v, 16) ||
       !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(o, 16) || !aligned(a->kv_len, 4) || !aligned(ws, 256) ||
@@ -291,7 +294,7 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
     if (p.own_cached) p.own_pages.pages = a->pages.pages + b0 * a->pages.stride;
     p.grain = c.grain;
     p.nq_rows = c.nq_rows;
-    p.entry_rows = group * c.nq_rows;
+    p.entry_rows = c.entry_rows;
     p.rows = static_cast<int>(c.rows);
     p.copies = c.copies;
     p.row_tile = c.row_tile;
@@ -303,6 +306,7 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
     p.by_shard.set(p.rows_per_shard > 0 ? p.rows_per_shard : 1);
     p.split = c.plan.split;
     p.waves = c.plan.waves;
+    p.grid = c.plan.grid;
     if ((tall ? launch_prefix_tall : launch_prefix_flat)(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;
     if (p.split && launch_prefix_join(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;
   }
