@@ -11,14 +11,19 @@
 // e4m3 has 4 significant bits, bf16 8. A row that holds a NaN or an infinity gets the scale
 // byte 255 and reads as NaN.
 //
-// Bound: HBM, every value read once and written once (3 bytes a value from or to bf16). A lane
-// has eight columns of a row, a row the power of two of lanes at or above d / 8, its maximum
-// comes by shuffles; kRows rows a thread are loaded before the first is used.
+// Bound: HBM, every value read once and written once (3 bytes a value from or to bf16), once the
+// instructions are few enough. So a lane has 16 columns of a row (one vector of codes, two or four
+// of values), a row the power of two of lanes at or above d / 16; 16-bit magnitudes are compared in
+// pairs, the maximum of a row comes by shuffles; and a thread's two rows are loaded before the first
+// is used. Measured at 65536 rows of 24 heads of 128 (1.21 GB): read 178 us = 6.8 TB/s, write 202 us
+// = 6.0 TB/s; with 8 columns a lane and four rows 246 and 382 us, with 16 and one row 211 and 243,
+// with four rows 194 and 194 but the small calls up to 1.6 times as long.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/xs.h"
 #include "cache.h"
@@ -27,7 +32,10 @@
 namespace xs {
 namespace {
 
-constexpr int kCacheThreads = 256, kRows = 4;
+constexpr int kCacheThreads = 256, kRows = 2, kColumns = 16;
+// CTAs that an SM holds: what bounds the registers, without spills.
+template <class T, bool WRITE>
+constexpr int kBlocks = !WRITE ? 8 : sizeof(T) == 4 ? 4 : 5;
 
 struct CacheParams {
   PageLists lists;
@@ -39,30 +47,58 @@ struct CacheParams {
   int lanes;                            // lanes of a row
 };
 
-// Eight values to and from fp32.
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
-  const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+// A lane's columns of a row as they lie in memory, and the pairs of values that they are.
+template <class T>
+struct Columns {
+  static constexpr int kVecs = kColumns * static_cast<int>(sizeof(T)) / 16;
+  uint4 w[kVecs];
+  __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < kVecs; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
   }
-}
-__device__ __forceinline__ void load8(const __half *p, float (&f)[8]) {
-  const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __half2 h;
-    memcpy(&h, &u[i], 4);
-    const float2 t = __half22float2(h);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
+    for (int i = 0; i < kVecs; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    const uint4 &v = w[i >> 2];
+    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+  }
+};
+__device__ __forceinline__ float2 pair_at(const Columns<float> &c, int i) {
+  return make_float2(__uint_as_float(c.word(2 * i)), __uint_as_float(c.word(2 * i + 1)));
+}
+__device__ __forceinline__ float2 pair_at(const Columns<__nv_bfloat16> &c, int i) {
+  const uint32_t u = c.word(i);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_at(const Columns<__half> &c, int i) {
+  const uint32_t u = c.word(i);
+  __half2 h;
+  memcpy(&h, &u, 4);
+  return __half22float2(h);
+}
+
+// The bits of the largest magnitude of a row, as fp32, over its lanes. Magnitudes order as their
+// bits do, infinities and NaN above all; 16-bit ones are compared in pairs.
+__device__ __forceinline__ uint32_t biggest(const Columns<float> &c, int lanes) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < kColumns; ++i) big = max(big, c.word(i) & 0x7fffffffu);
+  for (int o = 1; o < lanes; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+  return big;
+}
+template <class T>
+__device__ __forceinline__ uint32_t biggest(const Columns<T> &c, int lanes) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < kColumns / 2; ++i) big = __vmaxu2(big, c.word(i) & 0x7fff7fffu);
+  for (int o = 1; o < lanes; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
+  big = max(big >> 16, big & 0xffffu);
+  if constexpr (std::is_same<T, __half>::value) {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(big))));
+  } else {
+    return big << 16;
   }
 }
 __device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
@@ -126,61 +162,59 @@ __device__ __forceinline__ long long row_at(const CacheParams &p, int b, int h, 
 }
 
 template <class T, bool WRITE>
-__global__ void __launch_bounds__(kCacheThreads) cache_kernel(const __grid_constant__ CacheParams p) {
+__global__ void __launch_bounds__(kCacheThreads, kBlocks<T, WRITE>) cache_kernel(const __grid_constant__ CacheParams p) {
   const int kv = blockIdx.y & 1;
   const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, groups = kCacheThreads / p.lanes;
-  const long long base = static_cast<long long>(blockIdx.x) * groups * kRows + group;
-  const bool in_row = lane * 8 < p.d;
-  const long long rows = static_cast<long long>(p.Hk) * p.N;
+  const int c0 = lane * kColumns;
+  const bool in_row = c0 < p.d;
+  // Rows base, base + groups, ... of the Hk * N; the division is done for the first of them.
+  const long long base = static_cast<long long>(blockIdx.x) * groups * kRows + group, rows = static_cast<long long>(p.Hk) * p.N;
   for (int b = blockIdx.y >> 1; b < p.B; b += gridDim.y >> 1) {
     const int live = p.lens ? min(max(__ldg(p.lens + b), 0), p.N) : p.N;
     const long long first = p.start ? __ldg(p.start + b) : 0;
+    T *const xb = const_cast<T *>(static_cast<const T *>(p.x[kv])) + b * p.x_b[kv] + c0;
+    const unsigned r0 = static_cast<unsigned>(min(base, rows));
+    int h = static_cast<int>(r0 / static_cast<unsigned>(p.N)), n = static_cast<int>(r0 - static_cast<unsigned>(h) * static_cast<unsigned>(p.N));
     long long at[kRows];
     T *x[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const long long r = base + static_cast<long long>(u) * groups;
-      const int h = static_cast<int>(static_cast<unsigned>(min(r, rows - 1)) / static_cast<unsigned>(p.N));
-      const int n = static_cast<int>(r - static_cast<long long>(h) * p.N);
-      at[u] = r < rows && n < live ? row_at(p, b, h, n, first) : -2;
-      x[u] = const_cast<T *>(static_cast<const T *>(p.x[kv])) + b * p.x_b[kv] + h * p.x_h[kv] + n * p.x_n[kv] + lane * 8;
+      at[u] = h < p.Hk && n < live ? row_at(p, b, h, n, first) : -2;
+      x[u] = xb + h * p.x_h[kv] + n * p.x_n[kv];
+      n += groups;
+      while (n >= p.N && h < p.Hk) n -= p.N, ++h;
     }
     if constexpr (WRITE) {
-      float f[kRows][8];
+      Columns<T> c[kRows];
 #pragma unroll
       for (int u = 0; u < kRows; ++u)
-        if (at[u] >= 0 && in_row) {
-          load8(x[u], f[u]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
-        }
+        if (at[u] >= 0 && in_row)
+          c[u].load(x[u]);
+        else
+          c[u].clear();
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
-        uint32_t big = 0;   // magnitudes order as their bits do, infinities and NaN above all
-#pragma unroll
-        for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(f[u][i]) & 0x7fffffffu);
-        for (int o = 1; o < p.lanes; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+        const int byte = scale_byte(biggest(c[u], p.lanes));
         if (at[u] < 0) continue;
-        const int byte = scale_byte(big);
-        uint2 code = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-        if (byte != kNanScale) {
-          const float s = __int_as_float((254 - byte) << 23);   // 2^-e
-          code.x = codes4(f[u][0] * s, f[u][1] * s, f[u][2] * s, f[u][3] * s);
-          code.y = codes4(f[u][4] * s, f[u][5] * s, f[u][6] * s, f[u][7] * s);
+        const float s = __int_as_float((254 - byte) << 23);   // 2^-e
+        uint32_t code[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 l = pair_at(c[u], 2 * j), r = pair_at(c[u], 2 * j + 1);
+          code[j] = byte == kNanScale ? 0x7f7f7f7fu : codes4(l.x * s, l.y * s, r.x * s, r.y * s);
         }
-        if (in_row) *reinterpret_cast<uint2 *>(p.codes[kv] + at[u] * p.d + lane * 8) = code;
+        if (in_row) *reinterpret_cast<uint4 *>(p.codes[kv] + at[u] * p.d + c0) = make_uint4(code[0], code[1], code[2], code[3]);
         if (lane == 0) p.scales[kv][at[u]] = static_cast<uint8_t>(byte);
       }
     } else {
-      uint2 code[kRows];
+      uint4 code[kRows];
       int byte[kRows];
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
-        code[u] = make_uint2(0, 0);
+        code[u] = make_uint4(0, 0, 0, 0);
         byte[u] = kNanScale;   // a place that no page holds
         if (at[u] >= 0 && in_row) {
-          code[u] = __ldcs(reinterpret_cast<const uint2 *>(p.codes[kv] + at[u] * p.d + lane * 8));
+          code[u] = __ldcs(reinterpret_cast<const uint4 *>(p.codes[kv] + at[u] * p.d + c0));
           byte[u] = __ldg(p.scales[kv] + at[u]);
         }
       }
@@ -188,15 +222,19 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const __grid_const
       for (int u = 0; u < kRows; ++u) {
         if (at[u] == -2 || !in_row) continue;
         const float s = power_of(byte[u]);
-        float f[8];
-        const uint32_t w[4] = {code[u].x, code[u].x >> 16, code[u].y, code[u].y >> 16};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 t = values2(w[i]);
-          f[2 * i] = t.x * s;
-          f[2 * i + 1] = t.y * s;
+        for (int j = 0; j < 2; ++j) {
+          float f[8];
+          const uint32_t a = j ? code[u].z : code[u].x, b = j ? code[u].w : code[u].y;
+          const uint32_t w[4] = {a, a >> 16, b, b >> 16};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 t = values2(w[i]);
+            f[2 * i] = t.x * s;
+            f[2 * i + 1] = t.y * s;
+          }
+          store8(x[u] + 8 * j, f);
         }
-        store8(x[u], f);
       }
     }
   }
@@ -249,8 +287,8 @@ xs_status cache_call(bool write, const xs_cache *c, const void *k, const void *v
   p.Hk = c->H_kv;
   p.N = N;
   p.d = c->d;
-  p.lanes = 2;
-  while (p.lanes * 8 < c->d) p.lanes *= 2;
+  p.lanes = 1;
+  while (p.lanes * kColumns < c->d) p.lanes *= 2;
   const long long rows = static_cast<long long>(c->H_kv) * N, each = kCacheThreads / p.lanes * kRows;
   const dim3 grid(static_cast<unsigned>((rows + each - 1) / each), 2u * static_cast<unsigned>(B < 32767 ? B : 32767));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
