@@ -179,13 +179,14 @@ MapEntry g_maps[kMapCache] = {};
 unsigned long long g_map_clock = 0;
 
 bool encode_now(CUtensorMap *m, void *base, int rank, const cuuint64_t *dims,
-                const cuuint64_t *strides_bytes, const cuuint32_t *box) {
+                const cuuint64_t *strides_bytes, const cuuint32_t *box,
+                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), base, dims,
             strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -365,7 +366,7 @@ namespace xs {
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 bool encode_map(CUtensorMap *m, const void *base, int rank, const unsigned long long *dims,
-                const unsigned long long *strides_bytes, const unsigned *box) {
+                const unsigned long long *strides_bytes, const unsigned *box, int swizzle_bytes) {
   cuuint64_t d[4], st[3];
   cuuint32_t bx[4];
   for (int i = 0; i < rank; ++i) {
@@ -373,7 +374,8 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const unsigned long 
     bx[i] = box[i];
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
-  return encode_now(m, const_cast<void *>(base), rank, d, st, bx);
+  return encode_now(m, const_cast<void *>(base), rank, d, st, bx,
+                    swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace xs

@@ -26,7 +26,7 @@
 // keys a tile's codes are written (256 cycles at d = 128) and read (256), its operands written (512)
 // and read (512), about as long as its 33 KB take from HBM at this SM's share of the bandwidth (1450).
 
-constexpr int kFlatOperands = 4, kFlatValues = 8, kFlatOperandWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
+constexpr int kFlatValues = 4, kFlatGroupWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
 // Requests whose values are not numbers, a bit each and one (kPrefixEntries) for the prefix: by item modulo two
 // and warp of V. A row of V that is not a number must not meet the zero weights of other requests' rows, so its
 // place in the operand is cleared, and the rows that see it become NaN at the end.
@@ -35,27 +35,29 @@ constexpr int kBadWords = kPrefixEntries / 32 + 1;
 template <int D>
 struct FlatCfg {
   static constexpr int THREADS = 512;
-  static constexpr int TILE = BN * D * 2, RAW = BN * D + BN;   // a bf16 tile; codes and scale bytes
-  static constexpr int KS = 2, VS = 2, FK = D == 128 ? 2 : 5, FV = D == 128 ? 3 : 5, FS = FK + FV;
-  static constexpr int OFF_K = 0, OFF_V = OFF_K + KS * TILE, OFF_F = OFF_V + VS * TILE;
-  static constexpr int OFF_STG = OFF_F + FS * RAW;
+  static constexpr int TILE = BN * D * 2, RAW = BN * D + BN;   // a bf16 tile; V's codes and scale bytes
+  // K's slots hold a tile of codes or 64 columns of a bf16 one; V's operands a slot a group, its raw ring FV a group.
+  static constexpr int KN = D == 128 ? 5 : 7, VS = 2, FV = D == 128 ? 2 : 4;
+  static constexpr int OFF_K = 0, OFF_V = OFF_K + KN * kHalf, OFF_F = OFF_V + VS * TILE;
+  static constexpr int OFF_KS = OFF_F + 2 * FV * RAW;          // scale bytes of K's slots
+  static constexpr int OFF_STG = OFF_KS + KN * BN;
   static constexpr int OFF_FIN = OFF_STG + BM * 16 * 4;
   static constexpr int OFF_FAC = OFF_FIN + BM * 4;             // scales of cached keys, of four tiles
   static constexpr int OFF_QF = OFF_FAC + 4 * BN * 4;          // factors of the rows
-  static constexpr int OFF_BAD = OFF_QF + BM * 4;              // see poison_words
-  static constexpr int OFF_TAB = OFF_BAD + 2 * kFlatOperandWarps * kBadWords * 4;
+  static constexpr int OFF_BAD = OFF_QF + BM * 4;              // see kBadWords
+  static constexpr int OFF_TAB = OFF_BAD + 2 * 2 * kFlatGroupWarps * kBadWords * 4;
   static constexpr int OFF_BAR = OFF_TAB + kTable * 4;
   static constexpr int SMEM = OFF_BAR + 768;
-  static constexpr uint32_t COL_O = 256, COL_QH = 384, COL_Q = 448;
+  static constexpr uint32_t COL_O = 256, COL_Q8 = 384, COL_Q = 448;
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(OFF_BAR % 16 == 0 && RAW % 16 == 0, "alignment");
 };
 
 struct FlatBars {
   uint64_t q_full, q_empty;
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t k_full[7], k_empty[7], v_full[2], v_empty[2];
   uint64_t raw[2];                   // V tiles whose rows behind a request's last key are still to be cleared
-  uint64_t f_full[10], f_empty[10];
+  uint64_t f_full[8], f_empty[8];    // V's raw slots, the second group's behind the first one's
   uint64_t s_full[2], p_full[2], pv_done[2], o_full;
   uint64_t drain, q_seen;
   PrefixStart start;
@@ -93,7 +95,15 @@ __device__ __forceinline__ int own_pos(const PrefixParams &p, const PrefixUnit &
   return (u.t0 + j - p.n_prefix) * BN;
 }
 
-// ------------------------------------------------------------------ loader of codes
+// Whether a tile's keys (a Grain each in lanes 0 to 7) are of one request, one after the other from lane 0 on.
+__device__ __forceinline__ bool one_request(const Grain &g) {
+  const int lane = threadIdx.x & 31;
+  const int first_b = __shfl_sync(0xffffffffu, g.b, 0), first_off = __shfl_sync(0xffffffffu, g.off, 0);
+  return __shfl_sync(0xffffffffu, g.valid, 0) > 0 &&
+         __all_sync(0xffffffffu, g.valid == 0 || (g.b == first_b && g.off == first_off + 16 * lane));
+}
+
+// ------------------------------------------------------------------ loaders
 // Sixteen bytes to shared memory, and an arrival when this thread's copies so far have landed.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -101,68 +111,187 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// A warp of its own each for K and V: at the others' pace a tile's copies take one about 1000 cycles to issue.
-template <int D, bool V>
-__device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table) {
+// A lane's sixteen rows of a cached tile: page number `page` (as it was read: nothing looks at it before the
+// tile's turn, so that the load has a tile's time), from row `at` on; none: at < 0.
+struct Part {
+  int page, at;
+};
+__device__ __forceinline__ Part part_at(const PrefixParams &p, const int *table, const PrefixItem &item, int j) {
+  const int lane = threadIdx.x & 31;
+  Part r{0, -1};
+  if (j >= item.kv1 || !is_cached(p, j) || lane >= BN / 16) return r;
+  const bool prefix = j < p.n_prefix;
+  const PageLists &list = prefix ? p.prefix_pages : p.own_pages;
+  int b = 0, place = j * BN + lane * 16;
+  bool live = place < p.Np;
+  if (!prefix) {
+    const Grain g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+    b = g.b;
+    place = g.off;
+    live = g.valid > 0;
+  }
+  if (!live) return r;
+  r.at = place & (list.page - 1);
+  r.page = -1;
+  if ((place >> list.shift) < list.count) r.page = __ldg(list.pages + b * list.stride + (place >> list.shift));
+  return r;
+}
+// Rows that follow each other in a page: whether this lane's are there, and the lanes of its run.
+struct Run {
+  bool held;
+  int first, end;
+  unsigned lanes;   // those that hold rows
+};
+__device__ __forceinline__ Run run_of(const PrefixParams &p, const Part &r) {
+  const int lane = threadIdx.x & 31;
+  Run x;
+  x.held = r.at >= 0 && static_cast<unsigned>(r.page) < static_cast<unsigned>(p.prefix_pages.n_pages);
+  const int last_page = __shfl_up_sync(0xffffffffu, x.held ? r.page : -1, 1);
+  const int last_at = __shfl_up_sync(0xffffffffu, r.at, 1);
+  // (Lanes 8 to 31 hold nothing.)
+  const unsigned heads = __ballot_sync(0xffffffffu, !x.held || lane == 0 || last_page != r.page || last_at + 16 != r.at);
+  x.lanes = __ballot_sync(0xffffffffu, x.held);
+  x.first = 31 - __clz(heads & (0xffffffffu >> (31 - lane)));
+  x.end = lane + (lane < 31 ? __ffs(heads >> (lane + 1)) : 1);
+  return x;
+}
+
+// K's warp loads every tile of K, a slot of its ring for a tile of codes or for 64 columns of a bf16 one.
+template <int D>
+__device__ void flat_load_keys(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table) {
   using C = FlatCfg<D>;
-  constexpr uint32_t F = V ? C::FV : C::FK, F0 = V ? C::FK : 0;   // slots, the first
   volatile int *abort_flag = &bars->abort;
   const int lane = threadIdx.x & 31;
-  uint32_t use = 0;   // cached tiles so far
+  uint32_t slot = 0, parity = 1, used = 0;   // the ring's next; slots filled so far
   PrefixWalk walk = bars->start.walk;
   PrefixItem item = bars->start.item;
   bool more = bars->start.any != 0;
   bool ok = true;
   const int psize = p.prefix_pages.page;   // one cache: all its pages have one size
-  // Lanes 0-7: sixteen rows of a tile each, in page number `page` (as it was read: nothing looks at it before
-  // the tile's turn, so that the load has a tile's time) from row `at` on; none: at < 0.
-  struct Part {
-    int page, at;
-  };
-  auto part_at = [&](int j) {
-    Part r{0, -1};
-    if (j >= item.kv1 || !is_cached(p, j) || lane >= BN / 16) return r;
-    const bool prefix = j < p.n_prefix;
-    const PageLists &list = prefix ? p.prefix_pages : p.own_pages;
-    int b = 0, place = j * BN + lane * 16;
-    bool live = place < p.Np;
-    if (!prefix) {
-      const Grain g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
-      b = g.b;
-      place = g.off;
-      live = g.valid > 0;
-    }
-    if (!live) return r;
-    r.at = place & (psize - 1);
-    r.page = -1;
-    if ((place >> list.shift) < list.count) r.page = __ldg(list.pages + b * list.stride + (place >> list.shift));
-    return r;
+  const int big = min(psize, BN) / 16;     // lanes whose rows a large box has
+  auto next_slot = [&] {
+    ++used;
+    if (++slot == C::KN) slot = 0, parity ^= 1;
   };
   for (; ok && more; more = next_item(&bars->start, table, &walk, &item)) {
     int j = item.kv0;
     if (p.prefix_cached && psize >= BN) {
       // The prefix's whole tiles, each in one page: a loop of few instructions.
       const int whole = min(item.kv1, p.Np / BN);
-      const uint8_t *codes = p.codes[V ? 1 : 0], *scales = p.scales[V ? 1 : 0] + lane * 16;
-      uint32_t slot = use % F, parity = (use / F & 1) ^ 1;
+      const uint8_t *scales = p.scales[0] + lane * 16;
       const int shift = p.prefix_pages.shift, n_pages = p.prefix_pages.n_pages, count = p.prefix_pages.count;
       auto page_at = [&](int t) {
         const int i = t * BN >> shift;
         return t < whole && i < count ? __ldg(p.prefix_pages.pages + i) : -1;
       };
-      if (j < whole) use += whole - j;
       int next = page_at(j);
 #pragma unroll 1
       for (; j < whole; ++j) {
+        const int page = next, at = j * BN & (psize - 1);
+        next = page_at(j + 1);   // (not looked at before its turn)
+        const bool held = static_cast<unsigned>(page) < static_cast<unsigned>(n_pages);
+        const long long row = (static_cast<long long>(page) * p.Hk + item.hk) * psize + at;
+        const uint32_t full = smem_u32(&bars->k_full[slot]);
+        if (!(ok = wait_for<true>(smem_u32(&bars->k_empty[slot]), parity, abort_flag, p))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, held ? BN * D : 0);
+          if (held) tma_load_4d(smem_u32(smem + C::OFF_K + slot * kHalf), &p.tm_c, full, 0, at, item.hk, page);
+        }
+        if (lane < BN / 16) {
+          copy16(smem_u32(smem + C::OFF_KS + slot * BN + lane * 16), held ? static_cast<const void *>(scales + row) : g_nan_scales);
+          copies_arrive(full);
+        }
+        __syncwarp();
+        next_slot();
+      }
+    }
+    Part ahead = part_at(p, table, item, j);
+    for (; ok && j < item.kv1; ++j) {
+      const Part r = ahead;
+      ahead = part_at(p, table, item, j + 1);
+      if (is_cached(p, j)) {
+        // A run's rows in large boxes as far as they go, the rest in boxes of sixteen rows.
+        const Run x = run_of(p, r);
+        const int in = lane - x.first, whole = (x.end - x.first) / big * big;
+        if (!(ok = wait_for<true>(smem_u32(&bars->k_empty[slot]), parity, abort_flag, p))) break;
+        const uint32_t full = smem_u32(&bars->k_full[slot]), dst = smem_u32(smem + C::OFF_K + slot * kHalf);
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(x.lanes) * 16u * D);
+        __syncwarp();
+        if (x.held && (in >= whole || in % big == 0))
+          tma_load_4d(dst + lane * 16 * D, in < whole ? &p.tm_c : &p.tm_c16, full, 0, r.at, item.hk, r.page);
+        if (lane < BN / 16) {
+          const long long row = (static_cast<long long>(r.page) * p.Hk + item.hk) * psize + r.at;
+          if (r.at >= 0)
+            copy16(smem_u32(smem + C::OFF_KS + slot * BN + lane * 16),
+                   x.held ? static_cast<const void *>(p.scales[0] + row) : g_nan_scales);
+          copies_arrive(full);
+        }
+        __syncwarp();
+        next_slot();
+        continue;
+      }
+      // A bf16 tile, 64 columns at a time.
+      Grain g{0, 0, 0};
+      bool one = true;   // a box of 128 rows: the prefix's (rows past Np come as zeros) and one request's, past its last key too
+      if (j >= p.n_prefix) {
+        if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+        one = one_request(g);
+      }
+      const uint32_t bytes = one ? kHalf : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * 128;
+      for (int hf = 0; hf < D / 64; ++hf) {
+        if (!(ok = wait_for<true>(smem_u32(&bars->k_empty[slot]), parity, abort_flag, p))) break;
+        const uint32_t full = smem_u32(&bars->k_full[slot]), dst = smem_u32(smem + C::OFF_K + slot * kHalf);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        if (lane < BN / 16) mbar_arrive(full);
+        if (j < p.n_prefix) {
+          if (lane == 0) tma_load_4d(dst, &p.tm_pk, full, hf * 64, j * BN, item.hk, 0);
+        } else if (one ? lane == 0 : g.valid > 0) {
+          tma_load_4d(dst + lane * 2048, one ? &p.tm_k : &p.tm_k16, full, hf * 64, g.off, item.hk, p.b0 + g.b);
+        }
+        __syncwarp();
+        next_slot();
+      }
+    }
+  }
+  // Every load issued must land before the CTA releases its shared memory.
+  for (uint32_t s = 0; s < C::KN && s < used; ++s)
+    drain(smem_u32(&bars->k_full[(used - 1 - s) % C::KN]), (used - 1 - s) / C::KN & 1);
+}
+
+// V's warp loads the codes and scales of cached tiles; tile t is of group t mod 2.
+template <int D>
+__device__ void flat_load_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table) {
+  using C = FlatCfg<D>;
+  volatile int *abort_flag = &bars->abort;
+  const int lane = threadIdx.x & 31;
+  uint32_t tile = 0, use[2] = {0, 0};   // tiles so far; cached ones of each group
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
+  bool ok = true;
+  const int psize = p.prefix_pages.page;
+  for (; ok && more; more = next_item(&bars->start, table, &walk, &item)) {
+    int j = item.kv0;
+    if (p.prefix_cached && psize >= BN) {
+      // The prefix's whole tiles, each in one page: a loop of few instructions.
+      const int whole = min(item.kv1, p.Np / BN);
+      const uint8_t *codes = p.codes[1], *scales = p.scales[1] + lane * 16;
+      const int shift = p.prefix_pages.shift, n_pages = p.prefix_pages.n_pages, count = p.prefix_pages.count;
+      auto page_at = [&](int t) {
+        const int i = t * BN >> shift;
+        return t < whole && i < count ? __ldg(p.prefix_pages.pages + i) : -1;
+      };
+      int next = page_at(j);
+#pragma unroll 1
+      for (; j < whole; ++j, ++tile) {
         const int page = next;
         next = page_at(j + 1);   // (not looked at before its turn)
         const bool held = static_cast<unsigned>(page) < static_cast<unsigned>(n_pages);
         const long long row = (static_cast<long long>(page) * p.Hk + item.hk) * psize + (j * BN & (psize - 1));
-        const uint32_t full = smem_u32(&bars->f_full[F0 + slot]), dst = smem_u32(smem + C::OFF_F + (F0 + slot) * C::RAW);
-        if (!(ok = wait_for<true>(smem_u32(&bars->f_empty[F0 + slot]), parity, abort_flag, p))) {
-          use -= whole - j;
-          break;
-        }
+        const uint32_t u = tile & 1 ? use[1] : use[0], slot = (tile & 1) * C::FV + u % C::FV;
+        const uint32_t full = smem_u32(&bars->f_full[slot]), dst = smem_u32(smem + C::OFF_F + slot * C::RAW);
+        if (!(ok = wait_for<true>(smem_u32(&bars->f_empty[slot]), (u / C::FV & 1) ^ 1, abort_flag, p))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(full, held ? BN * D : 0);
           if (held) bulk_load(dst, codes + row * D, BN * D, full);
@@ -172,43 +301,37 @@ __device__ void flat_loader(const PrefixParams &p, uint8_t *smem, FlatBars *bars
           copies_arrive(full);
         }
         __syncwarp();
-        if (++slot == F) slot = 0, parity ^= 1;
+        if (tile & 1) ++use[1]; else ++use[0];
       }
     }
-    Part ahead = part_at(j);
-    for (; ok && j < item.kv1; ++j) {
+    Part ahead = part_at(p, table, item, j);
+    for (; ok && j < item.kv1; ++j, ++tile) {
       const Part r = ahead;
-      ahead = part_at(j + 1);
+      ahead = part_at(p, table, item, j + 1);
       if (!is_cached(p, j)) continue;
-      // Rows that follow each other in a page go in one copy, issued by the first one's lane.
-      const bool held = r.at >= 0 && static_cast<unsigned>(r.page) < static_cast<unsigned>(p.prefix_pages.n_pages);
-      const int last_page = __shfl_up_sync(0xffffffffu, held ? r.page : -1, 1);
-      const int last_at = __shfl_up_sync(0xffffffffu, r.at, 1);
-      const bool first = held && (lane == 0 || last_page != r.page || last_at + 16 != r.at);
-      const unsigned heads = __ballot_sync(0xffffffffu, first || !held);   // (lanes 8 to 31 hold nothing)
-      const unsigned bytes = __popc(__ballot_sync(0xffffffffu, held)) * 16u * D;
+      const Run x = run_of(p, r);
       const long long row = (static_cast<long long>(r.page) * p.Hk + item.hk) * psize + r.at;
-      const uint32_t slot = F0 + use % F;
-      ok = wait_for<true>(smem_u32(&bars->f_empty[slot]), (use / F & 1) ^ 1, abort_flag, p);
-      if (!ok) break;
+      const uint32_t u = tile & 1 ? use[1] : use[0], slot = (tile & 1) * C::FV + u % C::FV;
+      if (!(ok = wait_for<true>(smem_u32(&bars->f_empty[slot]), (u / C::FV & 1) ^ 1, abort_flag, p))) break;
       const uint32_t full = smem_u32(&bars->f_full[slot]), dst = smem_u32(smem + C::OFF_F + slot * C::RAW);
-      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+      if (lane == 0) mbar_arrive_expect_tx(full, __popc(x.lanes) * 16u * D);
       __syncwarp();
-      if (first)
-        bulk_load(dst + lane * 16 * D, p.codes[V ? 1 : 0] + row * D, (__ffs(heads >> (lane + 1)) * 16) * D, full);
+      if (x.held && lane == x.first) bulk_load(dst + lane * 16 * D, p.codes[1] + row * D, (x.end - lane) * 16 * D, full);
       // The scales by the load/store unit, sixteen a lane: a bulk copy takes the copy engine about 300 cycles,
       // however small.
       if (lane < BN / 16) {
         if (r.at >= 0)
-          copy16(dst + BN * D + lane * 16, held ? static_cast<const void *>(p.scales[V ? 1 : 0] + row) : g_nan_scales);
+          copy16(dst + BN * D + lane * 16, x.held ? static_cast<const void *>(p.scales[1] + row) : g_nan_scales);
         copies_arrive(full);
       }
       __syncwarp();
-      ++use;
+      if (tile & 1) ++use[1]; else ++use[0];
     }
   }
   // Every load issued must land before the CTA releases its shared memory.
-  for (uint32_t s = 0; s < F && s < use; ++s) drain(smem_u32(&bars->f_full[F0 + s]), ((use - 1 - s) / F) & 1);
+  for (uint32_t g = 0; g < 2; ++g)
+    for (uint32_t s = 0; s < C::FV && s < use[g]; ++s)
+      drain(smem_u32(&bars->f_full[g * C::FV + (use[g] - 1 - s) % C::FV]), (use[g] - 1 - s) / C::FV & 1);
 }
 
 // ------------------------------------------------------------------ operands
@@ -243,51 +366,12 @@ __device__ __forceinline__ uint4 to_bf16(uint32_t c0, uint32_t c1, uint32_t byte
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// A thread has one 16-byte group of every STEP-th row, so its place in the swizzle stays. Short loops: with all
+// groups unrolled the warps waited for instructions.
 // This warp has read a raw slot: its arrival at the slot's barrier.
 __device__ __forceinline__ void slot_read(uint32_t empty) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
-}
-
-// Codes of K's raw slot to a tile in fp16, which holds every code exactly; the keys' scales go to the scores.
-// A thread has one 16-byte group of every STEP-th row, so its place in the swizzle stays. Short loops: with all
-// groups unrolled the warps waited for instructions.
-template <int D>
-__device__ __noinline__ void convert_keys(const uint8_t *src, uint8_t *dst, uint32_t tid, uint32_t empty) {
-  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR, U = BN / STEP;   // groups of a row's codes
-  const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
-  src += tid * 16;
-  dst += (cc / 4) * kHalf + row0 * 128;
-  // (Of a group's two chunks the second half's lanes store the second one first, which spares conflicts.)
-  const uint32_t first0 = ((first + odd) ^ (row0 & 7)) * 16, second0 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
-  auto halves = [](uint32_t a, uint32_t b) {
-    uint4 r;
-    asm("{.reg .b16 t, u;\n\t"
-        "mov.b32 {t, u}, %4;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t"
-        "mov.b32 {t, u}, %5;\n\tcvt.rn.f16x2.e4m3x2 %2, t;\n\tcvt.rn.f16x2.e4m3x2 %3, u;}"
-        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-        : "r"(a), "r"(b));
-    return r;
-  };
-  // (Two groups at a time, the next two's loads before their stores.)
-  uint4 c[2], next[2];
-#pragma unroll
-  for (uint32_t k = 0; k < 2; ++k) c[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
-#pragma unroll 1
-  for (uint32_t i = 0; i < U; i += 2, dst += 2 * STEP * 128) {
-    src += 2 * STEP * D;
-    if (i + 2 < U)
-#pragma unroll
-      for (uint32_t k = 0; k < 2; ++k) next[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
-#pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) {
-      uint8_t *to = dst + k * STEP * 128;
-      *reinterpret_cast<uint4 *>(to + first0) = halves(odd ? c[k].z : c[k].x, odd ? c[k].w : c[k].y);
-      *reinterpret_cast<uint4 *>(to + second0) = halves(odd ? c[k].x : c[k].z, odd ? c[k].y : c[k].w);
-      c[k] = next[k];
-    }
-  }
-  slot_read(empty);
 }
 
 // Codes and scale bytes of V's raw slot to a bf16 tile; `valid`, `entry`: of the sixteen rows of lanes 0-7
@@ -295,7 +379,7 @@ __device__ __noinline__ void convert_keys(const uint8_t *src, uint8_t *dst, uint
 template <int D>
 __device__ __noinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, int entry, uint32_t *bad, uint32_t tid,
                                            uint32_t empty) {
-  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatOperandWarps / CPR, U = BN / STEP;   // groups of a row's codes
+  constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatGroupWarps / CPR, U = BN / STEP;   // groups of a row's codes
   const uint32_t lane = tid & 31;
   const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
   const uint32_t bytes = *reinterpret_cast<const uint32_t *>(src + BN * D + lane * 4);
@@ -371,11 +455,34 @@ __device__ __noinline__ void clear_rows(uint8_t *tile, int valid, int entry, uin
   }
 }
 
-// An item's queries to Tensor Memory by four warps of different lane quarters, a row a thread (the copies begin
-// at multiples of row_tile).
+// Two pairs of values to two words of four e4m3 codes, whose sum they are as far as the codes reach: what rounding to
+// the four bits of the first leaves of a bf16 value's eight fits the second's four.
+__device__ __forceinline__ void two_codes(float a, float b, float c, float d, uint32_t &first, uint32_t &rest) {
+  auto pair = [](float x, float y, uint16_t &hi, uint16_t &lo) {
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y), "f"(x));
+    uint32_t back;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
+    float bx, by;
+    asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.f32.f16 %0, t;\n\tcvt.f32.f16 %1, u;}" : "=f"(bx), "=f"(by) : "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y - by), "f"(x - bx));
+  };
+  uint16_t h0, l0, h1, l1;
+  pair(a, b, h0, l0);
+  pair(c, d, h1, l1);
+  first = h0 | static_cast<uint32_t>(h1) << 16;
+  rest = l0 | static_cast<uint32_t>(l1) << 16;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// An item's queries to Tensor Memory by the warps of V, every second 32 columns of a row a thread and group (the
+// copies begin at multiples of row_tile).
 template <int D>
 __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const PrefixItem &item,
-                                          uint32_t items, uint32_t tmem) {
+                                          uint32_t items, uint32_t tmem, int group) {
   using C = FlatCfg<D>;
   volatile int *abort_flag = &bars->abort;
   const int tid = threadIdx.x & 127;
@@ -394,11 +501,11 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
     return v;
   };
   const bool cached = p.prefix_cached || p.own_cached;
-  float s = 1.f;
+  float s = 1.f, back = 1.f;
   if (cached) {
-    // fp16 for cached keys: times the power of two that brings the row's largest magnitude to [2^14, 2^15).
-    // Exact then for values down to 2^-31 of that, and off by 2^-40 of it at most below. (Of a row whose
-    // largest is an infinity or NaN, and of zeros, nothing is asked.)
+    // For cached keys: times the power of two that brings the row's largest magnitude to [2^7, 2^8), in two
+    // parts. Their sum is exact for values down to 2^-9 of that, and off by 2^-17 of it at most below. A row
+    // with an infinity or NaN becomes NaN by its factor.
     uint32_t big = 0;   // largest magnitudes, as bits, of the even and of the odd columns
     uint4 x[D / 8];
 #pragma unroll
@@ -408,21 +515,18 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
       const uint4 v = x[i];
       big = __vmaxu2(__vmaxu2(big, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
     }
-    const int e = min(max(static_cast<int>(max(big & 0xffffu, big >> 16) >> 7), 1), 254);
-    const int up = min(268 - e, 253);   // 2^(up - 127), 2^(141 - e) mostly
+    const int e = static_cast<int>(max(big & 0xffffu, big >> 16) >> 7);
+    const int up = min(261 - e, 253);   // 2^(up - 127), 2^(134 - e) mostly
     s = __int_as_float(up << 23);
-    big = (254 - up) << 23;
-    if (items > 0 && (!wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p) ||
-                      !wait_for<true>(smem_u32(&bars->q_seen), (items - 1) & 1, abort_flag, p)))
-      return false;
-    reinterpret_cast<float *>(smem + C::OFF_QF)[tid] = __int_as_float(big);
-  } else if (items > 0 && (!wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p) ||
-                           !wait_for<true>(smem_u32(&bars->q_seen), (items - 1) & 1, abort_flag, p))) {
-    return false;
+    back = e == 255 ? NAN : __int_as_float((254 - up) << 23);
   }
+  if (items > 0 && (!wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p) ||
+                    !wait_for<true>(smem_u32(&bars->q_seen), (items - 1) & 1, abort_flag, p)))
+    return false;
+  if (group == 0) reinterpret_cast<float *>(smem + C::OFF_QF)[tid] = back;
   tc_fence_after();   // (the last item's scores, read from here, are done)
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
+  for (int c = group; c < D / 32; c += 2) {
     uint32_t q[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -434,10 +538,13 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
     }
     if (!p.prefix_cached || !p.own_cached) tmem_st16(to + C::COL_Q + 16 * c, q);
     if (cached) {
+      uint32_t first[8], rest[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(__uint_as_float(q[i] & 0xffff0000u) * s), "f"(__uint_as_float(q[i] << 16) * s));
-      tmem_st16(to + C::COL_QH + 16 * c, q);
+      for (int i = 0; i < 8; ++i)
+        two_codes(__uint_as_float(q[2 * i] << 16) * s, __uint_as_float(q[2 * i] & 0xffff0000u) * s,
+                  __uint_as_float(q[2 * i + 1] << 16) * s, __uint_as_float(q[2 * i + 1] & 0xffff0000u) * s, first[i], rest[i]);
+      tmem_st8(to + C::COL_Q8 + 8 * c, first);
+      tmem_st8(to + C::COL_Q8 + D / 4 + 8 * c, rest);
     }
   }
   tmem_wait_st();
@@ -446,30 +553,25 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
   return true;
 }
 
-// The warps of K, or of V: each tile's operand, in order.
-template <int D, bool V>
-__device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem) {
+// The warps of V, two groups of four: every second tile's operand each, in a slot of its own.
+template <int D>
+__device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem, int group) {
   using C = FlatCfg<D>;
-  constexpr uint32_t S = V ? C::VS : C::KS, F = V ? C::FV : C::FK, F0 = V ? C::FK : 0;   // slots; raw slots, the first
   volatile int *abort_flag = &bars->abort;
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const bool issuer = tid < 32;
-  uint64_t *full_of = V ? bars->v_full : bars->k_full, *empty_of = V ? bars->v_empty : bars->k_empty;
-  auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<true>(smem_u32(&bar), parity, abort_flag, p); };
-  uint32_t use = 0, f_use = 0, items = 0;   // uses of the ring, of the raw one
-  uint32_t raw_parity = 0;                  // of the next wait, a bit a slot
-  // Loads of this warp that nobody may have waited for: a bit a slot of the ring (0, 1) and of `raw`
-  // (2, 3), with the phase that they complete.
-  uint32_t pending = 0, phase = 0;
-  auto loading = [&](uint32_t bit, uint32_t parity) {
-    pending |= 1u << bit;
-    phase = (phase & ~(1u << bit)) | parity << bit;
-  };
+  uint8_t *dst = smem + C::OFF_V + group * C::TILE;
+  const uint32_t full = smem_u32(&bars->v_full[group]), empty = smem_u32(&bars->v_empty[group]);
+  const uint32_t raw_full = smem_u32(&bars->raw[group]);
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_for<true>(bar, parity, abort_flag, p); };
+  uint32_t tile = 0, items = 0;            // tiles of all items before this one
+  uint32_t use = 0, f_use = 0, r_use = 0;  // uses of the slot, of the group's raw ring, of raw_full
+  bool loading = false, raw_loading = false;   // the slot's last use, raw_full's last, are loads of this warp's
   PrefixWalk walk = bars->start.walk;
   PrefixItem item = bars->start.item;
   bool more = bars->start.any != 0;
 
-  uint32_t *bad = nullptr;   // V: the item's words
+  uint32_t *bad = nullptr;   // the item's words
   // Lanes 0-7: of sixteen keys each, whose they are and how many count. (Rows of V behind a request's last key
   // have the weight 0, but what lies there may not be a number.)
   auto valid_of = [&](int j) {
@@ -477,156 +579,137 @@ __device__ void flat_operands(const PrefixParams &p, uint8_t *smem, FlatBars *ba
     if (j < p.n_prefix) return Grain{kPrefixEntries, 0, min(max(p.Np - j * BN - lane * 16, 0), 16)};
     return grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
   };
-  // TMA loads of a tile that is not cached, use `u` of the ring. All warps wait for the slot and arrive at its
-  // barrier, though one of them issues: a phase then cannot end before each has seen the one before it. (One
-  // that fell two phases behind would take the next for its own.)
-  auto issue = [&](int j, uint32_t u) {
-    if (j >= item.kv1 || is_cached(p, j)) return true;
-    const uint32_t slot = u % S, parity = u / S & 1;
-    if (!wait(empty_of[slot], parity ^ 1)) return false;
-    const uint32_t dst = smem_u32(smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE);
-    uint32_t full = smem_u32(full_of + slot);
+  // A cached tile; `valid`, `entry` as convert_values takes them.
+  auto convert = [&](int valid, int entry) {
+    const uint32_t f = group * C::FV + f_use % C::FV;
+    if (!wait(smem_u32(&bars->f_full[f]), f_use / C::FV & 1) || !wait(empty, (use & 1) ^ 1)) return false;
+    convert_values<D>(smem + C::OFF_F + f * C::RAW, dst, valid, entry, bad, tid, smem_u32(&bars->f_empty[f]));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
+    ++f_use;
+    ++use;
+    loading = false;
+    return true;
+  };
+  // A tile that is not cached, by TMA. All warps wait for the slot and arrive at its barrier, though one of them
+  // issues: a phase then cannot end before each has seen the one before it. (One that fell two phases behind
+  // would take the next for its own.)
+  auto load = [&](int j) {
+    if (!wait(empty, (use & 1) ^ 1)) return false;
+    ++use;
+    loading = true;
     if (j < p.n_prefix) {   // (rows past Np come as zeros)
       if (issuer && lane == 0) {
         mbar_arrive_expect_tx(full, C::TILE);
-        for (int hf = 0; hf < D / 64; ++hf)
-          tma_load_4d(dst + hf * kHalf, V ? &p.tm_pv : &p.tm_pk, full, hf * 64, j * BN, item.hk, 0);
-      }
-      if (!issuer && lane == 0) mbar_arrive(full);
-      loading(slot, parity);
-    } else {
-      Grain g{0, 0, 0};
-      if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
-      // Keys of one request lie one after the other: a box of 128 rows, which may reach past its last.
-      const int first_b = __shfl_sync(0xffffffffu, g.b, 0), first_off = __shfl_sync(0xffffffffu, g.off, 0);
-      const bool one = __shfl_sync(0xffffffffu, g.valid, 0) > 0 &&
-                       __all_sync(0xffffffffu, g.valid == 0 || (g.b == first_b && g.off == first_off + 16 * lane));
-      const uint32_t bytes = one ? C::TILE : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
-      // V's rows behind a request's last key are still to be cleared then, and those of an item of several
-      // requests to be looked through.
-      const bool whole = !V || (item.b_lo == item.b_hi && __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16);
-      if (!whole) full = smem_u32(&bars->raw[slot]);
-      if (issuer) {
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-        if (one ? lane == 0 : g.valid > 0)
-          for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_4d(dst + hf * kHalf + lane * 2048, one ? (V ? &p.tm_v : &p.tm_k) : V ? &p.tm_v16 : &p.tm_k16, full,
-                        hf * 64, g.off, item.hk, p.b0 + g.b);
-      } else if (whole && lane == 0) {
+        for (int hf = 0; hf < D / 64; ++hf) tma_load_4d(smem_u32(dst) + hf * kHalf, &p.tm_pv, full, hf * 64, j * BN, item.hk, 0);
+      } else if (lane == 0) {
         mbar_arrive(full);
       }
-      pending &= ~(1u << slot);
-      if (whole) loading(slot, parity); else loading(2 + slot, raw_parity >> slot & 1);
+      __syncwarp();
+      return true;
+    }
+    Grain g{0, 0, 0};
+    if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+    // Keys of one request lie one after the other: a box of 128 rows, which may reach past its last.
+    const bool one = one_request(g);
+    const uint32_t bytes = one ? C::TILE : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
+    // Rows behind a request's last key are still to be cleared then, and those of an item of several requests to
+    // be looked through.
+    const bool whole = item.b_lo == item.b_hi && __popc(__ballot_sync(0xffffffffu, g.valid == 16)) == BN / 16;
+    const uint32_t bar = whole ? full : raw_full;
+    if (issuer) {
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if (one ? lane == 0 : g.valid > 0)
+        for (int hf = 0; hf < D / 64; ++hf)
+          tma_load_4d(smem_u32(dst) + hf * kHalf + lane * 2048, one ? &p.tm_v : &p.tm_v16, bar, hf * 64, g.off, item.hk, p.b0 + g.b);
+    } else if (whole && lane == 0) {
+      mbar_arrive(full);
     }
     __syncwarp();
-    return true;
-  };
-  // A cached tile, or the rest of a V tile that is not.
-  auto finish = [&](int j) {
-    const uint32_t slot = use % S;
-    const bool cached = is_cached(p, j);
-    if (!cached && (!V || j < p.n_prefix)) return true;
-    Grain g{0, 0, 16};
-    if (V) g = valid_of(j);
-    const int valid = g.valid;
-    uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
-    if (cached) {
-      const uint32_t f = F0 + f_use % F, empty = smem_u32(&bars->f_empty[f]);
-      if (!wait(bars->f_full[f], f_use / F & 1) || !wait(empty_of[slot], (use / S & 1) ^ 1)) return false;
-      pending &= ~(1u << slot);
-      const uint8_t *raw = smem + C::OFF_F + f * C::RAW;
-      if (V) {
-        convert_values<D>(raw, dst, valid, g.b, bad, tid, empty);
-      } else {
-        reinterpret_cast<float *>(smem + C::OFF_FAC)[(use & 3) * BN + tid] = power_of(raw[BN * D + tid]) * p.scale_log2;
-        convert_keys<D>(raw, dst, tid, empty);
-      }
-      ++f_use;
-    } else {
-      if (item.b_lo == item.b_hi && !__any_sync(0xffffffffu, valid < 16)) return true;
-      if (!wait(bars->raw[slot], raw_parity >> slot & 1)) return false;
-      raw_parity ^= 1u << slot;
-      pending &= ~(4u << slot);
-      clear_rows<D>(dst, valid, g.b, bad, tid);
-    }
+    if (whole) return true;
+    loading = false;
+    raw_loading = true;
+    if (!wait(raw_full, r_use & 1)) return false;
+    ++r_use;
+    raw_loading = false;
+    const Grain v = valid_of(j);
+    clear_rows<D>(dst, v.valid, v.b, bad, tid);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(full_of + slot));
+    if (lane == 0) mbar_arrive(full);
     return true;
   };
 
   bool ok = true;
   for (; ok && more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
-    if (V) ok = flat_queries<D>(p, smem, bars, item, items, tmem);
+    ok = flat_queries<D>(p, smem, bars, item, items, tmem, group);
     if (!ok) break;
-    if (V) {   // (the softmax is done with the item before last, as it has begun the last one)
-      bad = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD) + ((items & 1) * kFlatOperandWarps + tid / 32) * kBadWords;
-      if (lane < kBadWords) bad[lane] = 0;
-      __syncwarp();
-    }
-    int j = item.kv0;
+    // (The softmax is done with the item before last, as it has begun the last one.)
+    bad = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD) + ((items & 1) * 2 * kFlatGroupWarps + group * kFlatGroupWarps + tid / 32) * kBadWords;
+    if (lane < kBadWords) bad[lane] = 0;
+    __syncwarp();
+    int j = item.kv0 + ((tile ^ group) & 1);
+    tile += item.kv1 - item.kv0;
     if (p.prefix_cached) {
       // The prefix's whole tiles, in a loop of few instructions.
       const int whole = min(item.kv1, p.Np / BN);
-      uint32_t slot = use % S, parity = (use / S & 1) ^ 1, f = f_use % F, f_parity = f_use / F & 1;
-      if (j < whole) {
-        use += whole - j;
-        f_use += whole - j;
-        pending &= ~3u;
-      }
 #pragma unroll 1
-      for (; j < whole; ++j) {
-        if (!(ok = wait(bars->f_full[F0 + f], f_parity) && wait(empty_of[slot], parity))) break;
-        const uint8_t *raw = smem + C::OFF_F + (F0 + f) * C::RAW;
-        uint8_t *dst = smem + (V ? C::OFF_V : C::OFF_K) + slot * C::TILE;
-        const uint32_t empty = smem_u32(&bars->f_empty[F0 + f]);
-        if (V) {
-          convert_values<D>(raw, dst, 16, kPrefixEntries, bad, tid, empty);
-        } else {
-          // (The scores' slot of the scales: tile `use` modulo four.)
-          reinterpret_cast<float *>(smem + C::OFF_FAC)[((use - (whole - j)) & 3) * BN + tid] = power_of(raw[BN * D + tid]) * p.scale_log2;
-          convert_keys<D>(raw, dst, tid, empty);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(full_of + slot));
-        if (++slot == S) slot = 0, parity ^= 1;
-        if (++f == F) f = 0, f_parity ^= 1;
+      for (; ok && j < whole; j += 2) ok = convert(16, kPrefixEntries);
+    }
+    for (; ok && j < item.kv1; j += 2) {
+      if (is_cached(p, j)) {
+        const Grain g = valid_of(j);
+        ok = convert(g.valid, g.b);
+      } else {
+        ok = load(j);
       }
     }
-    // TMA loads go out one tile ahead of the clearing that V's may need.
-    ok = ok && issue(j, use);
-    for (; ok && j < item.kv1; ++j, ++use) ok = issue(j + 1, use + 1) && finish(j);
   }
   // Every load issued must land before the CTA releases its shared memory.
-  if (issuer)
-    for (int s = 0; s < 2; ++s) {
-      if (pending >> s & 1) drain(smem_u32(full_of + s), phase >> s & 1);
-      if (pending >> (2 + s) & 1) drain(smem_u32(&bars->raw[s]), phase >> (2 + s) & 1);
-    }
+  if (issuer && loading) drain(full, (use - 1) & 1);
+  if (issuer && raw_loading) drain(raw_full, r_use & 1);
 }
 
 // ------------------------------------------------------------------ MMA issuer
+// Scores of a tile of codes: the queries' two parts one after the other. (Formats 0: e4m3.)
 template <int D>
-__device__ __forceinline__ void issue_qk_ts(uint32_t dcol, uint32_t qcol, uint64_t kdesc, bool half) {
-  // (Formats of A and B in bits 7-9 and 10-12: 1 bf16, 0 fp16.)
-  const uint32_t idesc = idesc_bf16_f32(128, 128, 0) & (half ? ~(9u << 7) : ~0u);
+__device__ __forceinline__ void issue_qk_codes(uint32_t dcol, uint32_t qcol, uint64_t kdesc) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0) & ~(9u << 7);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    tc_mma_ts(dcol, qcol + kk * 8, kdesc + static_cast<uint64_t>(((kk / 4) * kHalf + (kk % 4) * 32) >> 4), idesc,
-              kk > 0 ? 1u : 0u);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dcol),
+        "r"(qcol + kk * 8), "l"(kdesc + static_cast<uint64_t>((kk % (D / 32) * 32) >> 4)), "r"(idesc), "r"(kk > 0 ? 1u : 0u)
+        : "memory");
+}
+// 64 columns of a bf16 tile.
+__device__ __forceinline__ void issue_qk_half(uint32_t dcol, uint32_t qcol, uint64_t kdesc, uint32_t accumulate) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+    tc_mma_ts(dcol, qcol + kk * 8, kdesc + kk * 2, idesc_bf16_f32(128, 128, 0), kk > 0 || accumulate ? 1u : 0u);
 }
 // Scores and products have a warp each: a thread is held for about as long as the MMAs run that it issues.
-// QK(i) overwrites P(i-2), so it waits until that product is done.
+// QK(i) overwrites P(i-2), so it waits until that product is done. The warp of the scores also turns the scale
+// bytes of cached keys to factors.
 template <int D>
 __device__ void flat_scores(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const int *table, uint32_t tmem_in) {
   using C = FlatCfg<D>;
   volatile int *abort_flag = &bars->abort;
-  const uint32_t tmem = uniform(tmem_in);
+  const uint32_t tmem = uniform(tmem_in), lane = threadIdx.x & 31;
   uint32_t g = 0, items = 0;   // tiles, items so far
+  uint32_t slot = 0, parity = 0;
+  // Slots of codes have rows of D bytes, of bf16 64 columns: 128 bytes; the swizzle is as wide.
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+  const uint64_t cdesc0 = D == 128 ? kdesc0
+                                   : (smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 512) & ~(7ull << 61)) | 4ull << 61;
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
+  auto next_slot = [&] {
+    if (++slot == C::KN) slot = 0, parity ^= 1;
+  };
   PrefixWalk walk = bars->start.walk;
   PrefixItem item = bars->start.item;
   bool more = bars->start.any != 0;
@@ -634,18 +717,44 @@ __device__ void flat_scores(const PrefixParams &p, uint8_t *smem, FlatBars *bars
     const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
     if (!wait(bars->q_full, items & 1)) goto done;
     for (int j = kv0; j < kv1; ++j, ++g) {
-      const uint32_t t = g & 1, ks = g % C::KS;
-      const bool half = uniform(is_cached(p, j));   // cached keys are in fp16, others in bf16
-      if (g >= 2 && !wait(bars->pv_done[t], (g >> 1 & 1) ^ 1)) goto done;   // of tile g - 2
-      if (!wait(bars->k_full[ks], g / C::KS & 1)) goto done;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_qk_ts<D>(tmem + t * 128, tmem + (half ? C::COL_QH : C::COL_Q), kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)), half);
-        tc_commit(smem_u32(&bars->s_full[t]));
-        tc_commit(smem_u32(&bars->k_empty[ks]));
-        if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+      const uint32_t t = g & 1, dcol = tmem + t * 128;
+      if (!wait(bars->k_full[slot], parity)) goto done;
+      if (uniform(is_cached(p, j))) {
+        // (The softmax is done with tile g - 4, as the scores of g - 1 followed the product of g - 3.)
+        const uint32_t bytes = *reinterpret_cast<const uint32_t *>(smem + C::OFF_KS + slot * BN + lane * 4);
+        reinterpret_cast<float4 *>(smem + C::OFF_FAC)[(g & 3) * (BN / 4) + lane] =
+            make_float4(power_of(bytes & 255) * p.scale_log2, power_of(bytes >> 8 & 255) * p.scale_log2,
+                        power_of(bytes >> 16 & 255) * p.scale_log2, power_of(bytes >> 24) * p.scale_log2);
+        if (g >= 2 && !wait(bars->pv_done[t], (g >> 1 & 1) ^ 1)) goto done;   // of tile g - 2
+        __syncwarp();
+        tc_fence_after();
+        if (elect_one()) {
+          issue_qk_codes<D>(dcol, tmem + C::COL_Q8, cdesc0 + static_cast<uint64_t>(slot * (kHalf >> 4)));
+          tc_commit(smem_u32(&bars->s_full[t]));
+          tc_commit(smem_u32(&bars->k_empty[slot]));
+          if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+          mbar_arrive(smem_u32(&bars->s_full[t]));   // the factors
+        }
+        __syncwarp();
+        next_slot();
+        continue;
       }
-      __syncwarp();
+      if (g >= 2 && !wait(bars->pv_done[t], (g >> 1 & 1) ^ 1)) goto done;
+      for (int hf = 0; hf < D / 64; ++hf) {
+        if (hf > 0 && !wait(bars->k_full[slot], parity)) goto done;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_qk_half(dcol, tmem + C::COL_Q + 32 * hf, kdesc0 + static_cast<uint64_t>(slot * (kHalf >> 4)), hf);
+          tc_commit(smem_u32(&bars->k_empty[slot]));
+          if (hf == D / 64 - 1) {
+            tc_commit(smem_u32(&bars->s_full[t]));
+            if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+            mbar_arrive(smem_u32(&bars->s_full[t]));
+          }
+        }
+        __syncwarp();
+        next_slot();
+      }
     }
   }
 done:
@@ -777,7 +886,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
     const bool idle = item.row0 + (wq * 32) % RT >= p.rows;   // no row in this warp
     const PrefixRange own = range_of(p, table, row);
     wait(bars->q_full, items & 1);
-    const float row_factor = reinterpret_cast<const float *>(smem + C::OFF_QF)[tid];   // (of rows in fp16)
+    const float row_factor = reinterpret_cast<const float *>(smem + C::OFF_QF)[tid];   // (of rows in codes)
     mbar_arrive(smem_u32(&bars->q_seen));
     float m = -INFINITY, l = 0.f;
     for (int j = item.kv0; j < item.kv1; ++j, ++step) {
@@ -899,11 +1008,11 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
     wait(bars->o_full, items & 1);
     tc_fence_after();
     {
-      const uint32_t *bad = reinterpret_cast<const uint32_t *>(smem + C::OFF_BAD) + (items & 1) * kFlatOperandWarps * kBadWords;
+      const uint32_t *bad = reinterpret_cast<const uint32_t *>(smem + C::OFF_BAD) + (items & 1) * 2 * kFlatGroupWarps * kBadWords;
       const int b = p.by_entry.of(min(row, p.rows - 1));
       uint32_t any = 0;
 #pragma unroll
-      for (int w = 0; w < kFlatOperandWarps; ++w)
+      for (int w = 0; w < 2 * kFlatGroupWarps; ++w)
         any |= bad[w * kBadWords + (b >> 5)] >> (b & 31) | bad[w * kBadWords + kPrefixEntries / 32];
       if (any & 1) l = NAN;
     }
@@ -1033,20 +1142,22 @@ __global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_consta
   int *table = reinterpret_cast<int *>(smem + C::OFF_TAB);
   const int warp = uniform(threadIdx.x / 32);
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars->q_full), BM);
+    mbar_init(smem_u32(&bars->q_full), 2 * BM);
     mbar_init(smem_u32(&bars->q_empty), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), kFlatOperandWarps);
-      mbar_init(smem_u32(&bars->k_empty[s]), 1);
-      mbar_init(smem_u32(&bars->v_full[s]), kFlatOperandWarps);
+      mbar_init(smem_u32(&bars->v_full[s]), kFlatGroupWarps);
       mbar_init(smem_u32(&bars->v_empty[s]), 1);
       mbar_init(smem_u32(&bars->raw[s]), 1);
-      mbar_init(smem_u32(&bars->s_full[s]), 1);
+      mbar_init(smem_u32(&bars->s_full[s]), 2);     // the scores, and the keys' factors
       mbar_init(smem_u32(&bars->p_full[s]), 128);
     }
-    for (int s = 0; s < C::FS; ++s) {
-      mbar_init(smem_u32(&bars->f_full[s]), 1 + BN / 16);   // the codes, and the lanes with scales
-      mbar_init(smem_u32(&bars->f_empty[s]), kFlatOperandWarps);
+    for (int s = 0; s < C::KN; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 1 + BN / 16);   // the keys, and the lanes with scales
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    }
+    for (int s = 0; s < 2 * C::FV; ++s) {
+      mbar_init(smem_u32(&bars->f_full[s]), 1 + BN / 16);
+      mbar_init(smem_u32(&bars->f_empty[s]), kFlatGroupWarps);
     }
     mbar_init(smem_u32(&bars->pv_done[0]), 1);
     mbar_init(smem_u32(&bars->pv_done[1]), 1);
@@ -1067,7 +1178,7 @@ __global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_consta
   tc_fence_after();
   if (p.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits for this grid's end itself
   const uint32_t tmem = bars->tmem_base;
-  if (warp < kFlatOperands) {
+  if (warp < kFlatValues) {
     if (p.copies == 1)
       flat_softmax<D, 4>(p, smem, bars, table, tmem);
     else if (p.copies == 2)
@@ -1075,18 +1186,15 @@ __global__ void __launch_bounds__(512, 1) prefix_flat_kernel(const __grid_consta
     else
       flat_softmax<D, 1>(p, smem, bars, table, tmem);
   } else if (warp < kFlatScores) {
-    if (warp >= kFlatValues)
-      flat_operands<D, true>(p, smem, bars, table, tmem);
-    else
-      flat_operands<D, false>(p, smem, bars, table, tmem);
+    flat_values<D>(p, smem, bars, table, tmem, (warp - kFlatValues) / kFlatGroupWarps);
   } else if (warp == kFlatScores) {
     flat_scores<D>(p, smem, bars, table, tmem);
   } else if (warp == kFlatProducts) {
     flat_products<D>(p, smem, bars, table, tmem);
   } else if (warp == kFlatLoadKeys) {
-    flat_loader<D, false>(p, smem, bars, table);
+    flat_load_keys<D>(p, smem, bars, table);
   } else {
-    flat_loader<D, true>(p, smem, bars, table);
+    flat_load_values<D>(p, smem, bars, table);
   }
   __syncwarp();
   tc_fence_before();

@@ -47,6 +47,9 @@ struct PrefixParams : PrefixGeo {
   // strides: maps {d, rows, heads, batch} with boxes of 64 columns and 128 rows, 128-byte swizzle; the flat
   // kernel's own ones also with boxes of 16 rows. The tall kernel's queries: boxes of 8 rows.
   CUtensorMap tm_q, tm_pk, tm_pv, tm_k, tm_v, tm_k16, tm_v16;
+  // The flat kernel's cached keys, two codes as one element: map {d / 2, rows of a page, heads, pages}, boxes of a page's
+  // rows, 128 at most, and of 16; the swizzle is as wide as a row.
+  CUtensorMap tm_c, tm_c16;
   // Those that lie in the cache.
   PageLists prefix_pages, own_pages;
   const uint8_t *codes[2], *scales[2];   // of k and v

@@ -45,6 +45,15 @@ bool encode_operand(CUtensorMap *m, const void *base, long long B, int H, int N,
   return encode_map(m, base, 4, dims, st, box);
 }
 
+// Codes of a cache's keys, two as one element: a map {d / 2, rows of a page, heads, pages}.
+bool encode_codes(CUtensorMap *m, const xs_cache &c, unsigned box_rows) {
+  const unsigned long long page = c.page_size, d = c.d;
+  const unsigned long long dims[4] = {d / 2, page, static_cast<unsigned long long>(c.H_kv), static_cast<unsigned long long>(c.n_pages)};
+  const unsigned long long st[3] = {d, page * d, c.H_kv * page * d};
+  const unsigned box[4] = {static_cast<unsigned>(c.d / 2), box_rows, 1, 1};
+  return encode_map(m, c.k, 4, dims, st, box, c.d);
+}
+
 // Whole units on min(units, sms) CTAs, or with `room` bytes for partial results the split schedule,
 // whichever should end earlier; costs in KV tiles. `mean`, `most`: tiles of a unit; `join`: what pieces and
 // the launch that joins them cost.
@@ -264,6 +273,10 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
       p.codes[1] = static_cast<const uint8_t *>(a->cache.v);
       p.scales[0] = a->cache.k_scale;
       p.scales[1] = a->cache.v_scale;
+      // (A cache without a page has nothing to load.)
+      const unsigned most = a->cache.page_size < kTileRows ? a->cache.page_size : kTileRows;
+      if (a->cache.n_pages > 0 && (!encode_codes(&p.tm_c, a->cache, most) || !encode_codes(&p.tm_c16, a->cache, 16)))
+        return XS_ERR_CUDA;
     }
   }
   p.parts = reinterpret_cast<float *>(area);
