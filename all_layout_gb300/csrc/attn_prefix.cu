@@ -88,8 +88,18 @@ __device__ __forceinline__ PrefixUnit unit_of(const PrefixGeo &p, const int *sta
   return u;
 }
 
-// The split region: its places (kPrefixCost for a unit and then one for each of its KV tiles), the
-// CTAs that share it, and the unit where this CTA begins in it.
+// The split region: its places (unit_cost for a unit, then one for each of the prefix's tiles and own_cost for
+// each own one, which begins at the first of them), the CTAs that share it, and the unit where this CTA begins
+// in it.
+__device__ __forceinline__ unsigned place_of(const PrefixGeo &p, int tile) {
+  return tile <= p.n_prefix ? tile : p.n_prefix + (tile - p.n_prefix) * static_cast<unsigned>(p.own_cost);
+}
+// The first tile that begins at a place or behind it.
+__device__ __forceinline__ int tile_at(const PrefixGeo &p, unsigned place) {
+  const unsigned np = p.n_prefix, each = p.own_cost;
+  return static_cast<int>(place <= np ? place : np + (place - np + each - 1) / each);
+}
+__device__ __forceinline__ unsigned places_of(const PrefixGeo &p, int n) { return p.unit_cost + place_of(p, n); }
 struct PrefixPlan {
   unsigned total, per;   // places; of a CTA
   unsigned begin;        // first place of `unit`
@@ -131,16 +141,18 @@ struct PrefixWalk {
     }
     while (pos < end) {
       static_cast<PrefixUnit &>(it) = unit_of(p, table, unit);
-      if (pos < begin + it.n + kPrefixCost) {
-        it.u0 = begin + kPrefixCost;
+      const unsigned past = begin + places_of(p, it.n);
+      if (pos < past) {
+        it.u0 = begin + p.unit_cost;
         if (end <= it.u0) break;   // the range ends before the unit's first tile
-        it.kv0 = pos > it.u0 ? static_cast<int>(pos - it.u0) : 0;
-        it.kv1 = end - it.u0 < it.n ? static_cast<int>(end - it.u0) : it.n;
+        it.kv0 = pos > it.u0 ? tile_at(p, pos - it.u0) : 0;
+        it.kv1 = min(tile_at(p, end - it.u0), it.n);
         it.piece = it.kv0 > 0 || it.kv1 < it.n;
-        pos = it.u0 + it.kv1;
-        return true;
+        pos = min(end, past);
+        if (it.kv0 < it.kv1) return true;
+        continue;   // behind the beginning of the unit's last tile
       }
-      begin += it.n + kPrefixCost;
+      begin = past;
       ++unit;
     }
     pos = end;
@@ -165,7 +177,7 @@ __device__ __noinline__ bool next_item(const PrefixStart *start, const int *tabl
 // The split region's size and this CTA's place in it, by one warp.
 __device__ PrefixPlan plan_split(const PrefixParams &p, const int *table) {
   const int lane = threadIdx.x & 31, first = p.waves * static_cast<int>(gridDim.x);
-  auto size_of = [&](int u) -> unsigned { return u < p.n_units ? unit_of(p, table, u).n + kPrefixCost : 0; };
+  auto size_of = [&](int u) -> unsigned { return u < p.n_units ? places_of(p, unit_of(p, table, u).n) : 0; };
   unsigned total = 0;
   for (int u = first + lane; u < p.n_units; u += 32) total += size_of(u);
   total = __reduce_add_sync(0xffffffffu, total);
@@ -219,8 +231,9 @@ __device__ __forceinline__ int4 *cut_place(const PrefixParams &p, int unit) {
   return p.cuts + (cut_by_unit(p) ? unit - p.waves * static_cast<int>(gridDim.x) : static_cast<int>(blockIdx.x));
 }
 // How many consecutive CTAs, from the one that begins the unit, its pieces run on.
-__device__ __forceinline__ int pieces_of(const PrefixPlan &plan, unsigned u0, int n) {
-  return static_cast<int>((u0 + n - 1) / plan.per - u0 / plan.per) + 1;
+// (No range between is without a tile, as none is shorter than own_cost.)
+__device__ __forceinline__ int pieces_of(const PrefixGeo &p, const PrefixPlan &plan, unsigned u0, int n) {
+  return static_cast<int>((u0 + place_of(p, n - 1)) / plan.per - u0 / plan.per) + 1;
 }
 
 // One row of a k/v head's rows; n >= Nq or h past the k/v head's: padding.

@@ -6,25 +6,26 @@
 // keys, the weights of the others being zero: a tile's exponentials are then halved (quartered),
 // and the epilogue adds the copies' results, each with its own maximum and sum.
 //
-// Cached keys and values: the loader copies a tile's codes and scales into a ring of raw slots, and
-// four warps each turn K's and V's into operands in rings of their own. K's codes become fp16 as they
-// are, and the scores are multiplied by the keys' scales; the queries that meet them are in fp16 too,
-// each row times a power of two. V's become bf16 (what it is multiplied with, the weights, needs
-// bf16's range): a code's bits moved to bf16's place stand for code * 2^-120, so one product with
-// 2^(120 + e) is exact (e > 7 takes two).
+// Cached keys. Their codes are operands as they are: TMA brings them from the cache's pages in the layout that the
+// MMAs read, and the scores are multiplied by the keys' scales. The queries that meet them are two e4m3 matrices, each
+// row times a power of two: a bf16 value has 8 significant bits, e4m3 4, and what rounding to 4 leaves fits 4. An
+// MMA in e4m3 takes half as long, so the two cost what one in bf16 would.
+// Cached values. Their codes and scales go to raw slots, and two groups of four warps turn every second tile of them
+// into a bf16 operand (what it is multiplied with, the weights, needs bf16's range): a code's bits moved to bf16's
+// place stand for code * 2^-120, so one product with 2^(120 + e) is exact (e > 7 takes two).
 //
 // Roles (512 threads, one CTA per SM):
 //   warps 0-3   softmax, row r of the tile = TMEM lane r
-//   warps 4-7   K: codes to fp16, TMA loads of tiles that are not cached
-//   warps 8-11  V: codes to bf16, TMA loads, and the queries to Tensor Memory
-//   warp 12     issues the scores; Tensor Memory allocation
+//   warps 4-11  V: codes to bf16, TMA loads of tiles that are not cached, and the queries to Tensor Memory
+//   warp 12     issues the scores; scales of the keys; Tensor Memory allocation
 //   warp 13     issues the products with V
-//   warps 14-15 load K's and V's codes and scales
-// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) Q in fp16 [384,384+d/2), in bf16 [448,448+d/2);
+//   warp 14     loads K; warp 15 loads V's codes and scales
+// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) the queries in e4m3 [384,384+d/2), in bf16 [448,448+d/2);
 // P_t over S_t's first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax.
-// Q is read from Tensor Memory because shared memory is what the SM has least of here: with cached
-// keys a tile's codes are written (256 cycles at d = 128) and read (256), its operands written (512)
-// and read (512), about as long as its 33 KB take from HBM at this SM's share of the bandwidth (1450).
+// Queries are read from Tensor Memory because shared memory is what the SM has least of here. Measured at one token
+// for 16 requests of 24 heads behind 64K keys (420 MB of codes): 92 us; with K's codes turned to fp16 operands by four
+// warps and V's by four others 120 us, the warps of V setting the pace; a KV tile then takes 1560 cycles, of which
+// HBM asks 1450 at this SM's share.
 
 constexpr int kFlatValues = 4, kFlatGroupWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
 // Requests whose values are not numbers, a bit each and one (kPrefixEntries) for the prefix: by item modulo two
@@ -76,15 +77,21 @@ __device__ __align__(16) const unsigned g_nan_scales[32] = {
 struct Grain {
   int b, off, valid;
 };
-__device__ __forceinline__ Grain grain_of(const PrefixParams &p, const int *table, const PrefixUnit &u, int pos) {
+// `b`: the entry of an earlier place of the item, or first_entry's.
+__device__ __forceinline__ Grain grain_at(const int *table, const PrefixUnit &u, int pos, int &b) {
   if (pos < table[u.b_lo] || pos >= table[u.b_hi + 1]) return Grain{u.b_lo, 0, 0};
-  int lo = u.b_lo, hi = u.b_hi;   // the last entry that begins at or before pos (those without keys end there too)
+  while (pos >= table[b + 1]) ++b;   // (those without keys end where they begin)
+  const int off = pos - table[b];
+  return Grain{b, off, min(max(len_of(table, b) - off, 0), 16)};
+}
+// An entry at or before that of `pos`, or the item's first one.
+__device__ __noinline__ int first_entry(const int *table, int lo, int hi, int pos) {
+  if (pos < table[lo]) return lo;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if (table[mid] <= pos) lo = mid; else hi = mid - 1;
   }
-  const int off = pos - table[lo];
-  return Grain{lo, off, min(max(len_of(table, lo) - off, 0), 16)};
+  return lo;
 }
 
 // Whether tile j of a unit lies in the cache, and the first packed own key of an own tile.
@@ -93,6 +100,10 @@ __device__ __forceinline__ bool is_cached(const PrefixParams &p, int j) {
 }
 __device__ __forceinline__ int own_pos(const PrefixParams &p, const PrefixUnit &u, int j) {
   return (u.t0 + j - p.n_prefix) * BN;
+}
+// Of this lane's sixteen keys, lanes 0 to 7, in the first own tile from j on.
+__device__ __forceinline__ int entry_of(const PrefixParams &p, const int *table, const PrefixUnit &u, int j) {
+  return first_entry(table, u.b_lo, u.b_hi, own_pos(p, u, max(j, p.n_prefix)) + (threadIdx.x & 7) * 16);
 }
 
 // Whether a tile's keys (a Grain each in lanes 0 to 7) are of one request, one after the other from lane 0 on.
@@ -116,7 +127,7 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 struct Part {
   int page, at;
 };
-__device__ __forceinline__ Part part_at(const PrefixParams &p, const int *table, const PrefixItem &item, int j) {
+__device__ __forceinline__ Part part_at(const PrefixParams &p, const int *table, const PrefixItem &item, int j, int &entry) {
   const int lane = threadIdx.x & 31;
   Part r{0, -1};
   if (j >= item.kv1 || !is_cached(p, j) || lane >= BN / 16) return r;
@@ -125,7 +136,7 @@ __device__ __forceinline__ Part part_at(const PrefixParams &p, const int *table,
   int b = 0, place = j * BN + lane * 16;
   bool live = place < p.Np;
   if (!prefix) {
-    const Grain g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+    const Grain g = grain_at(table, item, own_pos(p, item, j) + lane * 16, entry);
     b = g.b;
     place = g.off;
     live = g.valid > 0;
@@ -168,7 +179,7 @@ __device__ void flat_load_keys(const PrefixParams &p, uint8_t *smem, FlatBars *b
   bool more = bars->start.any != 0;
   bool ok = true;
   const int psize = p.prefix_pages.page;   // one cache: all its pages have one size
-  const int big = min(psize, BN) / 16;     // lanes whose rows a large box has
+  const int big = min(p.prefix_pages.shift, 7) - 4;   // log2 of the lanes whose rows a large box has
   auto next_slot = [&] {
     ++used;
     if (++slot == C::KN) slot = 0, parity ^= 1;
@@ -205,19 +216,20 @@ __device__ void flat_load_keys(const PrefixParams &p, uint8_t *smem, FlatBars *b
         next_slot();
       }
     }
-    Part ahead = part_at(p, table, item, j);
+    int entry = entry_of(p, table, item, j), beside = entry;   // of part_at and of bf16 tiles
+    Part ahead = part_at(p, table, item, j, entry);
     for (; ok && j < item.kv1; ++j) {
       const Part r = ahead;
-      ahead = part_at(p, table, item, j + 1);
+      ahead = part_at(p, table, item, j + 1, entry);
       if (is_cached(p, j)) {
         // A run's rows in large boxes as far as they go, the rest in boxes of sixteen rows.
         const Run x = run_of(p, r);
-        const int in = lane - x.first, whole = (x.end - x.first) / big * big;
+        const int in = lane - x.first, whole = (x.end - x.first) >> big << big;
         if (!(ok = wait_for<true>(smem_u32(&bars->k_empty[slot]), parity, abort_flag, p))) break;
         const uint32_t full = smem_u32(&bars->k_full[slot]), dst = smem_u32(smem + C::OFF_K + slot * kHalf);
         if (lane == 0) mbar_arrive_expect_tx(full, __popc(x.lanes) * 16u * D);
         __syncwarp();
-        if (x.held && (in >= whole || in % big == 0))
+        if (x.held && (in >= whole || (in & ((1 << big) - 1)) == 0))
           tma_load_4d(dst + lane * 16 * D, in < whole ? &p.tm_c : &p.tm_c16, full, 0, r.at, item.hk, r.page);
         if (lane < BN / 16) {
           const long long row = (static_cast<long long>(r.page) * p.Hk + item.hk) * psize + r.at;
@@ -234,7 +246,7 @@ __device__ void flat_load_keys(const PrefixParams &p, uint8_t *smem, FlatBars *b
       Grain g{0, 0, 0};
       bool one = true;   // a box of 128 rows: the prefix's (rows past Np come as zeros) and one request's, past its last key too
       if (j >= p.n_prefix) {
-        if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+        if (lane < BN / 16) g = grain_at(table, item, own_pos(p, item, j) + lane * 16, beside);
         one = one_request(g);
       }
       const uint32_t bytes = one ? kHalf : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * 128;
@@ -304,10 +316,11 @@ __device__ void flat_load_values(const PrefixParams &p, uint8_t *smem, FlatBars 
         if (tile & 1) ++use[1]; else ++use[0];
       }
     }
-    Part ahead = part_at(p, table, item, j);
+    int entry = entry_of(p, table, item, j);
+    Part ahead = part_at(p, table, item, j, entry);
     for (; ok && j < item.kv1; ++j, ++tile) {
       const Part r = ahead;
-      ahead = part_at(p, table, item, j + 1);
+      ahead = part_at(p, table, item, j + 1, entry);
       if (!is_cached(p, j)) continue;
       const Run x = run_of(p, r);
       const long long row = (static_cast<long long>(r.page) * p.Hk + item.hk) * psize + r.at;
@@ -455,9 +468,9 @@ __device__ __noinline__ void clear_rows(uint8_t *tile, int valid, int entry, uin
   }
 }
 
-// Two pairs of values to two words of four e4m3 codes, whose sum they are as far as the codes reach: what rounding to
-// the four bits of the first leaves of a bf16 value's eight fits the second's four.
-__device__ __forceinline__ void two_codes(float a, float b, float c, float d, uint32_t &first, uint32_t &rest) {
+// Two bf16 pairs, times s, to two words of four e4m3 codes, whose sum they are as far as the codes reach: what
+// rounding to the four bits of the first leaves of a bf16 value's eight fits the second's four.
+__device__ __forceinline__ void two_codes(uint32_t u, uint32_t v, float s, uint32_t &first, uint32_t &rest) {
   auto pair = [](float x, float y, uint16_t &hi, uint16_t &lo) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y), "f"(x));
     uint32_t back;
@@ -467,18 +480,20 @@ __device__ __forceinline__ void two_codes(float a, float b, float c, float d, ui
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y - by), "f"(x - bx));
   };
   uint16_t h0, l0, h1, l1;
-  pair(a, b, h0, l0);
-  pair(c, d, h1, l1);
+  pair(__uint_as_float(u << 16) * s, __uint_as_float(u & 0xffff0000u) * s, h0, l0);
+  pair(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s, h1, l1);
   first = h0 | static_cast<uint32_t>(h1) << 16;
   rest = l0 | static_cast<uint32_t>(l1) << 16;
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 
-// An item's queries to Tensor Memory by the warps of V, every second 32 columns of a row a thread and group (the
+// An item's queries to Tensor Memory by the warps of V, every second eight columns of a row a thread and group (the
 // copies begin at multiples of row_tile).
 template <int D>
 __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const PrefixItem &item,
@@ -526,25 +541,15 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
   if (group == 0) reinterpret_cast<float *>(smem + C::OFF_QF)[tid] = back;
   tc_fence_after();   // (the last item's scores, read from here, are done)
 #pragma unroll 1
-  for (int c = group; c < D / 32; c += 2) {
-    uint32_t q[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = part(4 * c + i);
-      q[4 * i] = v.x;
-      q[4 * i + 1] = v.y;
-      q[4 * i + 2] = v.z;
-      q[4 * i + 3] = v.w;
-    }
-    if (!p.prefix_cached || !p.own_cached) tmem_st16(to + C::COL_Q + 16 * c, q);
+  for (int c = group; c < D / 8; c += 2) {
+    const uint4 v = part(c);
+    if (!p.prefix_cached || !p.own_cached) tmem_st4(to + C::COL_Q + 4 * c, v.x, v.y, v.z, v.w);
     if (cached) {
-      uint32_t first[8], rest[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        two_codes(__uint_as_float(q[2 * i] << 16) * s, __uint_as_float(q[2 * i] & 0xffff0000u) * s,
-                  __uint_as_float(q[2 * i + 1] << 16) * s, __uint_as_float(q[2 * i + 1] & 0xffff0000u) * s, first[i], rest[i]);
-      tmem_st8(to + C::COL_Q8 + 8 * c, first);
-      tmem_st8(to + C::COL_Q8 + D / 4 + 8 * c, rest);
+      uint32_t first[2], rest[2];
+      two_codes(v.x, v.y, s, first[0], rest[0]);
+      two_codes(v.z, v.w, s, first[1], rest[1]);
+      tmem_st2(to + C::COL_Q8 + 2 * c, first[0], first[1]);
+      tmem_st2(to + C::COL_Q8 + D / 4 + 2 * c, rest[0], rest[1]);
     }
   }
   tmem_wait_st();
@@ -572,12 +577,13 @@ __device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars
   bool more = bars->start.any != 0;
 
   uint32_t *bad = nullptr;   // the item's words
+  int entry = 0;             // see grain_at
   // Lanes 0-7: of sixteen keys each, whose they are and how many count. (Rows of V behind a request's last key
   // have the weight 0, but what lies there may not be a number.)
   auto valid_of = [&](int j) {
     if (lane >= BN / 16) return Grain{0, 0, 16};
     if (j < p.n_prefix) return Grain{kPrefixEntries, 0, min(max(p.Np - j * BN - lane * 16, 0), 16)};
-    return grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+    return grain_at(table, item, own_pos(p, item, j) + lane * 16, entry);
   };
   // A cached tile; `valid`, `entry` as convert_values takes them.
   auto convert = [&](int valid, int entry) {
@@ -610,7 +616,7 @@ __device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars
       return true;
     }
     Grain g{0, 0, 0};
-    if (lane < BN / 16) g = grain_of(p, table, item, own_pos(p, item, j) + lane * 16);
+    if (lane < BN / 16) g = grain_at(table, item, own_pos(p, item, j) + lane * 16, entry);
     // Keys of one request lie one after the other: a box of 128 rows, which may reach past its last.
     const bool one = one_request(g);
     const uint32_t bytes = one ? C::TILE : __popc(__ballot_sync(0xffffffffu, g.valid > 0)) * 16u * D * 2;
@@ -658,6 +664,7 @@ __device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars
 #pragma unroll 1
       for (; ok && j < whole; j += 2) ok = convert(16, kPrefixEntries);
     }
+    entry = entry_of(p, table, item, j);
     for (; ok && j < item.kv1; j += 2) {
       if (is_cached(p, j)) {
         const Grain g = valid_of(j);
@@ -913,9 +920,12 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       bool times = is_cached(p, j);
       const float scale = times ? row_factor : p.scale_log2;
       const float4 *fac = reinterpret_cast<const float4 *>(smem + C::OFF_FAC) + (step & 3) * (BN / 4) + copy * NC * 8;
-      if (__any_sync(0xffffffffu, lo > 0 || hi < NC * 32)) {
+      // Mostly a row sees all of the tile's keys or none: that takes no masking of scores.
+      bool live = lo < NC * 32 && hi > 0;
+      if (__any_sync(0xffffffffu, live && (lo > 0 || hi < NC * 32))) {
         mask_scores<NC>(tC, times ? reinterpret_cast<const float *>(fac) : nullptr, lo, hi);
         times = false;
+        live = true;
       }
       constexpr int W = NC > 1 ? 2 : 1;   // chunks loaded at a time
       uint32_t s[W][32];
@@ -943,9 +953,12 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         for (int k = 0; k < W; ++k) {
           finish(c + k, k);
           mx = max32(s[k], mx);
+          if (NC == 4 && times) tmem_st32(tC + 32 * (c + k), s[k]);   // (shorter than to multiply twice)
         }
       }
-      const float m_new = fmaxf(m, mx * scale);
+      if (NC == 4 && times) tmem_wait_st();
+      times = false;
+      const float m_new = live ? fmaxf(m, mx * scale) : m;
       float alpha = 1.f;
       bool rescale = false;
       if (j == item.kv0) {
@@ -975,6 +988,8 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
           if constexpr (NC == 4) finish(c + k, k);
           uint32_t pk[16];
           weights32(s[k], scale2, negm2, pk, sum);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = live ? pk[i] : 0;
           tmem_st16(tS + 16 * (copy * NC + c + k), pk);
         }
       }
@@ -986,7 +1001,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         for (int c = 0; c < 4; ++c)
           if (c / NC != copy) tmem_st16(tS + 16 * c, zero);
       }
-      l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (live) l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       if (rescale) {
         // (The products before the last are done, as these scores followed them.)
         wait(bars->pv_done[t ^ 1], (step - 1) >> 1 & 1);
@@ -1026,7 +1041,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         __stcg(part + (D + 1) * BM + tid, l);
       }
       if (tid == 0 && item.kv0 == 0)
-        __stcg(cut_place(p, item.unit), make_int4(blockIdx.x, dead ? 0 : pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
+        __stcg(cut_place(p, item.unit), make_int4(blockIdx.x, dead ? 0 : pieces_of(p, bars->start.plan, item.u0, item.n), item.hk, item.row0));
       if (!idle) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {

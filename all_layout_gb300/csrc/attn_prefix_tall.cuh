@@ -389,7 +389,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
         __stcg(part + (D + 1) * 2 * BM + at, l);
       }
       if (tid == 0 && item.kv0 == 0) {
-        __stcg(cut_place(p, item.unit), make_int4(blockIdx.x, pieces_of(bars->start.plan, item.u0, item.n), item.hk, item.row0));
+        __stcg(cut_place(p, item.unit), make_int4(blockIdx.x, pieces_of(p, bars->start.plan, item.u0, item.n), item.hk, item.row0));
       }
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {

@@ -11,10 +11,6 @@ namespace xs {
 
 // Batch entries of one launch: their places among the packed own keys lie in shared memory.
 constexpr int kPrefixEntries = 256;
-// What a unit costs beside its KV tiles (its queries' loads and its epilogue), in tiles. In the
-// split schedule a unit takes so many places more than it has tiles.
-constexpr int kPrefixCost = 2;
-
 // Division of n in [0, 2^31) by a fixed d: with l the least l for which d <= 2^l, n m >> (31 + l) for
 // m = ceil(2^(31 + l) / d). (A plain division is some forty instructions, and a launch's first ones wait
 // for instructions more than for anything else.)
@@ -39,6 +35,7 @@ struct PrefixGeo {
   int row_tile, n_tiles, n_units;        // rows of a unit; units of a head, of all
   int n_prefix;                          // 128-key tiles of the prefix
   int split, waves, min_places;          // see PrefixWalk
+  int unit_cost, own_cost;               // see place_of; own_cost <= min_places
   Divisor by_entry, by_tiles;            // entry_rows, n_tiles
 };
 

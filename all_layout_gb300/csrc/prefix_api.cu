@@ -61,12 +61,12 @@ struct Plan {
   int split, waves, grid;
   double cost;
 };
-Plan plan(long long units, int sms, double mean, double most, int least, double join, unsigned long long per_cta,
+Plan plan(long long units, int sms, double cost_each, double mean, double most, int least, double join, unsigned long long per_cta,
           unsigned long long room) {
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
   const long long rounds = (units + grid0 - 1) / grid0;
-  const double unit = mean + kPrefixCost;
-  const Plan whole{0, 0, grid0, (rounds - 1) * unit + most + kPrefixCost};
+  const double unit = mean + cost_each;
+  const Plan whole{0, 0, grid0, (rounds - 1) * unit + most + cost_each};
   if (most < 2 || static_cast<unsigned long long>(sms) * sizeof(int4) > kCutsBytes) return whole;
   const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
   const long long left = units - static_cast<long long>(waves) * sms;
@@ -89,7 +89,7 @@ struct Shape {
 };
 struct Choice {
   bool tall;
-  int grain, nq_rows, entry_rows, copies, row_tile, n_tiles;
+  int grain, nq_rows, entry_rows, copies, row_tile, n_tiles, unit_cost, own_cost;
   long long rows;
   Plan plan;
   double us;
@@ -117,14 +117,20 @@ Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
   const double top = entry >= c.row_tile ? (met > c.n_tiles ? 2 : 1)
                                          : std::fmin(s.B, (c.row_tile + entry - 1) / entry + (c.row_tile % entry == 0 ? 0 : 1));
   const double prefix = (s.Np + kTileRows - 1) / kTileRows;
-  // Times of a KV tile (GB300, us; 64 tiles a CTA, 128, 64 and 32 rows): the flat kernel at d = 128 1.67, 1.5
-  // and 1.5 with keys in tensors, 1.8, 1.2 and 1.15 with cached ones; at d = 64 1.06, 0.8 and 0.8, 1.55, 0.9 and
-  // 0.75. The tall kernel's, for a pair of row tiles: 1.46 and 1.27. The join: 6 us, in the tall kernel 10.
+  // Times of a KV tile (GB300, us; 64 tiles a CTA, 128, 64 and 32 rows): the flat kernel at d = 128 1.74, 1.61
+  // and 1.57 with keys in tensors, 1.82, 1.19 and 1.03 with cached ones; at d = 64 1.26, 0.94 and 0.93, 1.59, 1.0
+  // and 0.85. The tall kernel's, for a pair of row tiles: 1.46 and 1.27. The join: 6 us, in the tall kernel 10.
   const bool half = s.d == 64, one = c.copies == 1;
   const double us = tall ? (half ? 1.27 : 1.46)
-                         : s.cached ? (half ? (one ? 1.55 : 0.85) : one ? 1.8 : 1.2) : half ? (one ? 1.06 : 0.8) : one ? 1.67 : 1.5;
-  c.plan = plan(static_cast<long long>(s.Hk) * c.n_tiles, sms, prefix + own * here * (s.ragged ? 0.75 : 1.0), prefix + own * top,
-                kLeast, (tall ? 10 : 6) / us, 2ull * prefix_part_floats(s.d, c.row_tile) * 4, room);
+                         : s.cached ? (half ? (one ? 1.59 : 0.93) : one ? 1.82 : 1.1) : half ? (one ? 1.26 : 0.94) : one ? 1.74 : 1.6;
+  // What a unit costs beside its tiles (its queries, its epilogue, the pipeline's start and end), and an own tile
+  // whose rows are of several requests, in tiles (see place_of): one token for 8 requests takes 27.6 us so and 33
+  // with 2 and 1, for 16 behind 64K keys 92 and 105; the tall kernel's costs are 2 and 1.
+  c.unit_cost = tall ? 2 : 8;
+  c.own_cost = !tall && top > 1 ? 2 : 1;
+  const double own_places = own * c.own_cost;
+  c.plan = plan(static_cast<long long>(s.Hk) * c.n_tiles, sms, c.unit_cost, prefix + own_places * here * (s.ragged ? 0.75 : 1.0),
+                prefix + own_places * top, kLeast, (tall ? 10 : 6) / us, 2ull * prefix_part_floats(s.d, c.row_tile) * 4, room);
   c.us = c.plan.cost * us;
   return c;
 }
@@ -317,6 +323,8 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
     p.by_entry.set(p.entry_rows);
     p.by_tiles.set(p.n_tiles);
     p.by_shard.set(p.rows_per_shard > 0 ? p.rows_per_shard : 1);
+    p.unit_cost = c.unit_cost;
+    p.own_cost = c.own_cost;
     p.split = c.plan.split;
     p.waves = c.plan.waves;
     p.grid = c.plan.grid;
