@@ -7,9 +7,10 @@
 // and the epilogue adds the copies' results, each with its own maximum and sum.
 //
 // Cached keys. Their codes are operands as they are: TMA brings them from the cache's pages in the layout that the
-// MMAs read, and the scores are multiplied by the keys' scales. The queries that meet them are two e4m3 matrices, each
-// row times a power of two: a bf16 value has 8 significant bits, e4m3 4, and what rounding to 4 leaves fits 4. An
-// MMA in e4m3 takes half as long, so the two cost what one in bf16 would.
+// MMAs read, and the scores are multiplied by the keys' scales. The queries that meet them are two 8-bit matrices, each
+// row times a power of two: of a bf16 value's 8 significant bits e5m2 takes the first 3, and what that rounding
+// leaves, an integer of at most 16 in units of the last one, fits e4m3's 4. An MMA in 8 bits takes half as long, so
+// the two cost what one in bf16 would; its sums are as exact (a term 2^-26 of the others' came through).
 // Cached values. Their codes and scales go to raw slots, and two groups of four warps turn every second tile of them
 // into a bf16 operand (what it is multiplied with, the weights, needs bf16's range): a code's bits moved to bf16's
 // place stand for code * 2^-120, so one product with 2^(120 + e) is exact (e > 7 takes two).
@@ -20,7 +21,7 @@
 //   warp 12     issues the scores; scales of the keys; Tensor Memory allocation
 //   warp 13     issues the products with V
 //   warp 14     loads K; warp 15 loads V's codes and scales
-// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) the queries in e4m3 [384,384+d/2), in bf16 [448,448+d/2);
+// Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) the queries in 8 bits [384,384+d/2), in bf16 [448,448+d/2);
 // P_t over S_t's first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax.
 // Queries are read from Tensor Memory because shared memory is what the SM has least of here. Measured at one token
 // for 16 requests of 24 heads behind 64K keys (420 MB of codes): 92 us; with K's codes turned to fp16 operands by four
@@ -468,13 +469,12 @@ __device__ __noinline__ void clear_rows(uint8_t *tile, int valid, int entry, uin
   }
 }
 
-// Two bf16 pairs, times s, to two words of four e4m3 codes, whose sum they are as far as the codes reach: what
-// rounding to the four bits of the first leaves of a bf16 value's eight fits the second's four.
+// Two bf16 pairs, times s, to a word of four e5m2 codes and one of four e4m3 codes of what they leave.
 __device__ __forceinline__ void two_codes(uint32_t u, uint32_t v, float s, uint32_t &first, uint32_t &rest) {
   auto pair = [](float x, float y, uint16_t &hi, uint16_t &lo) {
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y), "f"(x));
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y), "f"(x));
     uint32_t back;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(back) : "h"(hi));
     float bx, by;
     asm("{.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.f32.f16 %0, t;\n\tcvt.f32.f16 %1, u;}" : "=f"(bx), "=f"(by) : "r"(back));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y - by), "f"(x - bx));
@@ -518,9 +518,9 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
   const bool cached = p.prefix_cached || p.own_cached;
   float s = 1.f, back = 1.f;
   if (cached) {
-    // For cached keys: times the power of two that brings the row's largest magnitude to [2^7, 2^8), in two
-    // parts. Their sum is exact for values down to 2^-9 of that, and off by 2^-17 of it at most below. A row
-    // with an infinity or NaN becomes NaN by its factor.
+    // For cached keys: times the power of two that brings the row's largest magnitude to [2^11, 2^12) (e4m3 then
+    // holds what is left of it), in two parts. Their sum is exact for values down to 2^-13 of that, and off by 2^-10,
+    // 2^-21 of it, at most below. A row with an infinity or NaN becomes NaN by its factor.
     uint32_t big = 0;   // largest magnitudes, as bits, of the even and of the odd columns
     uint4 x[D / 8];
 #pragma unroll
@@ -531,7 +531,7 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
       big = __vmaxu2(__vmaxu2(big, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
     }
     const int e = static_cast<int>(max(big & 0xffffu, big >> 16) >> 7);
-    const int up = min(261 - e, 253);   // 2^(up - 127), 2^(134 - e) mostly
+    const int up = min(265 - e, 253);   // 2^(up - 127), 2^(138 - e) mostly
     s = __int_as_float(up << 23);
     back = e == 255 ? NAN : __int_as_float((254 - up) << 23);
   }
@@ -680,17 +680,17 @@ __device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars
 }
 
 // ------------------------------------------------------------------ MMA issuer
-// Scores of a tile of codes: the queries' two parts one after the other. (Formats 0: e4m3.)
+// Scores of a tile of codes: the queries' two parts one after the other. (Formats: 0 e4m3, 1 e5m2.)
 template <int D>
 __device__ __forceinline__ void issue_qk_codes(uint32_t dcol, uint32_t qcol, uint64_t kdesc) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0) & ~(9u << 7);
+  constexpr uint32_t rest = idesc_bf16_f32(128, 128, 0) & ~(9u << 7), first = rest | 1u << 7;
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dcol),
-        "r"(qcol + kk * 8), "l"(kdesc + static_cast<uint64_t>((kk % (D / 32) * 32) >> 4)), "r"(idesc), "r"(kk > 0 ? 1u : 0u)
+        "r"(qcol + kk * 8), "l"(kdesc + static_cast<uint64_t>((kk % (D / 32) * 32) >> 4)), "r"(kk < D / 32 ? first : rest), "r"(kk > 0 ? 1u : 0u)
         : "memory");
 }
 // 64 columns of a bf16 tile.

@@ -219,7 +219,7 @@ def test_scales_over_their_range(xs, Nq):
 
 
 def test_queries_over_their_range(xs):
-    """Rows of queries from 2^-100 to 2^60, columns that stand out by 2^20, zeros: cached keys meet them in fp16."""
+    """Rows of queries from 2^-100 to 2^60, columns that stand out by 2^20, zeros: each row meets cached keys times a power of two."""
     p = Problem(xs, 1, 1, 1, 64, 64, 300, 0, None, "cache", "bf16", page=16, seed=7)
     e = torch.linspace(-100, 20, 64, device="cuda").round()
     p.q.copy_((p.q.float() * torch.exp2(e)[None, None, :, None]).bfloat16())
@@ -236,6 +236,56 @@ def test_queries_over_their_range(xs):
         got = p.run(ws)
         check(got[0, 0][small[:, 0]], (want[0][0, 0][small[:, 0]], want[1][0, 0][small[:, 0]]))
         assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 100])
+def test_queries_with_a_column_that_stands_out(xs, d, Nq):
+    """A column 2^12 times the others that the keys have nothing in: the parts of a query that meet cached keys still
+    hold the others in full (to 2^-13 of a row's largest)."""
+    p = Problem(xs, 1, 1, 1, d, Nq, 300, 0, None, "cache", "bf16", page=128, seed=11, scale=d ** -0.5)
+    p.q.copy_((torch.rand_like(p.q, dtype=torch.float32) + 1).bfloat16() * torch.randn_like(p.q).sign())
+    p.q[p.q >= 2] = 1
+    p.q[p.q <= -2] = -1
+    p.q[..., 5] = 4096
+    p.codes[0][..., 5] = 0
+    p.prefix[0][..., 5] = 0
+    for ws in (None, p.workspace()):
+        check(p.run(ws), p.want())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_of_codes(xs, d):
+    """Two keys whose scores differ by 2^-24 of what cancels in them: the sums hold fp32's bits."""
+    cache = xs.alloc_cache(1, 1, 16, d)
+    rows = torch.zeros(2, d, device="cuda")
+    rows[:, 0:d - 2:2], rows[:, 1:d - 2:2] = 448.0, -448.0
+    rows[0, d - 1] = 2.0 ** -9
+    cache.k[0, 0, :2] = rows.to(torch.float8_e4m3fn)
+    cache.v[0, 0, :1] = torch.ones(1, d, device="cuda").to(torch.float8_e4m3fn)
+    q = torch.ones(1, 1, 1, d, device="cuda", dtype=torch.bfloat16)
+    o = torch.empty_like(q)
+    pages = torch.zeros(1, dtype=torch.int32, device="cuda")
+    xs.prefix_attn(q, o, cache=cache, prefix_pages=pages, prefix_len=2, scale=2.0 ** 9)   # scores 1 and 0
+    want = 1 / (1 + math.exp(-1))
+    assert (o.double() - want).abs().max() <= (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11) * want   # as in check
+
+
+@pytest.mark.parametrize("kind", ["bf16", "cache"])
+@pytest.mark.parametrize("Nq", [20, 300])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_queries_that_are_not_numbers(xs, kind, Nq, value):
+    """A query with a NaN or an infinity: its row is NaN, the others are as without it."""
+    p = Problem(xs, 2, 2, 1, 64, Nq, 200, 100, [100, 30], kind, kind, seed=12)
+    p.q[1, 0, 7] = 1.0                    # (the formula's own row, put aside)
+    want = p.want()
+    p.q[1, 0, 7, 3] = value
+    for ws in (None, p.workspace()):
+        got = p.run(ws)
+        assert torch.isnan(got[1, 0, 7]).all()
+        rest = torch.ones(2, 2, Nq, dtype=torch.bool, device="cuda")
+        rest[1, 0, 7] = False
+        check(got[rest], (want[0][rest], want[1][rest]))
 
 
 def test_identical_values(xs):
