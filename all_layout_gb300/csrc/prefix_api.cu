@@ -66,7 +66,7 @@ Plan plan(long long units, int sms, double cost_each, double mean, double most, 
   const int grid0 = units < sms ? static_cast<int>(units) : sms;
   const long long rounds = (units + grid0 - 1) / grid0;
   const double unit = mean + cost_each;
-  const Plan whole{0, 0, grid0, (rounds - 1) * unit + most + cost_each};
+  const Plan whole{0, 0, grid0, (rounds - 1) * unit + most};   // (every CTA pays for the start of one unit)
   if (most < 2 || static_cast<unsigned long long>(sms) * sizeof(int4) > kCutsBytes) return whole;
   const int waves = units >= sms ? static_cast<int>(units / sms) - 1 : 0;
   const long long left = units - static_cast<long long>(waves) * sms;
