@@ -131,14 +131,14 @@ Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
   const double own_places = own * c.own_cost;
   c.plan = plan(static_cast<long long>(s.Hk) * c.n_tiles, sms, c.unit_cost, prefix + own_places * here * (s.ragged ? 0.75 : 1.0),
                 prefix + own_places * top, kLeast, (tall ? 10 : 6) / us, 2ull * prefix_part_floats(s.d, c.row_tile) * 4, room);
-  c.us = c.plan.cost * us;
+  c.us = c.plan.cost * us + (tall ? 6.5 : 7.5);   // to the first tile's scores and from the last product to the end
   return c;
 }
 
 // Bytes of the workspace that hold cached keys and values read back to bf16, K and V.
 unsigned long long unpacked(long long rows, int d) { return (4ull * rows * d + 511) / 512 * 512; }
 // Their time: half as much is read as is written.
-double unpack_us(unsigned long long bytes) { return bytes == 0 ? 0.0 : 3.0 + bytes * 1.5 / 5.0e6; }
+double unpack_us(unsigned long long bytes) { return bytes == 0 ? 0.0 : 3.0 + bytes * 1.5 / 6.3e6; }
 
 xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_stride, void *const *shards, int P,
                       void *ws, unsigned long long ws_bytes, void *stream) {

@@ -459,9 +459,13 @@ typedef struct {
  * included), non-causal. The prefix's keys are read once for a whole tile of queries,
  * whichever requests and heads of one k/v head they belong to. A request without any key
  * gives zeros. fp32 accumulation and statistics, softmax weights rounded to bf16 for the
- * product with v, output rounded to bf16; cached keys and values are exact in bf16. A cached
- * key whose place no page holds counts as NaN. Outputs must not overlap each other or an
- * input. Nq, Np, Nk: any size, also 0 or 1.
+ * product with v, output rounded to bf16; cached keys and values count as they are. A query
+ * that meets cached keys may be taken in two 8-bit parts: exact for values down to 2^-13 of its
+ * largest magnitude, to within 2^-21 of that below. A NaN or infinity in a query, or among
+ * the keys and values that count, makes NaN of whole rows (or of what the formula gives) of the
+ * requests that see it, and touches no other request. A cached key whose place no page holds
+ * counts as NaN. Outputs must not overlap each other or an input. Nq, Np, Nk: any size, also 0
+ * or 1.
  *   o, o_stride  [B][H][Nq][d] bf16 (device), strides in elements (batch, head, row)
  *   out_shards   host array of P device pointers, shard p [B][Nq/P][H][d] bf16, as in
  *                xs_attn_fused; the warps that finish a row store it in its shard
