@@ -8,18 +8,23 @@
 // each; a tile of rows takes the prefix and its own request's keys. (Its zero weights never meet another
 // request's values, which might not be numbers.)
 //
-// Roles (320 threads, one CTA per SM):
+// Roles (320 threads, at d = 64 352, one CTA per SM):
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, row r of the tile = TMEM lane r
 //   warp 8          MMA issuer, Tensor Memory allocation
 //   warp 9          TMA loader
+//   warp 10         d = 64: issuer of the products
 // Tensor Memory: S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [256+d,256+2d); P_t over S_t's first 64.
 // Issue order at KV tile j, for t = 0, 1: O_t += P_t(j-1) V(j-1), S_t = Q_t K(j)^T: one thread's
 // order keeps S_t(j) from overwriting P_t(j-1) before its product, and the commit that signals
 // S_t(j) covers O_t. One tile's softmax runs beside the other's products.
+// At d = 64 P has columns of its own, P_t [384+64t,448+64t), and a warp of its own issues the products: the scores
+// of the next tile are computed as soon as the softmax has loaded this one's, so it never waits for them (19 heads of
+// 2048 queries against 16384 keys: 153 us = 1068 TFLOP/s, 176 in d = 128's order; 195 us = 1678 TFLOP/s at d = 128).
 
 template <int D>
 struct TallCfg {
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = D == 64 ? 352 : 320;
+  static constexpr uint32_t COL_P = D == 64 ? 384 : 0, P_STEP = D == 64 ? 64 : 128;   // P_t at COL_P + t * P_STEP
   static constexpr int TILE = BM * D * 2;
   static constexpr int KS = D == 128 ? 2 : 3, VS = KS;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE;
@@ -29,12 +34,13 @@ struct TallCfg {
   static constexpr int SMEM = OFF_BAR + 416;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
-constexpr int kTallMma = 8, kTallLoad = 9;
+constexpr int kTallMma = 8, kTallLoad = 9, kTallProducts = 10;
 
 struct TallBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_read[2], pv_done[2];   // d = 64
   uint64_t drain;
   PrefixStart start;
   uint32_t tmem_base;
@@ -140,27 +146,134 @@ __device__ void tall_loader(const PrefixParams &p, uint8_t *smem, TallBars *bars
   if (items > 0) drain(q_full, (items - 1) & 1);
 }
 
-// ------------------------------------------------------------------ MMA issuer
+// ------------------------------------------------------------------ MMA issuers
+// A key behind a request's last one has weight 0, but what lies in its row of V may not be a number. By one warp.
+template <int D>
+__device__ __forceinline__ void clear_tail(uint8_t *tile, int valid) {
+  for (int hf = 0; hf < D / 64; ++hf)
+    for (int o = valid * 128 + (threadIdx.x & 31) * 16; o < kHalf; o += 512)
+      *reinterpret_cast<uint4 *>(tile + hf * kHalf + o) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// d = 64: the scores, each row tile's as soon as its softmax has loaded the last ones.
+template <int D>
+__device__ void tall_scores(const PrefixParams &p, uint8_t *smem, TallBars *bars, const int *table, uint32_t tmem_in) {
+  using C = TallCfg<D>;
+  volatile int *abort_flag = &bars->abort;
+  const uint32_t tmem = uniform(tmem_in);
+  uint32_t use = 0, items = 0, done[2] = {0, 0};   // uses of the ring; scores issued of each row tile
+  const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+  const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+  auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
+  for (; more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
+    const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
+    TallTiles tiles[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const TallTiles x = tiles_of(p, table, item, t);
+      tiles[t] = TallTiles{uniform(x.kv0), uniform(x.prefix), uniform(x.own0), uniform(x.own1)};
+    }
+    if (!wait(bars->q_full, items & 1)) goto done;
+    for (int j = kv0; j < kv1; ++j, ++use) {
+      const uint32_t ks = use % C::KS;
+      if (!wait(bars->k_full[ks], use / C::KS & 1)) goto done;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (tiles[t].has(j)) {
+          if (done[t] > 0 && !wait(bars->s_read[t], (done[t] - 1) & 1)) goto done;
+          ++done[t];
+          tc_fence_after();
+          if (elect_one()) {
+            issue_qk<D>(tmem + t * 128, qdesc + static_cast<uint64_t>(t * (C::TILE >> 4)), kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4)));
+            tc_commit(smem_u32(&bars->s_full[t]));
+          }
+          __syncwarp();
+        }
+      }
+      if (elect_one()) {
+        tc_commit(smem_u32(&bars->k_empty[ks]));
+        if (j == kv1 - 1) tc_commit(smem_u32(&bars->q_empty));
+      }
+      __syncwarp();
+    }
+  }
+done:
+  // All MMAs issued must finish before Tensor Memory is released.
+  if (elect_one()) tc_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  drain(smem_u32(&bars->drain), 0);
+}
+
+// d = 64: the products with V.
+template <int D>
+__device__ void tall_products(const PrefixParams &p, uint8_t *smem, TallBars *bars, const int *table, uint32_t tmem_in) {
+  using C = TallCfg<D>;
+  volatile int *abort_flag = &bars->abort;
+  const uint32_t tmem = uniform(tmem_in);
+  uint32_t use = 0, pc = 0;   // uses of the ring; parities of p_full, a bit a row tile
+  const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), kHalf, 1024);
+  auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
+  PrefixWalk walk = bars->start.walk;
+  PrefixItem item = bars->start.item;
+  bool more = bars->start.any != 0;
+  for (; more; more = next_item(&bars->start, table, &walk, &item)) {
+    const int kv0 = uniform(item.kv0), kv1 = uniform(item.kv1);
+    TallTiles tiles[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const TallTiles x = tiles_of(p, table, item, t);
+      tiles[t] = TallTiles{uniform(x.kv0), uniform(x.prefix), uniform(x.own0), uniform(x.own1)};
+    }
+    int b = item.b_lo;
+    bool fresh[2] = {true, true};   // no product of this item yet
+    for (int j = kv0; j < kv1; ++j, ++use) {
+      const uint32_t vs = use % C::VS;
+      if (!wait(bars->v_full[vs], use / C::VS & 1)) goto done;
+      if (j >= p.n_prefix) {
+        const int valid = uniform(own_tile(p, table, item, j, b).valid);
+        if (valid < BN) clear_tail<D>(smem + C::OFF_V + vs * C::TILE, valid);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (tiles[t].has(j)) {
+          if (!wait(bars->p_full[t], pc >> t & 1)) goto done;
+          pc ^= 1u << t;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv<D>(tmem + 256 + t * D, tmem + C::COL_P + t * C::P_STEP, vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), fresh[t] ? 0u : 1u);
+            tc_commit(smem_u32(&bars->pv_done[t]));
+            if (j == tiles[t].last()) tc_commit(smem_u32(&bars->o_full[t]));
+          }
+          __syncwarp();
+          fresh[t] = false;
+        }
+      }
+      if (elect_one()) tc_commit(smem_u32(&bars->v_empty[vs]));
+      __syncwarp();
+    }
+  }
+done:
+  if (elect_one()) tc_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  drain(smem_u32(&bars->drain), 0);
+}
+
+// d = 128: both.
 template <int D>
 __device__ void tall_mma(const PrefixParams &p, uint8_t *smem, TallBars *bars, const int *table, uint32_t tmem_in) {
   using C = TallCfg<D>;
   volatile int *abort_flag = &bars->abort;
   const uint32_t tmem = uniform(tmem_in);
-  const int lane = threadIdx.x & 31;
   uint32_t use = 0, items = 0, pc = 0;   // uses of the rings; parities of p_full, a bit a row tile
   const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
   const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::OFF_V), kHalf, 1024);
   auto wait = [&](uint64_t &bar, uint32_t parity) { return wait_for<false>(smem_u32(&bar), parity, abort_flag, p); };
-  // A key behind a request's last one has weight 0, but what lies in its row of V may not be a number.
-  auto clear_tail = [&](uint32_t slot, int valid) {
-    uint8_t *tile = smem + C::OFF_V + slot * C::TILE;
-    for (int hf = 0; hf < D / 64; ++hf)
-      for (int o = valid * 128 + lane * 16; o < kHalf; o += 512)
-        *reinterpret_cast<uint4 *>(tile + hf * kHalf + o) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-    __syncwarp();
-  };
   PrefixWalk walk = bars->start.walk;
   PrefixItem item = bars->start.item;
   bool more = bars->start.any != 0;
@@ -218,7 +331,7 @@ __device__ void tall_mma(const PrefixParams &p, uint8_t *smem, TallBars *bars, c
         if (!wait(bars->v_full[vs], (use - 1) / C::VS & 1)) goto done;
         if (j - 1 >= p.n_prefix) {
           const int valid = uniform(own_tile(p, table, item, j - 1, b).valid);
-          if (valid < BN) clear_tail(vs, valid);
+          if (valid < BN) clear_tail<D>(smem + C::OFF_V + vs * C::TILE, valid);
         }
       }
       const uint64_t vd = vdesc0 + static_cast<uint64_t>(vs * (C::TILE >> 4)), kd = kdesc0 + static_cast<uint64_t>(ks * (C::TILE >> 4));
@@ -281,7 +394,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
   using C = TallCfg<D>;
   const int tid = threadIdx.x, t = tid >> 7, in = tid & 127, wq = in >> 5, lane = tid & 31;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-  const uint32_t tS = lanes + t * 128, tO = lanes + 256 + t * D;
+  const uint32_t tS = lanes + t * 128, tP = lanes + C::COL_P + t * C::P_STEP, tO = lanes + 256 + t * D;
   const uint32_t s_full = smem_u32(&bars->s_full[t]), p_full = smem_u32(&bars->p_full[t]);
   const uint32_t o_full = smem_u32(&bars->o_full[t]);
   volatile int *abort_flag = &bars->abort;
@@ -311,9 +424,28 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
         break;
       }
       tc_fence_after();
+      // d = 64: the scores have been loaded; the last product, whose weights lie where the next ones go, is done.
+      auto scores_read = [&] {
+        if constexpr (D == 64) {
+          tc_fence_before();
+          mbar_arrive(smem_u32(&bars->s_read[t]));
+        }
+      };
+      auto product_done = [&] {
+        if constexpr (D == 64) {
+          if (step == 0) return true;
+          const bool done = wait_for<true>(smem_u32(&bars->pv_done[t]), (step - 1) & 1, abort_flag, p);
+          tc_fence_after();
+          return done;
+        }
+        return true;
+      };
       if (masked) {
         if (__all_sync(0xffffffffu, lo >= BN || hi <= 0)) {   // nothing for any row: no weight
-          zero_weights(tS);
+          scores_read();
+          ok = product_done();
+          if (!ok) break;
+          zero_weights(tP);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_full);
@@ -332,6 +464,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
       float mx = max32(s[1], max32(s[0], -INFINITY));
       tmem_wait_ld_regs(s[2]);
       tmem_wait_ld_regs(s[3]);
+      scores_read();
       mx = max32(s[3], max32(s[2], mx));
       const float m_new = fmaxf(m, mx * scale);
       float alpha = 1.f;
@@ -350,13 +483,15 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
       }
       // (Without any key so far the weights are 2^(-inf - 0) = 0.)
       const float neg = m == -INFINITY ? 0.f : -m;
+      ok = product_done();
+      if (!ok) break;
       const uint64_t scale2 = f2_pack(scale, scale), negm2 = f2_pack(neg, neg);
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
         weights32(s[c], scale2, negm2, pk, sum);
-        tmem_st16(tS + 16 * c, pk);
+        tmem_st16(tP + 16 * c, pk);
       }
       l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       if (rescale) {
@@ -445,7 +580,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
 }
 
 template <int D>
-__global__ void __launch_bounds__(320, 1) prefix_tall_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(TallCfg<D>::THREADS, 1) prefix_tall_kernel(const __grid_constant__ PrefixParams p) {
   using C = TallCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle pattern repeats every 1024 bytes
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -468,8 +603,10 @@ __global__ void __launch_bounds__(320, 1) prefix_tall_kernel(const __grid_consta
       mbar_init(smem_u32(&bars->s_full[t]), 1);
       mbar_init(smem_u32(&bars->p_full[t]), BM);
       mbar_init(smem_u32(&bars->o_full[t]), 1);
+      mbar_init(smem_u32(&bars->s_read[t]), BM);
+      mbar_init(smem_u32(&bars->pv_done[t]), 1);
     }
-    mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->drain), D == 64 ? 2 : 1);   // a commit of each issuer
     bars->abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -486,10 +623,16 @@ __global__ void __launch_bounds__(320, 1) prefix_tall_kernel(const __grid_consta
   const uint32_t tmem = bars->tmem_base;
   if (warp < kTallMma)
     tall_softmax<D>(p, smem, bars, table, tmem);
-  else if (warp == kTallMma)
-    tall_mma<D>(p, smem, bars, table, tmem);
-  else
+  else if (warp == kTallLoad)
     tall_loader<D>(p, smem, bars, table);
+  else if constexpr (D == 64) {
+    if (warp == kTallMma)
+      tall_scores<D>(p, smem, bars, table, tmem);
+    else
+      tall_products<D>(p, smem, bars, table, tmem);
+  } else {
+    tall_mma<D>(p, smem, bars, table, tmem);
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
