@@ -498,10 +498,13 @@ def _prefix_args(q, prefix_k, prefix_v, k, v, kv_len, cache, prefix_pages, prefi
         ps, contiguous = a[:2] + b[:2], contiguous and a[2] == 1 and b[2] == 1
     elif prefix_pages is not None:
         _require(cache is not None, "prefix_pages needs a cache")
-        _require(prefix_pages.dim() == 1, "prefix_pages must be [n]")
+        _require(prefix_v is None, "prefix_v needs prefix_k")
+        _require(isinstance(prefix_pages, torch.Tensor) and prefix_pages.dim() == 1, "prefix_pages must be [n]")
         lists = _page_list("prefix_pages", prefix_pages, 1, dev)
         Np = lists[2] * fields[6] if prefix_len is None else prefix_len
         _require(0 <= Np <= lists[2] * fields[6], f"prefix_pages hold {lists[2] * fields[6]} keys, not {prefix_len}")
+    else:
+        _require(prefix_v is None and prefix_len is None, "prefix_v needs prefix_k, prefix_len prefix_pages")
     if k is not None:
         _require(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be a CUDA tensor [B, H_kv, Nk, d]")
         _require(pages is None and max_len is None, "the own keys lie in k and v or in pages")
@@ -511,9 +514,12 @@ def _prefix_args(q, prefix_k, prefix_v, k, v, kv_len, cache, prefix_pages, prefi
         ks, contiguous = a[:3] + b[:3], contiguous and a[3] == 1 and b[3] == 1
     elif pages is not None:
         _require(cache is not None, "pages needs a cache")
+        _require(v is None, "v needs k")
         own_lists = _page_list("pages", pages, B, dev)
         Nk = own_lists[2] * fields[6] if max_len is None else max_len
         _require(0 <= Nk <= own_lists[2] * fields[6], f"pages hold {own_lists[2] * fields[6]} keys, not {max_len}")
+    else:
+        _require(v is None and max_len is None, "v needs k, max_len pages")
     if not contiguous and d > 1:
         raise ValueError("the last dimension of q, prefix_k, prefix_v, k and v must be contiguous")
     packed = _PREFIX_ARGS.pack(q.data_ptr(), *(p if n else 0 for p, n in zip(pointers, (Np, Np, Nk, Nk))),

@@ -405,8 +405,8 @@ typedef struct {
  *     codes = e4m3(x * 2^-e), to nearest even, at most 448; byte = e + 127.
  * A row with a NaN or an infinity gets the byte 255. Nothing else of the cache changes:
  * tokens from lens[b] on, and those whose place no page holds (negative, past the list, or
- * a page that is not in [0, n_pages)), are not stored. Two tokens of one place in one call
- * leave either's values.
+ * a page that is not in [0, n_pages)), are not stored. What a place holds that two tokens of
+ * one call go to is not specified (columns and scale may be of different ones).
  *   k, v, strides   [B][H_kv][N][d] of in_type (device), rows of d contiguous values,
  *                   strides in elements (batch, head, token)
  *   start           [B] int32 (device), or NULL: 0

@@ -448,3 +448,28 @@ def test_layer_from_projection_to_shards(xs):
         mine = read(own, n_new + step + 1, B)
         check(o, prefix_formula(q.double(), prefix, mine, [n_new + step + 1] * B, d ** -0.5), f"token {step}")
     assert xs.last_device_status() == xs.OK
+
+
+def test_binding_refuses(xs):
+    """Operands that do not belong together, on the host, before any launch."""
+    q = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16, device="cuda")
+    o = torch.full_like(q, 3.0)
+    kv, pre = torch.zeros(2, 2, 20, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 20, 64, dtype=torch.bfloat16, device="cuda")
+    cache = xs.alloc_cache(4, 2, 16, 64)
+    one, two = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    for kw in (dict(k=kv), dict(v=kv), dict(prefix_v=pre), dict(prefix_k=pre), dict(prefix_len=3), dict(max_len=3),
+               dict(prefix_pages=one), dict(pages=two), dict(cache=cache, prefix_pages=two), dict(cache=cache, prefix_pages=[0]),
+               dict(cache=cache, prefix_pages=one, prefix_len=49), dict(cache=cache, prefix_pages=one, prefix_len=-1),
+               dict(cache=cache, pages=two, max_len=49), dict(cache=cache, pages=two, v=kv),
+               dict(cache=cache, prefix_pages=one, prefix_v=pre), dict(cache=cache, prefix_pages=one, prefix_k=pre, prefix_v=pre),
+               dict(cache=cache, pages=two[:1]), dict(cache=cache, pages=two.long()), dict(k=kv, v=kv[:, :1]),
+               dict(k=kv, v=kv.float()), dict(k=kv.transpose(2, 3), v=kv), dict(k=kv, v=kv, kv_len=one),
+               dict(k=kv.cpu(), v=kv.cpu()), dict(k=kv, v=kv, workspace=torch.zeros(8))):
+        with pytest.raises(ValueError):
+            xs.prefix_attn(q, o, **kw)
+            pytest.fail(f"took {sorted(kw)}")
+    with pytest.raises(ValueError):
+        xs.prefix_attn_fused(q, xs.alloc_shards(2, 8, 4, 64, 2)[:1], k=kv, v=kv)
+    with pytest.raises(xs.XsError):
+        xs.prefix_attn(q, o, cache=xs.alloc_cache(4, 4, 16, 64), prefix_pages=one, k=kv, v=kv)
+    assert (o == 3).all()
