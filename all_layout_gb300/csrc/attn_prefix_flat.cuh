@@ -391,7 +391,7 @@ __device__ __forceinline__ void slot_read(uint32_t empty) {
 // Codes and scale bytes of V's raw slot to a bf16 tile; `valid`, `entry`: of the sixteen rows of lanes 0-7
 // (valid_of); `bad`: this warp's words for requests whose values are not numbers.
 template <int D>
-__device__ __noinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, int entry, uint32_t *bad, uint32_t tid,
+__device__ __forceinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, int entry, uint32_t *bad, uint32_t tid,
                                            uint32_t empty) {
   constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatGroupWarps / CPR, U = BN / STEP;   // groups of a row's codes
   const uint32_t lane = tid & 31;
@@ -658,16 +658,13 @@ __device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars
     __syncwarp();
     int j = item.kv0 + ((tile ^ group) & 1);
     tile += item.kv1 - item.kv0;
-    if (p.prefix_cached) {
-      // The prefix's whole tiles, in a loop of few instructions.
-      const int whole = min(item.kv1, p.Np / BN);
-#pragma unroll 1
-      for (; ok && j < whole; j += 2) ok = convert(16, kPrefixEntries);
-    }
+    const int whole = p.Np / BN;   // of the prefix's tiles
     entry = entry_of(p, table, item, j);
+#pragma unroll 1
     for (; ok && j < item.kv1; j += 2) {
       if (is_cached(p, j)) {
-        const Grain g = valid_of(j);
+        Grain g{kPrefixEntries, 0, 16};
+        if (j >= whole) g = valid_of(j);
         ok = convert(g.valid, g.b);
       } else {
         ok = load(j);

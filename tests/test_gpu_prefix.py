@@ -470,6 +470,8 @@ def test_binding_refuses(xs):
             pytest.fail(f"took {sorted(kw)}")
     with pytest.raises(ValueError):
         xs.prefix_attn_fused(q, xs.alloc_shards(2, 8, 4, 64, 2)[:1], k=kv, v=kv)
-    with pytest.raises(xs.XsError):
+    with pytest.raises(ValueError):   # other heads than k's
         xs.prefix_attn(q, o, cache=xs.alloc_cache(4, 4, 16, 64), prefix_pages=one, k=kv, v=kv)
+    with pytest.raises(xs.XsError):   # other columns than q's
+        xs.prefix_attn(q, o, cache=xs.alloc_cache(4, 2, 16, 128), prefix_pages=one, k=kv, v=kv)
     assert (o == 3).all()
