@@ -367,7 +367,8 @@ __device__ __forceinline__ void issue_pv(uint32_t dcol, uint32_t pcol, uint64_t 
 // (blockIdx.z of gridDim.z) a block, a lane per row. The eight warps share the parts and the groups of eight
 // columns between them: with few parts a warp takes all of them, with many each takes every eighth. Six parts
 // are under way at a time and joined with a running maximum, the warps' sums in order, so the result does not
-// depend on the order in which the pieces ended.
+// depend on the order in which the pieces ended. Bound by the latency of its loads: from cold
+// memory 8.5 us for the pieces of 24 units of 16 rows (11 MB), 21 us for 38 MB of pieces of 256 rows.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PrefixParams p) {
