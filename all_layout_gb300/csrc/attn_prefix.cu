@@ -181,7 +181,8 @@ __device__ PrefixPlan plan_split(const PrefixParams &p, const int *table) {
   unsigned total = 0;
   for (int u = first + lane; u < p.n_units; u += 32) total += size_of(u);
   total = __reduce_add_sync(0xffffffffu, total);
-  // (blockIdx.x * per stays below total + per * gridDim.x, far from 2^32 for lengths up to 2^29.)
+  // (Lengths up to 2^29 are 2^22 tiles, own ones two places each, and there are fewer than two units for each CTA here:
+  // with 152 of them no place, and no multiple of `per`, reaches 2^32.)
   PrefixPlan plan{total, max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(p.min_places)), 0, first};
   const unsigned pos = blockIdx.x * plan.per;
   if (pos >= total) return plan;
