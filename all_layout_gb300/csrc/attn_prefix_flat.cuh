@@ -848,9 +848,10 @@ __device__ __noinline__ void zero_weights(uint32_t taddr) {
   tmem_st32(taddr, zero);
   tmem_st32(taddr + 32, zero);
 }
-// Weights 2^(s * scale - m) of 32 scores as bf16 pairs, and their sum added to `sum`.
+// Weights 2^(s * scale - m) of 32 scores as bf16 pairs, and their sums added to `sum`, in fp32 pairs: an add for two
+// weights (in the tall kernel four images took 983 us with an add for each, 943 so).
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scale2, uint64_t negm2, uint32_t (&pk)[16],
-                                          float (&sum)[4]) {
+                                          uint64_t (&sum)[2]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, negm2);
@@ -858,9 +859,14 @@ __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scal
     f2_unpack(x2, x0, x1);
     x0 = ex2_approx(x0);
     x1 = ex2_approx(x1);
-    sum[i & 3] += x0 + x1;
+    sum[i & 1] = f2_add(sum[i & 1], f2_pack(x0, x1));
     pk[i] = pack_bf16x2(x0, x1);
   }
+}
+__device__ __forceinline__ float total(const uint64_t (&sum)[2]) {
+  float a, b;
+  f2_unpack(f2_add(sum[0], sum[1]), a, b);
+  return a + b;
 }
 // The factor 2^(a - b) of a maximum that moved from a to b; 0 where there was none.
 __device__ __forceinline__ float shrink(float a, float b) { return a == -INFINITY ? 0.f : ex2_approx(a - b); }
@@ -973,7 +979,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
       // (Without any key so far the weights are 2^(-inf - 0) = 0.)
       const float neg = m == -INFINITY ? 0.f : -m;
       const uint64_t scale2 = f2_pack(scale, scale), negm2 = f2_pack(neg, neg);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[2] = {0, 0};
 #pragma unroll 1
       for (int c = 0; c < NC; c += W) {
         if constexpr (NC == 4) {
@@ -998,7 +1004,7 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         for (int c = 0; c < 4; ++c)
           if (c / NC != copy) tmem_st16(tS + 16 * c, zero);
       }
-      if (live) l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (live) l = fmaf(l, alpha, total(sum));
       if (rescale) {
         // (The products before the last are done, as these scores followed them.)
         wait(bars->pv_done[t ^ 1], (step - 1) >> 1 & 1);
@@ -1058,21 +1064,21 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
     }
     if (tid == 0 && item.u0 > 0 && cut_by_unit(p)) __stcg(cut_place(p, item.unit), make_int4(0, 0, 0, 0));
     // (m, l) of all copies of a row.
-    float top = m, total = l, f = 1.f;
+    float top = m, all = l, f = 1.f;
     if constexpr (COPIES > 1) {
       exch[tid] = make_float2(m, l);
       softmax_sync();
 #pragma unroll
       for (int k = 0; k < COPIES; ++k) top = fmaxf(top, exch[k * RT + in].x);
-      total = 0.f;
+      all = 0.f;
 #pragma unroll
       for (int k = 0; k < COPIES; ++k) {
         const float2 e = exch[k * RT + in];
-        total = fmaf(shrink(e.x, top), e.y, total);
+        all = fmaf(shrink(e.x, top), e.y, all);
       }
       f = shrink(m, top);
     }
-    const float norm = total == 0.f ? 0.f : 1.f / total;
+    const float norm = all == 0.f ? 0.f : 1.f / all;
     if constexpr (COPIES == 1) {
       uint16_t *dst = dead ? nullptr : out_row(p, item.hk, row, D);
       if (!idle) {

@@ -119,9 +119,9 @@ Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
   const double prefix = (s.Np + kTileRows - 1) / kTileRows;
   // Times of a KV tile (GB300, us; 64 tiles a CTA, 128, 64 and 32 rows): the flat kernel at d = 128 1.74, 1.61
   // and 1.57 with keys in tensors, 1.82, 1.19 and 1.03 with cached ones; at d = 64 1.26, 0.94 and 0.93, 1.59, 1.0
-  // and 0.85. The tall kernel's, for a pair of row tiles: 1.46 and 1.1. The join: 6 us, in the tall kernel 10.
+  // and 0.85. The tall kernel's, for a pair of row tiles: 1.4 and 1.05. The join: 6 us, in the tall kernel 10.
   const bool half = s.d == 64, one = c.copies == 1;
-  const double us = tall ? (half ? 1.1 : 1.46)
+  const double us = tall ? (half ? 1.05 : 1.4)
                          : s.cached ? (half ? (one ? 1.59 : 0.93) : one ? 1.82 : 1.1) : half ? (one ? 1.26 : 0.94) : one ? 1.74 : 1.6;
   // What a unit costs beside its tiles (its queries, its epilogue, the pipeline's start and end), and an own tile
   // whose rows are of several requests, in tiles (see place_of): one token for 8 requests takes 27.6 us so and 33
