@@ -31,7 +31,9 @@
 constexpr int kFlatValues = 4, kFlatGroupWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
 // Requests whose values are not numbers, a bit each and one (kPrefixEntries) for the prefix: by item modulo two
 // and warp of V. A row of V that is not a number must not meet the zero weights of other requests' rows, so its
-// place in the operand is cleared, and the rows that see it become NaN at the end.
+// place in the operand is cleared, and the rows that see it become NaN at the end. Each warp clears its words before
+// it arrives for the item's queries: that arrival alone orders them before the softmax's reading, as a group may
+// have no tile of the item to arrive for.
 constexpr int kBadWords = kPrefixEntries / 32 + 1;
 
 template <int D>
@@ -494,10 +496,10 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
 }
 
 // An item's queries to Tensor Memory by the warps of V, every second eight columns of a row a thread and group (the
-// copies begin at multiples of row_tile).
+// copies begin at multiples of row_tile). `bad`: this warp's words of the item (kBadWords), cleared here.
 template <int D>
 __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *smem, FlatBars *bars, const PrefixItem &item,
-                                          uint32_t items, uint32_t tmem, int group) {
+                                          uint32_t items, uint32_t tmem, int group, uint32_t *bad) {
   using C = FlatCfg<D>;
   volatile int *abort_flag = &bars->abort;
   const int tid = threadIdx.x & 127;
@@ -538,6 +540,9 @@ __device__ __forceinline__ bool flat_queries(const PrefixParams &p, uint8_t *sme
   if (items > 0 && (!wait_for<true>(smem_u32(&bars->q_empty), (items - 1) & 1, abort_flag, p) ||
                     !wait_for<true>(smem_u32(&bars->q_seen), (items - 1) & 1, abort_flag, p)))
     return false;
+  // (The softmax is done with the item before last, as it has begun the last one.)
+  if ((tid & 31) < kBadWords) bad[tid & 31] = 0;
+  __syncwarp();
   if (group == 0) reinterpret_cast<float *>(smem + C::OFF_QF)[tid] = back;
   tc_fence_after();   // (the last item's scores, read from here, are done)
 #pragma unroll 1
@@ -650,12 +655,9 @@ __device__ void flat_values(const PrefixParams &p, uint8_t *smem, FlatBars *bars
 
   bool ok = true;
   for (; ok && more; ++items, more = next_item(&bars->start, table, &walk, &item)) {
-    ok = flat_queries<D>(p, smem, bars, item, items, tmem, group);
-    if (!ok) break;
-    // (The softmax is done with the item before last, as it has begun the last one.)
     bad = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD) + ((items & 1) * 2 * kFlatGroupWarps + group * kFlatGroupWarps + tid / 32) * kBadWords;
-    if (lane < kBadWords) bad[lane] = 0;
-    __syncwarp();
+    ok = flat_queries<D>(p, smem, bars, item, items, tmem, group, bad);
+    if (!ok) break;
     int j = item.kv0 + ((tile ^ group) & 1);
     tile += item.kv1 - item.kv0;
     const int whole = p.Np / BN;   // of the prefix's tiles

@@ -1,0 +1,69 @@
+"""prefix_attn where a CTA takes many items one after the other, and cached values that are not numbers."""
+import pytest
+import torch
+
+from test_gpu_prefix import Problem, check, xs   # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def row_of(p, pages, i):
+    """(page, row in it) of place i of a list."""
+    size = p.codes[0].shape[2]
+    return int(pages[i // size]), i % size
+
+
+@pytest.mark.parametrize("Np", [0, 300])          # one tile, and several
+@pytest.mark.parametrize("Nq", [1, 33, 200])
+def test_cached_values_without_a_scale(xs, Nq, Np):
+    """A value row with the scale byte 255 beside a finite key makes NaN of the rows that see it and of no others."""
+    p = Problem(xs, 4, 4, 2, 128, Nq, Np, 60, [60, 3, 60, 17], "cache", "cache", seed=21)
+    ws = p.workspace()
+    before = p.run(ws).clone(), p.run().clone()
+    scale = p.scales[1]
+    page, row = row_of(p, p.kw["pages"][2], 5)
+    keep = int(scale[page, 0, row])
+    scale[page, 0, row] = 255
+    for got, ref in zip((p.run(ws), p.run()), before):
+        assert got[2, :2].isnan().all()
+        assert torch.equal(got[[0, 1, 3]], ref[[0, 1, 3]]) and torch.equal(got[2, 2:], ref[2, 2:])
+    scale[page, 0, row] = keep
+    if Np:
+        page, row = row_of(p, p.kw["prefix_pages"], 131)
+        scale[page, 1, row] = 255
+        for got, ref in zip((p.run(ws), p.run()), before):
+            assert got[:, 2:].isnan().all() and torch.equal(got[:, :2], ref[:, :2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 20, 50])
+@pytest.mark.parametrize("Np,Nk,own", [(100, 0, "bf16"), (0, 90, "cache"), (0, 90, "bf16"), (100, 90, "cache"), (300, 40, "bf16")])
+def test_items_in_turn(xs, d, Nq, Np, Nk, own):
+    """Five and more items a CTA, of one tile (a group of warps then has none of them) and of several; what one item
+    finds among its values is not another's."""
+    Hk = 5 * sms() + 3
+    p = Problem(xs, 2, Hk, Hk, d, Nq, Np, Nk, [Nk, Nk // 2], "cache", own, page=16, seed=22)
+    want = p.want()
+    check(p.run(), want)
+    g = torch.Generator(device="cuda").manual_seed(23)
+    bad = torch.rand(Hk, generator=g, device="cuda") < 0.3
+    if Np:
+        page, row = row_of(p, p.kw["prefix_pages"], 7)
+        p.scales[1][page, bad, row] = 255
+    elif own == "cache":
+        for b in range(2):
+            page, row = row_of(p, p.kw["pages"][b], 7)
+            p.scales[1][page, bad, row] = 255
+    else:
+        p.kw["v"][:, bad, 7, 3] = float("nan")
+    first = p.run().clone()
+    assert (first[:, bad].isnan().all() if Np or own == "cache" else first[:, bad][..., 3].isnan().all())
+    check(first[:, ~bad], (want[0][:, ~bad], want[1][:, ~bad]))
+    for _ in range(10):
+        again = p.run()
+        assert torch.equal(again[:, ~bad], first[:, ~bad]) and torch.equal(again.isnan(), first.isnan())
+    assert xs.last_device_status() == xs.OK
