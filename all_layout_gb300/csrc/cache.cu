@@ -153,12 +153,12 @@ __device__ __forceinline__ int scale_byte(uint32_t big) {
   return min(max(e, -120), 119) + 127;
 }
 
-// Place of row (b, h, n) in the cache, in rows; -1 where there is none.
-__device__ __forceinline__ long long row_at(const CacheParams &p, int b, int h, int n, long long first) {
-  const long long pos = first + n;
+// Place of a row of request b in the cache, in rows; -1 where there is none.
+__device__ __forceinline__ long long row_at(const CacheParams &p, int b, const TokenAt &t, long long first) {
+  const long long pos = first + t.n;
   const int page = page_of(p.lists, b, pos);
   if (page < 0) return -1;
-  return (static_cast<long long>(page) * p.Hk + h) * p.lists.page + (pos & (p.lists.page - 1));
+  return (static_cast<long long>(page) * p.Hk + t.h) * p.lists.page + (pos & (p.lists.page - 1));
 }
 
 template <class T, bool WRITE>
@@ -170,19 +170,17 @@ __global__ void __launch_bounds__(kCacheThreads, kBlocks<T, WRITE>) cache_kernel
   // Rows base, base + groups, ... of the Hk * N; the division is done for the first of them.
   const long long base = static_cast<long long>(blockIdx.x) * groups * kRows + group, rows = static_cast<long long>(p.Hk) * p.N;
   for (int b = blockIdx.y >> 1; b < p.B; b += gridDim.y >> 1) {
-    const int live = p.lens ? min(max(__ldg(p.lens + b), 0), p.N) : p.N;
+    const unsigned N = p.N, live = p.lens ? min(max(__ldg(p.lens + b), 0), p.N) : p.N;
     const long long first = p.start ? __ldg(p.start + b) : 0;
     T *const xb = const_cast<T *>(static_cast<const T *>(p.x[kv])) + b * p.x_b[kv] + c0;
-    const unsigned r0 = static_cast<unsigned>(min(base, rows));
-    int h = static_cast<int>(r0 / static_cast<unsigned>(p.N)), n = static_cast<int>(r0 - static_cast<unsigned>(h) * static_cast<unsigned>(p.N));
+    TokenAt t = token_at(static_cast<unsigned>(min(base, rows)), N);
     long long at[kRows];
     T *x[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      at[u] = h < p.Hk && n < live ? row_at(p, b, h, n, first) : -2;
-      x[u] = xb + h * p.x_h[kv] + n * p.x_n[kv];
-      n += groups;
-      while (n >= p.N && h < p.Hk) n -= p.N, ++h;
+      at[u] = t.h < p.Hk && t.n < live ? row_at(p, b, t, first) : -2;
+      x[u] = xb + t.h * p.x_h[kv] + t.n * p.x_n[kv];
+      step_token(t, groups, N, p.Hk);
     }
     if constexpr (WRITE) {
       Columns<T> c[kRows];

@@ -16,6 +16,27 @@ struct PageLists {
   int page, shift;       // rows of a page, a power of two
 };
 
+#ifdef __CUDACC__
+#define XS_HOST_DEVICE __host__ __device__
+#else
+#define XS_HOST_DEVICE
+#endif
+// Head and token of row h * N + n among H * N < 2^31; h = H: past the last one. The token is unsigned, as N and
+// a step together may pass 2^31.
+struct TokenAt {
+  int h;
+  unsigned n;
+};
+XS_HOST_DEVICE inline TokenAt token_at(unsigned row, unsigned N) {
+  const unsigned h = row / N;
+  return TokenAt{static_cast<int>(h), row - h * N};
+}
+// `by` rows on.
+XS_HOST_DEVICE inline void step_token(TokenAt &t, unsigned by, unsigned N, int H) {
+  t.n += by;
+  while (t.n >= N && t.h < H) t.n -= N, ++t.h;
+}
+
 xs_status check_cache(const xs_cache *c);
 xs_status check_pages(const xs_pages *l, int B);
 PageLists lists_of(const xs_cache &c, const xs_pages *l);

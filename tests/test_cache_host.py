@@ -82,3 +82,39 @@ def test_plain_form_against_torch():
     assert torch.equal(values(code, byte), code.view(torch.float8_e4m3fn).double() * torch.pow(2.0, byte.double() - 127)[:, None])
     top = scaled.abs().amax(-1)
     assert (top <= 448).all() and (top > 224).all()
+
+
+def test_rows_of_a_thread(tmp_path):
+    """The second row of a thread, where heads have few tokens and where tokens number nearly 2^31: one head's last rows
+    lead past the end, never to a token in front of the first."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "t.cpp"
+    src.write_text(r"""
+#include "all_layout_gb300/csrc/cache.h"
+#include <initializer_list>
+#include <cstdio>
+int main() {
+  const long long sizes[][2] = {{1, 1}, {24, 1}, {7, 3}, {3, 255}, {5, 257}, {1, 0x7fffffff}, {1, 0x7fffffff - 255}, {1, 0x7fffff00},
+                                {2, 0x3fffffff}, {0x7fffffff, 1}, {46341, 46340}, {1, 1 << 30}};
+  long long bad = 0;
+  for (const auto &s : sizes)
+    for (unsigned by = 16; by <= 256; by *= 2) {
+      const long long H = s[0], N = s[1], rows = H * N;
+      for (long long k = 0; k < 4096; ++k)
+        for (const long long row : {k, rows / 2 + k, rows - k}) {
+          if (row < 0 || row > rows) continue;
+          xs::TokenAt t = xs::token_at(static_cast<unsigned>(row), static_cast<unsigned>(N));
+          for (int u = 0; u < 2; ++u) {
+            const long long want = row + u * by;
+            bad += want < rows ? t.h != want / N || t.n != want % N : t.h < H;
+            xs::step_token(t, by, static_cast<unsigned>(N), static_cast<int>(H));
+          }
+        }
+    }
+  std::printf("%lld", bad);
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", root, str(src), "-o", str(tmp_path / "t")], check=True)
+    assert subprocess.run([str(tmp_path / "t")], capture_output=True, text=True, check=True).stdout == "0"
