@@ -382,32 +382,44 @@ __device__ __forceinline__ uint4 to_bf16(uint32_t c0, uint32_t c1, uint32_t byte
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A thread has one 16-byte group of every STEP-th row, so its place in the swizzle stays. Short loops: with all
-// groups unrolled the warps waited for instructions.
 // This warp has read a raw slot: its arrival at the slot's barrier.
 __device__ __forceinline__ void slot_read(uint32_t empty) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
 }
 
+// The top bit of each byte of `codes` that is a NaN (0x7f or 0xff); in the others nothing below it counts.
+__device__ __forceinline__ uint32_t nan_bits(uint32_t codes) { return (codes & 0x7f7f7f7fu) + 0x01010101u; }
+__device__ __forceinline__ uint32_t nan_bits(const uint4 &c) {
+  return nan_bits(c.x) | nan_bits(c.y) | nan_bits(c.z) | nan_bits(c.w);
+}
+// Whether any of two bf16 values is an infinity or NaN, for each of the halves.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
+
 // Codes and scale bytes of V's raw slot to a bf16 tile; `valid`, `entry`: of the sixteen rows of lanes 0-7
-// (valid_of); `bad`: this warp's words for requests whose values are not numbers.
+// (valid_of); `bad`: this warp's words for requests whose values are not numbers. A thread has one 16-byte group of
+// every STEP-th row, so its place in the swizzle stays. Short loops: with all groups unrolled the warps waited for
+// instructions. A tile whose rows all count, with scales of 2^7 at most and no code of a NaN, goes through the first
+// loop; another one (the codes show it at that loop's end, before anyone reads the operand) through the second, which
+// looks at each row. Looking for NaN's codes takes long history 92.5 us instead of 90; in a pass of its own, while the
+// operand's slot is still in use, 94.
 template <int D>
 __device__ __forceinline__ void convert_values(const uint8_t *src, uint8_t *dst, int valid, int entry, uint32_t *bad, uint32_t tid,
                                            uint32_t empty) {
   constexpr uint32_t CPR = D / 16, STEP = 32 * kFlatGroupWarps / CPR, U = BN / STEP;   // groups of a row's codes
   const uint32_t lane = tid & 31;
-  const uint32_t cc = tid % CPR, row0 = tid / CPR, first = cc % 4 * 2, odd = cc / 4 & 1;
+  // (Of eight lanes that store together four are in a row's second half: of the neighbouring row, whose swizzle
+  // gives them the other banks.)
+  const uint32_t cc = tid % CPR, row0 = tid / CPR ^ cc / 4, first = cc % 4 * 2;
   const uint32_t bytes = *reinterpret_cast<const uint32_t *>(src + BN * D + lane * 4);
   const uint8_t *scales = src + BN * D + row0;
-  src += tid * 16;
+  src += row0 * D + cc * 16;
   dst += (cc / 4) * kHalf + row0 * 128;
-  // (Of a group's two chunks the second half's lanes store the second one first, which spares conflicts.)
-  const uint32_t first0 = ((first + odd) ^ (row0 & 7)) * 16, second0 = ((first + 1 - odd) ^ (row0 & 7)) * 16;
+  const uint32_t first0 = (first ^ (row0 & 7)) * 16, second0 = ((first + 1) ^ (row0 & 7)) * 16;
   const bool clear = __any_sync(0xffffffffu, valid < 16);
   if (!clear && !__any_sync(0xffffffffu, __vcmpgtu4(bytes, 0x86868686u) != 0)) {
     uint4 c[2], next[2];
-    uint32_t byte[2], next_byte[2];
+    uint32_t byte[2], next_byte[2], nan = 0;
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) {
       c[k] = *reinterpret_cast<const uint4 *>(src + k * STEP * D);
@@ -426,24 +438,33 @@ __device__ __forceinline__ void convert_values(const uint8_t *src, uint8_t *dst,
 #pragma unroll
       for (uint32_t k = 0; k < 2; ++k) {
         uint8_t *to = dst + k * STEP * 128;
-        *reinterpret_cast<uint4 *>(to + first0) = to_bf16<true>(odd ? c[k].z : c[k].x, odd ? c[k].w : c[k].y, byte[k]);
-        *reinterpret_cast<uint4 *>(to + second0) = to_bf16<true>(odd ? c[k].x : c[k].z, odd ? c[k].y : c[k].w, byte[k]);
+        *reinterpret_cast<uint4 *>(to + first0) = to_bf16<true>(c[k].x, c[k].y, byte[k]);
+        *reinterpret_cast<uint4 *>(to + second0) = to_bf16<true>(c[k].z, c[k].w, byte[k]);
+        nan |= nan_bits(c[k]);
         c[k] = next[k];
         byte[k] = next_byte[k];
       }
     }
-    slot_read(empty);
-    return;
+    if (!__any_sync(0xffffffffu, (nan & 0x80808080u) != 0)) {
+      slot_read(empty);
+      return;
+    }
+    src -= U * STEP * D;
+    scales -= U * STEP;
+    dst -= U * STEP * 128;
   }
 #pragma unroll 1
   for (uint32_t i = 0; i < BN / STEP; ++i) {
     const uint4 c = *reinterpret_cast<const uint4 *>(src + i * STEP * D);
     const uint32_t byte = scales[i * STEP], row = row0 + i * STEP;
-    uint4 x = to_bf16<false>(odd ? c.z : c.x, odd ? c.w : c.y, byte), y = to_bf16<false>(odd ? c.x : c.z, odd ? c.y : c.w, byte);
+    uint4 x = to_bf16<false>(c.x, c.y, byte), y = to_bf16<false>(c.z, c.w, byte);
     const bool counts = static_cast<int>(row & 15) < __shfl_sync(0xffffffffu, valid, row >> 4);
     const int b = __shfl_sync(0xffffffffu, entry, row >> 4);
-    if (!counts || byte == kNanScale) x = y = make_uint4(0, 0, 0, 0);
-    if (counts && byte == kNanScale) atomicOr(bad + (b >> 5), 1u << (b & 31));
+    // (A scale byte of 255 makes NaN of every value, one past 246 infinities of large ones.)
+    const bool odd_row = (nan_bits(c) & 0x80808080u) != 0 || (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w) |
+                                                              not_finite(y.x) | not_finite(y.y) | not_finite(y.z) | not_finite(y.w)) != 0;
+    if (!counts || odd_row) x = y = make_uint4(0, 0, 0, 0);
+    if (counts && odd_row) atomicOr(bad + (b >> 5), 1u << (b & 31));
     uint8_t *to = dst + i * STEP * 128;
     *reinterpret_cast<uint4 *>(to + first0) = x;
     *reinterpret_cast<uint4 *>(to + second0) = y;
@@ -462,8 +483,7 @@ __device__ __noinline__ void clear_rows(uint8_t *tile, int valid, int entry, uin
     const bool counts = (row & 15) < __shfl_sync(0xffffffffu, valid, row >> 4);
     const int b = __shfl_sync(0xffffffffu, entry, row >> 4);
     uint4 v = *chunk;
-    auto odd = [](uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); };   // exponents of infinities and NaN
-    const uint32_t x = odd(v.x), y = odd(v.y), z = odd(v.z), w = odd(v.w);
+    const uint32_t x = not_finite(v.x), y = not_finite(v.y), z = not_finite(v.z), w = not_finite(v.w);
     if (counts && (x | y | z | w) == 0) continue;
     if (counts) atomicOr(bad + (b >> 5), 1u << (b & 31));
     v = counts ? make_uint4(v.x & ~x, v.y & ~y, v.z & ~z, v.w & ~w) : make_uint4(0, 0, 0, 0);

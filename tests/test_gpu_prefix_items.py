@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from cache_ref import values
 from test_gpu_prefix import Problem, check, xs   # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +68,37 @@ def test_items_in_turn(xs, d, Nq, Np, Nk, own):
         again = p.run()
         assert torch.equal(again[:, ~bad], first[:, ~bad]) and torch.equal(again.isnan(), first.isnan())
     assert xs.last_device_status() == xs.OK
+
+
+def run_both(p, ws):
+    """The call with cached parts read as they are, and with a workspace (for many rows: read back first)."""
+    return p.run().clone(), p.run(ws).clone()
+
+
+@pytest.mark.parametrize("code,byte", [(0x7f, 127), (0xff, 3), (0x7e, 254), (0xfe, 247), (0x7f, 140)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 33, 200])
+def test_cached_values_that_are_not_numbers(xs, Nq, d, code, byte):
+    """A NaN's code under an ordinary scale byte, or a value past the largest bf16: the rows that see it have no finite
+    number in its column, the others are as they were."""
+    p = Problem(xs, 4, 4, 2, d, Nq, 300, 60, [60, 3, 60, 17], "cache", "cache", seed=24)
+    ws = p.workspace()
+    before = run_both(p, ws)
+    page, row = row_of(p, p.kw["pages"][2], 5)
+    keep = p.codes[1][page, 0, row].clone(), int(p.scales[1][page, 0, row])
+    p.codes[1][page, 0, row, 37] = code
+    p.scales[1][page, 0, row] = byte
+    for got, ref in zip(run_both(p, ws), before):
+        assert not torch.isfinite(got[2, :2, :, 37]).any()
+        assert torch.equal(got[[0, 1, 3]], ref[[0, 1, 3]]) and torch.equal(got[2, 2:], ref[2, 2:])
+    p.codes[1][page, 0, row], p.scales[1][page, 0, row] = keep
+    for i in (131, 299):   # a whole tile of the prefix, and its last one
+        page, row = row_of(p, p.kw["prefix_pages"], i)
+        keep = p.codes[1][page, 1, row].clone(), int(p.scales[1][page, 1, row])
+        p.codes[1][page, 1, row, 40] = code
+        p.scales[1][page, 1, row] = byte
+        for got, ref in zip(run_both(p, ws), before):
+            assert not torch.isfinite(got[:, 2:, :, 40]).any() and torch.equal(got[:, :2], ref[:, :2])
+        p.codes[1][page, 1, row], p.scales[1][page, 1, row] = keep
+    for got, ref in zip(run_both(p, ws), before):
+        assert torch.equal(got, ref)
