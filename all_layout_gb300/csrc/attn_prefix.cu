@@ -22,6 +22,8 @@
 //
 // Waits are bounded: a role that gives up records a timeout; the softmax warps then run their
 // control flow to its end without waiting, the others drain what they issued.
+#include <cfloat>
+#include <climits>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>

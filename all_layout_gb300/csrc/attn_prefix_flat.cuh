@@ -11,6 +11,10 @@
 // row times a power of two: of a bf16 value's 8 significant bits e5m2 takes the first 3, and what that rounding
 // leaves, an integer of at most 16 in units of the last one, fits e4m3's 4. An MMA in 8 bits takes half as long, so
 // the two cost what one in bf16 would; its sums are as exact (a term 2^-26 of the others' came through).
+// Scores come out below 2^28 in magnitude (queries below 2^12, codes 448, 128 columns), and scales reach 2^119. So a key's
+// factor is its scale times kKeyDown, and a row's factor has the rest: the product of a score and a key's factor is finite, and
+// exact or off by 2^-150, times 2^128 at most. A row whose factor would not be finite (queries of 2^119 and more) has kKeyDown
+// taken back as its scores are masked.
 // Cached values. Their codes and scales go to raw slots, and two groups of four warps turn every second tile of them
 // into a bf16 operand (what it is multiplied with, the weights, needs bf16's range): a code's bits moved to bf16's
 // place stand for code * 2^-120, so one product with 2^(120 + e) is exact (e > 7 takes two).
@@ -35,6 +39,8 @@ constexpr int kFlatValues = 4, kFlatGroupWarps = 4, kFlatScores = 12, kFlatProdu
 // it arrives for the item's queries: that arrival alone orders them before the softmax's reading, as a group may
 // have no tile of the item to arrive for.
 constexpr int kBadWords = kPrefixEntries / 32 + 1;
+
+constexpr float kKeyDown = 1.f / (1 << 20);
 
 template <int D>
 struct FlatCfg {
@@ -749,8 +755,8 @@ __device__ void flat_scores(const PrefixParams &p, uint8_t *smem, FlatBars *bars
         // (The softmax is done with tile g - 4, as the scores of g - 1 followed the product of g - 3.)
         const uint32_t bytes = *reinterpret_cast<const uint32_t *>(smem + C::OFF_KS + slot * BN + lane * 4);
         reinterpret_cast<float4 *>(smem + C::OFF_FAC)[(g & 3) * (BN / 4) + lane] =
-            make_float4(power_of(bytes & 255) * p.scale_log2, power_of(bytes >> 8 & 255) * p.scale_log2,
-                        power_of(bytes >> 16 & 255) * p.scale_log2, power_of(bytes >> 24) * p.scale_log2);
+            make_float4(power_of(bytes & 255) * kKeyDown, power_of(bytes >> 8 & 255) * kKeyDown,
+                        power_of(bytes >> 16 & 255) * kKeyDown, power_of(bytes >> 24) * kKeyDown);
         if (g >= 2 && !wait(bars->pv_done[t], (g >> 1 & 1) ^ 1)) goto done;   // of tile g - 2
         __syncwarp();
         tc_fence_after();
@@ -843,10 +849,10 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m) {
   m = max3(m, __uint_as_float(s[30]), __uint_as_float(s[31]));
   return max3(m, mp[0], mp[1]);
 }
-// Scores of N times 32 keys in Tensor Memory, times fac where given, with those outside [lo, hi) -inf, whatever
-// they were. (In place and out of line: the softmax's loop stays short.)
+// Scores of N times 32 keys in Tensor Memory, times fac and back where fac is given, with those outside [lo, hi) -inf,
+// whatever they were. (In place and out of line: the softmax's loop stays short.)
 template <int N>
-__device__ __noinline__ void mask_scores(uint32_t taddr, const float *fac, int lo, int hi) {
+__device__ __noinline__ void mask_scores(uint32_t taddr, const float *fac, float back, int lo, int hi) {
 #pragma unroll 1
   for (int c = 0; c < N; ++c) {
     uint32_t s[32];
@@ -855,7 +861,7 @@ __device__ __noinline__ void mask_scores(uint32_t taddr, const float *fac, int l
     const uint32_t keep = bits_of(lo - 32 * c, hi - 32 * c);
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      if (fac) s[k] = __float_as_uint(__uint_as_float(s[k]) * fac[32 * c + k]);
+      if (fac) s[k] = __float_as_uint(__uint_as_float(s[k]) * fac[32 * c + k] * back);
       s[k] = keep >> k & 1 ? s[k] : 0xff800000u;
     }
     tmem_st32(taddr + 32 * c, s);
@@ -919,6 +925,12 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
     const PrefixRange own = range_of(p, table, row);
     wait(bars->q_full, items & 1);
     const float row_factor = reinterpret_cast<const float *>(smem + C::OFF_QF)[tid];   // (of rows in codes)
+    float row_scale = row_factor * (1.f / kKeyDown) * p.scale_log2;
+    int whole = NC * 32;   // a tile's keys from the first to here or further: no masking
+    if (row_scale > FLT_MAX) {   // (not a NaN)
+      whole = INT_MAX;
+      row_scale = fminf(row_factor * p.scale_log2, FLT_MAX);   // (finite, so that a score of 0 stays one)
+    }
     mbar_arrive(smem_u32(&bars->q_seen));
     float m = -INFINITY, l = 0.f;
     for (int j = item.kv0; j < item.kv1; ++j, ++step) {
@@ -941,14 +953,14 @@ __device__ void flat_softmax(const PrefixParams &p, uint8_t *smem, FlatBars *bar
         mbar_arrive(smem_u32(&bars->p_full[t]));
         continue;
       }
-      // Scores of cached keys are times the key's scale (and scale_log2) times the row's factor.
+      // Scores of cached keys are times the key's factor, then times the row's and the scale of all scores.
       bool times = is_cached(p, j);
-      const float scale = times ? row_factor : p.scale_log2;
+      const float scale = times ? row_scale : p.scale_log2;
       const float4 *fac = reinterpret_cast<const float4 *>(smem + C::OFF_FAC) + (step & 3) * (BN / 4) + copy * NC * 8;
       // Mostly a row sees all of the tile's keys or none: that takes no masking of scores.
       bool live = lo < NC * 32 && hi > 0;
-      if (__any_sync(0xffffffffu, live && (lo > 0 || hi < NC * 32))) {
-        mask_scores<NC>(tC, times ? reinterpret_cast<const float *>(fac) : nullptr, lo, hi);
+      if (__any_sync(0xffffffffu, live && (lo > 0 || hi < whole))) {
+        mask_scores<NC>(tC, times ? reinterpret_cast<const float *>(fac) : nullptr, whole == INT_MAX ? 1.f / kKeyDown : 1.f, lo, hi);
         times = false;
         live = true;
       }

@@ -453,7 +453,7 @@ __device__ void tall_softmax(const PrefixParams &p, uint8_t *smem, TallBars *bar
           mbar_arrive(p_full);
           continue;
         }
-        mask_scores<4>(tS, nullptr, lo, hi);
+        mask_scores<4>(tS, nullptr, 1.f, lo, hi);
       }
       uint32_t s[4][32];
       tmem_ld32(tS, s[0]);

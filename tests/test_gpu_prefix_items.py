@@ -102,3 +102,44 @@ def test_cached_values_that_are_not_numbers(xs, Nq, d, code, byte):
         p.codes[1][page, 1, row], p.scales[1][page, 1, row] = keep
     for got, ref in zip(run_both(p, ws), before):
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 33, 300])
+@pytest.mark.parametrize("e", [100, 113, 116, -112, -120])
+def test_scores_of_scales_far_from_queries(xs, Nq, d, e):
+    """Keys of some 2^e against queries of 2^-e: their products are ordinary scores. Other keys in the same tiles are far
+    smaller (at -120 all are alike, and queries reach 2^120); rows of queries of zeros see weights that are all the same."""
+    B, H, Hk, Np, Nk = 2, 2, 1, 260, 140
+    p = Problem(xs, B, H, Hk, d, Nq, Np, Nk, [140, 0], "cache", "cache", page=16, seed=25)
+    g = torch.Generator(device="cuda").manual_seed(26)
+    t = p.scales[0]
+    far = torch.rand(t.shape, generator=g, device="cuda") < 0.5
+    lower = torch.randint(-120, e - 30 if e > 0 else max(e - 3, -119), t.shape, generator=g, device="cuda")
+    t.copy_((torch.where(far, torch.full_like(lower, e), lower) + 127).to(torch.uint8))
+    p.q.copy_((p.q.double() * 2.0 ** (-e - 2)).bfloat16())
+    p.q[0, 1, 0] = 0
+    n = p.kw["prefix_pages"].long()
+    k = values(p.codes[0], t)
+    p.prefix[0] = k[n].transpose(0, 1).flatten(1, 2)[:, :Np]
+    p.own[0] = torch.stack([k[p.kw["pages"][b].long()].transpose(0, 1).flatten(1, 2)[:, :Nk] for b in range(B)])
+    used = torch.zeros(t.shape[0], 16, dtype=torch.bool, device="cuda")
+    for pages, count in ((p.kw["prefix_pages"], Np), (p.kw["pages"][0], Nk)):
+        for i in range(count):
+            used[row_of(p, pages, i)] = True
+    for behind in (0, 127, 246, 254, 255):     # scale bytes of rows that no request sees
+        t.masked_fill_(~used[:, None], behind)
+        p.test()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_requests_of_different_scales_in_one_tile(xs, d):
+    """One request's keys are large and its queries small, the other's the reverse."""
+    p = Problem(xs, 2, 2, 1, d, 1, 0, 48, [48, 48], "cache", "cache", page=16, seed=27)
+    t = p.scales[0]
+    for b, e in enumerate((116, -114)):
+        t[p.kw["pages"][b].long()] = e + 127
+        p.q[b] = (p.q[b].double() * 2.0 ** (-e - 2)).bfloat16()
+    k = values(p.codes[0], t)
+    p.own[0] = torch.stack([k[p.kw["pages"][b].long()].transpose(0, 1).flatten(1, 2)[:, :48] for b in range(2)])
+    p.test()
