@@ -143,3 +143,37 @@ def test_requests_of_different_scales_in_one_tile(xs, d):
     k = values(p.codes[0], t)
     p.own[0] = torch.stack([k[p.kw["pages"][b].long()].transpose(0, 1).flatten(1, 2)[:, :48] for b in range(2)])
     p.test()
+
+
+@pytest.mark.parametrize("prefix,own", [("cache", "cache"), ("cache", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("d,B,Nq", [(128, 2, 1), (64, 3, 17), (128, 2, 50), (64, 1, 128)])      # 4, 2, 1 and 1 copies of the rows
+@pytest.mark.parametrize("full", [1, 2, 3])
+def test_units_past_full_waves(xs, full, d, B, Nq, prefix, own):
+    """A few units more than fill all SMs once, twice, three times, one tile of rows each: with a workspace the last ones
+    (more than SMs) are cut after none, one and two whole units a CTA, without one a CTA takes up to four."""
+    H = full * sms() + 9
+    p = Problem(xs, B, H, H, d, Nq, 1500, 140, [140, 0, 33][:B], prefix, own, page=64, seed=30 + full)
+    want, ws = p.want(), p.workspace()
+    whole, cut = p.run(), p.run(ws)
+    check(whole, want, "whole units")
+    check(cut, want, "cut units")
+    assert not torch.equal(whole, cut)     # (other sums: some were cut)
+    for _ in range(5):
+        assert torch.equal(p.run(ws.fill_(0xff)), cut) and torch.equal(p.run(), whole)
+    assert xs.last_device_status() == xs.OK
+
+
+@pytest.mark.parametrize("own", ["cache", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("full", [1, 2, 3])
+def test_pairs_of_tiles_past_full_waves(xs, full, d, own):
+    """The same with many rows: five units of two row tiles a head, requests whose ends lie inside one."""
+    Hk = (full * sms() + 9 + 4) // 5
+    p = Problem(xs, 3, Hk, Hk, d, 300, 2500, 400, [400, 0, 129], "bf16", own, page=64, seed=40 + full)
+    want, ws = p.want(), p.workspace()
+    got = p.run(ws)
+    check(got, want, "cut units")
+    for _ in range(5):
+        assert torch.equal(p.run(ws.fill_(0xff)), got)
+    check(p.run(), want, "whole units")
+    assert xs.last_device_status() == xs.OK
