@@ -177,3 +177,30 @@ def test_pairs_of_tiles_past_full_waves(xs, full, d, own):
         assert torch.equal(p.run(ws.fill_(0xff)), got)
     check(p.run(), want, "whole units")
     assert xs.last_device_status() == xs.OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 20, 50, 200])
+def test_every_code(xs, Nq, d):
+    """All finite codes of keys and values, zeros and the format's subnormals among them, under scales down to 2^-120 (values)."""
+    p = Problem(xs, 2, 2, 1, d, Nq, 300, 70, [70, 13], "cache", "cache", page=32, seed=28, scale=2.0 ** -7)
+    g = torch.Generator(device="cuda").manual_seed(29)
+    for c in p.codes:
+        size = torch.randint(0, 127, c.shape, generator=g, device="cuda", dtype=torch.uint8)
+        c.copy_(size | (c & 0x80))
+    p.scales[0].copy_(torch.randint(112, 119, p.scales[0].shape, generator=g, device="cuda", dtype=torch.uint8))
+    p.scales[1].copy_(torch.where(torch.rand(p.scales[1].shape, generator=g, device="cuda") < 0.5, 7, 150).to(torch.uint8))
+    k, v = (values(p.codes[i], p.scales[i]) for i in range(2))
+    n = p.kw["prefix_pages"].long()
+    for i, x in enumerate((k, v)):
+        p.prefix[i] = x[n].transpose(0, 1).flatten(1, 2)[:, :300]
+        p.own[i] = torch.stack([x[p.kw["pages"][b].long()].transpose(0, 1).flatten(1, 2)[:, :70] for b in range(2)])
+    p.test()
+    p.scales[1].fill_(7)       # (values below bf16's normal ones, in tiles of the short loop too)
+    v = values(p.codes[1], p.scales[1])
+    p.prefix[1] = v[n].transpose(0, 1).flatten(1, 2)[:, :300]
+    p.own[1] = torch.stack([v[p.kw["pages"][b].long()].transpose(0, 1).flatten(1, 2)[:, :70] for b in range(2)])
+    want, ws = p.want(), p.workspace()
+    for got in (p.run(), p.run(ws)):
+        # as in check, with a subnormal result's rounding, 2^-134, and fp32's own at most 2^-149 a key in the sums
+        assert ((got.double() - want[0]).abs() <= 2.0 ** -8 * want[0].abs() + (2.0 ** -8 + 2.0 ** -11) * want[1] + 2.0 ** -133).all()
