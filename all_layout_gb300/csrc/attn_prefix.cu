@@ -2,7 +2,7 @@
 // Tensor Memory, TMA).
 //
 // Per request b and query head h, whose k/v head is hk:
-//     o = softmax(q [K_p | K_b]^T s) [V_p | V_b],   s = 1/sqrt(d),
+//     o = softmax(q [K_p | K_b]^T s) [V_p | V_b],   s the caller's scale,
 // K_p, V_p [Np][d] the same for every request, K_b, V_b [kv_len[b]][d] its own; both in bf16
 // tensors or in pages of an e4m3 cache (cache.cu). A row without any key gives zeros.
 //
@@ -482,13 +482,13 @@ cudaError_t launch_tall(const PrefixParams &p, int grid, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_join(const PrefixParams &p, int grid, cudaStream_t s) {
+cudaError_t launch_join(const PrefixParams &p, int grid, int sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   // Slices of the columns: about eight blocks an SM at most, of the units that may be cut.
   const int rows = ((p.row_tile < p.rows ? p.row_tile : p.rows) + 31) / 32;
   const long long cut = static_cast<long long>(p.n_units) - static_cast<long long>(p.waves) * grid;
   int slices = D / 8;
-  while (slices > 1 && (cut < grid ? cut : grid) * rows * slices > 8 * 152) slices /= 2;
+  while (slices > 1 && (cut < grid ? cut : grid) * rows * slices > 8 * sms) slices /= 2;
   cfg.gridDim = dim3(static_cast<unsigned>(cut < grid ? cut : grid), rows, slices);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
@@ -512,8 +512,8 @@ cudaError_t launch_prefix_tall(const PrefixParams &p, int d, int grid, cudaStrea
   return d == 64 ? launch_tall<64>(p, grid, s) : launch_tall<128>(p, grid, s);
 }
 
-cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, cudaStream_t s) {
-  return d == 64 ? launch_join<64>(p, grid, s) : launch_join<128>(p, grid, s);
+cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, int sms, cudaStream_t s) {
+  return d == 64 ? launch_join<64>(p, grid, sms, s) : launch_join<128>(p, grid, sms, s);
 }
 
 }  // namespace xs

@@ -28,9 +28,9 @@
 // Tensor Memory: S0 [0,128) S1 [128,256) O [256,256+d) the queries in 8 bits [384,384+d/2), in bf16 [448,448+d/2);
 // P_t over S_t's first 64 columns. Scores are double-buffered: QK(i+1) runs beside tile i's softmax.
 // Queries are read from Tensor Memory because shared memory is what the SM has least of here. Measured at one token
-// for 16 requests of 24 heads behind 64K keys (420 MB of codes): 90 us; with K's codes turned to fp16 operands by four
-// warps and V's by four others 120 us, the warps of V setting the pace; a KV tile then takes 1560 cycles, of which
-// HBM asks 1450 at this SM's share.
+// for 16 requests of 24 heads behind 64K keys (420 MB of codes): 93 us; with K's codes turned to fp16 operands by four
+// warps and V's by four others 120 us, the warps of V setting the pace. A KV tile takes 0.81 us (the same behind 128K
+// keys: 159 us), 1570 cycles, of which HBM asks 1450 at this SM's share; start, own tiles and join are the other 28 us.
 
 constexpr int kFlatValues = 4, kFlatGroupWarps = 4, kFlatScores = 12, kFlatProducts = 13, kFlatLoadKeys = 14;   // warps
 // Requests whose values are not numbers, a bit each and one (kPrefixEntries) for the prefix: by item modulo two
@@ -876,7 +876,8 @@ __device__ __noinline__ void zero_weights(uint32_t taddr) {
   tmem_st32(taddr, zero);
   tmem_st32(taddr + 32, zero);
 }
-// Weights 2^(s * scale - m) of 32 scores as bf16 pairs, and their sums added to `sum`, in fp32 pairs: an add for two
+// Weights 2^(s * scale - m) of 32 scores as bf16 pairs (the type of V, as both operands of an MMA have one: off by at most
+// 2^-8 of a weight, as the output's own rounding is of it), and their sums added to `sum`, in fp32 pairs: an add for two
 // weights (in the tall kernel four images took 983 us with an add for each, 943 so).
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scale2, uint64_t negm2, uint32_t (&pk)[16],
                                           uint64_t (&sum)[2]) {

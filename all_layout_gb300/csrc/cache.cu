@@ -5,8 +5,8 @@
 //     e = the least integer with a <= 448 * 2^e   (in [-120, 119]; 0 for a row of zeros),
 //     code = e4m3(x * 2^-e), to nearest even,   scale byte = e + 127,
 // and what a code stands for is code * 2^e. A power of two costs no precision beside a
-// scale of full width (the codes are floating-point numbers themselves; only what lies 2^15
-// below the row's maximum loses bits to the range), and makes both x * 2^-e and code * 2^e
+// scale of full width (the codes are floating-point numbers themselves: values down to 2^-13 of
+// the row's maximum keep all 4 bits, and smaller ones are off by at most 2^-10 * 2^e), and makes both x * 2^-e and code * 2^e
 // exact, so that a code is the only rounding between a key and what attention sees of it:
 // e4m3 has 4 significant bits, bf16 8. A row that holds a NaN or an infinity gets the scale
 // byte 255 and reads as NaN.
@@ -17,7 +17,8 @@
 // pairs, the maximum of a row comes by shuffles; and a thread's two rows are loaded before the first
 // is used. Measured at 65536 rows of 24 heads of 128 (1.21 GB): read 178 us = 6.8 TB/s, write 202 us
 // = 6.0 TB/s; with 8 columns a lane and four rows 246 and 382 us, with 16 and one row 211 and 243,
-// with four rows 194 and 194 but the small calls up to 1.6 times as long.
+// with four rows 194 and 194 but the small calls up to 1.6 times as long. To and from fp32 (2.02 GB): read 384 us = 5.3 TB/s,
+// write 315 us = 6.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -77,7 +77,7 @@ int prefix_part_floats(int d, int rows);   // fp32 values of one piece's partial
 cudaError_t launch_prefix_flat(const PrefixParams &p, int d, int grid, cudaStream_t s);
 // Many rows: pairs of 128-row tiles; keys and values in tensors.
 cudaError_t launch_prefix_tall(const PrefixParams &p, int d, int grid, cudaStream_t s);
-// Joins the pieces of cut units, after a launch that had split set.
-cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, cudaStream_t s);
+// Joins the pieces of cut units, after a launch of `grid` CTAs that had split set; sms: of the device.
+cudaError_t launch_prefix_join(const PrefixParams &p, int d, int grid, int sms, cudaStream_t s);
 
 }  // namespace xs

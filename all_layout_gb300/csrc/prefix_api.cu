@@ -117,15 +117,15 @@ Choice choose(const Shape &s, bool tall, int sms, unsigned long long room) {
   const double top = entry >= c.row_tile ? (met > c.n_tiles ? 2 : 1)
                                          : std::fmin(s.B, (c.row_tile + entry - 1) / entry + (c.row_tile % entry == 0 ? 0 : 1));
   const double prefix = (s.Np + kTileRows - 1) / kTileRows;
-  // Times of a KV tile (GB300, us; 64 tiles a CTA, 128, 64 and 32 rows): the flat kernel at d = 128 1.74, 1.61
-  // and 1.57 with keys in tensors, 1.82, 1.19 and 1.03 with cached ones; at d = 64 1.26, 0.94 and 0.93, 1.59, 1.0
-  // and 0.85. The tall kernel's, for a pair of row tiles: 1.4 and 1.05. The join: 6 us, in the tall kernel 10.
+  // Times of a KV tile (GB300, us; 64 tiles a CTA, 128, 64 and 32 rows): the flat kernel at d = 128 1.76, 1.64
+  // and 1.60 with keys in tensors, 1.79, 1.23 and 1.06 with cached ones; at d = 64 1.22, 0.95 and 0.93, 1.53, 1.03
+  // and 0.87. The tall kernel's, for a pair of row tiles: 1.4 and 1.05. The join: 6 us, in the tall kernel 10.
   const bool half = s.d == 64, one = c.copies == 1;
   const double us = tall ? (half ? 1.05 : 1.4)
                          : s.cached ? (half ? (one ? 1.59 : 0.93) : one ? 1.82 : 1.1) : half ? (one ? 1.26 : 0.94) : one ? 1.74 : 1.6;
   // What a unit costs beside its tiles (its queries, its epilogue, the pipeline's start and end), and an own tile
-  // whose rows are of several requests, in tiles (see place_of): one token for 8 requests takes 27.6 us so and 33
-  // with 2 and 1, for 16 behind 64K keys 92 and 105; the tall kernel's costs are 2 and 1.
+  // whose rows are of several requests, in tiles (see place_of): one token for 8 requests takes 28 us so and 33
+  // with 2 and 1, for 16 behind 64K keys 93 and 105; the tall kernel's costs are 2 and 1.
   c.unit_cost = tall ? 2 : 8;
   c.own_cost = !tall && top > 1 ? 2 : 1;
   const double own_places = own * c.own_cost;
@@ -179,7 +179,7 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
   }
   if (st == XS_ERR_UNSUPPORTED || (d != 64 && d != 128)) return XS_ERR_UNSUPPORTED;
   if (Np > kMostLength || Nk > kMostLength || Nq > kMostLength) return XS_ERR_UNSUPPORTED;
-  // Entries of a launch: as many as the kernels' table holds, and as their packed keys stay below 2^30 for.
+  // Entries of a launch: as many as the kernels' table holds, and as their packed keys stay within 2^29 for.
   const long long padded = (static_cast<long long>(Nk) + kTileRows - 1) / kTileRows * kTileRows;
   int chunk = kPrefixEntries;
   if (padded > 0 && kMostLength / padded < chunk) chunk = static_cast<int>(kMostLength / padded);
@@ -329,7 +329,7 @@ xs_status prefix_call(const xs_prefix_args *a, void *o, const long long *o_strid
     p.waves = c.plan.waves;
     p.grid = c.plan.grid;
     if ((tall ? launch_prefix_tall : launch_prefix_flat)(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;
-    if (p.split && launch_prefix_join(p, d, c.plan.grid, s) != cudaSuccess) return XS_ERR_CUDA;
+    if (p.split && launch_prefix_join(p, d, c.plan.grid, sms, s) != cudaSuccess) return XS_ERR_CUDA;
   }
   return XS_OK;
 }

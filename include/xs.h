@@ -383,7 +383,10 @@ xs_status xs_diff_workspace_bytes(int B, int H, int Nq, int Nk, int d, int norm,
  * e4m3, each row with a power of two as its scale. Row i of head h of a page is
  * page * H_kv * page_size + h * page_size + i; its values are code * 2^(byte - 127),
  * codes in k or v at row * d, the byte in k_scale or v_scale at row. A byte of 255
- * makes the whole row NaN. The caller owns all four arrays (device). */
+ * makes the whole row NaN, the codes 0x7f and 0xff are NaN under any byte. xs_cache_write
+ * gives bytes from 7 to 246 and 255; under bytes from 247 to 254 what is past the largest
+ * bf16 counts as an infinity in bf16 outputs and among values under attention, and may
+ * do so among keys. The caller owns all four arrays (device). */
 typedef struct {
   void *k, *v;                         /* [n_pages][H_kv][page_size][d] e4m3 */
   unsigned char *k_scale, *v_scale;    /* [n_pages][H_kv][page_size] */
@@ -463,8 +466,10 @@ typedef struct {
  * that meets cached keys may be taken in two 8-bit parts: exact for values down to 2^-13 of its
  * largest magnitude, to within 2^-21 of that below. A NaN or infinity in a query, or among
  * the keys and values that count, makes NaN of whole rows (or of what the formula gives) of the
- * requests that see it, and touches no other request. A cached key whose place no page holds
- * counts as NaN. Outputs must not overlap each other or an input. Nq, Np, Nk: any size, also 0
+ * requests that see it, and touches no other request; a row whose scores are all -inf (they
+ * overflowed) gives zeros. Scores times scale are taken below 2^30 in magnitude (beyond it
+ * fp32 no longer holds a weight's exponent, and a row may come out as zeros or not a number).
+ * A cached key whose place no page holds counts as NaN. Outputs must not overlap each other or an input. Nq, Np, Nk: any size, also 0
  * or 1.
  *   o, o_stride  [B][H][Nq][d] bf16 (device), strides in elements (batch, head, row)
  *   out_shards   host array of P device pointers, shard p [B][Nq/P][H][d] bf16, as in
